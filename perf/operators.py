@@ -117,7 +117,7 @@ def _plain_pack(x, fmt: str, g):
     else:
         s8 = (amax / (6.0 * g)).clamp(max=448.0).to(torch.float8_e4m3fn)
         t = s8.to(torch.float32) * g
-        y = torch.where(t > 0, x / t, 0.0)
+        y = torch.where(t >= 2.0 ** -126, x * (1.0 / t), 0.0)
         s = torch.where(fine, s8.view(torch.uint8), 0x7F)
     a = y.abs()
     q = (a > 0.25).to(torch.uint8)
@@ -330,7 +330,7 @@ def work(case):
 
 def _exact_pack(x, fmt, g):
     """Bytes from the definition in 64 bits: nearest of the listed values (ties to the even code); the nv form's
-    divisions and product are defined as rounded to 32 bits."""
+    quotient, products and reciprocal are defined as rounded to 32 bits."""
     rows, K = x.shape
     bs = BLOCK[fmt]
     Kp = _up(K, 32)
@@ -348,7 +348,7 @@ def _exact_pack(x, fmt, g):
         want = (amax.float() / (6 * g.float())).double().clamp(max=448.0)
         s = _nearest(want, steps)
         t = (steps[s.long()].float() * g.float()).unsqueeze(-1)
-        y = torch.where(t > 0, x.float() / t, torch.zeros_like(t)).double()
+        y = torch.where(t >= 2.0 ** -126, x.float() * t.double().reciprocal().float(), torch.zeros_like(t)).double()
     q = _nearest(y.abs(), torch.tensor(E2M1[:8], dtype=torch.float64, device=x.device))
     q = (q + 8 * torch.signbit(y)).reshape(rows, Kp).to(torch.uint8)
     out = torch.zeros((rows, _scale_pitch(fmt, K)), dtype=torch.uint8, device=x.device)
