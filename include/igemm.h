@@ -352,6 +352,115 @@ IGEMM_API int igemm_time_next_gemm(cudaEvent_t start, cudaEvent_t stop);
  */
 IGEMM_API int unpack_int4(const uint8_t *packed, int8_t *logical, int64_t rows, int64_t K, cudaStream_t stream);
 
+/*
+ * Microscaled 4-bit floating point (OCP microscaling formats; nvfp4), and the
+ * passes of a mixture-of-experts layer around its products.
+ *
+ * Operand format, shared by packing and products.  A matrix of `rows` rows of K
+ * values is held as
+ *   codes  [rows, ceil(K/32) * 16] bytes: two e2m1 values per byte, the even k in
+ *          the low nibble (values 0, 0.5, 1, 1.5, 2, 3, 4, 6, bit 3 the sign);
+ *          codes past K are zero
+ *   scales [rows, P] bytes: one per block of 32 k (mxfp4: ue8m0, 2^(byte - 127),
+ *          0xFF = NaN) or 16 k (nvfp4: e4m3, 0x7F = NaN), rows padded to P =
+ *          16 * ceil(K/512) (mxfp4) or 16 * ceil(K/256) (nvfp4) bytes;
+ *          products ignore the padding bytes, packing zeroes them
+ * both row-major and 16-byte aligned (IGEMM_MISALIGNED otherwise).  Scales stay
+ * row-major: there is no tiled layout to convert to.
+ * K <= IGEMM_FP4_MAX_K (IGEMM_OVERFLOW_BOUND); any K, whole blocks or not.
+ */
+typedef enum igemm_type { IGEMM_F32 = 0, IGEMM_BF16 = 1, IGEMM_F16 = 2 } igemm_type;
+#define IGEMM_FP4_MAX_K (1 << 22)
+
+/*
+ * Quantise x into codes and scales.
+ *   mxfp4: per block e = max(floor(log2(max |x|)) - 2, -127), scale byte e + 127,
+ *          codes e2m1(x * 2^-e) (an all-zero block: e = -127)
+ *   nvfp4: per block s = e4m3(min(max |x| / (6 g), 448)), t = s * g, codes
+ *          e2m1(x * (1 / t)), zero where t < 2^-126; g = *tensor_scale (device,
+ *          finite and positive), 1 for a null pointer; every operation float32
+ * rounded to nearest, ties to even, saturating at 6.  A block that holds a NaN
+ * or an infinity gets the NaN scale and zero codes.
+ *   x       of x_type (igemm_type): element (r, k) at x[r * ld + k], ld >= K, or,
+ *           with transposed != 0, at x[k * ld + r], ld >= x_rows (device, naturally
+ *           aligned; rows that start on 16-byte boundaries load fastest)
+ *   index   [rows] or null: output row r is x row index[r], a row of zeros where
+ *           index[r] is outside [0, x_rows) (not with transposed:
+ *           IGEMM_UNSUPPORTED_SHAPE); null needs x_rows >= rows
+ * rows == 0 or K == 0 is a no-op.
+ */
+IGEMM_API int pack_mxfp4(const void *x, int x_type, int64_t ld, int transposed, const int32_t *index, int x_rows,
+                         uint8_t *codes, uint8_t *scales, int rows, int K, cudaStream_t stream);
+IGEMM_API int pack_nvfp4(const void *x, int x_type, int64_t ld, int transposed, const int32_t *index, int x_rows,
+                         const float *tensor_scale, uint8_t *codes, uint8_t *scales, int rows, int K,
+                         cudaStream_t stream);
+
+/*
+ * C[m,n] = alpha * sum_k (a[m,k] sfa[m,block]) (b[n,k] sfb[n,block]), accumulated in
+ * float32 on the tensor cores in a fixed order (repeated calls give the same
+ * bits) and rounded once to c_type.
+ *   A, SFA  codes and scales of M rows of K; B, SFB of N rows (device)
+ *   alpha   nvfp4: [1] float32 (device), or null for 1: the product of the operands'
+ *           tensor scales
+ *   C       [M, N] of c_type, row-major, naturally aligned; every element written
+ * A NaN scale makes its row (column) of C NaN.  M == 0 or N == 0 is a no-op,
+ * K == 0 zeroes C.
+ */
+IGEMM_API int igemm_mxfp4(const uint8_t *A, const uint8_t *B, const uint8_t *SFA, const uint8_t *SFB, void *C,
+                          int c_type, int M, int N, int K, cudaStream_t stream);
+IGEMM_API int igemm_nvfp4(const uint8_t *A, const uint8_t *B, const uint8_t *SFA, const uint8_t *SFB,
+                          const float *alpha, void *C, int c_type, int M, int N, int K, cudaStream_t stream);
+
+/*
+ * The same products grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of A
+ * times the transpose of B[e], for e = 0 .. E-1.
+ *   A, SFA   codes and scales of `rows` rows; B, SFB of E * N rows ([E, N, ...])
+ *   offsets  [E + 1] int32, non-decreasing (device; never read on the host); values
+ *            outside [0, rows] are clamped, a group whose end is not past its
+ *            start is empty
+ *   alpha    nvfp4: [E] float32, or null for 1
+ *   C        [rows, N]; rows of no group are left as they were
+ * E <= 1024 and E * N < 2^31 - 512 (IGEMM_UNSUPPORTED_SHAPE, as K == 0 is);
+ * rows, N or E of 0 is a no-op.
+ */
+IGEMM_API int igemm_mxfp4_grouped(const uint8_t *A, const uint8_t *B, const uint8_t *SFA, const uint8_t *SFB,
+                                  const int32_t *offsets, void *C, int c_type, int rows, int E, int N, int K,
+                                  cudaStream_t stream);
+IGEMM_API int igemm_nvfp4_grouped(const uint8_t *A, const uint8_t *B, const uint8_t *SFA, const uint8_t *SFB,
+                                  const int32_t *offsets, const float *alpha, void *C, int c_type, int rows, int E,
+                                  int N, int K, cudaStream_t stream);
+
+/*
+ * Routing: the k largest logits of each token, their weights, and the pairs
+ * (token, choice) sorted by expert, ties by token.
+ *   logits   [T, E] of logits_type (device); equal logits: the lowest expert first;
+ *            -inf and NaN are never chosen
+ *   experts  [T, k] int32, by falling logit; -1 where fewer than k can be chosen
+ *   weights  [T, k] float32: exp(logit - max) over the sum of the chosen
+ *            (normalize != 0) or of all E (normalize == 0); 0 where experts is -1
+ *   offsets  [E + 1] int32: the sorted pairs of expert e are offsets[e] ..
+ *            offsets[e+1] - 1
+ *   tokens   [T * k] int32: token of each sorted pair, -1 past offsets[E] (the
+ *            `index` of pack_*)
+ *   slots    [T, k] int32: sorted place of each pair, -1 where experts is -1
+ * E <= 1024, k <= 32, k <= E, T * k < 2^31 (IGEMM_UNSUPPORTED_SHAPE).  T == 0 or
+ * k == 0 zeroes offsets.  More than 64 tokens use a workspace of about E * T / 16
+ * bytes from the library's pool.
+ */
+IGEMM_API int igemm_moe_route(const void *logits, int logits_type, int32_t *experts, float *weights,
+                              int32_t *offsets, int32_t *tokens, int32_t *slots, int T, int E, int k, int normalize,
+                              cudaStream_t stream);
+
+/*
+ * out[t,:] = sum_j weights[t,j] * Y[slots[t,j],:], float32 sums in the order of j,
+ * rounded once; slots outside [0, T * k) add nothing.
+ *   Y [T * k, N], out [T, N] of `type` (device, naturally aligned); slots, weights
+ *   [T, k] as igemm_moe_route writes them; k <= 32 (IGEMM_UNSUPPORTED_SHAPE)
+ * T == 0 or N == 0 is a no-op, k == 0 zeroes out.
+ */
+IGEMM_API int igemm_moe_combine(const void *Y, const int32_t *slots, const float *weights, void *out, int type, int T,
+                                int k, int N, cudaStream_t stream);
+
 /* Static, human-readable text for an igemm_status value. */
 IGEMM_API const char *igemm_strerror(int code);
 

@@ -24,6 +24,9 @@ __all__ = [
     "igemm_strerror",
     "igemm_last_status", "igemm_watchdog_selftest", "igemm_kernels_launched", "igemm_time_next_gemm",
     "igemm_skinny_plan", "igemm_ss_plan", "igemm_route",
+    "pack_mxfp4", "pack_nvfp4", "igemm_mxfp4", "igemm_nvfp4",
+    "igemm_mxfp4_grouped", "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine",
+    "fp4_code_bytes", "mxfp4_scale_pitch", "nvfp4_scale_pitch",
     "EXPORTED_SYMBOLS", "LIB_PATH", "build_library",
 ]
 
@@ -31,7 +34,9 @@ EXPORTED_SYMBOLS = ("i4i4_gemm", "i4i4_gemm_noalloc", "w4a8_gemm", "i4i4_gemm_ho
                     "fp8_gemm_e5m2", "fp8_blockscaled_gemm", "fp8_blockscaled_gemm_e5m2", "fp8_gemm_host",
                     "fp8_gemm_e5m2_host", "fp8_blockscaled_gemm_host", "fp8_blockscaled_gemm_e5m2_host", "pack_int4", "unpack_int4", "igemm_strerror", "igemm_last_status",
                     "igemm_watchdog_selftest", "igemm_kernels_launched",
-                    "igemm_time_next_gemm", "igemm_skinny_plan", "igemm_ss_plan", "igemm_route")
+                    "igemm_time_next_gemm", "igemm_skinny_plan", "igemm_ss_plan", "igemm_route",
+                    "pack_mxfp4", "pack_nvfp4", "igemm_mxfp4", "igemm_nvfp4", "igemm_mxfp4_grouped",
+                    "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine")
 
 IGEMM_OK = 0
 IGEMM_INVALID_ARGUMENT = 1
@@ -104,6 +109,17 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.igemm_route.restype = i
     lib.igemm_kernels_launched.argtypes = []
     lib.igemm_kernels_launched.restype = ctypes.c_uint64
+    lib.pack_mxfp4.argtypes = [p, i, i64, i, p, i, p, p, i, i, p]
+    lib.pack_nvfp4.argtypes = [p, i, i64, i, p, i, p, p, p, i, i, p]
+    lib.igemm_mxfp4.argtypes = [p, p, p, p, p, i, i, i, i, p]
+    lib.igemm_nvfp4.argtypes = [p, p, p, p, p, p, i, i, i, i, p]
+    lib.igemm_mxfp4_grouped.argtypes = [p, p, p, p, p, p, i, i, i, i, i, p]
+    lib.igemm_nvfp4_grouped.argtypes = [p, p, p, p, p, p, p, i, i, i, i, i, p]
+    lib.igemm_moe_route.argtypes = [p, i, p, p, p, p, p, i, i, i, i, p]
+    lib.igemm_moe_combine.argtypes = [p, p, p, p, i, i, i, i, p]
+    for name in ("pack_mxfp4", "pack_nvfp4", "igemm_mxfp4", "igemm_nvfp4", "igemm_mxfp4_grouped",
+                 "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine"):
+        getattr(lib, name).restype = i
     lib.igemm_watchdog_selftest.argtypes = [ctypes.c_uint32, p]
     lib.igemm_watchdog_selftest.restype = i
     return lib
@@ -275,6 +291,145 @@ def unpack_int4(packed, logical, rows: int, K: int, stream=None) -> None:
     _check(load().unpack_int4(_arg(packed, _n(rows, K) // 2, True, "unpack_int4: packed"),
                               _arg(logical, _n(rows, K), True, "unpack_int4: logical"), rows, K, _stream(stream)),
            "unpack_int4")
+
+
+# ---------------------------------------------------------------- 4-bit floating point, mixture of experts
+_TYPES = {"torch.float32": (0, 4), "torch.bfloat16": (1, 2), "torch.float16": (2, 2)}
+
+
+def fp4_code_bytes(K: int) -> int:
+    """Bytes of a row of K packed e2m1 codes (whole blocks of 32)."""
+    return -(-K // 32) * 16
+
+
+def mxfp4_scale_pitch(K: int) -> int:
+    """Bytes of a row of mxfp4 scales: one per 32 k, rounded up to 16."""
+    return -(-K // 512) * 16
+
+
+def nvfp4_scale_pitch(K: int) -> int:
+    """Bytes of a row of nvfp4 scales: one per 16 k, rounded up to 16."""
+    return -(-K // 256) * 16
+
+
+def _type(x, what: str) -> tuple[int, int]:
+    """(igemm_type, bytes per element) of a tensor."""
+    t = _TYPES.get(str(x.dtype))
+    if t is None:
+        raise ValueError(f"{what} must be float32, bfloat16 or float16, not {x.dtype}")
+    return t
+
+
+def _typed(x, dtype: str, count: int, what: str):
+    """_arg for a device array of `count` 4-byte elements of torch type `dtype`."""
+    if x is not None and not isinstance(x, int) and str(x.dtype) != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {x.dtype}")
+    return _arg(x, 4 * count, True, what)
+
+
+def _pack_fp4(fn, where, x, extra, codes, scales, rows, K, index, pitch, stream):
+    t, _ = _type(x, f"{where}: x")
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{where}: x must be a CUDA matrix")
+    if x.shape[1] != K or (index is None and x.shape[0] != rows):
+        raise ValueError(f"{where}: x is {tuple(x.shape)}; the call packs {rows} rows of {K}")
+    (r, c), (sr, sc) = x.shape, x.stride()
+    # a dimension of one element has no stride of its own
+    if c == 1 or sc == 1:
+        transposed, ld = 0, (sr if r > 1 else max(sr, c))
+    elif r == 1 or sr == 1:
+        transposed, ld = 1, sc
+    else:
+        raise ValueError(f"{where}: x must have unit stride along one dimension")
+    if ld < (r if transposed else c):
+        raise ValueError(f"{where}: x has overlapping rows")
+    if transposed and index is not None:
+        raise ValueError(f"{where}: rows of a transposed x cannot be gathered")
+    _check(fn(x.data_ptr(), t, ld, transposed, _typed(index, "torch.int32", _n(rows), f"{where}: index"), r, *extra,
+              _arg(codes, _n(rows) * fp4_code_bytes(K), True, f"{where}: codes"),
+              _arg(scales, _n(rows) * pitch, True, f"{where}: scales"), rows, K, _stream(stream)), where)
+
+
+def pack_mxfp4(x, codes, scales, rows: int, K: int, index=None, stream=None) -> None:
+    """codes [rows, fp4_code_bytes(K)], scales [rows, mxfp4_scale_pitch(K)] (uint8) = x quantised to e2m1 with one
+    power-of-two scale per 32 k.  x: CUDA matrix [rows, K] (float32, bfloat16 or float16) with unit stride along
+    one dimension; with `index` (int32 [rows]) row r is x[index[r]], zeros where index[r] is out of range."""
+    _pack_fp4(load().pack_mxfp4, "pack_mxfp4", x, (), codes, scales, rows, K, index, mxfp4_scale_pitch(K), stream)
+
+
+def pack_nvfp4(x, tensor_scale, codes, scales, rows: int, K: int, index=None, stream=None) -> None:
+    """pack_mxfp4 with one e4m3 scale per 16 k, relative to tensor_scale (float32 [1] on the device, None: 1);
+    scales [rows, nvfp4_scale_pitch(K)]."""
+    _pack_fp4(load().pack_nvfp4, "pack_nvfp4", x, (_typed(tensor_scale, "torch.float32", 1, "pack_nvfp4: tensor_scale"),),
+              codes, scales, rows, K, index, nvfp4_scale_pitch(K), stream)
+
+
+def _fp4_args(A, B, SFA, SFB, C, M, E, N, K, pitch, where):
+    kb = fp4_code_bytes(K)
+    t, size = _type(C, f"{where}: C")
+    return ((_arg(A, _n(M, kb), True, f"{where}: A"), _arg(B, _n(E, N, kb), True, f"{where}: B"),
+             _arg(SFA, _n(M, pitch), True, f"{where}: SFA"), _arg(SFB, _n(E, N, pitch), True, f"{where}: SFB")),
+            (_arg(C, size * _n(M, N), True, f"{where}: C"), t))
+
+
+def igemm_mxfp4(A, B, SFA, SFB, C, M: int, N: int, K: int, stream=None) -> None:
+    """C[M,N] (float32, bfloat16 or float16) = A . B^T of mxfp4 matrices (codes and scales as pack_mxfp4 writes them)."""
+    w = "igemm_mxfp4"
+    ops, c = _fp4_args(A, B, SFA, SFB, C, M, 1, N, K, mxfp4_scale_pitch(K), w)
+    _check(load().igemm_mxfp4(*ops, *c, M, N, K, _stream(stream)), w)
+
+
+def igemm_nvfp4(A, B, SFA, SFB, alpha, C, M: int, N: int, K: int, stream=None) -> None:
+    """C[M,N] (float32, bfloat16 or float16) = alpha * A . B^T of nvfp4 matrices; alpha: float32 [1] on the device
+    (the product of the operands' tensor scales), None: 1."""
+    w = "igemm_nvfp4"
+    ops, c = _fp4_args(A, B, SFA, SFB, C, M, 1, N, K, nvfp4_scale_pitch(K), w)
+    _check(load().igemm_nvfp4(*ops, _typed(alpha, "torch.float32", 1, f"{w}: alpha"), *c, M, N, K, _stream(stream)), w)
+
+
+def igemm_mxfp4_grouped(A, B, SFA, SFB, offsets, C, rows: int, E: int, N: int, K: int, stream=None) -> None:
+    """Rows offsets[e] .. offsets[e+1]-1 of C [rows, N] = those rows of A times the transpose of B[e] (B: E matrices
+    of N rows); offsets: int32 [E+1] on the device.  Rows of no group are left as they were."""
+    w = "igemm_mxfp4_grouped"
+    ops, c = _fp4_args(A, B, SFA, SFB, C, rows, E, N, K, mxfp4_scale_pitch(K), w)
+    _check(load().igemm_mxfp4_grouped(*ops, _typed(offsets, "torch.int32", _n(E + 1), f"{w}: offsets"), *c, rows, E, N,
+                                      K, _stream(stream)), w)
+
+
+def igemm_nvfp4_grouped(A, B, SFA, SFB, offsets, alpha, C, rows: int, E: int, N: int, K: int, stream=None) -> None:
+    """igemm_mxfp4_grouped for nvfp4 matrices; alpha: float32 [E] on the device, None: 1."""
+    w = "igemm_nvfp4_grouped"
+    ops, c = _fp4_args(A, B, SFA, SFB, C, rows, E, N, K, nvfp4_scale_pitch(K), w)
+    _check(load().igemm_nvfp4_grouped(*ops, _typed(offsets, "torch.int32", _n(E + 1), f"{w}: offsets"),
+                                      _typed(alpha, "torch.float32", _n(E), f"{w}: alpha"), *c, rows, E, N, K,
+                                      _stream(stream)), w)
+
+
+def igemm_moe_route(logits, experts, weights, offsets, tokens, slots, T: int, E: int, k: int, normalize: bool = True,
+                    stream=None) -> None:
+    """The k largest of logits [T,E] per token: experts [T,k] (int32, -1: none left), softmax weights [T,k] (float32,
+    over the chosen or, normalize False, over all E), and the pairs sorted by expert: offsets [E+1], tokens [T*k]
+    (sorted place -> token, -1 past the last), slots [T,k] (pair -> sorted place, -1), int32."""
+    w = "igemm_moe_route"
+    t, size = _type(logits, f"{w}: logits")
+    _check(load().igemm_moe_route(
+        _arg(logits, size * _n(T, E), True, f"{w}: logits"), t, _typed(experts, "torch.int32", _n(T, k), f"{w}: experts"),
+        _typed(weights, "torch.float32", _n(T, k), f"{w}: weights"),
+        _typed(offsets, "torch.int32", _n(E + 1), f"{w}: offsets"),
+        _typed(tokens, "torch.int32", _n(T, k), f"{w}: tokens"), _typed(slots, "torch.int32", _n(T, k), f"{w}: slots"),
+        T, E, k, int(bool(normalize)), _stream(stream)), w)
+
+
+def igemm_moe_combine(Y, slots, weights, out, T: int, k: int, N: int, stream=None) -> None:
+    """out [T,N] = sum over j of weights[t,j] * Y[slots[t,j]] (Y [T*k,N] and out of one type; slots of -1 add nothing)."""
+    w = "igemm_moe_combine"
+    t, size = _type(Y, f"{w}: Y")
+    if out.dtype != Y.dtype:
+        raise ValueError(f"{w}: out must have Y's type")
+    _check(load().igemm_moe_combine(
+        _arg(Y, size * _n(T, k, N), True, f"{w}: Y"), _typed(slots, "torch.int32", _n(T, k), f"{w}: slots"),
+        _typed(weights, "torch.float32", _n(T, k), f"{w}: weights"), _arg(out, size * _n(T, N), True, f"{w}: out"), t, T,
+        k, N, _stream(stream)), w)
 
 
 def igemm_strerror(code: int) -> str:

@@ -1,0 +1,171 @@
+// Host side of the 4-bit floating-point GEMM: plan and launch of
+// igemm_fp4_kernel for one format (the two formats are two translation units).
+#pragma once
+#include <cmath>
+#include <mutex>
+#include "launch.cuh"
+#include "fp4.cuh"
+#include "gemm_fp4_kernel.cuh"
+
+namespace igemm {
+
+// Shared memory of one launch: code stages, scale stages, the partials of a
+// split k, then barriers and the groups' tile counts.
+template <class Cfg>
+struct Fp4Smem {
+    int code_stages, scale_stages, off_scales, off_red, off_bars, total;
+    explicit Fp4Smem(int cs)
+    {
+        constexpr int kLimit = 227 * 1024 - 1024;  // less the alignment slack
+        const int red = cs > 1 ? Cfg::kRedBytes : 0;
+        const int per_unit = Cfg::kU * Cfg::kStage + Cfg::kScaleStage;
+        int units = (kLimit - Cfg::kTailBytes - red) / per_unit;
+        if (units * Cfg::kU > Cfg::kMaxStages) units = Cfg::kMaxStages / Cfg::kU;
+        code_stages = units * Cfg::kU;
+        scale_stages = units;
+        // an odd code stage that still fits
+        if (code_stages < Cfg::kMaxStages &&
+            units * per_unit + Cfg::kStage + red + Cfg::kTailBytes <= kLimit)
+            ++code_stages;
+        off_scales = code_stages * Cfg::kStage;
+        off_red = off_scales + scale_stages * Cfg::kScaleStage;
+        off_bars = off_red + red;
+        total = off_bars + Cfg::kTailBytes + 1024;
+    }
+};
+
+// Clusters of `csize` CTAs of igemm_fp4_kernel<Cfg> that can be resident at once
+// (asked once per device and size); sets the kernel's shared-memory limit.
+template <class Cfg>
+int fp4_clusters(int csize)
+{
+    static std::mutex mu;
+    static int cache[64][4] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    const int slot = csize == 1 ? 0 : csize == 2 ? 1 : csize == 4 ? 2 : 3;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!cache[dev][slot]) {
+        auto kernel = igemm_fp4_kernel<Cfg>;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
+            return 0;
+        if (csize == 1) {
+            cache[dev][slot] = sm_count();
+        } else {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = csize;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(csize * sm_count(), 1, 1);
+            cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+            cfg.dynamicSmemBytes = 227 * 1024;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) return 0;
+            cache[dev][slot] = n;
+        }
+    }
+    return cache[dev][slot];
+}
+
+template <class Cfg>
+int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
+{
+    const int csize = Cfg::PAIR ? 2 : plan.cs;
+    const int clusters = fp4_clusters<Cfg>(csize);
+    if (clusters < 1) return kCudaError;
+    const int code_bytes = fp4_code_bytes(c.K), pitch = fp4_scale_pitch(c.K, Cfg::NV);
+    const uint64_t p_rows = uint64_t(c.experts) * c.N;
+    CUtensorMap mapP, mapQ, mapSP, mapSQ;
+    constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (make_map(&mapP, kU8, c.B, p_rows, code_bytes, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
+        make_map(&mapQ, kU8, c.A, c.rows, code_bytes, Cfg::kQBox, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
+        make_map(&mapSP, kU8, c.SFB, p_rows, pitch, 128, 16, CU_TENSOR_MAP_SWIZZLE_NONE) != kOk ||
+        make_map(&mapSQ, kU8, c.SFA, c.rows, pitch, Cfg::BN, 16, CU_TENSOR_MAP_SWIZZLE_NONE) != kOk)
+        return kCudaError;
+    const Fp4Smem<Cfg> lay(csize > 1 && !Cfg::PAIR ? csize : 1);
+    Fp4Params prm{};
+    prm.C = c.C;
+    prm.c_type = c.c_type;
+    prm.alpha = c.alpha;
+    prm.offsets = c.offsets;
+    prm.rows = c.rows;
+    prm.N = c.N;
+    prm.experts = c.experts;
+    prm.k_steps = (c.K + 63) / 64;
+    prm.k_blocks = (c.K + (Cfg::NV ? 15 : 31)) / (Cfg::NV ? 16 : 32);
+    prm.stages = (c.K + 255) / 256;
+    prm.units = (prm.stages + Cfg::kU - 1) / Cfg::kU;
+    prm.qt = plan.qt;
+    prm.p_tiles = (c.N + 128 * Cfg::CL - 1) / (128 * Cfg::CL);
+    prm.group_p = plan.group_p;
+    prm.cs = plan.cs;
+    prm.units_per_slice = (prm.units + plan.cs - 1) / plan.cs;
+    prm.code_stages = lay.code_stages;
+    prm.scale_stages = lay.scale_stages;
+    prm.off_scales = lay.off_scales;
+    prm.off_red = lay.off_red;
+    prm.off_bars = lay.off_bars;
+    prm.status = device_status_word();
+    prm.limit_ns = watchdog_limit_ns();
+    if (!prm.status) return kCudaError;
+    // every slice of k holds at least one unit
+    if (plan.cs > 1 && prm.units_per_slice * (plan.cs - 1) >= prm.units) return kUnsupportedShape;
+    const int64_t q_tiles = (int64_t(c.rows) + plan.qt - 1) / plan.qt + (c.offsets ? std::min(c.rows, c.experts) - 1 : 0);
+    const int64_t tiles = q_tiles * prm.p_tiles;  // grouped: at most
+    const GemmEvents ev = take_gemm_events();
+    if (ev.start && cudaEventRecord(ev.start, stream) != cudaSuccess) return kCudaError;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    int na = 0;
+    if (csize > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = csize;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(csize * std::min<int64_t>(tiles, clusters)), 1, 1);
+    cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = lay.total;
+    cfg.stream = stream;
+    cfg.attrs = na ? attr : nullptr;
+    cfg.numAttrs = na;
+    if (cudaLaunchKernelEx(&cfg, igemm_fp4_kernel<Cfg>, mapP, mapQ, mapSP, mapSQ, prm) != cudaSuccess)
+        return kCudaError;
+    note_launch();
+    if (ev.stop && cudaEventRecord(ev.stop, stream) != cudaSuccess) return kCudaError;
+    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+}
+
+template <bool NV>
+int fp4_max_clusters(int bn, bool pair, int csize)
+{
+    if (pair) return fp4_clusters<Fp4Cfg<NV, 256, true>>(2);
+    switch (bn) {
+    case 16: return fp4_clusters<Fp4Cfg<NV, 16, false>>(csize);
+    case 32: return fp4_clusters<Fp4Cfg<NV, 32, false>>(csize);
+    case 64: return fp4_clusters<Fp4Cfg<NV, 64, false>>(csize);
+    default: return fp4_clusters<Fp4Cfg<NV, 128, false>>(csize);
+    }
+}
+
+template <bool NV>
+int launch_fp4_format(const Fp4Call &c, cudaStream_t stream)
+{
+    Fp4Plan plan;
+    const int rc = fp4_plan(c, fp4_max_clusters<NV>, &plan);
+    if (rc != kOk) return rc;
+    if (plan.pair) return launch_fp4_cfg<Fp4Cfg<NV, 256, true>>(c, plan, stream);
+    switch (plan.bn) {
+    case 16: return launch_fp4_cfg<Fp4Cfg<NV, 16, false>>(c, plan, stream);
+    case 32: return launch_fp4_cfg<Fp4Cfg<NV, 32, false>>(c, plan, stream);
+    case 64: return launch_fp4_cfg<Fp4Cfg<NV, 64, false>>(c, plan, stream);
+    default: return launch_fp4_cfg<Fp4Cfg<NV, 128, false>>(c, plan, stream);
+    }
+}
+
+}  // namespace igemm

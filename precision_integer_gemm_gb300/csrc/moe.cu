@@ -1,0 +1,365 @@
+// Routing of tokens to experts and the weighted sum of the experts' rows.
+//
+// Routing: a warp per token holds the token's logits in registers (E / 32 per
+// lane) and takes the largest k times (a warp reduction of order-preserving
+// integers, then one of the indices that hold it: the lowest wins).  A token
+// chooses an expert at most once, so the tokens of a block of kTB that chose
+// expert e are one bit mask, and a pair's place among its expert's is the
+// number of bits below its own: the sort is stable and needs no ordered
+// atomics.  One block does the whole job for up to kTB tokens; more tokens take
+// three launches (choice and counts per block, a scan over the blocks per
+// expert, places).
+//
+// Combine: bound by HBM, k rows read and one written per token.
+#include <algorithm>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include "launch.cuh"
+#include "moe.cuh"
+
+namespace igemm {
+
+constexpr int kTB = 64;           // tokens per block: two mask words
+constexpr int kMaxExperts = 1024;
+constexpr int kRouteThreads = 512;
+
+__device__ __forceinline__ float moe_float(float v) { return v; }
+__device__ __forceinline__ float moe_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float moe_float(__half v) { return __half2float(v); }
+
+struct RouteParams {
+    const void *logits;
+    int *experts;
+    float *weights;
+    int *offsets, *tokens, *slots;
+    int *counts;  // [E][blocks], then exclusive prefixes; null when one block does it all
+    int *totals;  // [E]
+    int T, E, k, blocks;
+    int normalize;
+};
+
+// Order-preserving integer of a logit: larger logits give larger keys, -0 and +0
+// the same; NaN counts as -inf, whose key is the lowest.
+__device__ __forceinline__ uint32_t route_key(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float route_value(uint32_t key)
+{
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+constexpr uint32_t kKeyNone = 0x007FFFFFu;  // of -inf
+
+// Sets in `first[e]` the running sum of `count(e)` over experts below e (warp 0).
+template <class F>
+__device__ __forceinline__ void route_scan(int *first, int E, F count)
+{
+    const int lane = threadIdx.x & 31;
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int n = e0 + lane < E ? count(e0 + lane) : 0;
+        int incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (e0 + lane < E) first[e0 + lane] = run + incl - n;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) first[E] = run;
+}
+
+// Places of this block's pairs: first[e] is where its pairs of expert e start.
+__device__ __forceinline__ void route_place(const RouteParams &p, const uint2 *mask, const int *first,
+                                            const int *experts)
+{
+    const int t0 = blockIdx.x * kTB;
+    const int n = min(kTB, p.T - t0) * p.k;
+    for (int i = threadIdx.x; i < n; i += kRouteThreads) {
+        const int e = experts[i], t = i / p.k;
+        int pos = -1;
+        if (e >= 0) {
+            const uint2 m = mask[e];
+            const uint32_t below = (1u << (t & 31)) - 1u;
+            pos = first[e] + (t < 32 ? __popc(m.x & below) : __popc(m.x) + __popc(m.y & below));
+            p.tokens[pos] = t0 + t;
+        }
+        p.slots[static_cast<int64_t>(t0) * p.k + i] = pos;
+    }
+}
+
+// Choice and weights of kTB tokens; their masks; one block: everything.
+// VPL: logits per lane (E <= 32 VPL).
+template <class T, int VPL>
+__global__ void __launch_bounds__(kRouteThreads) moe_choose_kernel(const RouteParams p)
+{
+    extern __shared__ uint2 mask[];  // [E], then (one block) first[E + 1], experts[kTB * k]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int *first = reinterpret_cast<int *>(mask + p.E);
+    int *chosen = first + p.E + 1;
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = make_uint2(0, 0);
+    __syncthreads();
+    const int t0 = blockIdx.x * kTB;
+    for (int i = warp; i < kTB && t0 + i < p.T; i += kRouteThreads / 32) {
+        const int64_t t = t0 + i;
+        const T *row = static_cast<const T *>(p.logits) + t * p.E;
+        uint32_t key[VPL];
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int e = 32 * j + lane;
+            const float v = e < p.E ? moe_float(row[e]) : 0.0f;
+            key[j] = e >= p.E ? 0u : v != v ? kKeyNone : route_key(v);
+        }
+        uint32_t local = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) local = max(local, key[j]);
+        uint32_t top = __reduce_max_sync(0xffffffffu, local);
+        const float m = top > kKeyNone ? route_value(top) : 0.0f;
+        float sum = 0.0f;
+        if (!p.normalize) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (key[j] > kKeyNone) sum += expf(route_value(key[j]) - m);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        }
+        // lane c keeps choice c
+        int my_e = -1;
+        float my_w = 0.0f;
+        for (int c = 0; c < p.k; ++c) {
+            if (top <= kKeyNone) break;  // only masked experts are left
+            int at = 0x7FFFFFFF;
+            if (local == top) {
+#pragma unroll
+                for (int j = VPL - 1; j >= 0; --j)
+                    if (key[j] == top) at = 32 * j + lane;
+            }
+            const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(at)));
+            if (lane == c) {
+                my_e = e;
+                my_w = expf(route_value(top) - m);
+            }
+            if (at == e) {  // taken: out of the next rounds
+                local = 0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    if (32 * j + lane == e) key[j] = 0u;
+                    local = max(local, key[j]);
+                }
+            }
+            top = __reduce_max_sync(0xffffffffu, local);
+        }
+        if (p.normalize) {
+            sum = my_w;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        }
+        if (lane < p.k) {
+            p.experts[t * p.k + lane] = my_e;
+            p.weights[t * p.k + lane] = my_e >= 0 ? __fdiv_rn(my_w, sum) : 0.0f;
+            if (!p.counts) chosen[i * p.k + lane] = my_e;
+            if (my_e >= 0) atomicOr(i < 32 ? &mask[my_e].x : &mask[my_e].y, 1u << (i & 31));
+        }
+    }
+    __syncthreads();
+    if (p.counts) {
+        for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
+            p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = __popc(mask[e].x) + __popc(mask[e].y);
+        return;
+    }
+    if (warp == 0) route_scan(first, p.E, [&](int e) { return __popc(mask[e].x) + __popc(mask[e].y); });
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = first[e];
+    for (int i = first[p.E] + threadIdx.x; i < p.T * p.k; i += kRouteThreads) p.tokens[i] = -1;
+    route_place(p, mask, first, chosen);
+}
+
+// A warp per expert: its counts per block become running sums.
+__global__ void __launch_bounds__(128) moe_scan_kernel(const RouteParams p)
+{
+    const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (e >= p.E) return;
+    int *c = p.counts + static_cast<int64_t>(e) * p.blocks;
+    int run = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += 32) {
+        const int n = b0 + lane < p.blocks ? c[b0 + lane] : 0;
+        int incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (b0 + lane < p.blocks) c[b0 + lane] = run + incl - n;
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) p.totals[e] = run;
+}
+
+__global__ void __launch_bounds__(kRouteThreads) moe_place_kernel(const RouteParams p)
+{
+    extern __shared__ uint2 mask[];  // [E], then first[E + 1]
+    int *first = reinterpret_cast<int *>(mask + p.E);
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = make_uint2(0, 0);
+    if (threadIdx.x < 32) route_scan(first, p.E, [&](int e) { return p.totals[e]; });
+    __syncthreads();
+    const int t0 = blockIdx.x * kTB;
+    const int n = min(kTB, p.T - t0) * p.k;
+    const int *experts = p.experts + static_cast<int64_t>(t0) * p.k;
+    for (int i = threadIdx.x; i < n; i += kRouteThreads) {
+        const int e = experts[i], t = i / p.k;
+        if (e >= 0) atomicOr(t < 32 ? &mask[e].x : &mask[e].y, 1u << (t & 31));
+    }
+    const int routed = first[p.E];
+    const int64_t pairs = static_cast<int64_t>(p.T) * p.k;
+    for (int64_t i = routed + static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x; i < pairs;
+         i += static_cast<int64_t>(gridDim.x) * kRouteThreads)
+        p.tokens[i] = -1;
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = first[e];
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
+        first[e] += p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
+    __syncthreads();
+    route_place(p, mask, first, experts);
+}
+
+template <class T>
+static void launch_choose(const RouteParams &p, int smem, cudaStream_t stream)
+{
+    if (p.E <= 64)
+        moe_choose_kernel<T, 2><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+    else if (p.E <= 128)
+        moe_choose_kernel<T, 4><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+    else if (p.E <= 256)
+        moe_choose_kernel<T, 8><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+    else if (p.E <= 512)
+        moe_choose_kernel<T, 16><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+    else
+        moe_choose_kernel<T, 32><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+}
+
+int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
+{
+    RouteParams p{};
+    p.logits = c.logits;
+    p.experts = c.experts;
+    p.weights = c.weights;
+    p.offsets = c.offsets;
+    p.tokens = c.tokens;
+    p.slots = c.slots;
+    p.T = c.T;
+    p.E = c.E;
+    p.k = c.k;
+    p.normalize = c.normalize ? 1 : 0;
+    p.blocks = (c.T + kTB - 1) / kTB;
+    void *ws = nullptr;
+    if (p.blocks > 1) {
+        const size_t counts = size_t(c.E) * p.blocks * 4;
+        if (workspace_alloc(&ws, counts + size_t(c.E) * 4, stream) != kOk) return kCudaError;
+        p.counts = static_cast<int *>(ws);
+        p.totals = reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + counts);
+    }
+    const int smem = c.E * 8 + (c.E + 1) * 4 + (p.blocks > 1 ? 0 : kTB * c.k * 4);
+    if (c.x_type == 0)
+        launch_choose<float>(p, smem, stream);
+    else if (c.x_type == 1)
+        launch_choose<__nv_bfloat16>(p, smem, stream);
+    else
+        launch_choose<__half>(p, smem, stream);
+    note_launch();
+    if (p.blocks > 1) {
+        moe_scan_kernel<<<(c.E + 3) / 4, 128, 0, stream>>>(p);
+        note_launch();
+        moe_place_kernel<<<p.blocks, kRouteThreads, smem, stream>>>(p);
+        note_launch();
+    }
+    int rc = cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+    if (ws && workspace_free(ws, stream) != kOk) rc = kCudaError;
+    return rc;
+}
+
+// ---------------------------------------------------------------- combine
+__device__ __forceinline__ void moe_out(float *o, float v) { *o = v; }
+__device__ __forceinline__ void moe_out(__nv_bfloat16 *o, float v) { *o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void moe_out(__half *o, float v) { *o = __float2half_rn(v); }
+
+// A thread per PER columns of a token (16 bytes, or one column where rows are not
+// 16-byte aligned), four rows in flight; float32 sums in the order of the choices.
+template <class T, int PER>
+__global__ void __launch_bounds__(128) moe_combine_kernel(const T *__restrict__ Y, const int *__restrict__ slots,
+                                                          const float *__restrict__ weights, T *__restrict__ out,
+                                                          int Tn, int k, int N)
+{
+    const uint32_t per_row = static_cast<uint32_t>(N / PER);
+    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 128 + threadIdx.x;
+    const int64_t t = static_cast<int64_t>(item / per_row);
+    if (t >= Tn) return;
+    const int n = static_cast<int>(item - static_cast<uint64_t>(t) * per_row) * PER;
+    const int64_t rows = static_cast<int64_t>(Tn) * k;
+    float acc[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += 4) {
+        alignas(16) T v[4][PER];
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t at = t * k + j0 + j;
+            const int64_t s = j0 + j < k ? __ldg(slots + at) : -1;
+            w[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) v[j][i] = T(0.0f);
+            if (s >= 0 && s < rows) {
+                w[j] = __ldg(weights + at);
+                if constexpr (PER > 1)
+                    *reinterpret_cast<uint4 *>(v[j]) = __ldcs(reinterpret_cast<const uint4 *>(Y + s * N + n));
+                else
+                    v[j][0] = Y[s * N + n];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] = fmaf(w[j], moe_float(v[j][i]), acc[i]);
+    }
+    alignas(16) T o[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) moe_out(&o[i], acc[i]);
+    if constexpr (PER > 1)
+        *reinterpret_cast<uint4 *>(out + t * N + n) = *reinterpret_cast<const uint4 *>(o);
+    else
+        out[t * N + n] = o[0];
+}
+
+template <class T>
+static int launch_combine_type(const MoeCombineCall &c, cudaStream_t stream)
+{
+    constexpr int kPer = 16 / sizeof(T);
+    const bool vec = (reinterpret_cast<uintptr_t>(c.Y) % 16) == 0 && (reinterpret_cast<uintptr_t>(c.out) % 16) == 0 &&
+                     c.N % kPer == 0;
+    const int64_t items = int64_t(c.T) * (c.N / (vec ? kPer : 1));
+    const int64_t blocks = (items + 127) / 128;
+    if (blocks > 0x7FFFFFFF) return kUnsupportedShape;
+    const T *Y = static_cast<const T *>(c.Y);
+    T *out = static_cast<T *>(c.out);
+    const unsigned b = static_cast<unsigned>(blocks);
+    if (vec)
+        moe_combine_kernel<T, kPer><<<b, 128, 0, stream>>>(Y, c.slots, c.weights, out, c.T, c.k, c.N);
+    else
+        moe_combine_kernel<T, 1><<<b, 128, 0, stream>>>(Y, c.slots, c.weights, out, c.T, c.k, c.N);
+    note_launch();
+    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+}
+
+int launch_moe_combine(const MoeCombineCall &c, cudaStream_t stream)
+{
+    switch (c.x_type) {
+    case 0: return launch_combine_type<float>(c, stream);
+    case 1: return launch_combine_type<__nv_bfloat16>(c, stream);
+    default: return launch_combine_type<__half>(c, stream);
+    }
+}
+
+}  // namespace igemm

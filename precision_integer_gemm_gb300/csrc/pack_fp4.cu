@@ -1,0 +1,264 @@
+// Packing into the microscaled 4-bit floating-point formats.
+//
+//   mx: e = max(floor(log2 amax) - 2, -127) per 32 k, scale byte e + 127, codes
+//       e2m1(x 2^-e): the power of two that puts the largest value in [4, 8),
+//       where 6 is the largest code (values above saturate).
+//   nv: s = e4m3(min(amax / (6 g), 448)) per 16 k with the tensor scale g, codes
+//       e2m1(x * (1 / (s g))); every operation rounded to float32.
+//   Rounding to nearest, ties to even.  A block with a NaN or an infinity gets
+//   the NaN scale (0xFF, 0x7F) and zero codes, so that products see NaN.
+//
+// Bound by HBM: x is read once, half a byte a value and the scales written.
+#include <algorithm>
+#include <type_traits>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include "launch.cuh"
+#include "fp4.cuh"
+
+namespace igemm {
+
+__device__ __forceinline__ float fp4_float(float v) { return v; }
+__device__ __forceinline__ float fp4_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float fp4_float(__half v) { return __half2float(v); }
+
+// Eight codes, element 0 in the lowest nibble.
+__device__ __forceinline__ uint32_t fp4_codes8(const float *y)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    return r;
+}
+
+// The scale byte of a block whose largest magnitude is `amax` (bits: NaN sorts
+// above infinity) and the factor that takes its values to codes (0: all
+// codes zero).
+template <bool NV>
+__device__ __forceinline__ uint8_t fp4_scale(uint32_t amax_bits, float g, float &factor)
+{
+    const bool fine = amax_bits < 0x7F800000u;
+    factor = 0.0f;
+    if constexpr (!NV) {
+        if (!fine) return 0xFF;
+        if (amax_bits == 0) {
+            factor = __uint_as_float(254u << 23);  // 2^127: the codes keep the zeros' signs
+            return 0;
+        }
+        // floor(log2): the exponent field, or the leading bit of a subnormal
+        const int lg = amax_bits >= 0x00800000u ? static_cast<int>(amax_bits >> 23) - 127
+                                                : -118 - __clz(static_cast<int>(amax_bits));
+        const int e = max(lg - 2, -127);
+        factor = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        return static_cast<uint8_t>(e + 127);
+    } else {
+        if (!fine) return 0x7F;
+        const float q = fminf(__fdiv_rn(__uint_as_float(amax_bits), 6.0f * g), 448.0f);
+        uint16_t h;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.0f), "f"(q));
+        const uint8_t s = static_cast<uint8_t>(h & 0xFF);
+        // the byte's value: 2^(e - 7) (1 + f / 8), subnormals 2^-6 f / 8
+        const float v = s >= 8 ? __uint_as_float(((s >> 3) + 120u) << 23 | static_cast<uint32_t>(s & 7) << 20)
+                               : static_cast<float>(s) * 0.001953125f;
+        const float t = v * g;
+        if (t >= 1.17549435e-38f) factor = __frcp_rn(t);
+        return s;
+    }
+}
+
+struct Fp4PackParams {
+    int64_t ld;
+    const int *index;
+    const float *g;
+    uint8_t *codes, *scales;
+    int x_rows, rows, K, code_bytes, pitch;
+};
+
+// 16 values of one row from k; zeros past K.
+template <class T, bool VEC>
+__device__ __forceinline__ void fp4_load16(const T *row, int k, int K, float (&v)[16])
+{
+    if (VEC && k + 16 <= K) {
+        constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte load
+        uint4 raw[16 / kPer];
+#pragma unroll
+        for (int i = 0; i < 16 / kPer; ++i) raw[i] = __ldg(reinterpret_cast<const uint4 *>(row + k) + i);
+        const T *t = reinterpret_cast<const T *>(raw);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = fp4_float(t[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = k + i < K ? fp4_float(row[k + i]) : 0.0f;
+    }
+}
+
+// Row-major x: a thread per 16 k of a row (mx: two neighbouring lanes share a
+// block's scale), so a warp reads and writes contiguous runs.
+template <bool NV, class T, bool VEC, class Index>
+__global__ void __launch_bounds__(256) pack_fp4_rows_kernel(const T *__restrict__ x, const Fp4PackParams p)
+{
+    const Index items = static_cast<Index>(p.code_bytes / 8);  // of 16 k, per row
+    const Index item = static_cast<Index>(blockIdx.x) * 256 + threadIdx.x;
+    const Index row_i = item / items;
+    const int k = static_cast<int>(item - row_i * items) * 16;
+    const bool live = row_i < static_cast<Index>(p.rows);
+    const int64_t row = static_cast<int64_t>(row_i);
+    int64_t src = row;
+    if (live && p.index) {
+        src = __ldg(p.index + row);
+        if (src >= p.x_rows) src = -1;
+    }
+    float v[16];
+    if (live && src >= 0) {
+        fp4_load16<T, VEC>(x + src * p.ld, k, p.K, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    }
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    if constexpr (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    if (!live) return;
+    float f;
+    const uint8_t s = fp4_scale<NV>(amax, NV && p.g ? __ldg(p.g) : 1.0f, f);
+    uint2 out = make_uint2(0, 0);
+    if (amax < 0x7F800000u && f > 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= f;
+        out = make_uint2(fp4_codes8(v), fp4_codes8(v + 8));
+    }
+    *reinterpret_cast<uint2 *>(p.codes + row * p.code_bytes + k / 2) = out;
+    uint8_t *sc = p.scales + row * p.pitch;
+    if (NV) {
+        if (k < p.K) sc[k / 16] = s;
+    } else if ((k & 16) == 0) {
+        sc[k / 32] = s;
+    }
+    // the row's last thread: zeros up to the pitch
+    if (k / 8 + 2 == p.code_bytes / 4) {
+        for (int b = (p.K + (NV ? 15 : 31)) / (NV ? 16 : 32); b < p.pitch; ++b) sc[b] = 0;
+    }
+}
+
+// Transposed x [K, rows]: a CTA takes 32 rows (a lane each, so loads run along
+// x's rows) by 256 k (32 per warp), and the packed rows go through shared
+// memory to leave as runs of 128 bytes.
+template <bool NV, class T>
+__global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__restrict__ x, const Fp4PackParams p)
+{
+    constexpr int kPerWarp = NV ? 2 : 1;  // scale bytes
+    __shared__ uint4 codes[32][9];        // (row pitch 144 bytes: no bank conflicts)
+    __shared__ uint8_t scales[32][16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32;
+    const int k0 = blockIdx.y * 256, k = k0 + 32 * warp;
+    const bool live = r0 + lane < p.rows;
+    float v[32];
+    const T *src = x + static_cast<int64_t>(k) * p.ld + r0 + lane;
+    if (live && k + 32 <= p.K) {
+        T raw[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) raw[i] = src[i * p.ld];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = fp4_float(raw[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = live && k + i < p.K ? fp4_float(src[i * p.ld]) : 0.0f;
+    }
+    const float g = NV && p.g ? __ldg(p.g) : 1.0f;
+    uint32_t out[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int b = 0; b < kPerWarp; ++b) {
+        constexpr int kBlock = 32 / kPerWarp;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) amax = max(amax, __float_as_uint(v[b * kBlock + i]) & 0x7FFFFFFFu);
+        float f;
+        scales[lane][warp * kPerWarp + b] = k + b * kBlock < p.K ? fp4_scale<NV>(amax, g, f) : 0;
+        if (k + b * kBlock < p.K && amax < 0x7F800000u && f > 0.0f) {
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) v[b * kBlock + i] *= f;
+#pragma unroll
+            for (int i = 0; i < kBlock / 8; ++i)
+                out[b * kBlock / 8 + i] = fp4_codes8(v + b * kBlock + 8 * i);
+        }
+    }
+    codes[lane][warp] = make_uint4(out[0], out[1], out[2], out[3]);
+    __syncthreads();
+    {
+        const int r = threadIdx.x >> 3, c = threadIdx.x & 7;  // a row's 128 bytes from eight lanes
+        const int at = k0 / 2 + 16 * c;
+        if (r0 + r < p.rows && at < p.code_bytes)
+            *reinterpret_cast<uint4 *>(p.codes + (r0 + r) * p.code_bytes + at) = codes[r][c];
+    }
+    for (int i = threadIdx.x; i < 32 * 8 * kPerWarp; i += 256) {
+        const int r = i / (8 * kPerWarp), b = i % (8 * kPerWarp), at = blockIdx.y * 8 * kPerWarp + b;
+        if (r0 + r < p.rows && at < p.pitch) p.scales[(r0 + r) * p.pitch + at] = scales[r][b];
+    }
+    // (mx: 256 k are half of 16 scale bytes) zeros from here up to the pitch
+    if (blockIdx.y == gridDim.y - 1 && warp == 0 && live)
+        for (int b = (blockIdx.y + 1) * 8 * kPerWarp; b < p.pitch; ++b) p.scales[(r0 + lane) * p.pitch + b] = 0;
+}
+
+template <bool NV, class T>
+static int launch_pack_type(const Fp4PackCall &c, const Fp4PackParams &p, cudaStream_t stream)
+{
+    const T *x = static_cast<const T *>(c.x);
+    if (c.transposed) {
+        const int64_t bx = (int64_t(c.rows) + 31) / 32;
+        const int by = (c.K + 255) / 256;
+        if (by > 65535) return kUnsupportedShape;
+        pack_fp4_transposed_kernel<NV, T><<<dim3(static_cast<unsigned>(bx), by), 256, 0, stream>>>(x, p);
+    } else {
+        // 16-byte loads where every row starts on 16 bytes
+        const bool vec = (reinterpret_cast<uintptr_t>(x) % 16) == 0 && (c.ld * sizeof(T)) % 16 == 0;
+        const int64_t items = int64_t(c.rows) * (p.code_bytes / 8);
+        const int64_t blocks = (items + 255) / 256;
+        if (blocks > 0x7FFFFFFF) return kUnsupportedShape;
+        const unsigned b = static_cast<unsigned>(blocks);
+        const bool narrow = blocks * 256 < (int64_t(1) << 32);
+        if (vec && narrow)
+            pack_fp4_rows_kernel<NV, T, true, uint32_t><<<b, 256, 0, stream>>>(x, p);
+        else if (vec)
+            pack_fp4_rows_kernel<NV, T, true, uint64_t><<<b, 256, 0, stream>>>(x, p);
+        else
+            pack_fp4_rows_kernel<NV, T, false, uint64_t><<<b, 256, 0, stream>>>(x, p);
+    }
+    note_launch();
+    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+}
+
+template <bool NV>
+static int launch_pack_format(const Fp4PackCall &c, cudaStream_t stream)
+{
+    Fp4PackParams p{};
+    p.ld = c.ld;
+    p.index = c.index;
+    p.g = c.tensor_scale;
+    p.codes = c.codes;
+    p.scales = c.scales;
+    p.x_rows = c.x_rows;
+    p.rows = c.rows;
+    p.K = c.K;
+    p.code_bytes = fp4_code_bytes(c.K);
+    p.pitch = fp4_scale_pitch(c.K, NV);
+    switch (c.x_type) {
+    case 0: return launch_pack_type<NV, float>(c, p, stream);
+    case 1: return launch_pack_type<NV, __nv_bfloat16>(c, p, stream);
+    default: return launch_pack_type<NV, __half>(c, p, stream);
+    }
+}
+
+int launch_fp4_pack(const Fp4PackCall &c, cudaStream_t stream)
+{
+    return c.nv ? launch_pack_format<true>(c, stream) : launch_pack_format<false>(c, stream);
+}
+
+}  // namespace igemm

@@ -548,6 +548,55 @@ __device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t smem_addr)
     return d;
 }
 
+// tma_load_2d of one CTA of a pair whose transaction bytes count on the
+// mbarrier at cluster address `bar_cluster` (this CTA's or its peer's).
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar_cluster, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
+        : "memory");
+}
+
+// D[tmem] (+)= (A * scales) . (B * scales)^T over 64 k of packed e2m1 codes (32
+// bytes a row of each K-major operand), one scale per row and 32 k (NV false:
+// ue8m0) or 16 k (NV true: ue4m3), read from TMEM: a row's four scale bytes
+// are one 32-bit word, the words of rows 32 j .. 32 j + 31 in column j of all four
+// lane quadrants.  PAIR: the .cta_group::2 form (see mma_f8f6f4_pair); each CTA's
+// TMEM holds the scales of its own A rows and of every B row.
+template <bool NV, bool PAIR>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+#define IGEMM_MMA_FP4(group, kind)                                                                              \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                             \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"( \
+                     d_tmem),                                                                                   \
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)              \
+                 : "memory")
+    if constexpr (NV && PAIR)
+        IGEMM_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (NV)
+        IGEMM_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (PAIR)
+        IGEMM_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+    else
+        IGEMM_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
+#undef IGEMM_MMA_FP4
+}
+
+// 32 lanes x 16 consecutive 32-bit columns from registers into TMEM.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // Instruction descriptor, kind::f8f6f4, dense: D f32 (bits 4-5 = 1), A and B
 // e4m3 (bits 7-9, 10-12 = 0), both K-major (bits 15, 16 = 0), N >> 3 at bits
 // 17-22, M >> 4 at bits 24-28.
@@ -561,6 +610,15 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N)
 __host__ __device__ constexpr uint32_t idesc_f8_f32(uint32_t M, uint32_t N, uint32_t fmt)
 {
     return idesc_e4m3_f32(M, N) | (fmt << 7) | (fmt << 10);
+}
+
+// Instruction descriptor of the block-scaled 4-bit kinds, dense, K = 64: A and B
+// e2m1 (bits 7-9, 10-12 = 1), both K-major, N >> 3 at bits 17-22, scale type
+// at bit 23 (0 = ue4m3, 1 = ue8m0), M >> 4 at bits 24-28.  The byte of the scale
+// words where this MMA's scales start goes to bits 4-5 (B) and 29-30 (A).
+__host__ __device__ constexpr uint32_t idesc_fp4(uint32_t M, uint32_t N, bool nv)
+{
+    return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((nv ? 0u : 1u) << 23) | ((M >> 4) << 24);
 }
 
 }  // namespace igemm
