@@ -18,15 +18,9 @@ struct Fp4Smem {
     {
         constexpr int kLimit = 227 * 1024 - 1024;  // less the alignment slack
         const int red = cs > 1 ? Cfg::kRedBytes : 0;
-        const int per_unit = Cfg::kU * Cfg::kStage + Cfg::kScaleStage;
-        int units = (kLimit - Cfg::kTailBytes - red) / per_unit;
-        if (units * Cfg::kU > Cfg::kMaxStages) units = Cfg::kMaxStages / Cfg::kU;
-        code_stages = units * Cfg::kU;
-        scale_stages = units;
-        // an odd code stage that still fits
-        if (code_stages < Cfg::kMaxStages &&
-            units * per_unit + Cfg::kStage + red + Cfg::kTailBytes <= kLimit)
-            ++code_stages;
+        const int per_stage = Cfg::kStage + Cfg::kU * Cfg::kScaleStage;
+        code_stages = std::min((kLimit - Cfg::kTailBytes - red) / per_stage, Cfg::kMaxStages / Cfg::kU);
+        scale_stages = code_stages * Cfg::kU;
         off_scales = code_stages * Cfg::kStage;
         off_red = off_scales + scale_stages * Cfg::kScaleStage;
         off_bars = off_red + red;
@@ -97,13 +91,13 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     prm.experts = c.experts;
     prm.k_steps = (c.K + 63) / 64;
     prm.k_blocks = (c.K + (Cfg::NV ? 15 : 31)) / (Cfg::NV ? 16 : 32);
-    prm.stages = (c.K + 255) / 256;
-    prm.units = (prm.stages + Cfg::kU - 1) / Cfg::kU;
+    prm.stages = (c.K + 511) / 512;
+    prm.units = Cfg::NV ? (c.K + 255) / 256 : prm.stages;
     prm.qt = plan.qt;
     prm.p_tiles = (c.N + 128 * Cfg::CL - 1) / (128 * Cfg::CL);
     prm.group_p = plan.group_p;
     prm.cs = plan.cs;
-    prm.units_per_slice = (prm.units + plan.cs - 1) / plan.cs;
+    prm.stages_per_slice = (prm.stages + plan.cs - 1) / plan.cs;
     prm.code_stages = lay.code_stages;
     prm.scale_stages = lay.scale_stages;
     prm.off_scales = lay.off_scales;
@@ -112,8 +106,8 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     prm.status = device_status_word();
     prm.limit_ns = watchdog_limit_ns();
     if (!prm.status) return kCudaError;
-    // every slice of k holds at least one unit
-    if (plan.cs > 1 && prm.units_per_slice * (plan.cs - 1) >= prm.units) return kUnsupportedShape;
+    // every slice of k holds at least one stage
+    if (plan.cs > 1 && prm.stages_per_slice * (plan.cs - 1) >= prm.stages) return kUnsupportedShape;
     const int64_t q_tiles = (int64_t(c.rows) + plan.qt - 1) / plan.qt + (c.offsets ? std::min(c.rows, c.experts) - 1 : 0);
     const int64_t tiles = q_tiles * prm.p_tiles;  // grouped: at most
     const GemmEvents ev = take_gemm_events();

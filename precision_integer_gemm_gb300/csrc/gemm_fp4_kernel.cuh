@@ -40,13 +40,13 @@ struct Fp4Params {
     int rows, N, experts;
     int k_steps;           // MMA steps of 64 k: ceil(K / 64)
     int k_blocks;          // scale bytes in use per row
-    int stages;            // 256-k stages: ceil(K / 256)
-    int units;             // scale units
+    int stages;            // pipeline stages of 512 k: ceil(K / 512)
+    int units;             // scale units: ceil(K / 512) (mx), ceil(K / 256) (nv)
     int qt;                // activation rows per tile (<= BN)
     int p_tiles;           // tiles of 128 weight rows (pair: of 256)
     int group_p;           // tiles run in groups of group_p weight tiles (fastest) by every activation tile
     int cs;                // CTAs of a cluster that split k (1: none)
-    int units_per_slice;
+    int stages_per_slice;
     int code_stages, scale_stages;
     int off_scales, off_red, off_bars;  // shared-memory offsets after the code stages
     int *status;
@@ -60,14 +60,16 @@ struct Fp4Cfg {
     static constexpr int BN = BN_;                     // most activation rows per tile
     static constexpr int CL = PAIR ? 2 : 1;
     static constexpr int kQBox = BN / CL;              // activation rows this CTA loads
-    static constexpr int kU = NV ? 1 : 2;              // code stages per scale unit
-    static constexpr int kTileP = 128 * 128;
-    static constexpr int kTileQ = kQBox * 128;
-    static constexpr int kStage = kTileP + kTileQ;     // bytes, one 256-k stage
+    static constexpr int kU = NV ? 2 : 1;              // scale units per stage
+    static constexpr int kBoxP = 128 * 128;            // bytes of 256 k
+    static constexpr int kBoxQ = kQBox * 128;
+    // a stage holds 512 k, two boxes of each operand: its 8 MMAs keep the tensor
+    // pipe busy while the issuing warp goes through its waits and commits
+    static constexpr int kStage = 2 * (kBoxP + kBoxQ);
     static constexpr int kScaleStage = (128 + BN) * 16;
     static constexpr int kQCols = BN <= 128 ? 4 : BN / 32;   // TMEM columns of one word of every activation row
     static constexpr int kSfCols = 16 + 4 * kQCols;    // TMEM columns of one unit's scales
-    static constexpr int kSfSlots = BN == 256 ? 2 : 4;
+    static constexpr int kSfSlots = BN == 256 && !NV ? 2 : 4;
     // two accumulators of BN columns; with BN = 256 the second starts before
     // the first ends (kOverlap columns), so that the scales fit beside them
     static constexpr int kAcc1 = BN == 256 ? 512 - kSfSlots * kSfCols - BN : BN;
@@ -83,7 +85,7 @@ struct Fp4Cfg {
     static constexpr int kNAlign = PAIR ? 32 : 16;
     static constexpr int kThreads = 320;
     static_assert(kQBox % 8 == 0 && kStage % 1024 == 0, "1024-byte aligned operand tiles");
-    static_assert(kTmemUse <= 512 && kOverlap >= 0 && kOverlap % 32 == 0, "TMEM budget");
+    static_assert(kTmemUse <= 512 && kOverlap >= 0 && kOverlap % 96 == 0, "TMEM budget");
     static_assert(!PAIR || BN == 256, "the pair form is built for 256 activation rows");
 };
 
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                      const Fp4Params prm)
 {
     constexpr bool NV = Cfg::NV, PAIR = Cfg::PAIR;
-    constexpr int BN = Cfg::BN, U = Cfg::kU;
+    constexpr int BN = Cfg::BN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *codes = smem;
@@ -302,72 +304,84 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int tiles = *total_slot;
     const Watchdog wd{abort_flag, prm.status, prm.limit_ns};
-    // this CTA's slice of k (split k: the cluster rank's), in units and stages
-    const int u0 = PAIR ? 0 : min(rank * prm.units_per_slice, prm.units);
-    const int u1 = PAIR ? prm.units : min(u0 + prm.units_per_slice, prm.units);
+    // this CTA's slice of k (split k: the cluster rank's), in stages
+    const int k0 = PAIR ? 0 : min(rank * prm.stages_per_slice, prm.stages);
+    const int k1 = PAIR ? prm.stages : min(k0 + prm.stages_per_slice, prm.stages);
 
     if (warp == 8) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            Fp4Ring cr(prm.code_stages), sr(prm.scale_stages);
-            uint32_t issued = 0, last = 0, s_issued = 0, s_last = 0;
-            bool ok = true;
-            for (int t = cid; ok && t < tiles; t += ncl) {
-                const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
-                const int py = x.e * prm.N + x.p0;
-                const int half = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : 0;
-                const int qy = x.q0 + pr * half;
-                for (int u = u0; ok && u < u1; ++u) {
-                    // scales of the unit
-                    if (!wait_bounded(&s_empty[sr.slot], sr.phase ^ 1u, wd)) {
+        Fp4Ring cr(prm.code_stages), sr(prm.scale_stages);
+        uint32_t issued = 0, last = 0, s_issued = 0, s_last = 0;
+        bool ok = true;
+        for (int t = cid; ok && t < tiles; t += ncl) {
+            const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
+            const int py = x.e * prm.N + x.p0;
+            const int half = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : 0;
+            const int qy = x.q0 + pr * half;
+            for (int k = k0; ok && k < k1; ++k) {
+#pragma unroll
+                for (int h = 0; h < Cfg::kU; ++h) {
+                    const int u = k * Cfg::kU + h;
+                    if (u >= prm.units) break;
+                    if (!fp4_warp_wait(&s_empty[sr.slot], sr.phase ^ 1u, wd)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *sc = scales + sr.slot * Cfg::kScaleStage;
-                    mbar_arrive_expect_tx(&s_full[sr.slot], Cfg::kScaleStage);
-                    tma_load_2d(sc, &mapSP, &s_full[sr.slot], u * 16, py);
-                    tma_load_2d(sc + 128 * 16, &mapSQ, &s_full[sr.slot], u * 16, x.q0);
+                    if (elect_one()) {
+                        uint8_t *sc = scales + sr.slot * Cfg::kScaleStage;
+                        mbar_arrive_expect_tx(&s_full[sr.slot], Cfg::kScaleStage);
+                        tma_load_2d(sc, &mapSP, &s_full[sr.slot], u * 16, py);
+                        tma_load_2d(sc + 128 * 16, &mapSQ, &s_full[sr.slot], u * 16, x.q0);
+                    }
+                    __syncwarp();
                     s_issued |= 1u << sr.slot;
                     s_last = (s_last & ~(1u << sr.slot)) | (sr.phase << sr.slot);
                     sr.next();
-                    const int k1 = min((u + 1) * U, prm.stages);
-                    for (int k = u * U; k < k1; ++k) {
-                        if (!wait_bounded(&empty[cr.slot], cr.phase ^ 1u, wd)) {
-                            ok = false;
-                            break;
+                }
+                if (!ok || !fp4_warp_wait(&empty[cr.slot], cr.phase ^ 1u, wd)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    uint8_t *st = codes + cr.slot * Cfg::kStage;
+                    if constexpr (PAIR) {
+                        // both CTAs' bytes count on the even CTA's barrier
+                        if (leader) mbar_arrive_expect_tx(&full[cr.slot], 2 * Cfg::kStage);
+                        const uint32_t bar = cluster_map(smem_u32(&full[cr.slot]), 0u);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            tma_load_2d_pair(st + h * Cfg::kBoxP, &mapP, bar, (2 * k + h) * 128, py);
+                            tma_load_2d_pair(st + 2 * Cfg::kBoxP + h * Cfg::kBoxQ, &mapQ, bar, (2 * k + h) * 128, qy);
                         }
-                        uint8_t *st = codes + cr.slot * Cfg::kStage;
-                        if constexpr (PAIR) {
-                            // both CTAs' bytes count on the even CTA's barrier
-                            if (leader) mbar_arrive_expect_tx(&full[cr.slot], 2 * Cfg::kStage);
-                            const uint32_t bar = cluster_map(smem_u32(&full[cr.slot]), 0u);
-                            tma_load_2d_pair(st, &mapP, bar, k * 128, py);
-                            tma_load_2d_pair(st + Cfg::kTileP, &mapQ, bar, k * 128, qy);
-                        } else {
-                            mbar_arrive_expect_tx(&full[cr.slot], Cfg::kStage);
-                            tma_load_2d(st, &mapP, &full[cr.slot], k * 128, py);
-                            tma_load_2d(st + Cfg::kTileP, &mapQ, &full[cr.slot], k * 128, qy);
+                    } else {
+                        mbar_arrive_expect_tx(&full[cr.slot], Cfg::kStage);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            tma_load_2d(st + h * Cfg::kBoxP, &mapP, &full[cr.slot], (2 * k + h) * 128, py);
+                            tma_load_2d(st + 2 * Cfg::kBoxP + h * Cfg::kBoxQ, &mapQ, &full[cr.slot],
+                                        (2 * k + h) * 128, qy);
                         }
-                        issued |= 1u << cr.slot;
-                        last = (last & ~(1u << cr.slot)) | (cr.phase << cr.slot);
-                        cr.next();
                     }
                 }
+                __syncwarp();
+                issued |= 1u << cr.slot;
+                last = (last & ~(1u << cr.slot)) | (cr.phase << cr.slot);
+                cr.next();
             }
-            // never leave with copies in flight, nor with an MMA commit on its way here
-#pragma unroll 1
-            for (int s = 0; s < prm.code_stages; ++s)
-                if ((issued >> s) & 1u) {
-                    if (leader) fp4_wait_drain(&full[s], (last >> s) & 1u, prm.limit_ns);
-                    fp4_wait_drain(&empty[s], (last >> s) & 1u, prm.limit_ns);
-                }
-#pragma unroll 1
-            for (int s = 0; s < prm.scale_stages; ++s)
-                if ((s_issued >> s) & 1u) fp4_wait_drain(&s_full[s], (s_last >> s) & 1u, prm.limit_ns);
         }
+        // never leave with copies in flight, nor with an MMA commit on its way here
+#pragma unroll 1
+        for (int s = 0; s < prm.code_stages; ++s)
+            if ((issued >> s) & 1u) {
+                if (leader) fp4_wait_drain(&full[s], (last >> s) & 1u, prm.limit_ns);
+                fp4_wait_drain(&empty[s], (last >> s) & 1u, prm.limit_ns);
+            }
+#pragma unroll 1
+        for (int s = 0; s < prm.scale_stages; ++s)
+            if ((s_issued >> s) & 1u) fp4_wait_drain(&s_full[s], (s_last >> s) & 1u, prm.limit_ns);
     } else if (warp == 9) {
         // ------------------------------------------------------------ MMA issuer
-        if (leader && lane == 0) {
+        if (leader) {
             Fp4Ring cr(prm.code_stages), fr(Cfg::kSfSlots);
             const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(codes));
             uint32_t nacc = 0;
@@ -380,66 +394,74 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 const uint32_t d_tmem = tmem + ab * Cfg::kAcc1;
                 if constexpr (Cfg::kOverlap > 0) {
                     // the tile before has left the columns that both accumulators use
-                    if (nacc > 0 && !wait_bounded(&acc_empty[ab ^ 1u], ((nacc - 1u) >> 1) & 1u, wd)) break;
+                    if (nacc > 0 && !fp4_warp_wait(&acc_empty[ab ^ 1u], ((nacc - 1u) >> 1) & 1u, wd)) break;
                 } else {
-                    if (!wait_bounded(&acc_empty[ab], ((nacc >> 1) & 1u) ^ 1u, wd)) break;
+                    if (!fp4_warp_wait(&acc_empty[ab], ((nacc >> 1) & 1u) ^ 1u, wd)) break;
                 }
-                tc_fence_after();
-                uint32_t acc = 0;
-                for (int u = u0; ok && u < u1; ++u) {
-                    if (!wait_bounded(&sf_ready[fr.slot], fr.phase, wd)) {
+                for (int k = k0; k < k1; ++k) {
+                    if (!fp4_warp_wait(&full[cr.slot], cr.phase, wd)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t sfp = tmem + Cfg::kSf0 + fr.slot * Cfg::kSfCols;
-                    const uint32_t sfq = sfp + 16;
+                    const uint64_t a0 = desc0 + static_cast<uint64_t>((cr.slot * Cfg::kStage) >> 4);
+                    const uint64_t b0 = a0 + static_cast<uint64_t>((2 * Cfg::kBoxP) >> 4);
+                    const int steps = prm.k_steps - 8 * k;
 #pragma unroll
-                    for (int h = 0; h < U; ++h) {
-                        const int k = u * U + h;
-                        if (k >= prm.stages) break;
-                        if (!wait_bounded(&full[cr.slot], cr.phase, wd)) {
+                    for (int h = 0; h < Cfg::kU; ++h) {
+                        if (k * Cfg::kU + h >= prm.units) break;
+                        if (!fp4_warp_wait(&sf_ready[fr.slot], fr.phase, wd)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t a0 = desc0 + static_cast<uint64_t>((cr.slot * Cfg::kStage) >> 4);
-                        const uint64_t b0 = a0 + static_cast<uint64_t>(Cfg::kTileP >> 4);
-                        const int steps = prm.k_steps - 4 * k;
+                        const uint32_t sfp = tmem + Cfg::kSf0 + fr.slot * Cfg::kSfCols;
+                        const uint32_t sfq = sfp + 16;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (q < steps) {
-                                const int step = 4 * h + q;            // of the unit
-                                const int word = NV ? step : step / 2;  // a word holds 64 (nv) or 128 (mx) k
-                                const uint32_t id = NV ? 0u : 2u * (step & 1);
-                                mma_fp4<NV, PAIR>(d_tmem, a0 + static_cast<uint64_t>(2 * q),
-                                                  b0 + static_cast<uint64_t>(2 * q), idesc | (id << 4) | (id << 29),
-                                                  sfp + 4 * word, sfq + Cfg::kQCols * word, acc);
-                                acc = 1;
+                            for (int q = 0; q < 8 / Cfg::kU; ++q) {  // MMA q of the unit
+                                const int step = h * (8 / Cfg::kU) + q;
+                                if (step < steps) {
+                                    const int word = NV ? q : q / 2;  // a word holds 64 (nv) or 128 (mx) k
+                                    const uint32_t id = NV ? 0u : 2u * (q & 1);
+                                    const int box = step / 4, in = step % 4;
+                                    mma_fp4<NV, PAIR>(d_tmem, a0 + static_cast<uint64_t>((box * Cfg::kBoxP >> 4) + 2 * in),
+                                                      b0 + static_cast<uint64_t>((box * Cfg::kBoxQ >> 4) + 2 * in),
+                                                      idesc | (id << 4) | (id << 29), sfp + 4 * word,
+                                                      sfq + Cfg::kQCols * word, k > k0 || step > 0 ? 1u : 0u);
+                                }
                             }
+                            if constexpr (PAIR)
+                                mma_commit_pair_multicast(&sf_free[fr.slot], 0x3);
+                            else
+                                mma_commit(&sf_free[fr.slot]);
                         }
+                        __syncwarp();
+                        fr.next();
+                    }
+                    if (!ok) break;
+                    if (elect_one()) {
                         if constexpr (PAIR)
                             mma_commit_pair_multicast(&empty[cr.slot], 0x3);
                         else
                             mma_commit(&empty[cr.slot]);
-                        cr.next();
                     }
-                    if constexpr (PAIR)
-                        mma_commit_pair_multicast(&sf_free[fr.slot], 0x3);
-                    else
-                        mma_commit(&sf_free[fr.slot]);
-                    fr.next();
+                    __syncwarp();
+                    cr.next();
                 }
-                if (ok) {
+                if (ok && elect_one()) {
                     if constexpr (PAIR)
                         mma_commit_pair_multicast(&acc_full[ab], 0x3);
                     else
                         mma_commit(&acc_full[ab]);
                 }
+                __syncwarp();
             }
-            if constexpr (PAIR)
-                mma_commit_pair(mma_drain);
-            else
-                mma_commit(mma_drain);
+            if (elect_one()) {
+                if constexpr (PAIR)
+                    mma_commit_pair(mma_drain);
+                else
+                    mma_commit(mma_drain);
+            }
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ scales into TMEM
@@ -449,7 +471,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         Fp4Ring sr(prm.scale_stages), fr(Cfg::kSfSlots);
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
-            for (int u = u0; u < u1; ++u) {
+            const int u1 = min(k1 * Cfg::kU, prm.units);
+            for (int u = k0 * Cfg::kU; u < u1; ++u) {
                 if (!fp4_warp_wait(&s_full[sr.slot], sr.phase, wd)) {
                     ok = false;
                     break;
@@ -573,19 +596,21 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 continue;
             }
             if constexpr (Cfg::kOverlap > 0) {
-                // the columns that the other accumulator shares first: once they are
-                // in registers the next tile may start
+                // the columns that the other accumulator shares first, 96 at a time: once
+                // they are in registers the next tile may start
                 const int shared0 = ab ? 0 : BN - Cfg::kOverlap;
                 uint32_t v[3][32];
+#pragma unroll 1
+                for (int c = shared0; c < shared0 + Cfg::kOverlap; c += 96) {
 #pragma unroll
-                for (int i = 0; i < Cfg::kOverlap / 32; ++i) tmem_ld_32x32b_x32(tacc + shared0 + 32 * i, v[i]);
-                tmem_ld_wait_regs(v[0], v[1]);
-                tmem_ld_wait_regs(v[2]);
-                release();
+                    for (int i = 0; i < 3; ++i) tmem_ld_32x32b_x32(tacc + c + 32 * i, v[i]);
+                    tmem_ld_wait_regs(v[0], v[1]);
+                    tmem_ld_wait_regs(v[2]);
+                    if (c + 96 == shared0 + Cfg::kOverlap) release();
 #pragma unroll
-                for (int i = 0; i < Cfg::kOverlap / 32; ++i)
-                    fp4_store<32>(prm, v[i], alpha, static_cast<int64_t>(x.q0) + shared0 + 32 * i,
-                                  x.nq - shared0 - 32 * i, n);
+                    for (int i = 0; i < 3; ++i)
+                        fp4_store<32>(prm, v[i], alpha, static_cast<int64_t>(x.q0) + c + 32 * i, x.nq - c - 32 * i, n);
+                }
                 const int c_end = min(x.nq, ab ? BN : BN - Cfg::kOverlap);
 #pragma unroll 1
                 for (int c = ab ? Cfg::kOverlap : 0; c < c_end; c += 32) {

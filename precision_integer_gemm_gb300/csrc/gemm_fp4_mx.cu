@@ -6,8 +6,7 @@ namespace igemm {
 
 int fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *plan)
 {
-    const int units = (c.K + (c.nv ? 255 : 511)) / (c.nv ? 256 : 512);
-    const int stages_per_unit = c.nv ? 1 : 2;
+    const int stages = (c.K + 511) / 512;
     // activation rows of a typical group, and the groups that have any
     double groups = 1.0;
     if (c.offsets) groups = c.experts * (1.0 - std::pow(1.0 - 1.0 / c.experts, double(c.rows)));
@@ -32,12 +31,12 @@ int fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *pla
     const double tiles = double(p_tiles) * std::ceil(typical / plan->bn) * groups;
     double best = -1;
     for (int cs = 1; cs <= (plan->bn == 128 ? 2 : 8); cs *= 2) {
-        const int per = (units + cs - 1) / cs;
-        if (cs > 1 && per * (cs - 1) >= units) break;
+        const int per = (stages + cs - 1) / cs;
+        if (cs > 1 && per * (cs - 1) >= stages) break;
         const int clusters = max_clusters(plan->bn, false, cs);
         if (clusters < 1) return kCudaError;
         // the busiest cluster's stages, plus a tile's fill and epilogue
-        const double cost = std::ceil(tiles / clusters) * (per * stages_per_unit + (cs > 1 ? 3 : 2));
+        const double cost = std::ceil(tiles / clusters) * (per + (cs > 1 ? 1.5 : 1.0));
         if (best < 0 || cost < best) {
             best = cost;
             plan->cs = cs;

@@ -190,6 +190,21 @@ __device__ __forceinline__ void tma_load_2d_multicast(void *dst, const CUtensorM
         : "memory");
 }
 
+// True in one lane of a converged warp, always the same one.  A warp that runs
+// its loop and its waits together and issues from the elected lane keeps the
+// operands of tcgen05.mma in uniform registers; a loop run by a single lane does
+// not, and issues more slowly.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_ctarank()
 {
     uint32_t r;
