@@ -9,22 +9,29 @@
 
 namespace igemm {
 
-// Shared memory of one launch: code stages, scale stages, the partials of a
-// split k, then barriers and the groups' tile counts.
+// Shared memory of one launch: code stages, the ring of scales, the partials of a
+// split k, the epilogue's staging, then barriers and the groups' tile counts.
 template <class Cfg>
 struct Fp4Smem {
-    int code_stages, scale_stages, off_scales, off_red, off_bars, total;
-    explicit Fp4Smem(int cs)
+    int code_stages, scale_stages, off_scales, off_red, off_store, off_bars, total;
+    Fp4Smem(int cs, int experts)
     {
         constexpr int kLimit = 227 * 1024 - 1024;  // less the alignment slack
         const int red = cs > 1 ? Cfg::kRedBytes : 0;
-        const int per_stage = Cfg::kStage + Cfg::kU * Cfg::kScaleStage;
-        code_stages = std::min((kLimit - Cfg::kTailBytes - red) / per_stage, Cfg::kMaxStages / Cfg::kU);
-        scale_stages = code_stages * Cfg::kU;
+        const int tail = Cfg::kTailBytes + 4 * (experts + 1);
+        const int left = kLimit - red - Cfg::kStoreBytes - tail;
+        // Three blocks of scales where they fit: their loads run ahead of the MMAs by
+        // the load's latency and the turning.  (2 scale_stages <= code_stages + 1: the
+        // producer learns from the codes' barriers that a block's scales are free, and
+        // a barrier must not complete its next phase before that.)
+        code_stages = std::min((left - 3 * Cfg::kScaleStage) / Cfg::kStage, static_cast<int>(Cfg::kMaxStages));
+        scale_stages = std::min(std::min((left - code_stages * Cfg::kStage) / Cfg::kScaleStage, (code_stages + 1) / 2),
+                                static_cast<int>(Cfg::kMaxScaleStages));
         off_scales = code_stages * Cfg::kStage;
         off_red = off_scales + scale_stages * Cfg::kScaleStage;
-        off_bars = off_red + red;
-        total = off_bars + Cfg::kTailBytes + 1024;
+        off_store = off_red + red;
+        off_bars = off_store + Cfg::kStoreBytes;
+        total = off_bars + tail + 1024;
     }
 };
 
@@ -77,10 +84,11 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (make_map(&mapP, kU8, c.B, p_rows, code_bytes, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
         make_map(&mapQ, kU8, c.A, c.rows, code_bytes, Cfg::kQBox, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
-        make_map(&mapSP, kU8, c.SFB, p_rows, pitch, 128, 16, CU_TENSOR_MAP_SWIZZLE_NONE) != kOk ||
-        make_map(&mapSQ, kU8, c.SFA, c.rows, pitch, Cfg::BN, 16, CU_TENSOR_MAP_SWIZZLE_NONE) != kOk)
+        make_map(&mapSP, kU8, c.SFB, p_rows, pitch, 128, 16 * Cfg::kH, CU_TENSOR_MAP_SWIZZLE_NONE) != kOk ||
+        make_map(&mapSQ, kU8, c.SFA, c.rows, pitch, Cfg::kQScaleRows, 16 * Cfg::kH,
+                 CU_TENSOR_MAP_SWIZZLE_NONE) != kOk)
         return kCudaError;
-    const Fp4Smem<Cfg> lay(csize > 1 && !Cfg::PAIR ? csize : 1);
+    const Fp4Smem<Cfg> lay(Cfg::PAIR ? 1 : csize, c.offsets ? c.experts : 0);
     Fp4Params prm{};
     prm.C = c.C;
     prm.c_type = c.c_type;
@@ -91,23 +99,25 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     prm.experts = c.experts;
     prm.k_steps = (c.K + 63) / 64;
     prm.k_blocks = (c.K + (Cfg::NV ? 15 : 31)) / (Cfg::NV ? 16 : 32);
-    prm.stages = (c.K + 511) / 512;
-    prm.units = Cfg::NV ? (c.K + 255) / 256 : prm.stages;
+    prm.blocks = (c.K + 511) / 512;
     prm.qt = plan.qt;
     prm.p_tiles = (c.N + 128 * Cfg::CL - 1) / (128 * Cfg::CL);
     prm.group_p = plan.group_p;
     prm.cs = plan.cs;
-    prm.stages_per_slice = (prm.stages + plan.cs - 1) / plan.cs;
+    prm.blocks_per_slice = (prm.blocks + plan.cs - 1) / plan.cs;
     prm.code_stages = lay.code_stages;
     prm.scale_stages = lay.scale_stages;
     prm.off_scales = lay.off_scales;
     prm.off_red = lay.off_red;
+    prm.off_store = lay.off_store;
     prm.off_bars = lay.off_bars;
+    const uintptr_t rows_at = reinterpret_cast<uintptr_t>(c.C) | (static_cast<uintptr_t>(c.N) * 2);
+    prm.store_bytes = rows_at % 16 == 0 ? 16 : rows_at % 4 == 0 ? 4 : 2;
     prm.status = device_status_word();
     prm.limit_ns = watchdog_limit_ns();
     if (!prm.status) return kCudaError;
-    // every slice of k holds at least one stage
-    if (plan.cs > 1 && prm.stages_per_slice * (plan.cs - 1) >= prm.stages) return kUnsupportedShape;
+    // every slice of k holds at least one block
+    if (plan.cs > 1 && prm.blocks_per_slice * (plan.cs - 1) >= prm.blocks) return kUnsupportedShape;
     const int64_t q_tiles = (int64_t(c.rows) + plan.qt - 1) / plan.qt + (c.offsets ? std::min(c.rows, c.experts) - 1 : 0);
     const int64_t tiles = q_tiles * prm.p_tiles;  // grouped: at most
     const GemmEvents ev = take_gemm_events();

@@ -10,15 +10,25 @@
 // descriptor, and a lane of the accumulator is an output column, so C rows are
 // written 32 consecutive columns at a time whatever their alignment.
 //
-// The scale of a row's 16 bytes (512 k mx, 256 k nv: one "unit") lands with its own
-// small TMA box, row-major as the caller has it, at any row (a group starts
-// anywhere).  The tensor core wants the words of 128 rows across 4 columns of
-// all four TMEM lane quadrants, so four warps, one per quadrant, read the rows'
-// 16 bytes (conflict-free) and store the 4 words of every row with two TMEM
-// stores per unit; no layout pass runs over the scales.
+// A block of 512 k is the unit of the loop: two stages of codes (256 k, 128 bytes a
+// row, each with its own slot) and the block's scales.  These stay row-major as
+// the caller has them, 16 (mx) or 32 (nv) bytes a row and block, at any row (a
+// group starts anywhere).  The tensor core wants the words (4 bytes) of 128 rows
+// across 4 columns of all four TMEM lane quadrants.  A block's rows land in a
+// small ring by TMA, in order with the codes; a warp per 128 rows turns them in
+// place (lane i reads rows i, 32 + i, 64 + i, 96 + i and writes word w of the four as 16
+// bytes of the w-th 512), and tcgen05.cp spreads the 512s over the quadrants, in
+// order with the MMAs.  So scales cost four times their bytes in shared-memory
+// traffic beside the codes' 32 KB written and read per stage.
+// (Loaded with plain loads, the scales waited microseconds behind the operand
+// stream: 338 us at 8192^3.  Stored to TMEM by a warp per quadrant, every scale
+// was read four times.)
 //
-// Warps 0-3 epilogue, 4-7 scales, 8 TMA producer, 9 MMA issue.  Persistent
-// CTAs (or CTA pairs, or clusters that split k).  Every wait is bounded.
+// The issuing warp sets the pace of the loop (an MMA takes it about 50 cycles, a
+// successful wait as much again), so a block has one joint wait and 8 MMAs.
+//
+// Warps 0-3 epilogue, 4 TMA producer, 5 MMA issue, 6 and up scales.  Persistent CTAs
+// (or CTA pairs, or clusters that split k).  Every wait is bounded.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -40,15 +50,15 @@ struct Fp4Params {
     int rows, N, experts;
     int k_steps;           // MMA steps of 64 k: ceil(K / 64)
     int k_blocks;          // scale bytes in use per row
-    int stages;            // pipeline stages of 512 k: ceil(K / 512)
-    int units;             // scale units: ceil(K / 512) (mx), ceil(K / 256) (nv)
+    int blocks;            // of 512 k: ceil(K / 512)
     int qt;                // activation rows per tile (<= BN)
     int p_tiles;           // tiles of 128 weight rows (pair: of 256)
     int group_p;           // tiles run in groups of group_p weight tiles (fastest) by every activation tile
     int cs;                // CTAs of a cluster that split k (1: none)
-    int stages_per_slice;
-    int code_stages, scale_stages;
-    int off_scales, off_red, off_bars;  // shared-memory offsets after the code stages
+    int blocks_per_slice;
+    int code_stages, scale_stages;  // ring slots: 256 k of codes, 512 k of scales (2 scale_stages <= code_stages + 1)
+    int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
+    int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
     int *status;
     unsigned long long limit_ns;
 };
@@ -60,16 +70,19 @@ struct Fp4Cfg {
     static constexpr int BN = BN_;                     // most activation rows per tile
     static constexpr int CL = PAIR ? 2 : 1;
     static constexpr int kQBox = BN / CL;              // activation rows this CTA loads
-    static constexpr int kU = NV ? 2 : 1;              // scale units per stage
+    static constexpr int kH = NV ? 2 : 1;              // 16-byte pieces of a row's scales per block
     static constexpr int kBoxP = 128 * 128;            // bytes of 256 k
     static constexpr int kBoxQ = kQBox * 128;
-    // a stage holds 512 k, two boxes of each operand: its 8 MMAs keep the tensor
-    // pipe busy while the issuing warp goes through its waits and commits
-    static constexpr int kStage = 2 * (kBoxP + kBoxQ);
-    static constexpr int kScaleStage = (128 + BN) * 16;
+    static constexpr int kStage = kBoxP + kBoxQ;
+    static constexpr int kQGroups = (BN + 127) / 128;  // groups of 128 activation rows
+    static constexpr int kQScaleRows = BN < 128 ? BN : 128;  // rows of a scale box of the activations
+    static constexpr int kGroupBytes = kH * 2048;            // a block's scales of 128 rows
+    static constexpr int kScaleStage = (1 + kQGroups) * kGroupBytes;
+    static constexpr int kScaleTx = (128 + BN) * 16 * kH;         // bytes that land in it
+    static constexpr int kMaxScaleStages = 4;
     static constexpr int kQCols = BN <= 128 ? 4 : BN / 32;   // TMEM columns of one word of every activation row
-    static constexpr int kSfCols = 16 + 4 * kQCols;    // TMEM columns of one unit's scales
-    static constexpr int kSfSlots = BN == 256 && !NV ? 2 : 4;
+    static constexpr int kSfCols = 16 + 4 * kQCols;    // TMEM columns of four words: a block (mx), a stage (nv)
+    static constexpr int kSfSlots = 2;                 // such sets of columns, used in turn
     // two accumulators of BN columns; with BN = 256 the second starts before
     // the first ends (kOverlap columns), so that the scales fit beside them
     static constexpr int kAcc1 = BN == 256 ? 512 - kSfSlots * kSfCols - BN : BN;
@@ -80,10 +93,12 @@ struct Fp4Cfg {
     static constexpr int kRedBufs = BN <= 32 ? 2 : 1;
     static constexpr int kRedBytes = kRedBufs * BN * 512;  // split k: partial tiles of the cluster's CTAs
     static constexpr int kMaxStages = 16;
-    static constexpr int kNumBars = 4 * kMaxStages + 2 * kSfSlots + 4 + 1 + 4;
-    static constexpr int kTailBytes = 8 * kNumBars + 64 + 4 * (kFp4MaxExperts + 1);
+    static constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxScaleStages + 4 + 1 + 4;
+    static constexpr int kStoreBytes = 4 * 1024;  // 16-bit C: 16 rows x 32 columns per epilogue warp
+    static constexpr int kTailBytes = 8 * kNumBars + 64;  // and the groups' tile counts
     static constexpr int kNAlign = PAIR ? 32 : 16;
-    static constexpr int kThreads = 320;
+    static constexpr int kWarpProd = 4, kWarpMma = 5, kWarpScale = 6;
+    static constexpr int kThreads = 32 * (kWarpScale + 1 + kQGroups);
     static_assert(kQBox % 8 == 0 && kStage % 1024 == 0, "1024-byte aligned operand tiles");
     static_assert(kTmemUse <= 512 && kOverlap >= 0 && kOverlap % 96 == 0, "TMEM budget");
     static_assert(!PAIR || BN == 256, "the pair form is built for 256 activation rows");
@@ -135,6 +150,16 @@ __device__ __forceinline__ bool fp4_warp_wait(uint64_t *bar, uint32_t parity, co
     return __all_sync(0xffffffffu, ok);
 }
 
+// Three barriers (their tests overlap when they are already complete).
+__device__ __forceinline__ bool fp4_warp_wait3(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb, uint64_t *c,
+                                               uint32_t pc, const Watchdog &wd)
+{
+    const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb), rc = mbar_try_wait(c, pc);
+    if (__all_sync(0xffffffffu, ra && rb && rc)) return true;
+    const bool ok = wait_bounded(a, pa, wd) && wait_bounded(b, pb, wd) && wait_bounded(c, pc, wd);
+    return __all_sync(0xffffffffu, ok);
+}
+
 __device__ __forceinline__ bool fp4_warp_wait_cluster(uint64_t *bar, uint32_t parity, const Watchdog &wd)
 {
     const bool ok = wait_bounded_cluster(bar, parity, wd);
@@ -168,28 +193,139 @@ __device__ __forceinline__ uint32_t fp4_keep(uint32_t v, int left)
     return left >= 4 ? v : left <= 0 ? 0u : v & (0xFFFFFFFFu >> (8 * (4 - left)));
 }
 
-// `count` accumulator columns (rows m0 .. of C) of this lane's output column n.
-template <int COUNT>
-__device__ __forceinline__ void fp4_store(const Fp4Params &prm, const uint32_t (&v)[COUNT], float alpha, int64_t m0,
-                                          int count, int n)
+// One value of C.
+__device__ __forceinline__ void fp4_store1(const Fp4Params &prm, float v, int64_t m, int n)
 {
     if (n >= prm.N) return;
-    const int64_t at = m0 * prm.N + n;
-    if (prm.c_type == kOutF32) {
-        float *c = static_cast<float *>(prm.C) + at;
-#pragma unroll
-        for (int j = 0; j < COUNT; ++j)
-            if (j < count) c[static_cast<int64_t>(j) * prm.N] = __uint_as_float(v[j]) * alpha;
-    } else if (prm.c_type == kOutBf16) {
-        __nv_bfloat16 *c = static_cast<__nv_bfloat16 *>(prm.C) + at;
-#pragma unroll
-        for (int j = 0; j < COUNT; ++j)
-            if (j < count) c[static_cast<int64_t>(j) * prm.N] = __float2bfloat16_rn(__uint_as_float(v[j]) * alpha);
+    const int64_t at = m * prm.N + n;
+    if (prm.c_type == kOutF32)
+        static_cast<float *>(prm.C)[at] = v;
+    else if (prm.c_type == kOutBf16)
+        static_cast<__nv_bfloat16 *>(prm.C)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half *>(prm.C)[at] = __float2half_rn(v);
+}
+
+// 16 accumulator columns (rows of C) of the warp's 32 lanes (columns of C).
+// float32: thread = lane, its 16 columns; a store is 128 contiguous bytes of a row.
+// 16-bit: in fragment order (tmem_ld_16x256b_x2, lanes 0-15 then 16-31), turned by
+// stmatrix so that a row's 32 columns are contiguous in the warp's 1 KB of
+// shared memory (64-byte rows, 16-byte chunk c of row r at c ^ (r / 2 % 4)) and
+// leave with wide stores.
+template <bool F32>
+__device__ __forceinline__ void fp4_load16_cols(uint32_t tacc, int c, uint32_t (&v)[16])
+{
+    if constexpr (F32) {
+        tmem_ld_32x32b_x16(tacc + c, v);
     } else {
-        __half *c = static_cast<__half *>(prm.C) + at;
+        tmem_ld_16x256b_x2(tacc + c, v);
+        tmem_ld_16x256b_x2(tacc + (16u << 16) + c, v + 8);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void fp4_store16_cols(const Fp4Params &prm, const uint32_t (&v)[16], float alpha, int64_t m0,
+                                                 int count, int n0, uint8_t *stage)
+{
+    const int lane = threadIdx.x & 31;
+    if constexpr (F32) {
+        if (n0 + lane < prm.N) {
+            float *c = static_cast<float *>(prm.C) + m0 * prm.N + n0 + lane;
 #pragma unroll
-        for (int j = 0; j < COUNT; ++j)
-            if (j < count) c[static_cast<int64_t>(j) * prm.N] = __float2half_rn(__uint_as_float(v[j]) * alpha);
+            for (int j = 0; j < 16; ++j) {
+                if (j < count) *c = __uint_as_float(v[j]) * alpha;
+                c += prm.N;
+            }
+        }
+    } else {
+        const bool bf16 = prm.c_type == kOutBf16;
+        uint32_t pk[8];  // matrix (half h, rows + 8 s, columns 8 j): pk[4 h + 2 j + s]
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float lo = __uint_as_float(v[2 * i]) * alpha, hi = __uint_as_float(v[2 * i + 1]) * alpha;
+            if (bf16) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+                pk[i] = *reinterpret_cast<const uint32_t *>(&b);
+            } else {
+                const __half2 b = __floats2half2_rn(lo, hi);
+                pk[i] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+        const uint32_t base = smem_u32(stage);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = 8 * j + (lane & 7), chunk = lane >> 3;
+            stmatrix_x4_trans(base + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4), pk[2 * j], pk[2 * j + 1], pk[4 + 2 * j],
+                              pk[4 + 2 * j + 1]);
+        }
+        __syncwarp();
+        uint16_t *c = static_cast<uint16_t *>(prm.C) + m0 * prm.N;
+        if (prm.store_bytes == 16) {  // (N is a multiple of 8)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * i + (lane >> 2), chunk = lane & 3, n = n0 + 8 * chunk;
+                const uint4 q = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
+                if (r < count && n < prm.N) *reinterpret_cast<uint4 *>(c + static_cast<int64_t>(r) * prm.N + n) = q;
+            }
+        } else if (prm.store_bytes == 4) {  // (N is even)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 2 * i + (lane >> 4), w = lane & 15, n = n0 + 2 * w;
+                const uint32_t q = *reinterpret_cast<const uint32_t *>(
+                    stage + r * 64 + (((w >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (w & 3));
+                if (r < count && n < prm.N) *reinterpret_cast<uint32_t *>(c + static_cast<int64_t>(r) * prm.N + n) = q;
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int n = n0 + lane;
+                const uint16_t q = *reinterpret_cast<const uint16_t *>(
+                    stage + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7));
+                if (r < count && n < prm.N) c[static_cast<int64_t>(r) * prm.N + n] = q;
+            }
+        }
+        __syncwarp();  // read before the next columns overwrite it
+    }
+}
+
+// A tile's accumulator to C; release() once its columns that the other
+// accumulator shares (with no overlap: all) are in registers.
+template <class Cfg, bool F32, class Release>
+__device__ __forceinline__ void fp4_store_tile(const Fp4Params &prm, const Fp4Tile &x, uint32_t tacc, uint32_t ab,
+                                               float alpha, int n0, uint8_t *stage, Release release)
+{
+    int c = 0, c_end = x.nq;
+    if constexpr (Cfg::kOverlap > 0) {
+        const int shared0 = ab ? 0 : Cfg::BN - Cfg::kOverlap;
+#pragma unroll 1
+        for (int s = shared0; s < shared0 + Cfg::kOverlap; s += 96) {
+            uint32_t v[6][16];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) fp4_load16_cols<F32>(tacc, s + 16 * i, v[i]);
+#pragma unroll
+            for (int i = 0; i < 6; i += 2) tmem_ld_wait_regs(v[i], v[i + 1]);
+            if (s + 96 == shared0 + Cfg::kOverlap) release();
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+                if (s + 16 * i < x.nq)
+                    fp4_store16_cols<F32>(prm, v[i], alpha, static_cast<int64_t>(x.q0) + s + 16 * i, x.nq - s - 16 * i,
+                                          n0, stage);
+        }
+        c = ab ? Cfg::kOverlap : 0;
+        c_end = min(x.nq, ab ? Cfg::BN : Cfg::BN - Cfg::kOverlap);
+    }
+#pragma unroll 1
+    for (; c < c_end; c += 32) {
+        uint32_t v[2][16];
+        fp4_load16_cols<F32>(tacc, c, v[0]);
+        fp4_load16_cols<F32>(tacc, c + 16, v[1]);
+        tmem_ld_wait_regs(v[0], v[1]);
+        if (Cfg::kOverlap == 0 && c + 32 >= c_end) release();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (c + 16 * i < c_end)
+                fp4_store16_cols<F32>(prm, v[i], alpha, static_cast<int64_t>(x.q0) + c + 16 * i, c_end - c - 16 * i, n0,
+                                      stage);
     }
 }
 
@@ -209,11 +345,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + prm.off_bars);
     uint64_t *full = bars;                          // [stages] codes landed (pair: both CTAs', in the even CTA)
     uint64_t *empty = full + Cfg::kMaxStages;       // [stages] codes consumed (MMA commit)
-    uint64_t *s_full = empty + Cfg::kMaxStages;     // [scale stages] scale bytes landed
-    uint64_t *s_empty = s_full + Cfg::kMaxStages;   // [scale stages] ... read (4 scale warps)
-    uint64_t *sf_ready = s_empty + Cfg::kMaxStages; // [slots] scales in TMEM (scale warps; pair: of both CTAs)
-    uint64_t *sf_free = sf_ready + Cfg::kSfSlots;   // [slots] ... consumed (MMA commit)
-    uint64_t *acc_full = sf_free + Cfg::kSfSlots;   // [2] accumulator complete (commit)
+    uint64_t *sf_raw = empty + Cfg::kMaxStages;     // [scale stages] scale rows landed
+    uint64_t *sf_full = sf_raw + Cfg::kMaxScaleStages;    // [scale stages] ... turned (scale warps; even CTA of a pair:
+                                                          // and the odd CTA's, its relay)
+    uint64_t *acc_full = sf_full + Cfg::kMaxScaleStages;  // [2] accumulator complete (commit)
     uint64_t *acc_empty = acc_full + 2;             // [2] accumulator (its overlap) read by the epilogue warps
     uint64_t *mma_drain = acc_empty + 2;
     uint64_t *red_full = mma_drain + 1;             // [2] split k: every CTA's partials of this CTA's columns written
@@ -238,12 +373,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < prm.scale_stages; ++s) {
-            mbar_init(&s_full[s], 1);
-            mbar_init(&s_empty[s], 4);
-        }
-        for (int s = 0; s < Cfg::kSfSlots; ++s) {
-            mbar_init(&sf_ready[s], 4 * Cfg::CL);
-            mbar_init(&sf_free[s], 1);
+            mbar_init(&sf_raw[s], 1);
+            mbar_init(&sf_full[s], 1 + Cfg::kQGroups + (PAIR && leader ? 1 : 0));
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -259,7 +390,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         tma_prefetch_map(&mapSP);
         tma_prefetch_map(&mapSQ);
     }
-    if (warp == 9) {
+    if (warp == Cfg::kWarpMma) {
         if constexpr (PAIR) {
             tmem_alloc_pair(tmem_slot, Cfg::kTmemCols);
             tmem_relinquish_pair();
@@ -304,69 +435,71 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int tiles = *total_slot;
     const Watchdog wd{abort_flag, prm.status, prm.limit_ns};
-    // this CTA's slice of k (split k: the cluster rank's), in stages
-    const int k0 = PAIR ? 0 : min(rank * prm.stages_per_slice, prm.stages);
-    const int k1 = PAIR ? prm.stages : min(k0 + prm.stages_per_slice, prm.stages);
+    // this CTA's slice of k (split k: the cluster rank's), in blocks
+    const int b0 = PAIR ? 0 : min(rank * prm.blocks_per_slice, prm.blocks);
+    const int b1 = PAIR ? prm.blocks : min(b0 + prm.blocks_per_slice, prm.blocks);
 
-    if (warp == 8) {
+    if (warp == Cfg::kWarpProd) {
         // ------------------------------------------------------------ producer
-        Fp4Ring cr(prm.code_stages), sr(prm.scale_stages);
+        // er: the last stage of the block that had the next scale slot before
+        Fp4Ring cr(prm.code_stages), sr(prm.scale_stages), er(prm.code_stages);
         uint32_t issued = 0, last = 0, s_issued = 0, s_last = 0;
+        int filled = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
             const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
             const int py = x.e * prm.N + x.p0;
             const int half = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : 0;
             const int qy = x.q0 + pr * half;
-            for (int k = k0; ok && k < k1; ++k) {
+            for (int b = b0; ok && b < b1; ++b) {
+                if (filled == prm.scale_stages) {
+                    er.next();
+                    if (!fp4_warp_wait(&empty[er.slot], er.phase, wd)) {
+                        ok = false;
+                        break;
+                    }
+                    er.next();
+                } else {
+                    ++filled;
+                }
+                if (elect_one()) {
+                    uint8_t *sc = scales + sr.slot * Cfg::kScaleStage;
+                    mbar_arrive_expect_tx(&sf_raw[sr.slot], Cfg::kScaleTx);
+                    tma_load_2d(sc, &mapSP, &sf_raw[sr.slot], b * 16 * Cfg::kH, py);
 #pragma unroll
-                for (int h = 0; h < Cfg::kU; ++h) {
-                    const int u = k * Cfg::kU + h;
-                    if (u >= prm.units) break;
-                    if (!fp4_warp_wait(&s_empty[sr.slot], sr.phase ^ 1u, wd)) {
+                    for (int j = 0; j < Cfg::kQGroups; ++j)
+                        tma_load_2d(sc + Cfg::kGroupBytes * (1 + j), &mapSQ, &sf_raw[sr.slot], b * 16 * Cfg::kH,
+                                    x.q0 + 128 * j);
+                }
+                __syncwarp();
+                s_issued |= 1u << sr.slot;
+                s_last = (s_last & ~(1u << sr.slot)) | (sr.phase << sr.slot);
+                sr.next();
+#pragma unroll 1
+                for (int k = 2 * b; k < 2 * b + 2; ++k) {
+                    if (!fp4_warp_wait(&empty[cr.slot], cr.phase ^ 1u, wd)) {
                         ok = false;
                         break;
                     }
                     if (elect_one()) {
-                        uint8_t *sc = scales + sr.slot * Cfg::kScaleStage;
-                        mbar_arrive_expect_tx(&s_full[sr.slot], Cfg::kScaleStage);
-                        tma_load_2d(sc, &mapSP, &s_full[sr.slot], u * 16, py);
-                        tma_load_2d(sc + 128 * 16, &mapSQ, &s_full[sr.slot], u * 16, x.q0);
+                        uint8_t *st = codes + cr.slot * Cfg::kStage;
+                        if constexpr (PAIR) {
+                            // both CTAs' bytes count on the even CTA's barrier
+                            if (leader) mbar_arrive_expect_tx(&full[cr.slot], 2 * Cfg::kStage);
+                            const uint32_t bar = cluster_map(smem_u32(&full[cr.slot]), 0u);
+                            tma_load_2d_pair(st, &mapP, bar, k * 128, py);
+                            tma_load_2d_pair(st + Cfg::kBoxP, &mapQ, bar, k * 128, qy);
+                        } else {
+                            mbar_arrive_expect_tx(&full[cr.slot], Cfg::kStage);
+                            tma_load_2d(st, &mapP, &full[cr.slot], k * 128, py);
+                            tma_load_2d(st + Cfg::kBoxP, &mapQ, &full[cr.slot], k * 128, qy);
+                        }
                     }
                     __syncwarp();
-                    s_issued |= 1u << sr.slot;
-                    s_last = (s_last & ~(1u << sr.slot)) | (sr.phase << sr.slot);
-                    sr.next();
+                    issued |= 1u << cr.slot;
+                    last = (last & ~(1u << cr.slot)) | (cr.phase << cr.slot);
+                    cr.next();
                 }
-                if (!ok || !fp4_warp_wait(&empty[cr.slot], cr.phase ^ 1u, wd)) {
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
-                    uint8_t *st = codes + cr.slot * Cfg::kStage;
-                    if constexpr (PAIR) {
-                        // both CTAs' bytes count on the even CTA's barrier
-                        if (leader) mbar_arrive_expect_tx(&full[cr.slot], 2 * Cfg::kStage);
-                        const uint32_t bar = cluster_map(smem_u32(&full[cr.slot]), 0u);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            tma_load_2d_pair(st + h * Cfg::kBoxP, &mapP, bar, (2 * k + h) * 128, py);
-                            tma_load_2d_pair(st + 2 * Cfg::kBoxP + h * Cfg::kBoxQ, &mapQ, bar, (2 * k + h) * 128, qy);
-                        }
-                    } else {
-                        mbar_arrive_expect_tx(&full[cr.slot], Cfg::kStage);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            tma_load_2d(st + h * Cfg::kBoxP, &mapP, &full[cr.slot], (2 * k + h) * 128, py);
-                            tma_load_2d(st + 2 * Cfg::kBoxP + h * Cfg::kBoxQ, &mapQ, &full[cr.slot],
-                                        (2 * k + h) * 128, qy);
-                        }
-                    }
-                }
-                __syncwarp();
-                issued |= 1u << cr.slot;
-                last = (last & ~(1u << cr.slot)) | (cr.phase << cr.slot);
-                cr.next();
             }
         }
         // never leave with copies in flight, nor with an MMA commit on its way here
@@ -378,13 +511,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             }
 #pragma unroll 1
         for (int s = 0; s < prm.scale_stages; ++s)
-            if ((s_issued >> s) & 1u) fp4_wait_drain(&s_full[s], (s_last >> s) & 1u, prm.limit_ns);
-    } else if (warp == 9) {
+            if ((s_issued >> s) & 1u) fp4_wait_drain(&sf_raw[s], (s_last >> s) & 1u, prm.limit_ns);
+    } else if (warp == Cfg::kWarpMma) {
         // ------------------------------------------------------------ MMA issuer
         if (leader) {
-            Fp4Ring cr(prm.code_stages), fr(Cfg::kSfSlots);
+            Fp4Ring cr(prm.code_stages), fr(prm.scale_stages);
             const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(codes));
-            uint32_t nacc = 0;
+            const uint64_t sdesc0 = sdesc_rows16(smem_u32(scales));
+            uint32_t nacc = 0, g = 0;
             bool ok = true;
             for (int t = cid; ok && t < tiles; t += ncl, ++nacc) {
                 const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
@@ -398,55 +532,59 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 } else {
                     if (!fp4_warp_wait(&acc_empty[ab], ((nacc >> 1) & 1u) ^ 1u, wd)) break;
                 }
-                for (int k = k0; k < k1; ++k) {
-                    if (!fp4_warp_wait(&full[cr.slot], cr.phase, wd)) {
+                for (int b = b0; b < b1; ++b, ++g) {
+                    const Fp4Ring c0 = cr;
+                    cr.next();
+                    if (!fp4_warp_wait3(&full[c0.slot], c0.phase, &full[cr.slot], cr.phase, &sf_full[fr.slot], fr.phase,
+                                        wd)) {
                         ok = false;
                         break;
                     }
-                    const uint64_t a0 = desc0 + static_cast<uint64_t>((cr.slot * Cfg::kStage) >> 4);
-                    const uint64_t b0 = a0 + static_cast<uint64_t>((2 * Cfg::kBoxP) >> 4);
-                    const int steps = prm.k_steps - 8 * k;
+                    tc_fence_after();
+                    const uint64_t s0 = sdesc0 + static_cast<uint64_t>(fr.slot * (Cfg::kScaleStage >> 4));
+                    const int steps = prm.k_steps - 8 * b;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < Cfg::kU; ++h) {
-                        if (k * Cfg::kU + h >= prm.units) break;
-                        if (!fp4_warp_wait(&sf_ready[fr.slot], fr.phase, wd)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t sfp = tmem + Cfg::kSf0 + fr.slot * Cfg::kSfCols;
-                        const uint32_t sfq = sfp + 16;
-                        if (elect_one()) {
+                        for (int h = 0; h < 2; ++h) {
+                            const int slot = h ? cr.slot : c0.slot;
+                            const uint64_t p0 = desc0 + static_cast<uint64_t>(slot * (Cfg::kStage >> 4));
+                            const uint64_t q0 = p0 + static_cast<uint64_t>(Cfg::kBoxP >> 4);
+                            // scale columns: mx the block's, alternating by block; nv the stage's
+                            const uint32_t sf = tmem + Cfg::kSf0 + (NV ? h : static_cast<int>(g & 1u)) * Cfg::kSfCols;
+                            if (NV || h == 0) {
 #pragma unroll
-                            for (int q = 0; q < 8 / Cfg::kU; ++q) {  // MMA q of the unit
-                                const int step = h * (8 / Cfg::kU) + q;
-                                if (step < steps) {
-                                    const int word = NV ? q : q / 2;  // a word holds 64 (nv) or 128 (mx) k
-                                    const uint32_t id = NV ? 0u : 2u * (q & 1);
-                                    const int box = step / 4, in = step % 4;
-                                    mma_fp4<NV, PAIR>(d_tmem, a0 + static_cast<uint64_t>((box * Cfg::kBoxP >> 4) + 2 * in),
-                                                      b0 + static_cast<uint64_t>((box * Cfg::kBoxQ >> 4) + 2 * in),
-                                                      idesc | (id << 4) | (id << 29), sfp + 4 * word,
-                                                      sfq + Cfg::kQCols * word, k > k0 || step > 0 ? 1u : 0u);
+                                for (int w = 0; w < 4; ++w) {
+                                    const uint64_t from = s0 + static_cast<uint64_t>((h * 2048 + w * 512) >> 4);
+                                    tmem_cp_32x128b_x4<PAIR>(sf + 4 * w, from);
+#pragma unroll
+                                    for (int j = 0; j < Cfg::kQGroups; ++j)
+                                        tmem_cp_32x128b_x4<PAIR>(
+                                            sf + 16 + Cfg::kQCols * w + 4 * j,
+                                            from + static_cast<uint64_t>(((1 + j) * Cfg::kGroupBytes) >> 4));
                                 }
                             }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if (4 * h + q < steps) {
+                                    // a word holds 64 k (nv) or 128 k (mx)
+                                    const int word = NV ? q : 2 * h + q / 2;
+                                    const uint32_t id = NV ? 0u : 2u * (q & 1);
+                                    mma_fp4<NV, PAIR>(d_tmem, p0 + static_cast<uint64_t>(2 * q),
+                                                      q0 + static_cast<uint64_t>(2 * q), idesc | (id << 4) | (id << 29),
+                                                      sf + 4 * word, sf + 16 + Cfg::kQCols * word,
+                                                      b > b0 || h > 0 || q > 0 ? 1u : 0u);
+                                }
+                            }
+                            // frees the stage's codes, and with the block's last stage its scales
                             if constexpr (PAIR)
-                                mma_commit_pair_multicast(&sf_free[fr.slot], 0x3);
+                                mma_commit_pair_multicast(&empty[slot], 0x3);
                             else
-                                mma_commit(&sf_free[fr.slot]);
+                                mma_commit(&empty[slot]);
                         }
-                        __syncwarp();
-                        fr.next();
-                    }
-                    if (!ok) break;
-                    if (elect_one()) {
-                        if constexpr (PAIR)
-                            mma_commit_pair_multicast(&empty[cr.slot], 0x3);
-                        else
-                            mma_commit(&empty[cr.slot]);
                     }
                     __syncwarp();
                     cr.next();
+                    fr.next();
                 }
                 if (ok && elect_one()) {
                     if constexpr (PAIR)
@@ -462,76 +600,61 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 else
                     mma_commit(mma_drain);
             }
+        } else {
+            // relay of the odd CTA: its scales of each block, in order, to the even CTA's
+            // MMA warp (an arrival from the warps that wrote them took about 1100
+            // cycles, their release to the other CTA; this warp wrote nothing)
+            const uint32_t peer = cluster_map(smem_u32(sf_full), 0u);
+            Fp4Ring fr(prm.scale_stages);
+            bool ok = true;
+            for (int t = cid; ok && t < tiles; t += ncl) {
+                for (int b = b0; b < b1; ++b) {
+                    ok = fp4_warp_wait(&sf_full[fr.slot], fr.phase, wd);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_peer(peer + 8u * static_cast<uint32_t>(fr.slot));
+                    fr.next();
+                }
+            }
         }
-    } else if (warp >= 4) {
-        // ------------------------------------------------------------ scales into TMEM
-        const uint32_t quad = static_cast<uint32_t>(warp & 3);
-        const uint32_t tq = tmem + ((quad * 32u) << 16) + Cfg::kSf0;
-        const uint32_t ready_leader = PAIR ? cluster_map(smem_u32(sf_ready), 0u) : 0u;
-        Fp4Ring sr(prm.scale_stages), fr(Cfg::kSfSlots);
+    } else if (warp >= Cfg::kWarpScale) {
+        // ------------------------------------------------------------ scales
+        // group 0: the tile's 128 weight rows; 1, 2: 128 activation rows each
+        constexpr int H = Cfg::kH;
+        const int group = warp - Cfg::kWarpScale;
+        const int rows = group == 0 ? 128 : Cfg::kQScaleRows;  // of the box
+        Fp4Ring fr(prm.scale_stages);
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
-            const int u1 = min(k1 * Cfg::kU, prm.units);
-            for (int u = k0 * Cfg::kU; u < u1; ++u) {
-                if (!fp4_warp_wait(&s_full[sr.slot], sr.phase, wd)) {
-                    ok = false;
-                    break;
-                }
-                const uint4 *sp = reinterpret_cast<const uint4 *>(scales + sr.slot * Cfg::kScaleStage);
-                const uint4 *sq = sp + 128;
-                uint32_t p[16], q[4 * Cfg::kQCols];
+            for (int b = b0; b < b1; ++b) {
+                ok = fp4_warp_wait(&sf_raw[fr.slot], fr.phase, wd);
+                if (!ok) break;
+                uint4 *at = reinterpret_cast<uint4 *>(scales + fr.slot * Cfg::kScaleStage + group * Cfg::kGroupBytes);
+                uint4 d[H][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 v = sp[32 * j + lane];
-                    p[j] = v.x;
-                    p[4 + j] = v.y;
-                    p[8 + j] = v.z;
-                    p[12 + j] = v.w;
-                }
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int j = 0; j < Cfg::kQCols; ++j) {
-                    const uint4 v = 32 * j < BN ? sq[(32 * j + lane) & (BN - 1)] : make_uint4(0, 0, 0, 0);
-                    q[j] = v.x;
-                    q[Cfg::kQCols + j] = v.y;
-                    q[2 * Cfg::kQCols + j] = v.z;
-                    q[3 * Cfg::kQCols + j] = v.w;
-                }
-                fence_proxy_async_smem();  // generic reads before the TMA refills the stage
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[sr.slot]);
-                sr.next();
-                // padding bytes past the last block count as zero scales
-                const int left = prm.k_blocks - 16 * u;
-                if (left < 16) {
+                    for (int h = 0; h < H; ++h)
+                        d[h][j] = 32 * j + lane < rows ? at[(32 * j + lane) * H + h] : make_uint4(0, 0, 0, 0);
+                __syncwarp();  // the warp's rows are read
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
+                for (int h = 0; h < H; ++h) {
+                    // padding bytes past the last block of values count as zero scales
+                    const int left = prm.k_blocks - 16 * (b * H + h);
+                    if (left < 16) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) p[4 * w + j] = fp4_keep(p[4 * w + j], left - 4 * w);
-#pragma unroll
-                        for (int j = 0; j < Cfg::kQCols; ++j)
-                            q[Cfg::kQCols * w + j] = fp4_keep(q[Cfg::kQCols * w + j], left - 4 * w);
+                        for (int j = 0; j < 4; ++j)
+                            d[h][j] = make_uint4(fp4_keep(d[h][j].x, left), fp4_keep(d[h][j].y, left - 4),
+                                                 fp4_keep(d[h][j].z, left - 8), fp4_keep(d[h][j].w, left - 12));
                     }
+                    uint4 *to = at + 128 * h + lane;
+                    to[0] = make_uint4(d[h][0].x, d[h][1].x, d[h][2].x, d[h][3].x);
+                    to[32] = make_uint4(d[h][0].y, d[h][1].y, d[h][2].y, d[h][3].y);
+                    to[64] = make_uint4(d[h][0].z, d[h][1].z, d[h][2].z, d[h][3].z);
+                    to[96] = make_uint4(d[h][0].w, d[h][1].w, d[h][2].w, d[h][3].w);
                 }
-                if (!fp4_warp_wait(&sf_free[fr.slot], fr.phase ^ 1u, wd)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t at = tq + fr.slot * Cfg::kSfCols;
-                tmem_st_32x32b_x16(at, p);
-                if constexpr (Cfg::kQCols == 4)
-                    tmem_st_32x32b_x16(at + 16, q);
-                else
-                    tmem_st_32x32b_x32(at + 16, q);
-                tmem_st_wait();
-                tc_fence_before();
+                fence_proxy_async_smem();  // read next by tcgen05.cp
                 __syncwarp();
-                if (lane == 0) {
-                    if (leader)
-                        mbar_arrive(&sf_ready[fr.slot]);
-                    else
-                        mbar_arrive_peer(ready_leader + 8u * static_cast<uint32_t>(fr.slot));
-                }
+                if (lane == 0) mbar_arrive(&sf_full[fr.slot]);
                 fr.next();
             }
         }
@@ -539,6 +662,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int quad = warp;
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        uint8_t *stage = smem + prm.off_store + quad * 1024;
         const uint32_t empty_leader = PAIR ? cluster_map(smem_u32(acc_empty), 0u) : 0u;
         uint32_t nacc = 0;
         for (int t = cid; t < tiles; t += ncl, ++nacc) {
@@ -587,60 +711,31 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 for (int c = 0; c < c1; ++c) {
                     float s = 0.0f;
                     for (int r = 0; r < cs; ++r) s += buf[(r * per + c) * 128 + quad * 32 + lane];
-                    uint32_t v[1] = {__float_as_uint(s)};
-                    fp4_store<1>(prm, v, alpha, static_cast<int64_t>(x.q0) + rank * per + c, 1, n);
+                    fp4_store1(prm, s * alpha, static_cast<int64_t>(x.q0) + rank * per + c, n);
                 }
                 __syncwarp();
                 if (lane < cs)
                     mbar_arrive_remote(cluster_map(smem_u32(&red_empty[rb]), static_cast<uint32_t>(lane)));
                 continue;
             }
-            if constexpr (Cfg::kOverlap > 0) {
-                // the columns that the other accumulator shares first, 96 at a time: once
-                // they are in registers the next tile may start
-                const int shared0 = ab ? 0 : BN - Cfg::kOverlap;
-                uint32_t v[3][32];
-#pragma unroll 1
-                for (int c = shared0; c < shared0 + Cfg::kOverlap; c += 96) {
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) tmem_ld_32x32b_x32(tacc + c + 32 * i, v[i]);
-                    tmem_ld_wait_regs(v[0], v[1]);
-                    tmem_ld_wait_regs(v[2]);
-                    if (c + 96 == shared0 + Cfg::kOverlap) release();
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        fp4_store<32>(prm, v[i], alpha, static_cast<int64_t>(x.q0) + c + 32 * i, x.nq - c - 32 * i, n);
-                }
-                const int c_end = min(x.nq, ab ? BN : BN - Cfg::kOverlap);
-#pragma unroll 1
-                for (int c = ab ? Cfg::kOverlap : 0; c < c_end; c += 32) {
-                    tmem_ld_32x32b_x32(tacc + c, v[0]);
-                    tmem_ld_wait_regs(v[0]);
-                    fp4_store<32>(prm, v[0], alpha, static_cast<int64_t>(x.q0) + c, c_end - c, n);
-                }
-            } else {
-#pragma unroll 1
-                for (int c = 0; c < x.nq; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(tacc + c, v);
-                    tmem_ld_wait_regs(v);
-                    fp4_store<16>(prm, v, alpha, static_cast<int64_t>(x.q0) + c, x.nq - c, n);
-                }
-                release();
-            }
+            const int n0 = x.p0 + quad * 32;
+            if (prm.c_type == kOutF32)
+                fp4_store_tile<Cfg, true>(prm, x, tacc, ab, alpha, n0, stage, release);
+            else
+                fp4_store_tile<Cfg, false>(prm, x, tacc, ab, alpha, n0, stage, release);
         }
     }
 
     // ---------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == Cfg::kWarpMma) {
         if (leader && lane == 0) fp4_wait_drain(mma_drain, 0, prm.limit_ns);
         __syncwarp();
     }
     // no CTA of a cluster frees TMEM or leaves while another may still reach it
     if (csize > 1) cluster_sync_all();
-    if (warp == 9) {
+    if (warp == Cfg::kWarpMma) {
         tc_fence_after();
         if constexpr (PAIR)
             tmem_dealloc_pair(tmem, Cfg::kTmemCols);

@@ -6,7 +6,7 @@ namespace igemm {
 
 int fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *plan)
 {
-    const int stages = (c.K + 511) / 512;
+    const int blocks = (c.K + 511) / 512;
     // activation rows of a typical group, and the groups that have any
     double groups = 1.0;
     if (c.offsets) groups = c.experts * (1.0 - std::pow(1.0 - 1.0 / c.experts, double(c.rows)));
@@ -31,8 +31,8 @@ int fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *pla
     const double tiles = double(p_tiles) * std::ceil(typical / plan->bn) * groups;
     double best = -1;
     for (int cs = 1; cs <= (plan->bn == 128 ? 2 : 8); cs *= 2) {
-        const int per = (stages + cs - 1) / cs;
-        if (cs > 1 && per * (cs - 1) >= stages) break;
+        const int per = (blocks + cs - 1) / cs;
+        if (cs > 1 && per * (cs - 1) >= blocks) break;
         const int clusters = max_clusters(plan->bn, false, cs);
         if (clusters < 1) return kCudaError;
         // the busiest cluster's stages, plus a tile's fill and epilogue

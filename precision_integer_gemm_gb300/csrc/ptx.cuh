@@ -424,6 +424,26 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "r"(taddr));
 }
 
+// 16 lanes x 16 consecutive 32-bit columns in fragment order: thread T gets lane
+// T / 4 (r[4 j], r[4 j + 1]) and lane T / 4 + 8 (r[4 j + 2], r[4 j + 3]), columns 8 j +
+// 2 (T % 4) and the next, for j = 0, 1.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+// Four 8 x 8 matrices of 16-bit elements, each thread holding a pair of
+// neighbouring columns of one row, stored transposed: thread T's address is where
+// row T % 8 of the transpose of matrix T / 8 goes (16 bytes).
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t smem_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 // tcgen05.ld fills its destination registers asynchronously; the compiler sees
 // them written by the load instruction itself.  These waits also mark the
 // registers as rewritten after the wait (an empty asm per register, ordered
@@ -601,15 +621,28 @@ __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_
 #undef IGEMM_MMA_FP4
 }
 
-// 32 lanes x 16 consecutive 32-bit columns from registers into TMEM.
-__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
+// 512 bytes of shared memory (32 rows of 16 bytes) into 4 TMEM columns: row i to
+// lane i of all four lane quadrants.  Runs in order with the MMAs that the same
+// thread issues.  PAIR: in each CTA of the pair, from its own shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_cp_32x128b_x4(uint32_t taddr, uint64_t sdesc)
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Shared-memory descriptor of contiguous rows of 16 bytes, no swizzle: groups of 8
+// rows 128 bytes apart (fields as in sdesc_kmajor_sw128).
+__device__ __forceinline__ uint64_t sdesc_rows16(uint32_t smem_addr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(128 >> 4) << 16;
+    d |= static_cast<uint64_t>(128 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    return d;
 }
 
 // Instruction descriptor, kind::f8f6f4, dense: D f32 (bits 4-5 = 1), A and B
