@@ -54,7 +54,7 @@ struct Fp4Params {
     int qt;                // activation rows per tile (<= BN)
     int p_tiles;           // tiles of 128 weight rows (pair: of 256)
     int group_p;           // tiles run in groups of group_p weight tiles (fastest) by every activation tile
-    int cs;                // CTAs of a cluster that split k (1: none)
+    int cs;                // CTAs of a cluster that split k (1: none; a power of two, 4 cs <= BN)
     int blocks_per_slice;
     int code_stages, scale_stages;  // ring slots: 256 k of codes, 512 k of scales (2 scale_stages <= code_stages + 1)
     int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
@@ -93,7 +93,7 @@ struct Fp4Cfg {
     static constexpr int kRedBufs = BN <= 32 ? 2 : 1;
     static constexpr int kRedBytes = kRedBufs * BN * 512;  // split k: partial tiles of the cluster's CTAs
     static constexpr int kMaxStages = 16;
-    static constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxScaleStages + 4 + 1 + 4;
+    static constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxScaleStages + 4 + 1 + 16;
     static constexpr int kStoreBytes = 4 * 1024;  // 16-bit C: 16 rows x 32 columns per epilogue warp
     static constexpr int kTailBytes = 8 * kNumBars + 64;  // and the groups' tile counts
     static constexpr int kNAlign = PAIR ? 32 : 16;
@@ -351,8 +351,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint64_t *acc_full = sf_full + Cfg::kMaxScaleStages;  // [2] accumulator complete (commit)
     uint64_t *acc_empty = acc_full + 2;             // [2] accumulator (its overlap) read by the epilogue warps
     uint64_t *mma_drain = acc_empty + 2;
-    uint64_t *red_full = mma_drain + 1;             // [2] split k: every CTA's partials of this CTA's columns written
-    uint64_t *red_empty = red_full + 2;             // [2] ... and every CTA's reads of what this CTA wrote done
+    uint64_t *red_full = mma_drain + 1;             // [2][4] split k: the other CTAs' partials of this warp's part landed
+    uint64_t *red_empty = red_full + 8;             // [2][4] ... and the other CTAs have read what this warp sent
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *total_slot = reinterpret_cast<int *>(tmem_slot + 2);
@@ -367,28 +367,32 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int cid = blockIdx.x / csize, ncl = gridDim.x / csize;
     const bool leader = !PAIR || rank == 0;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < prm.code_stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+    if (warp == Cfg::kWarpProd) {
+        if (lane < prm.code_stages) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 1);
         }
-        for (int s = 0; s < prm.scale_stages; ++s) {
-            mbar_init(&sf_raw[s], 1);
-            mbar_init(&sf_full[s], 1 + Cfg::kQGroups + (PAIR && leader ? 1 : 0));
+        if (lane < prm.scale_stages) {
+            mbar_init(&sf_raw[lane], 1);
+            mbar_init(&sf_full[lane], 1 + Cfg::kQGroups + (PAIR && leader ? 1 : 0));
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4 * Cfg::CL);
-            mbar_init(&red_full[b], 4 * cs);
-            mbar_init(&red_empty[b], 4 * cs);
+        if (lane < 2) {
+            mbar_init(&acc_full[lane], 1);
+            mbar_init(&acc_empty[lane], 4 * Cfg::CL);
         }
-        mbar_init(mma_drain, 1);
-        *abort_flag = 0;
+        if (cs > 1 && lane < 8) {
+            mbar_init(&red_full[lane], 1);
+            mbar_init(&red_empty[lane], cs - 1);
+        }
+        if (lane == 0) {
+            mbar_init(mma_drain, 1);
+            *abort_flag = 0;
+            tma_prefetch_map(&mapP);
+            tma_prefetch_map(&mapQ);
+            tma_prefetch_map(&mapSP);
+            tma_prefetch_map(&mapSQ);
+        }
         fence_mbar_init();
-        tma_prefetch_map(&mapP);
-        tma_prefetch_map(&mapQ);
-        tma_prefetch_map(&mapSP);
-        tma_prefetch_map(&mapSQ);
     }
     if (warp == Cfg::kWarpMma) {
         if constexpr (PAIR) {
@@ -684,38 +688,49 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             if (!fp4_warp_wait(&acc_full[ab], (nacc >> 1) & 1u, wd)) break;
             tc_fence_after();
             if (cs > 1) {
-                // split k: every CTA writes its partial of column group c / per to
-                // CTA c / per, which adds them in rank order
-                const int per = BN / cs, per_log2 = __ffs(per) - 1;  // cs is a power of two
-                const uint32_t rb = nacc % Cfg::kRedBufs, rph = (nacc / Cfg::kRedBufs) & 1u;
-                float *buf = red + rb * (BN * 128);
-                if (!fp4_warp_wait_cluster(&red_empty[rb], rph ^ 1u, wd)) break;
+                // split k: every CTA sends its partial of columns r BN / cs .. to CTA r of the
+                // cluster, which adds them in rank order (fixed, whatever arrives
+                // first): four columns of 128 lanes are 2 KB at [rank][column / 4]
+                const int per_log2 = __ffs(BN / cs) - 1, per = 1 << per_log2;
+                const uint32_t rb = nacc % Cfg::kRedBufs, rph = (nacc / Cfg::kRedBufs) & 1u, bar = rb * 4 + quad;
+                uint4 *buf = reinterpret_cast<uint4 *>(red) + rb * (BN * 32) + quad * 32 + lane;
+                if (lane == 0) mbar_arrive_expect_tx(&red_full[bar], static_cast<uint32_t>((cs - 1) * per * 128));
+                if (!fp4_warp_wait_cluster(&red_empty[bar], rph ^ 1u, wd)) break;
 #pragma unroll 1
-                for (int c0 = 0; c0 < x.nq; c0 += 16) {
+                for (int c0 = 0; c0 < BN; c0 += 16) {
                     uint32_t v[16];
                     tmem_ld_32x32b_x16(tacc + c0, v);
                     tmem_ld_wait_regs(v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < 16; j += 4) {
                         const int c = c0 + j, owner = c >> per_log2;
-                        st_cluster_u32(cluster_map(smem_u32(buf + (rank * per + (c & (per - 1))) * 128 + quad * 32 + lane),
-                                                   static_cast<uint32_t>(owner)),
-                                       v[j]);
+                        uint4 *to = buf + ((rank << per_log2) + (c & (per - 1))) / 4 * 128;
+                        if (owner == rank)
+                            *to = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        else
+                            st_async_v4(cluster_map(smem_u32(to), static_cast<uint32_t>(owner)), v + j,
+                                        cluster_map(smem_u32(&red_full[bar]), static_cast<uint32_t>(owner)));
                     }
                 }
                 release();
-                if (lane < cs)
-                    mbar_arrive_remote(cluster_map(smem_u32(&red_full[rb]), static_cast<uint32_t>(lane)));
-                if (!fp4_warp_wait_cluster(&red_full[rb], rph, wd)) break;
+                if (!fp4_warp_wait_cluster(&red_full[bar], rph, wd)) break;
                 const int c1 = min(per, x.nq - rank * per);
-                for (int c = 0; c < c1; ++c) {
-                    float s = 0.0f;
-                    for (int r = 0; r < cs; ++r) s += buf[(r * per + c) * 128 + quad * 32 + lane];
-                    fp4_store1(prm, s * alpha, static_cast<int64_t>(x.q0) + rank * per + c, n);
+                for (int c = 0; c < c1; c += 4) {
+                    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int r = 0; r < cs; ++r) {
+                        const uint4 v = buf[((r << per_log2) + c) / 4 * 128];
+                        s[0] += __uint_as_float(v.x);
+                        s[1] += __uint_as_float(v.y);
+                        s[2] += __uint_as_float(v.z);
+                        s[3] += __uint_as_float(v.w);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (c + j < c1) fp4_store1(prm, s[j] * alpha, static_cast<int64_t>(x.q0) + rank * per + c + j, n);
                 }
                 __syncwarp();
-                if (lane < cs)
-                    mbar_arrive_remote(cluster_map(smem_u32(&red_empty[rb]), static_cast<uint32_t>(lane)));
+                if (lane < cs && lane != rank)
+                    mbar_arrive_peer(cluster_map(smem_u32(&red_empty[bar]), static_cast<uint32_t>(lane)));
                 continue;
             }
             const int n0 = x.p0 + quad * 32;

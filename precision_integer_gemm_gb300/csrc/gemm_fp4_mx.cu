@@ -30,7 +30,7 @@ int fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *pla
     if (plan->pair) return kOk;
     const double tiles = double(p_tiles) * std::ceil(typical / plan->bn) * groups;
     double best = -1;
-    for (int cs = 1; cs <= (plan->bn == 128 ? 2 : 8); cs *= 2) {
+    for (int cs = 1; cs <= (plan->bn == 128 ? 2 : plan->bn == 16 ? 4 : 8); cs *= 2) {
         const int per = (blocks + cs - 1) / cs;
         if (cs > 1 && per * (cs - 1) >= blocks) break;
         const int clusters = max_clusters(plan->bn, false, cs);
