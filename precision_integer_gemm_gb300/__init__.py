@@ -152,10 +152,18 @@ def _n(*dims: int) -> int:
     return out
 
 
+_raw_stream = None  # device index -> handle of torch's current stream there
+
+
 def _stream(stream) -> int | None:
+    global _raw_stream
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            # (the handle alone: building a Stream object takes 2 us of a small call)
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda i: torch.cuda.current_stream(i).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -295,6 +303,8 @@ def unpack_int4(packed, logical, rows: int, K: int, stream=None) -> None:
 
 # ---------------------------------------------------------------- 4-bit floating point, mixture of experts
 _TYPES = {"torch.float32": (0, 4), "torch.bfloat16": (1, 2), "torch.float16": (2, 2)}
+_type_of = {}  # torch dtype -> (igemm_type, bytes), filled as dtypes are met
+_names = {}    # torch dtype -> its name
 
 
 def fp4_code_bytes(K: int) -> int:
@@ -314,26 +324,42 @@ def nvfp4_scale_pitch(K: int) -> int:
 
 def _type(x, what: str) -> tuple[int, int]:
     """(igemm_type, bytes per element) of a tensor."""
-    t = _TYPES.get(str(x.dtype))
+    t = _type_of.get(x.dtype)
     if t is None:
-        raise ValueError(f"{what} must be float32, bfloat16 or float16, not {x.dtype}")
+        t = _TYPES.get(str(x.dtype))
+        if t is None:
+            raise ValueError(f"{what}: a tensor of float32, bfloat16 or float16 is wanted, not of {x.dtype}")
+        _type_of[x.dtype] = t
     return t
 
 
-def _typed(x, dtype: str, count: int, what: str):
-    """_arg for a device array of `count` 4-byte elements of torch type `dtype`."""
-    if x is not None and not isinstance(x, int) and str(x.dtype) != dtype:
-        raise ValueError(f"{what} must be {dtype}, not {x.dtype}")
-    return _arg(x, 4 * count, True, what)
+def _dev(x, nbytes: int, where: str, name: str):
+    """_arg for device memory, its message made only when it is needed."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.is_cuda and x.is_contiguous() and x.nbytes >= nbytes:
+        return x.data_ptr()
+    return _arg(x, nbytes, True, f"{where}: {name}")
+
+
+def _typed(x, dtype: str, count: int, where: str, name: str):
+    """_dev for `count` 4-byte elements of torch type `dtype`."""
+    if x is None or isinstance(x, int):
+        return x
+    if _names.get(x.dtype) != dtype:
+        _names[x.dtype] = str(x.dtype)
+        if _names[x.dtype] != dtype:
+            raise ValueError(f"{where}: {name} must be {dtype}, not {x.dtype}")
+    return _dev(x, 4 * count, where, name)
 
 
 def _pack_fp4(fn, where, x, extra, codes, scales, rows, K, index, pitch, stream):
-    t, _ = _type(x, f"{where}: x")
-    if x.dim() != 2 or not x.is_cuda:
+    t, _ = _type(x, where)
+    if not x.is_cuda or x.dim() != 2:
         raise ValueError(f"{where}: x must be a CUDA matrix")
-    if x.shape[1] != K or (index is None and x.shape[0] != rows):
-        raise ValueError(f"{where}: x is {tuple(x.shape)}; the call packs {rows} rows of {K}")
     (r, c), (sr, sc) = x.shape, x.stride()
+    if c != K or (index is None and r != rows):
+        raise ValueError(f"{where}: x is {tuple(x.shape)}; the call packs {rows} rows of {K}")
     # a dimension of one element has no stride of its own
     if c == 1 or sc == 1:
         transposed, ld = 0, (sr if r > 1 else max(sr, c))
@@ -345,9 +371,9 @@ def _pack_fp4(fn, where, x, extra, codes, scales, rows, K, index, pitch, stream)
         raise ValueError(f"{where}: x has overlapping rows")
     if transposed and index is not None:
         raise ValueError(f"{where}: rows of a transposed x cannot be gathered")
-    _check(fn(x.data_ptr(), t, ld, transposed, _typed(index, "torch.int32", _n(rows), f"{where}: index"), r, *extra,
-              _arg(codes, _n(rows) * fp4_code_bytes(K), True, f"{where}: codes"),
-              _arg(scales, _n(rows) * pitch, True, f"{where}: scales"), rows, K, _stream(stream)), where)
+    _check(fn(x.data_ptr(), t, ld, transposed, _typed(index, "torch.int32", _n(rows), where, "index"), r, *extra,
+              _dev(codes, _n(rows) * fp4_code_bytes(K), where, "codes"),
+              _dev(scales, _n(rows) * pitch, where, "scales"), rows, K, _stream(stream)), where)
 
 
 def pack_mxfp4(x, codes, scales, rows: int, K: int, index=None, stream=None) -> None:
@@ -360,16 +386,16 @@ def pack_mxfp4(x, codes, scales, rows: int, K: int, index=None, stream=None) -> 
 def pack_nvfp4(x, tensor_scale, codes, scales, rows: int, K: int, index=None, stream=None) -> None:
     """pack_mxfp4 with one e4m3 scale per 16 k, relative to tensor_scale (float32 [1] on the device, None: 1);
     scales [rows, nvfp4_scale_pitch(K)]."""
-    _pack_fp4(load().pack_nvfp4, "pack_nvfp4", x, (_typed(tensor_scale, "torch.float32", 1, "pack_nvfp4: tensor_scale"),),
+    _pack_fp4(load().pack_nvfp4, "pack_nvfp4", x, (_typed(tensor_scale, "torch.float32", 1, "pack_nvfp4", "tensor_scale"),),
               codes, scales, rows, K, index, nvfp4_scale_pitch(K), stream)
 
 
 def _fp4_args(A, B, SFA, SFB, C, M, E, N, K, pitch, where):
     kb = fp4_code_bytes(K)
-    t, size = _type(C, f"{where}: C")
-    return ((_arg(A, _n(M, kb), True, f"{where}: A"), _arg(B, _n(E, N, kb), True, f"{where}: B"),
-             _arg(SFA, _n(M, pitch), True, f"{where}: SFA"), _arg(SFB, _n(E, N, pitch), True, f"{where}: SFB")),
-            (_arg(C, size * _n(M, N), True, f"{where}: C"), t))
+    t, size = _type(C, where)
+    return ((_dev(A, _n(M, kb), where, "A"), _dev(B, _n(E, N, kb), where, "B"),
+             _dev(SFA, _n(M, pitch), where, "SFA"), _dev(SFB, _n(E, N, pitch), where, "SFB")),
+            (_dev(C, size * _n(M, N), where, "C"), t))
 
 
 def igemm_mxfp4(A, B, SFA, SFB, C, M: int, N: int, K: int, stream=None) -> None:
@@ -384,7 +410,7 @@ def igemm_nvfp4(A, B, SFA, SFB, alpha, C, M: int, N: int, K: int, stream=None) -
     (the product of the operands' tensor scales), None: 1."""
     w = "igemm_nvfp4"
     ops, c = _fp4_args(A, B, SFA, SFB, C, M, 1, N, K, nvfp4_scale_pitch(K), w)
-    _check(load().igemm_nvfp4(*ops, _typed(alpha, "torch.float32", 1, f"{w}: alpha"), *c, M, N, K, _stream(stream)), w)
+    _check(load().igemm_nvfp4(*ops, _typed(alpha, "torch.float32", 1, w, "alpha"), *c, M, N, K, _stream(stream)), w)
 
 
 def igemm_mxfp4_grouped(A, B, SFA, SFB, offsets, C, rows: int, E: int, N: int, K: int, stream=None) -> None:
@@ -392,7 +418,7 @@ def igemm_mxfp4_grouped(A, B, SFA, SFB, offsets, C, rows: int, E: int, N: int, K
     of N rows); offsets: int32 [E+1] on the device.  Rows of no group are left as they were."""
     w = "igemm_mxfp4_grouped"
     ops, c = _fp4_args(A, B, SFA, SFB, C, rows, E, N, K, mxfp4_scale_pitch(K), w)
-    _check(load().igemm_mxfp4_grouped(*ops, _typed(offsets, "torch.int32", _n(E + 1), f"{w}: offsets"), *c, rows, E, N,
+    _check(load().igemm_mxfp4_grouped(*ops, _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"), *c, rows, E, N,
                                       K, _stream(stream)), w)
 
 
@@ -400,8 +426,8 @@ def igemm_nvfp4_grouped(A, B, SFA, SFB, offsets, alpha, C, rows: int, E: int, N:
     """igemm_mxfp4_grouped for nvfp4 matrices; alpha: float32 [E] on the device, None: 1."""
     w = "igemm_nvfp4_grouped"
     ops, c = _fp4_args(A, B, SFA, SFB, C, rows, E, N, K, nvfp4_scale_pitch(K), w)
-    _check(load().igemm_nvfp4_grouped(*ops, _typed(offsets, "torch.int32", _n(E + 1), f"{w}: offsets"),
-                                      _typed(alpha, "torch.float32", _n(E), f"{w}: alpha"), *c, rows, E, N, K,
+    _check(load().igemm_nvfp4_grouped(*ops, _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"),
+                                      _typed(alpha, "torch.float32", _n(E), w, "alpha"), *c, rows, E, N, K,
                                       _stream(stream)), w)
 
 
@@ -411,24 +437,24 @@ def igemm_moe_route(logits, experts, weights, offsets, tokens, slots, T: int, E:
     over the chosen or, normalize False, over all E), and the pairs sorted by expert: offsets [E+1], tokens [T*k]
     (sorted place -> token, -1 past the last), slots [T,k] (pair -> sorted place, -1), int32."""
     w = "igemm_moe_route"
-    t, size = _type(logits, f"{w}: logits")
+    t, size = _type(logits, w)
     _check(load().igemm_moe_route(
-        _arg(logits, size * _n(T, E), True, f"{w}: logits"), t, _typed(experts, "torch.int32", _n(T, k), f"{w}: experts"),
-        _typed(weights, "torch.float32", _n(T, k), f"{w}: weights"),
-        _typed(offsets, "torch.int32", _n(E + 1), f"{w}: offsets"),
-        _typed(tokens, "torch.int32", _n(T, k), f"{w}: tokens"), _typed(slots, "torch.int32", _n(T, k), f"{w}: slots"),
+        _dev(logits, size * _n(T, E), w, "logits"), t, _typed(experts, "torch.int32", _n(T, k), w, "experts"),
+        _typed(weights, "torch.float32", _n(T, k), w, "weights"),
+        _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"),
+        _typed(tokens, "torch.int32", _n(T, k), w, "tokens"), _typed(slots, "torch.int32", _n(T, k), w, "slots"),
         T, E, k, int(bool(normalize)), _stream(stream)), w)
 
 
 def igemm_moe_combine(Y, slots, weights, out, T: int, k: int, N: int, stream=None) -> None:
     """out [T,N] = sum over j of weights[t,j] * Y[slots[t,j]] (Y [T*k,N] and out of one type; slots of -1 add nothing)."""
     w = "igemm_moe_combine"
-    t, size = _type(Y, f"{w}: Y")
+    t, size = _type(Y, w)
     if out.dtype != Y.dtype:
         raise ValueError(f"{w}: out must have Y's type")
     _check(load().igemm_moe_combine(
-        _arg(Y, size * _n(T, k, N), True, f"{w}: Y"), _typed(slots, "torch.int32", _n(T, k), f"{w}: slots"),
-        _typed(weights, "torch.float32", _n(T, k), f"{w}: weights"), _arg(out, size * _n(T, N), True, f"{w}: out"), t, T,
+        _dev(Y, size * _n(T, k, N), w, "Y"), _typed(slots, "torch.int32", _n(T, k), w, "slots"),
+        _typed(weights, "torch.float32", _n(T, k), w, "weights"), _dev(out, size * _n(T, N), w, "out"), t, T,
         k, N, _stream(stream)), w)
 
 

@@ -1,14 +1,17 @@
 // Routing of tokens to experts and the weighted sum of the experts' rows.
 //
 // Routing: a warp per token holds the token's logits in registers (E / 32 per
-// lane) and takes the largest k times (a warp reduction of order-preserving
-// integers, then one of the indices that hold it: the lowest wins).  A token
-// chooses an expert at most once, so the tokens of a block of kTB that chose
-// expert e are one bit mask, and a pair's place among its expert's is the
-// number of bits below its own: the sort is stable and needs no ordered
-// atomics.  One block does the whole job for up to kTB tokens; more tokens take
-// three launches (choice and counts per block, a scan over the blocks per
-// expert, places).
+// lane) as order-preserving integers and takes the largest k times with a warp
+// reduction.  The integers of 16-bit logits leave 13 low bits for the expert
+// (lower experts count as larger), so one reduction finds value and expert, and up
+// to 8 of them are sorted per lane beforehand; float32 logits need a second
+// reduction for the lowest expert that holds the value.  A token chooses an expert
+// at most once, so the tokens of a block of kTB that chose expert e are one bit
+// mask, and a pair's place among its expert's is the number of bits below its
+// own: the sort is stable and needs no ordered atomics.  One block does the whole
+// job for up to kTB tokens; more tokens take three launches (choice and counts
+// per block, a scan over the blocks per expert, places).  Bound by instructions:
+// the choice reads 8 MB at 16384 x 256 bfloat16.
 //
 // Combine: bound by HBM, k rows read and one written per token.
 #include <algorithm>
@@ -22,6 +25,7 @@ namespace igemm {
 constexpr int kTB = 64;           // tokens per block: two mask words
 constexpr int kMaxExperts = 1024;
 constexpr int kRouteThreads = 512;
+constexpr int kChooseThreads = 1024;
 
 __device__ __forceinline__ float moe_float(float v) { return v; }
 __device__ __forceinline__ float moe_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -51,6 +55,16 @@ __device__ __forceinline__ float route_value(uint32_t key)
 }
 constexpr uint32_t kKeyNone = 0x007FFFFFu;  // of -inf
 
+// The 16-bit form: bits 13 and up of the key, then 0x1FFF - expert.
+__device__ __forceinline__ uint32_t route_packed(float v, int e)
+{
+    return (route_key(v) & ~0x1FFFu) | (0x1FFFu - static_cast<uint32_t>(e));
+}
+__device__ __forceinline__ float route_packed_value(uint32_t p)
+{
+    return __uint_as_float((p & 0x80000000u) ? p & 0x7FFFE000u : ~(p | 0x1FFFu));
+}
+
 // Sets in `first[e]` the running sum of `count(e)` over experts below e (warp 0).
 template <class F>
 __device__ __forceinline__ void route_scan(int *first, int E, F count)
@@ -77,7 +91,7 @@ __device__ __forceinline__ void route_place(const RouteParams &p, const uint2 *m
 {
     const int t0 = blockIdx.x * kTB;
     const int n = min(kTB, p.T - t0) * p.k;
-    for (int i = threadIdx.x; i < n; i += kRouteThreads) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int e = experts[i], t = i / p.k;
         int pos = -1;
         if (e >= 0) {
@@ -91,71 +105,114 @@ __device__ __forceinline__ void route_place(const RouteParams &p, const uint2 *m
 }
 
 // Choice and weights of kTB tokens; their masks; one block: everything.
-// VPL: logits per lane (E <= 32 VPL).
-template <class T, int VPL>
-__global__ void __launch_bounds__(kRouteThreads) moe_choose_kernel(const RouteParams p)
+// VPL: logits per lane (E <= 32 VPL); VEC: lane's logits in runs of V (16 bytes at
+// most), loaded together.
+template <class T, int VPL, bool VEC>
+__global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteParams p)
 {
+    constexpr bool kPacked = sizeof(T) == 2;
+    constexpr int V = !VEC ? 1 : VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
+    struct alignas(V * sizeof(T)) Run {
+        T v[V];
+    };
     extern __shared__ uint2 mask[];  // [E], then (one block) first[E + 1], experts[kTB * k]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *first = reinterpret_cast<int *>(mask + p.E);
     int *chosen = first + p.E + 1;
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = make_uint2(0, 0);
+    for (int e = threadIdx.x; e < p.E; e += kChooseThreads) mask[e] = make_uint2(0, 0);
     __syncthreads();
     const int t0 = blockIdx.x * kTB;
-    for (int i = warp; i < kTB && t0 + i < p.T; i += kRouteThreads / 32) {
+    for (int i = warp; i < kTB && t0 + i < p.T; i += kChooseThreads / 32) {
         const int64_t t = t0 + i;
         const T *row = static_cast<const T *>(p.logits) + t * p.E;
-        uint32_t key[VPL];
+        uint32_t key[VPL];  // of expert 32 V (j / V) + V lane + j % V
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            const int e = 32 * j + lane;
-            const float v = e < p.E ? moe_float(row[e]) : 0.0f;
-            key[j] = e >= p.E ? 0u : v != v ? kKeyNone : route_key(v);
+        for (int j = 0; j < VPL; j += V) {
+            const int e0 = 32 * j + V * lane;
+            Run run;
+            if (e0 < p.E) {  // (VEC: E is a multiple of V)
+                run = *reinterpret_cast<const Run *>(row + e0);
+            } else {
+#pragma unroll
+                for (int q = 0; q < V; ++q) run.v[q] = T(0.0f);
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float v = moe_float(run.v[q]);
+                const uint32_t kk = kPacked ? route_packed(v, e0 + q) : route_key(v);
+                key[j + q] = e0 >= p.E ? 0u : v != v ? kKeyNone : kk;
+            }
         }
-        uint32_t local = 0;
+        uint32_t local = 0;  // the lane's largest
+        if constexpr (kPacked && VPL <= 8) {
+            // sorted: the largest first
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) local = max(local, key[j]);
+            for (int r = 0; r < VPL; ++r)
+#pragma unroll
+                for (int j = r & 1; j + 1 < VPL; j += 2) {
+                    const uint32_t a = key[j], b = key[j + 1];
+                    key[j] = max(a, b);
+                    key[j + 1] = min(a, b);
+                }
+            local = key[0];
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) local = max(local, key[j]);
+        }
         uint32_t top = __reduce_max_sync(0xffffffffu, local);
-        const float m = top > kKeyNone ? route_value(top) : 0.0f;
+        const auto value = [](uint32_t kk) { return kPacked ? route_packed_value(kk) : route_value(kk); };
+        const float m = top > kKeyNone ? value(top) : 0.0f;
         float sum = 0.0f;
         if (!p.normalize) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                if (key[j] > kKeyNone) sum += expf(route_value(key[j]) - m);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (key[j] > kKeyNone) sum += expf(value(key[j]) - m);
         }
         // lane c keeps choice c
         int my_e = -1;
-        float my_w = 0.0f;
+        uint32_t my_top = 0;
         for (int c = 0; c < p.k; ++c) {
             if (top <= kKeyNone) break;  // only masked experts are left
-            int at = 0x7FFFFFFF;
-            if (local == top) {
+            int e;
+            bool owner;
+            if constexpr (kPacked) {
+                owner = local == top;
+                e = static_cast<int>(0x1FFFu - (top & 0x1FFFu));
+            } else {
+                int at = 0x7FFFFFFF;
+                if (local == top) {
 #pragma unroll
-                for (int j = VPL - 1; j >= 0; --j)
-                    if (key[j] == top) at = 32 * j + lane;
+                    for (int j = VPL - 1; j >= 0; --j)
+                        if (key[j] == top) at = 32 * (j / V * V) + V * lane + j % V;
+                }
+                e = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(at)));
+                owner = at == e;
             }
-            const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(at)));
             if (lane == c) {
                 my_e = e;
-                my_w = expf(route_value(top) - m);
+                my_top = top;
             }
-            if (at == e) {  // taken: out of the next rounds
-                local = 0;
+            if (owner) {  // taken: out of the next rounds
+                if constexpr (kPacked && VPL <= 8) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) {
-                    if (32 * j + lane == e) key[j] = 0u;
-                    local = max(local, key[j]);
+                    for (int j = 0; j + 1 < VPL; ++j) key[j] = key[j + 1];
+                    key[VPL - 1] = 0;
+                    local = key[0];
+                } else {
+                    local = 0;
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) {
+                        if (kPacked ? key[j] == top : 32 * (j / V * V) + V * lane + j % V == e) key[j] = 0u;
+                        local = max(local, key[j]);
+                    }
                 }
             }
             top = __reduce_max_sync(0xffffffffu, local);
         }
-        if (p.normalize) {
-            sum = my_w;
+        const float my_w = my_e >= 0 ? expf(value(my_top) - m) : 0.0f;
+        if (p.normalize) sum = my_w;
 #pragma unroll
-            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        }
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane < p.k) {
             p.experts[t * p.k + lane] = my_e;
             p.weights[t * p.k + lane] = my_e >= 0 ? __fdiv_rn(my_w, sum) : 0.0f;
@@ -165,33 +222,42 @@ __global__ void __launch_bounds__(kRouteThreads) moe_choose_kernel(const RoutePa
     }
     __syncthreads();
     if (p.counts) {
-        for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
+        for (int e = threadIdx.x; e < p.E; e += kChooseThreads)
             p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = __popc(mask[e].x) + __popc(mask[e].y);
         return;
     }
     if (warp == 0) route_scan(first, p.E, [&](int e) { return __popc(mask[e].x) + __popc(mask[e].y); });
     __syncthreads();
-    for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = first[e];
-    for (int i = first[p.E] + threadIdx.x; i < p.T * p.k; i += kRouteThreads) p.tokens[i] = -1;
+    for (int e = threadIdx.x; e <= p.E; e += kChooseThreads) p.offsets[e] = first[e];
+    for (int i = first[p.E] + threadIdx.x; i < p.T * p.k; i += kChooseThreads) p.tokens[i] = -1;
     route_place(p, mask, first, chosen);
 }
 
-// A warp per expert: its counts per block become running sums.
+// A warp per expert: its counts per block become running sums, 8 blocks a lane.
 __global__ void __launch_bounds__(128) moe_scan_kernel(const RouteParams p)
 {
     const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (e >= p.E) return;
     int *c = p.counts + static_cast<int64_t>(e) * p.blocks;
     int run = 0;
-    for (int b0 = 0; b0 < p.blocks; b0 += 32) {
-        const int n = b0 + lane < p.blocks ? c[b0 + lane] : 0;
-        int incl = n;
+    for (int b0 = 0; b0 < p.blocks; b0 += 256) {
+        int n[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n[j] = b0 + 8 * lane + j < p.blocks ? c[b0 + 8 * lane + j] : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += n[j];
+        int incl = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += o;
         }
-        if (b0 + lane < p.blocks) c[b0 + lane] = run + incl - n;
+        int at = run + incl - sum;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (b0 + 8 * lane + j < p.blocks) c[b0 + 8 * lane + j] = at;
+            at += n[j];
+        }
         run += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) p.totals[e] = run;
@@ -201,8 +267,12 @@ __global__ void __launch_bounds__(kRouteThreads) moe_place_kernel(const RoutePar
 {
     extern __shared__ uint2 mask[];  // [E], then first[E + 1]
     int *first = reinterpret_cast<int *>(mask + p.E);
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = make_uint2(0, 0);
-    if (threadIdx.x < 32) route_scan(first, p.E, [&](int e) { return p.totals[e]; });
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+        mask[e] = make_uint2(0, 0);
+        first[e] = p.totals[e];
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) route_scan(first, p.E, [&](int e) { return first[e]; });
     __syncthreads();
     const int t0 = blockIdx.x * kTB;
     const int n = min(kTB, p.T - t0) * p.k;
@@ -225,19 +295,29 @@ __global__ void __launch_bounds__(kRouteThreads) moe_place_kernel(const RoutePar
     route_place(p, mask, first, experts);
 }
 
+template <class T, int VPL>
+static void launch_choose_vpl(const RouteParams &p, int smem, cudaStream_t stream)
+{
+    constexpr int V = VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
+    if (p.E % V == 0 && reinterpret_cast<uintptr_t>(p.logits) % (V * sizeof(T)) == 0)
+        moe_choose_kernel<T, VPL, true><<<p.blocks, kChooseThreads, smem, stream>>>(p);
+    else
+        moe_choose_kernel<T, VPL, false><<<p.blocks, kChooseThreads, smem, stream>>>(p);
+}
+
 template <class T>
 static void launch_choose(const RouteParams &p, int smem, cudaStream_t stream)
 {
     if (p.E <= 64)
-        moe_choose_kernel<T, 2><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+        launch_choose_vpl<T, 2>(p, smem, stream);
     else if (p.E <= 128)
-        moe_choose_kernel<T, 4><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+        launch_choose_vpl<T, 4>(p, smem, stream);
     else if (p.E <= 256)
-        moe_choose_kernel<T, 8><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+        launch_choose_vpl<T, 8>(p, smem, stream);
     else if (p.E <= 512)
-        moe_choose_kernel<T, 16><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+        launch_choose_vpl<T, 16>(p, smem, stream);
     else
-        moe_choose_kernel<T, 32><<<p.blocks, kRouteThreads, smem, stream>>>(p);
+        launch_choose_vpl<T, 32>(p, smem, stream);
 }
 
 int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)

@@ -22,6 +22,44 @@ __device__ __forceinline__ float fp4_float(float v) { return v; }
 __device__ __forceinline__ float fp4_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float fp4_float(__half v) { return __half2float(v); }
 
+// The two values of a word of 16-bit ones.
+template <class T>
+__device__ __forceinline__ void fp4_floats(uint32_t w, float &lo, float &hi)
+{
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        lo = __uint_as_float(w << 16);
+        hi = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        lo = f.x;
+        hi = f.y;
+    }
+}
+
+// max(|a|, |b|) of each half, NaN where one is (the result's signs mean nothing).
+template <class T>
+__device__ __forceinline__ uint32_t fp4_absmax2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// a *= f, b *= f as one pair (each rounded as a product of its own).
+__device__ __forceinline__ void fp4_mul2(float &a, float &b, float f)
+{
+    asm("{\n\t.reg .b64 v, w;\n\t"
+        "mov.b64 v, {%0, %1};\n\t"
+        "mov.b64 w, {%2, %2};\n\t"
+        "mul.rn.f32x2 v, v, w;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f));
+}
+
 // Eight codes, element 0 in the lowest nibble.
 __device__ __forceinline__ uint32_t fp4_codes8(const float *y)
 {
@@ -80,70 +118,97 @@ struct Fp4PackParams {
     int x_rows, rows, K, code_bytes, pitch;
 };
 
-// 16 values of one row from k; zeros past K.
+// 16 values of one row from k (zeros past K), and the bits of the largest
+// magnitude: of pairs of 16-bit values as two 16-bit integers at a time.
 template <class T, bool VEC>
-__device__ __forceinline__ void fp4_load16(const T *row, int k, int K, float (&v)[16])
+__device__ __forceinline__ uint32_t fp4_load16(const T *row, int k, int K, float (&v)[16])
 {
+    uint32_t amax = 0;
     if (VEC && k + 16 <= K) {
-        constexpr int kPer = 16 / sizeof(T);  // values of a 16-byte load
-        uint4 raw[16 / kPer];
+        constexpr int kWords = 4 * sizeof(T);
+        uint32_t w[kWords];
 #pragma unroll
-        for (int i = 0; i < 16 / kPer; ++i) raw[i] = __ldg(reinterpret_cast<const uint4 *>(row + k) + i);
-        const T *t = reinterpret_cast<const T *>(raw);
+        for (int i = 0; i < kWords / 4; ++i)
+            *reinterpret_cast<uint4 *>(w + 4 * i) = __ldg(reinterpret_cast<const uint4 *>(row + k) + i);
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = fp4_float(t[i]);
+            for (int i = 0; i < 16; ++i) {
+                v[i] = __uint_as_float(w[i]);
+                amax = max(amax, w[i] & 0x7FFFFFFFu);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fp4_absmax2<T>(amax, w[i]);
+            amax = max(amax & 0x7FFFu, amax >> 16 & 0x7FFFu);
+            const uint16_t top = static_cast<uint16_t>(amax);
+            amax = __float_as_uint(fp4_float(*reinterpret_cast<const T *>(&top)));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fp4_floats<T>(w[i], v[2 * i], v[2 * i + 1]);
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = k + i < K ? fp4_float(row[k + i]) : 0.0f;
+        for (int i = 0; i < 16; ++i) {
+            v[i] = k + i < K ? fp4_float(row[k + i]) : 0.0f;
+            amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        }
     }
+    return amax;
 }
 
 // Row-major x: a thread per 16 k of a row (mx: two neighbouring lanes share a
-// block's scale), so a warp reads and writes contiguous runs.
-template <bool NV, class T, bool VEC, class Index>
-__global__ void __launch_bounds__(256) pack_fp4_rows_kernel(const T *__restrict__ x, const Fp4PackParams p)
+// block's scale), so a warp reads and writes contiguous runs.  A block of threads
+// is blockDim.x items (even) of blockDim.y rows; rows longer than that take
+// several (blockIdx.y), and a thread goes down the rows, its next row's index in
+// flight.  Issue-bound where x comes from L2 (gathered rows).
+template <bool NV, class T, bool VEC>
+__global__ void __launch_bounds__(256, 6) pack_fp4_rows_kernel(const T *__restrict__ x, const Fp4PackParams p)
 {
-    const Index items = static_cast<Index>(p.code_bytes / 8);  // of 16 k, per row
-    const Index item = static_cast<Index>(blockIdx.x) * 256 + threadIdx.x;
-    const Index row_i = item / items;
-    const int k = static_cast<int>(item - row_i * items) * 16;
-    const bool live = row_i < static_cast<Index>(p.rows);
-    const int64_t row = static_cast<int64_t>(row_i);
-    int64_t src = row;
-    if (live && p.index) {
-        src = __ldg(p.index + row);
-        if (src >= p.x_rows) src = -1;
-    }
-    float v[16];
-    if (live && src >= 0) {
-        fp4_load16<T, VEC>(x + src * p.ld, k, p.K, v);
-    } else {
+    const int k = (blockIdx.y * blockDim.x + threadIdx.x) * 16;
+    const bool in_row = k < 2 * p.code_bytes;
+    const bool last = k / 8 + 2 == p.code_bytes / 4;  // of the row: it writes the padding
+    const float g = NV && p.g ? __ldg(p.g) : 1.0f;
+    const int step = gridDim.x * blockDim.y;
+    // rows as unsigned: the last step past 2^31 does not wrap
+    uint32_t row = blockIdx.x * blockDim.y + threadIdx.y;
+    const uint32_t rows = static_cast<uint32_t>(p.rows);
+    const auto source = [&](uint32_t r) {
+        if (r >= rows) return -1;
+        const int s = p.index ? __ldg(p.index + r) : static_cast<int>(r);
+        return s < p.x_rows ? s : -1;
+    };
+    int src = source(row);
+    uint8_t *codes = p.codes + static_cast<int64_t>(row) * p.code_bytes + k / 2;
+    uint8_t *scales = p.scales + static_cast<int64_t>(row) * p.pitch;
+    const int64_t code_step = static_cast<int64_t>(step) * p.code_bytes, scale_step = static_cast<int64_t>(step) * p.pitch;
+    // (the same count for every lane of a warp)
+    for (; row - threadIdx.y < rows; row += step, codes += code_step, scales += scale_step) {
+        float v[16];
+        uint32_t amax = 0;
+        if (src >= 0 && in_row) {
+            amax = fp4_load16<T, VEC>(x + src * p.ld, k, p.K, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-    }
-    uint32_t amax = 0;
+            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        }
+        src = source(row + step);
+        if constexpr (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        if (!in_row || row >= rows) continue;
+        float f;
+        const uint8_t s = fp4_scale<NV>(amax, g, f);
+        uint2 out = make_uint2(0, 0);
+        if (amax < 0x7F800000u && f > 0.0f) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    if constexpr (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    if (!live) return;
-    float f;
-    const uint8_t s = fp4_scale<NV>(amax, NV && p.g ? __ldg(p.g) : 1.0f, f);
-    uint2 out = make_uint2(0, 0);
-    if (amax < 0x7F800000u && f > 0.0f) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= f;
-        out = make_uint2(fp4_codes8(v), fp4_codes8(v + 8));
-    }
-    *reinterpret_cast<uint2 *>(p.codes + row * p.code_bytes + k / 2) = out;
-    uint8_t *sc = p.scales + row * p.pitch;
-    if (NV) {
-        if (k < p.K) sc[k / 16] = s;
-    } else if ((k & 16) == 0) {
-        sc[k / 32] = s;
-    }
-    // the row's last thread: zeros up to the pitch
-    if (k / 8 + 2 == p.code_bytes / 4) {
-        for (int b = (p.K + (NV ? 15 : 31)) / (NV ? 16 : 32); b < p.pitch; ++b) sc[b] = 0;
+            for (int i = 0; i < 16; i += 2) fp4_mul2(v[i], v[i + 1], f);
+            out = make_uint2(fp4_codes8(v), fp4_codes8(v + 8));
+        }
+        *reinterpret_cast<uint2 *>(codes) = out;
+        if (NV) {
+            if (k < p.K) scales[k / 16] = s;
+        } else if ((k & 16) == 0) {
+            scales[k / 32] = s;
+        }
+        if (last)
+            for (int b = (p.K + (NV ? 15 : 31)) / (NV ? 16 : 32); b < p.pitch; ++b) scales[b] = 0;
     }
 }
 
@@ -219,17 +284,23 @@ static int launch_pack_type(const Fp4PackCall &c, const Fp4PackParams &p, cudaSt
     } else {
         // 16-byte loads where every row starts on 16 bytes
         const bool vec = (reinterpret_cast<uintptr_t>(x) % 16) == 0 && (c.ld * sizeof(T)) % 16 == 0;
-        const int64_t items = int64_t(c.rows) * (p.code_bytes / 8);
-        const int64_t blocks = (items + 255) / 256;
-        if (blocks > 0x7FFFFFFF) return kUnsupportedShape;
-        const unsigned b = static_cast<unsigned>(blocks);
-        const bool narrow = blocks * 256 < (int64_t(1) << 32);
-        if (vec && narrow)
-            pack_fp4_rows_kernel<NV, T, true, uint32_t><<<b, 256, 0, stream>>>(x, p);
-        else if (vec)
-            pack_fp4_rows_kernel<NV, T, true, uint64_t><<<b, 256, 0, stream>>>(x, p);
+        // a row's items in equal blocks of at most 256 threads, whole warps (short
+        // rows: a power of two, several rows a warp), and as many rows as fit
+        const int items = p.code_bytes / 8;
+        const int chunks = (items + 255) / 256;
+        int bx = ((items + chunks - 1) / chunks + 31) / 32 * 32;
+        if (items <= 16)
+            for (bx = 2; bx < items;) bx *= 2;
+        const int by = std::max(1, 256 / bx);
+        if (chunks > 65535) return kUnsupportedShape;
+        // blocks that are resident at once, fewer where the rows give one each
+        const int64_t full = std::max<int64_t>(1, int64_t(sm_count()) * 6 * std::max(1, 256 / (bx * by)) / chunks);
+        const int64_t gx = std::min((int64_t(c.rows) + by - 1) / by, full);
+        const dim3 grid(static_cast<unsigned>(gx), chunks), block(bx, by);
+        if (vec)
+            pack_fp4_rows_kernel<NV, T, true><<<grid, block, 0, stream>>>(x, p);
         else
-            pack_fp4_rows_kernel<NV, T, false, uint64_t><<<b, 256, 0, stream>>>(x, p);
+            pack_fp4_rows_kernel<NV, T, false><<<grid, block, 0, stream>>>(x, p);
     }
     note_launch();
     return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
