@@ -80,10 +80,11 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     if (clusters < 1) return kCudaError;
     const int code_bytes = fp4_code_bytes(c.K), pitch = fp4_scale_pitch(c.K, Cfg::NV);
     const uint64_t p_rows = uint64_t(c.experts) * c.N;
-    CUtensorMap mapP, mapQ, mapSP, mapSQ;
+    CUtensorMap mapP, mapQ, mapQs, mapSP, mapSQ;
     constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (make_map(&mapP, kU8, c.B, p_rows, code_bytes, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
         make_map(&mapQ, kU8, c.A, c.rows, code_bytes, Cfg::kQBox, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
+        make_map(&mapQs, kU8, c.A, c.rows, code_bytes, Cfg::kQRows, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
         make_map(&mapSP, kU8, c.SFB, p_rows, pitch, 128, 16 * Cfg::kH, CU_TENSOR_MAP_SWIZZLE_NONE) != kOk ||
         make_map(&mapSQ, kU8, c.SFA, c.rows, pitch, Cfg::kQScaleRows, 16 * Cfg::kH,
                  CU_TENSOR_MAP_SWIZZLE_NONE) != kOk)
@@ -138,7 +139,7 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = na ? attr : nullptr;
     cfg.numAttrs = na;
-    if (cudaLaunchKernelEx(&cfg, igemm_fp4_kernel<Cfg>, mapP, mapQ, mapSP, mapSQ, prm) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, igemm_fp4_kernel<Cfg>, mapP, mapQ, mapQs, mapSP, mapSQ, prm) != cudaSuccess)
         return kCudaError;
     note_launch();
     if (ev.stop && cudaEventRecord(ev.stop, stream) != cudaSuccess) return kCudaError;
