@@ -20,12 +20,10 @@ struct Fp4Smem {
         const int red = cs > 1 ? Cfg::kRedBytes : 0;
         const int tail = Cfg::kTailBytes + 4 * (experts + 1);
         const int left = kLimit - red - Cfg::kStoreBytes - tail;
-        // Three blocks of scales where they fit: their loads run ahead of the MMAs by
-        // the load's latency and the turning.  (2 scale_stages <= code_stages + 1: the
-        // producer learns from the codes' barriers that a block's scales are free, and
-        // a barrier must not complete its next phase before that.)
+        // (three blocks of scales at least: their loads run ahead by the load's latency
+        // and the turning)
         code_stages = std::min((left - 3 * Cfg::kScaleStage) / Cfg::kStage, static_cast<int>(Cfg::kMaxStages));
-        scale_stages = std::min(std::min((left - code_stages * Cfg::kStage) / Cfg::kScaleStage, (code_stages + 1) / 2),
+        scale_stages = std::min((left - code_stages * Cfg::kStage) / Cfg::kScaleStage,
                                 static_cast<int>(Cfg::kMaxScaleStages));
         off_scales = code_stages * Cfg::kStage;
         off_red = off_scales + scale_stages * Cfg::kScaleStage;

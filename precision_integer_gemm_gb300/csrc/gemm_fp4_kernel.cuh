@@ -24,11 +24,14 @@
 // stream: 338 us at 8192^3.  Stored to TMEM by a warp per quadrant, every scale
 // was read four times.)
 //
-// The issuing warp sets the pace of the loop (an MMA takes it about 50 cycles, a
-// successful wait as much again), so a block has one joint wait and 8 MMAs.
+// What a single warp issues sets the pace of the loop: an MMA takes it about 50
+// cycles, a TMA load 100, a successful wait 50 to 100, and a block's MMAs run for
+// 1024.  So a block has one joint wait for its 8 MMAs, and weights, activations and
+// scales each have a loading warp (one warp for all three took 1500 cycles a block).
 //
-// Warps 0-3 epilogue, 4 TMA producer, 5 MMA issue, 6 and up scales.  Persistent CTAs
-// (or CTA pairs, or clusters that split k).  Every wait is bounded.
+// Warps 0-3 epilogue, 4 MMA issue, 5 weight loads, 6 activation loads, 7 scale loads,
+// 8 and up scales.  Persistent CTAs (or CTA pairs, or clusters that split k).  Every
+// wait is bounded.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -56,7 +59,7 @@ struct Fp4Params {
     int group_p;           // tiles run in groups of group_p weight tiles (fastest) by every activation tile
     int cs;                // CTAs of a cluster that split k (1: none; a power of two, 4 cs <= BN)
     int blocks_per_slice;
-    int code_stages, scale_stages;  // ring slots: 256 k of codes, 512 k of scales (2 scale_stages <= code_stages + 1)
+    int code_stages, scale_stages;  // ring slots: 256 k of codes, 512 k of scales
     int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
     int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
     int *status;
@@ -96,11 +99,11 @@ struct Fp4Cfg {
     static constexpr int kRedBufs = BN <= 32 ? 2 : 1;
     static constexpr int kRedBytes = kRedBufs * BN * 512;  // split k: partial tiles of the cluster's CTAs
     static constexpr int kMaxStages = 16;
-    static constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxScaleStages + 4 + 1 + 16;
+    static constexpr int kNumBars = 2 * kMaxStages + 3 * kMaxScaleStages + 4 + 1 + 16;
     static constexpr int kStoreBytes = 4 * 1024;  // 16-bit C: 16 rows x 32 columns per epilogue warp
     static constexpr int kTailBytes = 8 * kNumBars + 64;  // and the groups' tile counts
     static constexpr int kNAlign = PAIR ? 32 : 16;
-    static constexpr int kWarpProd = 4, kWarpMma = 5, kWarpScale = 6;
+    static constexpr int kWarpMma = 4, kWarpLoadP = 5, kWarpLoadQ = 6, kWarpLoadS = 7, kWarpScale = 8;
     static constexpr int kThreads = 32 * (kWarpScale + 1 + kQGroups);
     static_assert(kQBox % 8 == 0 && kStage % 1024 == 0, "1024-byte aligned operand tiles");
     static_assert(kTmemUse <= 512 && kOverlap >= 0 && kOverlap % 96 == 0, "TMEM budget");
@@ -354,7 +357,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint64_t *sf_raw = empty + Cfg::kMaxStages;     // [scale stages] scale rows landed
     uint64_t *sf_full = sf_raw + Cfg::kMaxScaleStages;    // [scale stages] ... turned (scale warps; even CTA of a pair:
                                                           // and the odd CTA's, its relay)
-    uint64_t *acc_full = sf_full + Cfg::kMaxScaleStages;  // [2] accumulator complete (commit)
+    uint64_t *sf_empty = sf_full + Cfg::kMaxScaleStages;  // [scale stages] consumed (MMA commit)
+    uint64_t *acc_full = sf_empty + Cfg::kMaxScaleStages; // [2] accumulator complete (commit)
     uint64_t *acc_empty = acc_full + 2;             // [2] accumulator (its overlap) read by the epilogue warps
     uint64_t *mma_drain = acc_empty + 2;
     uint64_t *red_full = mma_drain + 1;             // [2][4] split k: the other CTAs' partials of this warp's part landed
@@ -373,13 +377,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int cid = blockIdx.x / csize, ncl = gridDim.x / csize;
     const bool leader = !PAIR || rank == 0;
 
-    if (warp == Cfg::kWarpProd) {
+    if (warp == Cfg::kWarpLoadP) {
         if (lane < prm.code_stages) {
-            mbar_init(&full[lane], 1);
+            mbar_init(&full[lane], 2);  // the two loading warps
             mbar_init(&empty[lane], 1);
         }
         if (lane < prm.scale_stages) {
             mbar_init(&sf_raw[lane], 1);
+            mbar_init(&sf_empty[lane], 1);
             mbar_init(&sf_full[lane], 1 + Cfg::kQGroups + (PAIR && leader ? 1 : 0));
         }
         if (lane < 2) {
@@ -450,86 +455,47 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int b0 = PAIR ? 0 : min(rank * prm.blocks_per_slice, prm.blocks);
     const int b1 = PAIR ? prm.blocks : min(b0 + prm.blocks_per_slice, prm.blocks);
 
-    if (warp == Cfg::kWarpProd) {
-        // ------------------------------------------------------------ producer
-        // er: the last stage of the block that had the next scale slot before
-        Fp4Ring cr(prm.code_stages), sr(prm.scale_stages), er(prm.code_stages);
-        uint32_t issued = 0, last = 0, s_issued = 0, s_last = 0;
-        int filled = 0;
+    if (warp == Cfg::kWarpLoadP || warp == Cfg::kWarpLoadQ) {
+        // ------------------------------------------------------------ codes
+        const bool q_side = warp == Cfg::kWarpLoadQ;
+        Fp4Ring cr(prm.code_stages);
+        uint32_t issued = 0, last = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
             const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
-            const int py = x.e * prm.N + x.p0;
-            // rows of the activations that this CTA loads (pair: half of the tile's)
+            // activation rows that this CTA loads (pair: half of the tile's)
             const int mine = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : x.nq;
-            const int qy = x.q0 + pr * mine;
-            const int boxes = mine > 2 * Cfg::kQRows || Cfg::kQRows == Cfg::kQBox ? 0 : mine > Cfg::kQRows ? 2 : 1;
-            const uint32_t tx =
-                static_cast<uint32_t>(Cfg::kBoxP + (boxes == 0 ? Cfg::kBoxQ : boxes * Cfg::kQRows * 128));
-            const int groups = (x.nq + 127) / 128;
-            for (int b = b0; ok && b < b1; ++b) {
-                if (filled == prm.scale_stages) {
-                    er.next();
-                    if (!fp4_warp_wait(&empty[er.slot], er.phase, wd)) {
-                        ok = false;
-                        break;
-                    }
-                    er.next();
-                } else {
-                    ++filled;
+            const bool small = Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
+            const bool two = small && mine > Cfg::kQRows;
+            const int y = q_side ? x.q0 + pr * mine : x.e * prm.N + x.p0;
+            const uint32_t tx = static_cast<uint32_t>(
+                !q_side ? Cfg::kBoxP : !small ? Cfg::kBoxQ : (two ? 2 : 1) * Cfg::kQRows * 128);
+            const CUtensorMap *map = !q_side ? &mapP : small ? &mapQs : &mapQ;
+            const uint32_t off = q_side ? Cfg::kBoxP : 0;
+#pragma unroll 1
+            for (int k = 2 * b0; k < 2 * b1; ++k) {
+                if (!fp4_warp_wait(&empty[cr.slot], cr.phase ^ 1u, wd)) {
+                    ok = false;
+                    break;
                 }
                 if (elect_one()) {
-                    uint8_t *sc = scales + sr.slot * Cfg::kScaleStage;
-                    mbar_arrive_expect_tx(&sf_raw[sr.slot],
-                                          static_cast<uint32_t>((128 + groups * Cfg::kQScaleRows) * 16 * Cfg::kH));
-                    tma_load_2d(sc, &mapSP, &sf_raw[sr.slot], b * 16 * Cfg::kH, py);
-#pragma unroll
-                    for (int j = 0; j < Cfg::kQGroups; ++j)
-                        if (j < groups)
-                            tma_load_2d(sc + Cfg::kGroupBytes * (1 + j), &mapSQ, &sf_raw[sr.slot], b * 16 * Cfg::kH,
-                                        x.q0 + 128 * j);
+                    uint8_t *to = codes + cr.slot * Cfg::kStage + off;
+                    if constexpr (PAIR) {
+                        // both CTAs' bytes count on the even CTA's barrier
+                        if (leader) mbar_arrive_expect_tx(&full[cr.slot], 2 * tx);
+                        const uint32_t bar = cluster_map(smem_u32(&full[cr.slot]), 0u);
+                        tma_load_2d_pair(to, map, bar, k * 128, y);
+                        if (two) tma_load_2d_pair(to + Cfg::kQRows * 128, map, bar, k * 128, y + Cfg::kQRows);
+                    } else {
+                        mbar_arrive_expect_tx(&full[cr.slot], tx);
+                        tma_load_2d(to, map, &full[cr.slot], k * 128, y);
+                        if (two) tma_load_2d(to + Cfg::kQRows * 128, map, &full[cr.slot], k * 128, y + Cfg::kQRows);
+                    }
                 }
                 __syncwarp();
-                s_issued |= 1u << sr.slot;
-                s_last = (s_last & ~(1u << sr.slot)) | (sr.phase << sr.slot);
-                sr.next();
-#pragma unroll 1
-                for (int k = 2 * b; k < 2 * b + 2; ++k) {
-                    if (!fp4_warp_wait(&empty[cr.slot], cr.phase ^ 1u, wd)) {
-                        ok = false;
-                        break;
-                    }
-                    if (elect_one()) {
-                        uint8_t *st = codes + cr.slot * Cfg::kStage;
-                        if constexpr (PAIR) {
-                            // both CTAs' bytes count on the even CTA's barrier
-                            if (leader) mbar_arrive_expect_tx(&full[cr.slot], 2 * tx);
-                            const uint32_t bar = cluster_map(smem_u32(&full[cr.slot]), 0u);
-                            tma_load_2d_pair(st, &mapP, bar, k * 128, py);
-                            if (boxes == 0)
-                                tma_load_2d_pair(st + Cfg::kBoxP, &mapQ, bar, k * 128, qy);
-                            else
-                                tma_load_2d_pair(st + Cfg::kBoxP, &mapQs, bar, k * 128, qy);
-                            if (boxes == 2)
-                                tma_load_2d_pair(st + Cfg::kBoxP + Cfg::kQRows * 128, &mapQs, bar, k * 128,
-                                                 qy + Cfg::kQRows);
-                        } else {
-                            mbar_arrive_expect_tx(&full[cr.slot], tx);
-                            tma_load_2d(st, &mapP, &full[cr.slot], k * 128, py);
-                            if (boxes == 0)
-                                tma_load_2d(st + Cfg::kBoxP, &mapQ, &full[cr.slot], k * 128, qy);
-                            else
-                                tma_load_2d(st + Cfg::kBoxP, &mapQs, &full[cr.slot], k * 128, qy);
-                            if (boxes == 2)
-                                tma_load_2d(st + Cfg::kBoxP + Cfg::kQRows * 128, &mapQs, &full[cr.slot], k * 128,
-                                            qy + Cfg::kQRows);
-                        }
-                    }
-                    __syncwarp();
-                    issued |= 1u << cr.slot;
-                    last = (last & ~(1u << cr.slot)) | (cr.phase << cr.slot);
-                    cr.next();
-                }
+                issued |= 1u << cr.slot;
+                last = (last & ~(1u << cr.slot)) | (cr.phase << cr.slot);
+                cr.next();
             }
         }
         // never leave with copies in flight, nor with an MMA commit on its way here
@@ -539,9 +505,44 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 if (leader) fp4_wait_drain(&full[s], (last >> s) & 1u, prm.limit_ns);
                 fp4_wait_drain(&empty[s], (last >> s) & 1u, prm.limit_ns);
             }
+    } else if (warp == Cfg::kWarpLoadS) {
+        // ------------------------------------------------------------ scale rows
+        Fp4Ring sr(prm.scale_stages);
+        uint32_t issued = 0, last = 0;
+        bool ok = true;
+        for (int t = cid; ok && t < tiles; t += ncl) {
+            const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
+            const int py = x.e * prm.N + x.p0;
+            const int groups = (x.nq + 127) / 128;
+            const uint32_t tx = static_cast<uint32_t>((128 + groups * Cfg::kQScaleRows) * 16 * Cfg::kH);
+#pragma unroll 1
+            for (int b = b0; b < b1; ++b) {
+                if (!fp4_warp_wait(&sf_empty[sr.slot], sr.phase ^ 1u, wd)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    uint8_t *to = scales + sr.slot * Cfg::kScaleStage;
+                    mbar_arrive_expect_tx(&sf_raw[sr.slot], tx);
+                    tma_load_2d(to, &mapSP, &sf_raw[sr.slot], b * 16 * Cfg::kH, py);
+#pragma unroll
+                    for (int j = 0; j < Cfg::kQGroups; ++j)
+                        if (j < groups)
+                            tma_load_2d(to + Cfg::kGroupBytes * (1 + j), &mapSQ, &sf_raw[sr.slot], b * 16 * Cfg::kH,
+                                        x.q0 + 128 * j);
+                }
+                __syncwarp();
+                issued |= 1u << sr.slot;
+                last = (last & ~(1u << sr.slot)) | (sr.phase << sr.slot);
+                sr.next();
+            }
+        }
 #pragma unroll 1
         for (int s = 0; s < prm.scale_stages; ++s)
-            if ((s_issued >> s) & 1u) fp4_wait_drain(&sf_raw[s], (s_last >> s) & 1u, prm.limit_ns);
+            if ((issued >> s) & 1u) {
+                fp4_wait_drain(&sf_raw[s], (last >> s) & 1u, prm.limit_ns);
+                fp4_wait_drain(&sf_empty[s], (last >> s) & 1u, prm.limit_ns);
+            }
     } else if (warp == Cfg::kWarpMma) {
         // ------------------------------------------------------------ MMA issuer
         if (leader) {
@@ -605,11 +606,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                                                       b > b0 || h > 0 || q > 0 ? 1u : 0u);
                                 }
                             }
-                            // frees the stage's codes, and with the block's last stage its scales
-                            if constexpr (PAIR)
+                            // frees the stage's codes, and after the block's last stage its scales
+                            if constexpr (PAIR) {
                                 mma_commit_pair_multicast(&empty[slot], 0x3);
-                            else
+                                if (h) mma_commit_pair_multicast(&sf_empty[fr.slot], 0x3);
+                            } else {
                                 mma_commit(&empty[slot]);
+                                if (h) mma_commit(&sf_empty[fr.slot]);
+                            }
                         }
                     }
                     __syncwarp();
