@@ -20,8 +20,8 @@ struct Fp4Smem {
         const int red = cs > 1 ? Cfg::kRedBytes : 0;
         const int tail = Cfg::kTailBytes + 4 * (experts + 1);
         const int left = kLimit - red - Cfg::kStoreBytes - tail;
-        // (three blocks of scales at least: their loads run ahead by the load's latency
-        // and the turning)
+        // (three blocks of scales at least: with two, nvfp4 8192^3 measured 176 us against
+        // 166, although that leaves room for a sixth stage of codes)
         code_stages = std::min((left - 3 * Cfg::kScaleStage) / Cfg::kStage, static_cast<int>(Cfg::kMaxStages));
         scale_stages = std::min((left - code_stages * Cfg::kStage) / Cfg::kScaleStage,
                                 static_cast<int>(Cfg::kMaxScaleStages));

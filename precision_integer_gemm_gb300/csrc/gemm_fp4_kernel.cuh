@@ -574,46 +574,49 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                     tc_fence_after();
                     const uint64_t s0 = sdesc0 + static_cast<uint64_t>(fr.slot * (Cfg::kScaleStage >> 4));
                     const int steps = prm.k_steps - 8 * b;
+                    // scale columns: mx the block's, alternating by block; nv a stage's each
+                    const uint32_t sf = tmem + Cfg::kSf0 + (NV ? 0u : (g & 1u) * Cfg::kSfCols);
                     if (elect_one()) {
+#pragma unroll
+                        for (int h = 0; h < Cfg::kH; ++h)
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                const uint64_t from = s0 + static_cast<uint64_t>((h * 2048 + w * 512) >> 4);
+                                const uint32_t to = sf + h * Cfg::kSfCols;
+                                tmem_cp_32x128b_x4<PAIR>(to + 4 * w, from);
+#pragma unroll
+                                for (int j = 0; j < Cfg::kQGroups; ++j)
+                                    tmem_cp_32x128b_x4<PAIR>(
+                                        to + 16 + Cfg::kQCols * w + 4 * j,
+                                        from + static_cast<uint64_t>(((1 + j) * Cfg::kGroupBytes) >> 4));
+                            }
+                        // the scales' slot is free once they are in TMEM
+                        if constexpr (PAIR)
+                            mma_commit_pair_multicast(&sf_empty[fr.slot], 0x3);
+                        else
+                            mma_commit(&sf_empty[fr.slot]);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int slot = h ? cr.slot : c0.slot;
                             const uint64_t p0 = desc0 + static_cast<uint64_t>(slot * (Cfg::kStage >> 4));
                             const uint64_t q0 = p0 + static_cast<uint64_t>(Cfg::kBoxP >> 4);
-                            // scale columns: mx the block's, alternating by block; nv the stage's
-                            const uint32_t sf = tmem + Cfg::kSf0 + (NV ? h : static_cast<int>(g & 1u)) * Cfg::kSfCols;
-                            if (NV || h == 0) {
-#pragma unroll
-                                for (int w = 0; w < 4; ++w) {
-                                    const uint64_t from = s0 + static_cast<uint64_t>((h * 2048 + w * 512) >> 4);
-                                    tmem_cp_32x128b_x4<PAIR>(sf + 4 * w, from);
-#pragma unroll
-                                    for (int j = 0; j < Cfg::kQGroups; ++j)
-                                        tmem_cp_32x128b_x4<PAIR>(
-                                            sf + 16 + Cfg::kQCols * w + 4 * j,
-                                            from + static_cast<uint64_t>(((1 + j) * Cfg::kGroupBytes) >> 4));
-                                }
-                            }
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 if (4 * h + q < steps) {
                                     // a word holds 64 k (nv) or 128 k (mx)
                                     const int word = NV ? q : 2 * h + q / 2;
                                     const uint32_t id = NV ? 0u : 2u * (q & 1);
+                                    const uint32_t at = sf + (NV ? h * Cfg::kSfCols : 0);
                                     mma_fp4<NV, PAIR>(d_tmem, p0 + static_cast<uint64_t>(2 * q),
                                                       q0 + static_cast<uint64_t>(2 * q), idesc | (id << 4) | (id << 29),
-                                                      sf + 4 * word, sf + 16 + Cfg::kQCols * word,
+                                                      at + 4 * word, at + 16 + Cfg::kQCols * word,
                                                       b > b0 || h > 0 || q > 0 ? 1u : 0u);
                                 }
                             }
-                            // frees the stage's codes, and after the block's last stage its scales
-                            if constexpr (PAIR) {
+                            if constexpr (PAIR)
                                 mma_commit_pair_multicast(&empty[slot], 0x3);
-                                if (h) mma_commit_pair_multicast(&sf_empty[fr.slot], 0x3);
-                            } else {
+                            else
                                 mma_commit(&empty[slot]);
-                                if (h) mma_commit(&sf_empty[fr.slot]);
-                            }
                         }
                     }
                     __syncwarp();
