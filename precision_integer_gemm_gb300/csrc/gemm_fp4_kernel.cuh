@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
             // activation rows that this CTA loads (pair: half of the tile's)
             const int mine = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : x.nq;
-            const bool small = Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
+            const bool small = q_side && Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
             const bool two = small && mine > Cfg::kQRows;
             const int y = q_side ? x.q0 + pr * mine : x.e * prm.N + x.p0;
             const uint32_t tx = static_cast<uint32_t>(
