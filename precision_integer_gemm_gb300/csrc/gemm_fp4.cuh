@@ -10,7 +10,7 @@
 namespace igemm {
 
 // Shared memory of one launch: code stages, the ring of scales, the partials of a
-// split k, the epilogue's staging, then barriers and the groups' tile counts.
+// split k, the epilogue's staging, then barriers and the groups' table.
 template <class Cfg>
 struct Fp4Smem {
     int code_stages, scale_stages, off_scales, off_red, off_store, off_bars, total;
@@ -18,7 +18,7 @@ struct Fp4Smem {
     {
         constexpr int kLimit = 227 * 1024 - 1024;  // less the alignment slack
         const int red = cs > 1 ? Cfg::kRedBytes : 0;
-        const int tail = Cfg::kTailBytes + 4 * (experts + 1);
+        const int tail = Cfg::kTailBytes + 16 * experts;
         const int left = kLimit - red - Cfg::kStoreBytes - tail;
         // (three blocks of scales at least: with two, nvfp4 8192^3 measured 176 us against
         // 166, although that leaves room for a sixth stage of codes)

@@ -101,7 +101,7 @@ struct Fp4Cfg {
     static constexpr int kMaxStages = 16;
     static constexpr int kNumBars = 2 * kMaxStages + 3 * kMaxScaleStages + 4 + 1 + 16;
     static constexpr int kStoreBytes = 4 * 1024;  // 16-bit C: 16 rows x 32 columns per epilogue warp
-    static constexpr int kTailBytes = 8 * kNumBars + 64;  // and the groups' tile counts
+    static constexpr int kTailBytes = 8 * kNumBars + 64 + 16;  // and the groups' table, 16 bytes each
     static constexpr int kNAlign = PAIR ? 32 : 16;
     static constexpr int kWarpMma = 4, kWarpLoadP = 5, kWarpLoadQ = 6, kWarpLoadS = 7, kWarpScale = 8;
     static constexpr int kThreads = 32 * (kWarpScale + 1 + kQGroups);
@@ -117,27 +117,35 @@ struct Fp4Tile {
     int nq;       // activation rows of the tile
 };
 
-// Tile t: expert by binary search in the running tile counts, then the grouped
-// order of its weight and activation tiles.
+// A group in shared memory: its first tile, first activation row, rows and tiles
+// of activations.
+using Fp4Group = int4;
+
+// Tile t: group by binary search over the first tiles, then the grouped order of
+// its weight and activation tiles.
 template <class Cfg>
-__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Params &prm, const int *first_tile, int t, int rank)
+__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Params &prm, const Fp4Group *groups, int t, int rank)
 {
     Fp4Tile x;
     int begin = 0, count = prm.rows, r = t;
     x.e = 0;
+    int q_tiles = 0;
     if (prm.offsets) {
-        int lo = 0, hi = prm.experts;  // first_tile[lo] <= t < first_tile[hi]
+        int lo = 0, hi = prm.experts;  // groups[lo].x <= t, t below every later group's
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (first_tile[mid] <= t) lo = mid;
+            if (groups[mid].x <= t) lo = mid;
             else hi = mid;
         }
+        const Fp4Group g = groups[lo];
         x.e = lo;
-        r = t - first_tile[lo];
-        begin = min(max(__ldg(prm.offsets + lo), 0), prm.rows);
-        count = min(max(__ldg(prm.offsets + lo + 1), begin), prm.rows) - begin;
+        r = t - g.x;
+        begin = g.y;
+        count = g.z;
+        q_tiles = g.w;
+    } else {
+        q_tiles = (count + prm.qt - 1) / prm.qt;
     }
-    const int q_tiles = (count + prm.qt - 1) / prm.qt;
     const int per_group = prm.group_p * q_tiles;
     const int grp = r / per_group;
     const int first = grp * prm.group_p;
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *total_slot = reinterpret_cast<int *>(tmem_slot + 2);
-    int *first_tile = reinterpret_cast<int *>(tmem_slot + 16);  // [experts + 1]
+    Fp4Group *groups = reinterpret_cast<Fp4Group *>(smem + ((prm.off_bars + 8 * Cfg::kNumBars + 64 + 15) & ~15));
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -421,25 +429,24 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             int run = 0;
             for (int e0 = 0; e0 < prm.experts; e0 += 32) {
                 const int e = e0 + lane;
-                int tiles = 0;
+                Fp4Group g = make_int4(0, 0, 0, 0);
                 if (e < prm.experts) {
-                    const int b = min(max(__ldg(prm.offsets + e), 0), prm.rows);
-                    const int n = min(max(__ldg(prm.offsets + e + 1), b), prm.rows) - b;
-                    tiles = (n + prm.qt - 1) / prm.qt * prm.p_tiles;
+                    g.y = min(max(__ldg(prm.offsets + e), 0), prm.rows);
+                    g.z = min(max(__ldg(prm.offsets + e + 1), g.y), prm.rows) - g.y;
+                    g.w = (g.z + prm.qt - 1) / prm.qt;
                 }
+                const int tiles = g.w * prm.p_tiles;
                 int incl = tiles;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const int o = __shfl_up_sync(0xffffffffu, incl, d);
                     if (lane >= d) incl += o;
                 }
-                if (e < prm.experts) first_tile[e] = run + incl - tiles;
+                g.x = run + incl - tiles;
+                if (e < prm.experts) groups[e] = g;
                 run += __shfl_sync(0xffffffffu, incl, 31);
             }
-            if (lane == 0) {
-                first_tile[prm.experts] = run;
-                *total_slot = run;
-            }
+            if (lane == 0) *total_slot = run;
         } else if (lane == 0) {
             *total_slot = (prm.rows + prm.qt - 1) / prm.qt * prm.p_tiles;
         }
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         uint32_t issued = 0, last = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
-            const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
+            const Fp4Tile x = fp4_tile<Cfg>(prm, groups, t, pr);
             // activation rows that this CTA loads (pair: half of the tile's)
             const int mine = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : x.nq;
             const bool small = q_side && Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
@@ -511,10 +518,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         uint32_t issued = 0, last = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
-            const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
+            const Fp4Tile x = fp4_tile<Cfg>(prm, groups, t, pr);
             const int py = x.e * prm.N + x.p0;
-            const int groups = (x.nq + 127) / 128;
-            const uint32_t tx = static_cast<uint32_t>((128 + groups * Cfg::kQScaleRows) * 16 * Cfg::kH);
+            const int q_groups = (x.nq + 127) / 128;
+            const uint32_t tx = static_cast<uint32_t>((128 + q_groups * Cfg::kQScaleRows) * 16 * Cfg::kH);
 #pragma unroll 1
             for (int b = b0; b < b1; ++b) {
                 if (!fp4_warp_wait(&sf_empty[sr.slot], sr.phase ^ 1u, wd)) {
@@ -527,7 +534,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                     tma_load_2d(to, &mapSP, &sf_raw[sr.slot], b * 16 * Cfg::kH, py);
 #pragma unroll
                     for (int j = 0; j < Cfg::kQGroups; ++j)
-                        if (j < groups)
+                        if (j < q_groups)
                             tma_load_2d(to + Cfg::kGroupBytes * (1 + j), &mapSQ, &sf_raw[sr.slot], b * 16 * Cfg::kH,
                                         x.q0 + 128 * j);
                 }
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             uint32_t nacc = 0, g = 0;
             bool ok = true;
             for (int t = cid; ok && t < tiles; t += ncl, ++nacc) {
-                const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
+                const Fp4Tile x = fp4_tile<Cfg>(prm, groups, t, pr);
                 const uint32_t nq = static_cast<uint32_t>((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1));
                 const uint32_t idesc = idesc_fp4(128 * Cfg::CL, nq, NV);
                 const uint32_t ab = nacc & 1u;
@@ -705,7 +712,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const uint32_t empty_leader = PAIR ? cluster_map(smem_u32(acc_empty), 0u) : 0u;
         uint32_t nacc = 0;
         for (int t = cid; t < tiles; t += ncl, ++nacc) {
-            const Fp4Tile x = fp4_tile<Cfg>(prm, first_tile, t, pr);
+            const Fp4Tile x = fp4_tile<Cfg>(prm, groups, t, pr);
             const float alpha = prm.alpha ? __ldg(prm.alpha + x.e) : 1.0f;
             const uint32_t ab = nacc & 1u;
             const int n = x.p0 + quad * 32 + lane;
