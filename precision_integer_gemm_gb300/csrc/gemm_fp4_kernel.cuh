@@ -97,7 +97,7 @@ struct Fp4Cfg {
     static constexpr int kTmemUse = kSf0 + kSfSlots * kSfCols;
     static constexpr int kTmemCols = kTmemUse <= 128 ? 128 : kTmemUse <= 256 ? 256 : 512;
     static constexpr int kRedBufs = BN <= 32 ? 2 : 1;
-    static constexpr int kRedBytes = kRedBufs * BN * 512;  // split k: partial tiles of the cluster's CTAs
+    static constexpr int kRedBytes = kRedBufs * BN * 512;  // split k (BN <= 64): partial tiles of the cluster's CTAs
     static constexpr int kMaxStages = 16;
     static constexpr int kNumBars = 2 * kMaxStages + 3 * kMaxScaleStages + 4 + 1 + 16;
     static constexpr int kStoreBytes = 4 * 1024;  // 16-bit C: 16 rows x 32 columns per epilogue warp
