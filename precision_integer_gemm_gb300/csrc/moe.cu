@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
         T v[V];
     };
     extern __shared__ uint2 mask[];  // [E], then (one block) first[E + 1], experts[kTB * k]
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *first = reinterpret_cast<int *>(mask + p.E);
     int *chosen = first + p.E + 1;
@@ -236,6 +237,8 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
 // A warp per expert: its counts per block become running sums, 8 blocks a lane.
 __global__ void __launch_bounds__(128) moe_scan_kernel(const RouteParams p)
 {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the blocks' counts
     const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (e >= p.E) return;
     int *c = p.counts + static_cast<int64_t>(e) * p.blocks;
@@ -267,10 +270,11 @@ __global__ void __launch_bounds__(kRouteThreads) moe_place_kernel(const RoutePar
 {
     extern __shared__ uint2 mask[];  // [E], then first[E + 1]
     int *first = reinterpret_cast<int *>(mask + p.E);
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-        mask[e] = make_uint2(0, 0);
-        first[e] = p.totals[e];
-    }
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = make_uint2(0, 0);
+    // the scan's sums; the choices come from the kernel before the scan, which the
+    // scan waited for
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) first[e] = p.totals[e];
     __syncthreads();
     if (threadIdx.x < 32) route_scan(first, p.E, [&](int e) { return first[e]; });
     __syncthreads();
@@ -320,6 +324,24 @@ static void launch_choose(const RouteParams &p, int smem, cudaStream_t stream)
         launch_choose_vpl<T, 32>(p, smem, stream);
 }
 
+static int launch_dependent(void (*kernel)(RouteParams), int blocks, int threads, int smem, const RouteParams &p,
+                            cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return kCudaError;
+    note_launch();
+    return kOk;
+}
+
 int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
 {
     RouteParams p{};
@@ -349,13 +371,13 @@ int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
     else
         launch_choose<__half>(p, smem, stream);
     note_launch();
+    int rc = kOk;
     if (p.blocks > 1) {
-        moe_scan_kernel<<<(c.E + 3) / 4, 128, 0, stream>>>(p);
-        note_launch();
-        moe_place_kernel<<<p.blocks, kRouteThreads, smem, stream>>>(p);
-        note_launch();
+        // both start while the kernel before them ends, and wait for it
+        rc = launch_dependent(moe_scan_kernel, (c.E + 3) / 4, 128, 0, p, stream);
+        if (rc == kOk) rc = launch_dependent(moe_place_kernel, p.blocks, kRouteThreads, smem, p, stream);
     }
-    int rc = cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+    if (cudaGetLastError() != cudaSuccess) rc = kCudaError;
     if (ws && workspace_free(ws, stream) != kOk) rc = kCudaError;
     return rc;
 }

@@ -75,11 +75,31 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float *y)
     return r;
 }
 
+// nv: the factor 1 / (s g) of every scale byte (0: all codes zero), made once per
+// block of threads; mx needs none.
+template <bool NV>
+struct Fp4Factors {
+    float of[NV ? 128 : 1];
+    __device__ void fill(float g)
+    {
+        if constexpr (NV) {
+            for (int s = threadIdx.x + threadIdx.y * blockDim.x; s < 128; s += blockDim.x * blockDim.y) {
+                // the byte's value: 2^(e - 7) (1 + f / 8), subnormals 2^-6 f / 8
+                const float v = s >= 8 ? __uint_as_float(((s >> 3) + 120u) << 23 | static_cast<uint32_t>(s & 7) << 20)
+                                       : static_cast<float>(s) * 0.001953125f;
+                const float t = v * g;
+                of[s] = t >= 1.17549435e-38f ? __frcp_rn(t) : 0.0f;
+            }
+            __syncthreads();
+        }
+    }
+};
+
 // The scale byte of a block whose largest magnitude is `amax` (bits: NaN sorts
 // above infinity) and the factor that takes its values to codes (0: all
-// codes zero).
+// codes zero).  g6: 6 g.
 template <bool NV>
-__device__ __forceinline__ uint8_t fp4_scale(uint32_t amax_bits, float g, float &factor)
+__device__ __forceinline__ uint8_t fp4_scale(uint32_t amax_bits, float g6, const Fp4Factors<NV> &factors, float &factor)
 {
     const bool fine = amax_bits < 0x7F800000u;
     factor = 0.0f;
@@ -97,16 +117,11 @@ __device__ __forceinline__ uint8_t fp4_scale(uint32_t amax_bits, float g, float 
         return static_cast<uint8_t>(e + 127);
     } else {
         if (!fine) return 0x7F;
-        const float q = fminf(__fdiv_rn(__uint_as_float(amax_bits), 6.0f * g), 448.0f);
+        const float q = fminf(__fdiv_rn(__uint_as_float(amax_bits), g6), 448.0f);
         uint16_t h;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.0f), "f"(q));
-        const uint8_t s = static_cast<uint8_t>(h & 0xFF);
-        // the byte's value: 2^(e - 7) (1 + f / 8), subnormals 2^-6 f / 8
-        const float v = s >= 8 ? __uint_as_float(((s >> 3) + 120u) << 23 | static_cast<uint32_t>(s & 7) << 20)
-                               : static_cast<float>(s) * 0.001953125f;
-        const float t = v * g;
-        if (t >= 1.17549435e-38f) factor = __frcp_rn(t);
-        return s;
+        factor = factors.of[h & 0x7F];
+        return static_cast<uint8_t>(h & 0xFF);
     }
 }
 
@@ -167,6 +182,9 @@ __global__ void __launch_bounds__(256, 6) pack_fp4_rows_kernel(const T *__restri
     const bool in_row = k < 2 * p.code_bytes;
     const bool last = k / 8 + 2 == p.code_bytes / 4;  // of the row: it writes the padding
     const float g = NV && p.g ? __ldg(p.g) : 1.0f;
+    __shared__ Fp4Factors<NV> factors;
+    factors.fill(g);
+    const float g6 = 6.0f * g;
     const int step = gridDim.x * blockDim.y;
     // rows as unsigned: the last step past 2^31 does not wrap
     uint32_t row = blockIdx.x * blockDim.y + threadIdx.y;
@@ -194,7 +212,7 @@ __global__ void __launch_bounds__(256, 6) pack_fp4_rows_kernel(const T *__restri
         if constexpr (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         if (!in_row || row >= rows) continue;
         float f;
-        const uint8_t s = fp4_scale<NV>(amax, g, f);
+        const uint8_t s = fp4_scale<NV>(amax, g6, factors, f);
         uint2 out = make_uint2(0, 0);
         if (amax < 0x7F800000u && f > 0.0f) {
 #pragma unroll
@@ -225,6 +243,10 @@ __global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__res
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 32;
     const int k0 = blockIdx.y * 256, k = k0 + 32 * warp;
     const bool live = r0 + lane < p.rows;
+    const float g = NV && p.g ? __ldg(p.g) : 1.0f;
+    __shared__ Fp4Factors<NV> factors;
+    factors.fill(g);
+    const float g6 = 6.0f * g;
     float v[32];
     const T *src = x + static_cast<int64_t>(k) * p.ld + r0 + lane;
     if (live && k + 32 <= p.K) {
@@ -237,7 +259,6 @@ __global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__res
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = live && k + i < p.K ? fp4_float(src[i * p.ld]) : 0.0f;
     }
-    const float g = NV && p.g ? __ldg(p.g) : 1.0f;
     uint32_t out[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int b = 0; b < kPerWarp; ++b) {
@@ -246,7 +267,7 @@ __global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__res
 #pragma unroll
         for (int i = 0; i < kBlock; ++i) amax = max(amax, __float_as_uint(v[b * kBlock + i]) & 0x7FFFFFFFu);
         float f;
-        scales[lane][warp * kPerWarp + b] = k + b * kBlock < p.K ? fp4_scale<NV>(amax, g, f) : 0;
+        scales[lane][warp * kPerWarp + b] = k + b * kBlock < p.K ? fp4_scale<NV>(amax, g6, factors, f) : 0;
         if (k + b * kBlock < p.K && amax < 0x7F800000u && f > 0.0f) {
 #pragma unroll
             for (int i = 0; i < kBlock; ++i) v[b * kBlock + i] *= f;
