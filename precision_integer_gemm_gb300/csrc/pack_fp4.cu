@@ -133,18 +133,44 @@ struct Fp4PackParams {
     int x_rows, rows, K, code_bytes, pitch;
 };
 
-// 16 values of one row from k (zeros past K), and the bits of the largest
-// magnitude: of pairs of 16-bit values as two 16-bit integers at a time.
+// 16 values of one row from k (zeros past K), as they lie in memory.
 template <class T, bool VEC>
-__device__ __forceinline__ uint32_t fp4_load16(const T *row, int k, int K, float (&v)[16])
-{
-    uint32_t amax = 0;
-    if (VEC && k + 16 <= K) {
-        constexpr int kWords = 4 * sizeof(T);
-        uint32_t w[kWords];
+struct Fp4Raw {
+    static constexpr int kWords = 4 * sizeof(T);
+    uint32_t w[kWords];
+    __device__ __forceinline__ void zero()
+    {
 #pragma unroll
-        for (int i = 0; i < kWords / 4; ++i)
-            *reinterpret_cast<uint4 *>(w + 4 * i) = __ldg(reinterpret_cast<const uint4 *>(row + k) + i);
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const T *row, int k, int K)
+    {
+        if (VEC && k + 16 <= K) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(row + k) + i);
+                w[4 * i] = q.x;
+                w[4 * i + 1] = q.y;
+                w[4 * i + 2] = q.z;
+                w[4 * i + 3] = q.w;
+            }
+        } else {
+            const auto bits = [&](int i) -> uint32_t {
+                if (k + i >= K) return 0;
+                if constexpr (sizeof(T) == 4) return __float_as_uint(row[k + i]);
+                else return reinterpret_cast<const uint16_t *>(row)[k + i];
+            };
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if constexpr (sizeof(T) == 4) w[i] = bits(i);
+                else w[i] = bits(2 * i) | bits(2 * i + 1) << 16;
+            }
+        }
+    }
+    // The values, and the bits of the largest magnitude: of 16-bit values as pairs.
+    __device__ __forceinline__ uint32_t unpack(float (&v)[16]) const
+    {
+        uint32_t amax = 0;
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -160,23 +186,18 @@ __device__ __forceinline__ uint32_t fp4_load16(const T *row, int k, int K, float
 #pragma unroll
             for (int i = 0; i < 8; ++i) fp4_floats<T>(w[i], v[2 * i], v[2 * i + 1]);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[i] = k + i < K ? fp4_float(row[k + i]) : 0.0f;
-            amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        }
+        return amax;
     }
-    return amax;
-}
+};
 
 // Row-major x: a thread per 16 k of a row (mx: two neighbouring lanes share a
 // block's scale), so a warp reads and writes contiguous runs.  A block of threads
 // is blockDim.x items (even) of blockDim.y rows; rows longer than that take
-// several (blockIdx.y), and a thread goes down the rows, its next row's index in
-// flight.  Issue-bound where x comes from L2 (gathered rows).
+// several (blockIdx.y), and a thread goes down the rows, the next row's values and
+// the index after that in flight.  Issue-bound where x comes from L2 (gathered
+// rows).
 template <bool NV, class T, bool VEC>
-__global__ void __launch_bounds__(256, 6) pack_fp4_rows_kernel(const T *__restrict__ x, const Fp4PackParams p)
+__global__ void __launch_bounds__(256, 5) pack_fp4_rows_kernel(const T *__restrict__ x, const Fp4PackParams p)
 {
     const int k = (blockIdx.y * blockDim.x + threadIdx.x) * 16;
     const bool in_row = k < 2 * p.code_bytes;
@@ -194,21 +215,22 @@ __global__ void __launch_bounds__(256, 6) pack_fp4_rows_kernel(const T *__restri
         const int s = p.index ? __ldg(p.index + r) : static_cast<int>(r);
         return s < p.x_rows ? s : -1;
     };
-    int src = source(row);
+    Fp4Raw<T, VEC> raw;
+    const auto load = [&](int src) {
+        if (src >= 0 && in_row) raw.load(x + src * p.ld, k, p.K);
+        else raw.zero();
+    };
+    load(source(row));
+    int src = source(row + step);
     uint8_t *codes = p.codes + static_cast<int64_t>(row) * p.code_bytes + k / 2;
     uint8_t *scales = p.scales + static_cast<int64_t>(row) * p.pitch;
     const int64_t code_step = static_cast<int64_t>(step) * p.code_bytes, scale_step = static_cast<int64_t>(step) * p.pitch;
     // (the same count for every lane of a warp)
     for (; row - threadIdx.y < rows; row += step, codes += code_step, scales += scale_step) {
         float v[16];
-        uint32_t amax = 0;
-        if (src >= 0 && in_row) {
-            amax = fp4_load16<T, VEC>(x + src * p.ld, k, p.K, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-        }
-        src = source(row + step);
+        uint32_t amax = raw.unpack(v);
+        load(src);
+        src = source(row + 2 * step);
         if constexpr (!NV) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         if (!in_row || row >= rows) continue;
         float f;
@@ -315,7 +337,7 @@ static int launch_pack_type(const Fp4PackCall &c, const Fp4PackParams &p, cudaSt
         const int by = std::max(1, 256 / bx);
         if (chunks > 65535) return kUnsupportedShape;
         // blocks that are resident at once, fewer where the rows give one each
-        const int64_t full = std::max<int64_t>(1, int64_t(sm_count()) * 6 * std::max(1, 256 / (bx * by)) / chunks);
+        const int64_t full = std::max<int64_t>(1, int64_t(sm_count()) * 5 * std::max(1, 256 / (bx * by)) / chunks);
         const int64_t gx = std::min((int64_t(c.rows) + by - 1) / by, full);
         const dim3 grid(static_cast<unsigned>(gx), chunks), block(bx, by);
         if (vec)
