@@ -122,8 +122,15 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     const GemmEvents ev = take_gemm_events();
     if (ev.start && cudaEventRecord(ev.start, stream) != cudaSuccess) return kCudaError;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     int na = 0;
+    // set up while the kernel before ends (with the timing events armed, the event
+    // between the two keeps them apart)
+    if (!ev.start) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
     if (csize > 1) {
         attr[na].id = cudaLaunchAttributeClusterDimension;
         attr[na].val.clusterDim.x = csize;

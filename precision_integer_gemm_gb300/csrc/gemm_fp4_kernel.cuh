@@ -376,6 +376,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     int *total_slot = reinterpret_cast<int *>(tmem_slot + 2);
     Fp4Group *groups = reinterpret_cast<Fp4Group *>(smem + ((prm.off_bars + 8 * Cfg::kNumBars + 64 + 15) & ~15));
 
+    // the next kernel may be set up on SMs that this one has left; it waits for the
+    // end of this grid before it touches memory
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int cs = PAIR ? 1 : prm.cs;
@@ -424,8 +427,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
     }
     if (warp == 0) {
-        // running tile counts of the groups
+        // running tile counts of the groups (the offsets may come from the kernel before)
         if (prm.offsets) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             int run = 0;
             for (int e0 = 0; e0 < prm.experts; e0 += 32) {
                 const int e = e0 + lane;
@@ -455,6 +459,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (csize > 1) cluster_sync_all();  // the other CTAs' barriers are initialised
+    // Up to here the kernel before this one in the stream may still run.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
     const int tiles = *total_slot;
     const Watchdog wd{abort_flag, prm.status, prm.limit_ns};

@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 #include "launch.cuh"
 #include "moe.cuh"
+#include "overlap.cuh"
 
 namespace igemm {
 
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
         T v[V];
     };
     extern __shared__ uint2 mask[];  // [E], then (one block) first[E + 1], experts[kTB * k]
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    overlap_begin();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *first = reinterpret_cast<int *>(mask + p.E);
     int *chosen = first + p.E + 1;
@@ -237,8 +238,7 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
 // A warp per expert: its counts per block become running sums, 8 blocks a lane.
 __global__ void __launch_bounds__(128) moe_scan_kernel(const RouteParams p)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the blocks' counts
+    overlap_begin();  // the blocks' counts
     const int e = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (e >= p.E) return;
     int *c = p.counts + static_cast<int64_t>(e) * p.blocks;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_place_kernel(const RoutePar
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = make_uint2(0, 0);
     // the scan's sums; the choices come from the kernel before the scan, which the
     // scan waited for
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    overlap_begin();
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) first[e] = p.totals[e];
     __syncthreads();
     if (threadIdx.x < 32) route_scan(first, p.E, [&](int e) { return first[e]; });
@@ -300,46 +300,22 @@ __global__ void __launch_bounds__(kRouteThreads) moe_place_kernel(const RoutePar
 }
 
 template <class T, int VPL>
-static void launch_choose_vpl(const RouteParams &p, int smem, cudaStream_t stream)
+static int launch_choose_vpl(const RouteParams &p, int smem, cudaStream_t stream)
 {
     constexpr int V = VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
-    if (p.E % V == 0 && reinterpret_cast<uintptr_t>(p.logits) % (V * sizeof(T)) == 0)
-        moe_choose_kernel<T, VPL, true><<<p.blocks, kChooseThreads, smem, stream>>>(p);
-    else
-        moe_choose_kernel<T, VPL, false><<<p.blocks, kChooseThreads, smem, stream>>>(p);
+    const bool vec = p.E % V == 0 && reinterpret_cast<uintptr_t>(p.logits) % (V * sizeof(T)) == 0;
+    return launch_overlapped(vec ? moe_choose_kernel<T, VPL, true> : moe_choose_kernel<T, VPL, false>, dim3(p.blocks),
+                             dim3(kChooseThreads), smem, stream, p);
 }
 
 template <class T>
-static void launch_choose(const RouteParams &p, int smem, cudaStream_t stream)
+static int launch_choose(const RouteParams &p, int smem, cudaStream_t stream)
 {
-    if (p.E <= 64)
-        launch_choose_vpl<T, 2>(p, smem, stream);
-    else if (p.E <= 128)
-        launch_choose_vpl<T, 4>(p, smem, stream);
-    else if (p.E <= 256)
-        launch_choose_vpl<T, 8>(p, smem, stream);
-    else if (p.E <= 512)
-        launch_choose_vpl<T, 16>(p, smem, stream);
-    else
-        launch_choose_vpl<T, 32>(p, smem, stream);
-}
-
-static int launch_dependent(void (*kernel)(RouteParams), int blocks, int threads, int smem, const RouteParams &p,
-                            cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(blocks, 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return kCudaError;
-    note_launch();
-    return kOk;
+    if (p.E <= 64) return launch_choose_vpl<T, 2>(p, smem, stream);
+    if (p.E <= 128) return launch_choose_vpl<T, 4>(p, smem, stream);
+    if (p.E <= 256) return launch_choose_vpl<T, 8>(p, smem, stream);
+    if (p.E <= 512) return launch_choose_vpl<T, 16>(p, smem, stream);
+    return launch_choose_vpl<T, 32>(p, smem, stream);
 }
 
 int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
@@ -364,20 +340,13 @@ int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
         p.totals = reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + counts);
     }
     const int smem = c.E * 8 + (c.E + 1) * 4 + (p.blocks > 1 ? 0 : kTB * c.k * 4);
-    if (c.x_type == 0)
-        launch_choose<float>(p, smem, stream);
-    else if (c.x_type == 1)
-        launch_choose<__nv_bfloat16>(p, smem, stream);
-    else
-        launch_choose<__half>(p, smem, stream);
-    note_launch();
-    int rc = kOk;
-    if (p.blocks > 1) {
-        // both start while the kernel before them ends, and wait for it
-        rc = launch_dependent(moe_scan_kernel, (c.E + 3) / 4, 128, 0, p, stream);
-        if (rc == kOk) rc = launch_dependent(moe_place_kernel, p.blocks, kRouteThreads, smem, p, stream);
-    }
-    if (cudaGetLastError() != cudaSuccess) rc = kCudaError;
+    int rc = c.x_type == 0   ? launch_choose<float>(p, smem, stream)
+             : c.x_type == 1 ? launch_choose<__nv_bfloat16>(p, smem, stream)
+                             : launch_choose<__half>(p, smem, stream);
+    if (rc == kOk && p.blocks > 1)
+        rc = launch_overlapped(moe_scan_kernel, dim3((c.E + 3) / 4), dim3(128), 0, stream, p);
+    if (rc == kOk && p.blocks > 1)
+        rc = launch_overlapped(moe_place_kernel, dim3(p.blocks), dim3(kRouteThreads), smem, stream, p);
     if (ws && workspace_free(ws, stream) != kOk) rc = kCudaError;
     return rc;
 }
@@ -394,6 +363,7 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const T *__restrict__ 
                                                           const float *__restrict__ weights, T *__restrict__ out,
                                                           int Tn, int k, int N)
 {
+    overlap_begin();
     const uint32_t per_row = static_cast<uint32_t>(N / PER);
     const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 128 + threadIdx.x;
     const int64_t t = static_cast<int64_t>(item / per_row);
@@ -447,12 +417,8 @@ static int launch_combine_type(const MoeCombineCall &c, cudaStream_t stream)
     const T *Y = static_cast<const T *>(c.Y);
     T *out = static_cast<T *>(c.out);
     const unsigned b = static_cast<unsigned>(blocks);
-    if (vec)
-        moe_combine_kernel<T, kPer><<<b, 128, 0, stream>>>(Y, c.slots, c.weights, out, c.T, c.k, c.N);
-    else
-        moe_combine_kernel<T, 1><<<b, 128, 0, stream>>>(Y, c.slots, c.weights, out, c.T, c.k, c.N);
-    note_launch();
-    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
+    return launch_overlapped(vec ? moe_combine_kernel<T, kPer> : moe_combine_kernel<T, 1>, dim3(b), dim3(128), 0,
+                             stream, Y, c.slots, c.weights, out, c.T, c.k, c.N);
 }
 
 int launch_moe_combine(const MoeCombineCall &c, cudaStream_t stream)

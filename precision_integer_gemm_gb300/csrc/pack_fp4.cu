@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 #include "launch.cuh"
 #include "fp4.cuh"
+#include "overlap.cuh"
 
 namespace igemm {
 
@@ -199,6 +200,7 @@ struct Fp4Raw {
 template <bool NV, class T, bool VEC>
 __global__ void __launch_bounds__(256, 5) pack_fp4_rows_kernel(const T *__restrict__ x, const Fp4PackParams p)
 {
+    overlap_begin();
     const int k = (blockIdx.y * blockDim.x + threadIdx.x) * 16;
     const bool in_row = k < 2 * p.code_bytes;
     const bool last = k / 8 + 2 == p.code_bytes / 4;  // of the row: it writes the padding
@@ -258,6 +260,7 @@ __global__ void __launch_bounds__(256, 5) pack_fp4_rows_kernel(const T *__restri
 template <bool NV, class T>
 __global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__restrict__ x, const Fp4PackParams p)
 {
+    overlap_begin();
     constexpr int kPerWarp = NV ? 2 : 1;  // scale bytes
     __shared__ uint4 codes[32][9];        // (row pitch 144 bytes: no bank conflicts)
     __shared__ uint8_t scales[32][16];
@@ -323,7 +326,8 @@ static int launch_pack_type(const Fp4PackCall &c, const Fp4PackParams &p, cudaSt
         const int64_t bx = (int64_t(c.rows) + 31) / 32;
         const int by = (c.K + 255) / 256;
         if (by > 65535) return kUnsupportedShape;
-        pack_fp4_transposed_kernel<NV, T><<<dim3(static_cast<unsigned>(bx), by), 256, 0, stream>>>(x, p);
+        return launch_overlapped(pack_fp4_transposed_kernel<NV, T>, dim3(static_cast<unsigned>(bx), by), dim3(256), 0,
+                                 stream, x, p);
     } else {
         // 16-byte loads where every row starts on 16 bytes
         const bool vec = (reinterpret_cast<uintptr_t>(x) % 16) == 0 && (c.ld * sizeof(T)) % 16 == 0;
@@ -340,13 +344,9 @@ static int launch_pack_type(const Fp4PackCall &c, const Fp4PackParams &p, cudaSt
         const int64_t full = std::max<int64_t>(1, int64_t(sm_count()) * 5 * std::max(1, 256 / (bx * by)) / chunks);
         const int64_t gx = std::min((int64_t(c.rows) + by - 1) / by, full);
         const dim3 grid(static_cast<unsigned>(gx), chunks), block(bx, by);
-        if (vec)
-            pack_fp4_rows_kernel<NV, T, true><<<grid, block, 0, stream>>>(x, p);
-        else
-            pack_fp4_rows_kernel<NV, T, false><<<grid, block, 0, stream>>>(x, p);
+        return launch_overlapped(vec ? pack_fp4_rows_kernel<NV, T, true> : pack_fp4_rows_kernel<NV, T, false>, grid,
+                                 block, 0, stream, x, p);
     }
-    note_launch();
-    return cudaGetLastError() == cudaSuccess ? kOk : kCudaError;
 }
 
 template <bool NV>

@@ -333,6 +333,46 @@ def test_operators_on_another_stream():
     check_product(C, values(codes, scales, "mx", 1024), b, 1024, "f32")
 
 
+def test_calls_back_to_back_see_each_other():
+    # each call reads what the call before it wrote and overwrites what the one before that read; nothing waits between
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    N = K = 512
+    B, SFB, _ = operand("mx", N, K, 3, 0.05)
+    for M in (4, 48, 300):
+        x0 = torch.randn((M, K), generator=gen, device="cuda")
+        codes = torch.empty((M, pig.fp4_code_bytes(K)), dtype=torch.uint8, device="cuda")
+        scales = torch.empty((M, pig.mxfp4_scale_pitch(K)), dtype=torch.uint8, device="cuda")
+
+        def chain(wait):
+            x, out = x0.clone(), []
+            for _ in range(40):
+                pig.pack_mxfp4(x, codes, scales, M, K)
+                wait()
+                pig.igemm_mxfp4(codes, B, scales, SFB, x, M, N, K)
+                wait()
+                out.append(x.clone())
+                wait()
+            torch.cuda.synchronize()
+            return out
+
+        for a, b in zip(chain(lambda: None), chain(torch.cuda.synchronize)):
+            assert torch.equal(a, b)
+
+
+def test_timing_events_around_a_product():
+    A, SFA, a = operand("nv", 8, 256, 1)
+    B, SFB, b = operand("nv", 64, 256, 2)
+    C = torch.empty((8, 64), device="cuda")
+    start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record(), stop.record()
+    before = pig.igemm_kernels_launched()
+    pig.igemm_time_next_gemm(start, stop)
+    pig.igemm_nvfp4(A, B, SFA, SFB, None, C, 8, 64, 256)
+    torch.cuda.synchronize()
+    assert pig.igemm_kernels_launched() == before + 1 and start.elapsed_time(stop) > 0
+    check_product(C, a, b, 256, "f32")
+
+
 # ---------------------------------------------------------------- grouped products
 
 def grouped(fmt, counts, N, K, typ, seed=0, alpha=None, rows=None, offsets=None):
