@@ -26,7 +26,9 @@
  * kernel is launched with programmatic stream serialization: its set-up and
  * the loads that do not depend on the pass run while the pass finishes, and it
  * waits for the pass (griddepcontrol.wait) before it reads or writes what the
- * pass touches.
+ * pass touches.  The kernels of the 4-bit floating-point and mixture-of-experts
+ * operators are launched that way behind whatever precedes them in the stream,
+ * and wait for its end before they touch memory.
  *
  * Operand formats
  *   Packed int4 matrix [rows, K/2] bytes, row-major: byte j of a row holds
@@ -69,9 +71,9 @@ extern "C" {
 typedef enum igemm_status {
     IGEMM_OK = 0,
     IGEMM_INVALID_ARGUMENT = 1,  /* null pointer for a non-empty operand, negative size */
-    IGEMM_UNSUPPORTED_SHAPE = 2, /* K % 32 != 0 (GEMM); odd K (pack_int4) */
-    IGEMM_MISALIGNED = 3,        /* a base address is not 16-byte aligned */
-    IGEMM_OVERFLOW_BOUND = 4,    /* K above the int32 bound (33554431 int4 x int4, 2097151 W4A8) */
+    IGEMM_UNSUPPORTED_SHAPE = 2, /* K % 32 != 0 (GEMM); odd K (pack_int4); the limits stated at the 4-bit operators */
+    IGEMM_MISALIGNED = 3,        /* a base address is not 16-byte aligned (4-bit operators: as stated there) */
+    IGEMM_OVERFLOW_BOUND = 4,    /* K above the int32 bound (33554431 int4 x int4, 2097151 W4A8) or IGEMM_FP4_MAX_K */
     IGEMM_CUDA_ERROR = 5,        /* tensor-map encoding, memset or launch failed */
     IGEMM_DEVICE_TIMEOUT = 6,    /* a kernel's bounded wait expired (see igemm_last_status) */
     IGEMM_WORKSPACE_LIMIT = 7    /* i4i4_gemm_noalloc: the problem needs more than its fixed workspace */
@@ -272,7 +274,8 @@ IGEMM_API int pack_int4(const int8_t *logical, uint8_t *packed, int64_t rows, in
  * devices and streams; a launch counts when it was enqueued).  One GEMM call
  * launches one kernel, or two: the preparation pass and the GEMM (prepared
  * codes), the zeroing of C and the GEMM (skinny shapes whose K slices are
- * summed with atomics), the scale transpose and the GEMM (block-scaled fp8).
+ * summed with atomics), the scale transpose and the GEMM (block-scaled fp8);
+ * a 4-bit operator one, igemm_moe_route of more than 64 tokens three.
  * The split K of the other paths adds a memset, which is not a kernel.
  */
 IGEMM_API uint64_t igemm_kernels_launched(void);

@@ -517,9 +517,14 @@ extern "C" const char *igemm_strerror(int code)
     case kInvalidArgument: return "invalid argument (null pointer for a non-empty operand, or a negative size)";
     case kUnsupportedShape:
         return "unsupported shape (integer GEMMs: K must be a multiple of 32; fp8_gemm: of 16; pack_int4 and "
-               "unpack_int4: K must be even)";
-    case kMisaligned: return "misaligned pointer (operand and C base addresses must be 16-byte aligned)";
-    case kOverflowBound: return "K above the int32 bound of the result (33554431 int4 x int4, 2097151 W4A8)";
+               "unpack_int4: K must be even; 4-bit floating point: the limits of igemm.h on experts, choices and rows, "
+               "and no gathered rows of a transposed matrix)";
+    case kMisaligned:
+        return "misaligned pointer (operand and C base addresses must be 16-byte aligned; 4-bit floating point: codes "
+               "and scales, other arrays naturally)";
+    case kOverflowBound:
+        return "K above the int32 bound of the result (33554431 int4 x int4, 2097151 W4A8) or above 4194304 (4-bit "
+               "floating point)";
     case kCudaError: return "CUDA error (tensor-map encoding, memset, launch or synchronization failed)";
     case kDeviceTimeout: return "device timeout (a kernel's bounded pipeline wait expired; its output is not valid)";
     case kWorkspaceLimit:

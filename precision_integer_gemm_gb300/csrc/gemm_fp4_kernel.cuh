@@ -183,11 +183,16 @@ __device__ __forceinline__ bool fp4_warp_wait_cluster(uint64_t *bar, uint32_t pa
     return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void fp4_wait_drain(uint64_t *bar, uint32_t parity, unsigned long long limit_ns)
+// Waits for the last phase of the ring slots in `issued` (their parities in `last`),
+// all within one limit: at the end of a kernel that may have given up.
+__device__ __forceinline__ void fp4_drain(uint64_t *bars, uint32_t issued, uint32_t last, uint64_t t0,
+                                          unsigned long long limit_ns)
 {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < limit_ns) {
-    }
+#pragma unroll 1
+    for (int s = 0; issued >> s; ++s)
+        if ((issued >> s) & 1u)
+            while (!mbar_try_wait(&bars[s], (last >> s) & 1u) && globaltimer_ns() - t0 < limit_ns) {
+            }
 }
 
 // Ring position: slot and phase parity, without divisions.
@@ -512,12 +517,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             }
         }
         // never leave with copies in flight, nor with an MMA commit on its way here
-#pragma unroll 1
-        for (int s = 0; s < prm.code_stages; ++s)
-            if ((issued >> s) & 1u) {
-                if (leader) fp4_wait_drain(&full[s], (last >> s) & 1u, prm.limit_ns);
-                fp4_wait_drain(&empty[s], (last >> s) & 1u, prm.limit_ns);
-            }
+        const uint64_t t0 = globaltimer_ns();
+        if (leader) fp4_drain(full, issued, last, t0, prm.limit_ns);
+        fp4_drain(empty, issued, last, t0, prm.limit_ns);
     } else if (warp == Cfg::kWarpLoadS) {
         // ------------------------------------------------------------ scale rows
         Fp4Ring sr(prm.scale_stages);
@@ -550,12 +552,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 sr.next();
             }
         }
-#pragma unroll 1
-        for (int s = 0; s < prm.scale_stages; ++s)
-            if ((issued >> s) & 1u) {
-                fp4_wait_drain(&sf_raw[s], (last >> s) & 1u, prm.limit_ns);
-                fp4_wait_drain(&sf_empty[s], (last >> s) & 1u, prm.limit_ns);
-            }
+        const uint64_t t0 = globaltimer_ns();
+        fp4_drain(sf_raw, issued, last, t0, prm.limit_ns);
+        fp4_drain(sf_empty, issued, last, t0, prm.limit_ns);
     } else if (warp == Cfg::kWarpMma) {
         // ------------------------------------------------------------ MMA issuer
         if (leader) {
@@ -793,7 +792,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == Cfg::kWarpMma) {
-        if (leader && lane == 0) fp4_wait_drain(mma_drain, 0, prm.limit_ns);
+        if (leader && lane == 0) fp4_drain(mma_drain, 1u, 0u, globaltimer_ns(), prm.limit_ns);
         __syncwarp();
     }
     // no CTA of a cluster frees TMEM or leaves while another may still reach it
