@@ -356,77 +356,106 @@ __device__ __forceinline__ void moe_out(float *o, float v) { *o = v; }
 __device__ __forceinline__ void moe_out(__nv_bfloat16 *o, float v) { *o = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void moe_out(__half *o, float v) { *o = __float2half_rn(v); }
 
-// A thread per PER columns of a token (16 bytes, or one column where rows are not
-// 16-byte aligned), four rows in flight; float32 sums in the order of the choices.
+// PER values as one load or store.
 template <class T, int PER>
+struct alignas(PER * sizeof(T)) MoeRun {
+    T v[PER];
+};
+
+// A thread per RUNS runs of PER columns of a token, four rows in flight; float32 sums
+// in the order of the choices.  Rows of whole 16- or 8-byte runs: one run, threads
+// laid over tokens and columns alike (4096 tokens x 8 bfloat16 rows of 4096: 48 us,
+// 0.93 of the copy rate).  Other rows: a block of threads per token and 128 RUNS PER
+// columns, so that the choices are read once for several narrow loads (rows of
+// 4095: 147 -> 72 us; of 4092, in 8-byte runs, that form took 66 us against 53).
+template <class T, int PER, int RUNS>
 __global__ void __launch_bounds__(128) moe_combine_kernel(const T *__restrict__ Y, const int *__restrict__ slots,
                                                           const float *__restrict__ weights, T *__restrict__ out,
                                                           int Tn, int k, int N)
 {
+    using Run = MoeRun<T, PER>;
     overlap_begin();
-    const uint32_t per_row = static_cast<uint32_t>(N / PER);
-    const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 128 + threadIdx.x;
-    const int64_t t = static_cast<int64_t>(item / per_row);
-    if (t >= Tn) return;
-    const int n = static_cast<int>(item - static_cast<uint64_t>(t) * per_row) * PER;
+    int64_t t;
+    int n;
+    if constexpr (RUNS == 1) {
+        const uint32_t per_row = static_cast<uint32_t>(N / PER);
+        const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 128 + threadIdx.x;
+        t = static_cast<int64_t>(item / per_row);
+        if (t >= Tn) return;
+        n = static_cast<int>(item - static_cast<uint64_t>(t) * per_row) * PER;
+    } else {
+        const uint32_t chunks = static_cast<uint32_t>((N + 128 * RUNS * PER - 1) / (128 * RUNS * PER));
+        t = blockIdx.x / chunks;
+        n = static_cast<int>(blockIdx.x - static_cast<uint32_t>(t) * chunks) * (128 * RUNS * PER) + threadIdx.x * PER;
+    }
     const int64_t rows = static_cast<int64_t>(Tn) * k;
-    float acc[PER];
+    float acc[RUNS][PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
+    for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[r][i] = 0.0f;
     for (int j0 = 0; j0 < k; j0 += 4) {
-        alignas(16) T v[4][PER];
+        Run v[4][RUNS];
         float w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t at = t * k + j0 + j;
             const int64_t s = j0 + j < k ? __ldg(slots + at) : -1;
-            w[j] = 0.0f;
+            const bool live = s >= 0 && s < rows;
+            w[j] = live ? __ldg(weights + at) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) v[j][i] = T(0.0f);
-            if (s >= 0 && s < rows) {
-                w[j] = __ldg(weights + at);
-                if constexpr (PER > 1)
-                    *reinterpret_cast<uint4 *>(v[j]) = __ldcs(reinterpret_cast<const uint4 *>(Y + s * N + n));
-                else
-                    v[j][0] = Y[s * N + n];
+            for (int r = 0; r < RUNS; ++r) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) v[j][r].v[i] = T(0.0f);
+                const int nr = n + r * (128 * PER);
+                if (live && nr < N) {
+                    const T *from = Y + s * N + nr;
+                    if constexpr (sizeof(Run) == 16)
+                        *reinterpret_cast<uint4 *>(&v[j][r]) = __ldcs(reinterpret_cast<const uint4 *>(from));
+                    else
+                        v[j][r] = *reinterpret_cast<const Run *>(from);
+                }
             }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < PER; ++i) acc[i] = fmaf(w[j], moe_float(v[j][i]), acc[i]);
-    }
-    alignas(16) T o[PER];
+            for (int r = 0; r < RUNS; ++r)
 #pragma unroll
-    for (int i = 0; i < PER; ++i) moe_out(&o[i], acc[i]);
-    if constexpr (PER > 1)
-        *reinterpret_cast<uint4 *>(out + t * N + n) = *reinterpret_cast<const uint4 *>(o);
-    else
-        out[t * N + n] = o[0];
+                for (int i = 0; i < PER; ++i) acc[r][i] = fmaf(w[j], moe_float(v[j][r].v[i]), acc[r][i]);
+    }
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+        const int nr = n + r * (128 * PER);
+        if (nr >= N) break;
+        Run o;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) moe_out(&o.v[i], acc[r][i]);
+        *reinterpret_cast<Run *>(out + t * N + nr) = o;
+    }
 }
 
-template <class T>
-static int launch_combine_type(const MoeCombineCall &c, cudaStream_t stream)
+template <class T, int PER>
+static int launch_combine_per(const MoeCombineCall &c, cudaStream_t stream)
 {
-    constexpr int kPer = 16 / sizeof(T);
-    const bool vec = (reinterpret_cast<uintptr_t>(c.Y) % 16) == 0 && (reinterpret_cast<uintptr_t>(c.out) % 16) == 0 &&
-                     c.N % kPer == 0;
-    const int64_t items = int64_t(c.T) * (c.N / (vec ? kPer : 1));
-    const int64_t blocks = (items + 127) / 128;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(c.Y) | reinterpret_cast<uintptr_t>(c.out);
+    if constexpr (PER > 1)
+        if (at % (PER * sizeof(T)) != 0 || c.N % PER != 0) return launch_combine_per<T, PER / 2>(c, stream);
+    constexpr int kRuns = PER * sizeof(T) >= 8 ? 1 : 4;
+    const int64_t chunk = int64_t(128) * kRuns * PER;
+    const int64_t blocks = kRuns == 1 ? (int64_t(c.T) * (c.N / PER) + 127) / 128 : c.T * ((c.N + chunk - 1) / chunk);
     if (blocks > 0x7FFFFFFF) return kUnsupportedShape;
-    const T *Y = static_cast<const T *>(c.Y);
-    T *out = static_cast<T *>(c.out);
-    const unsigned b = static_cast<unsigned>(blocks);
-    return launch_overlapped(vec ? moe_combine_kernel<T, kPer> : moe_combine_kernel<T, 1>, dim3(b), dim3(128), 0,
-                             stream, Y, c.slots, c.weights, out, c.T, c.k, c.N);
+    return launch_overlapped(moe_combine_kernel<T, PER, kRuns>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0,
+                             stream, static_cast<const T *>(c.Y), c.slots, c.weights, static_cast<T *>(c.out), c.T, c.k,
+                             c.N);
 }
 
 int launch_moe_combine(const MoeCombineCall &c, cudaStream_t stream)
 {
     switch (c.x_type) {
-    case 0: return launch_combine_type<float>(c, stream);
-    case 1: return launch_combine_type<__nv_bfloat16>(c, stream);
-    default: return launch_combine_type<__half>(c, stream);
+    case 0: return launch_combine_per<float, 4>(c, stream);
+    case 1: return launch_combine_per<__nv_bfloat16, 8>(c, stream);
+    default: return launch_combine_per<__half, 8>(c, stream);
     }
 }
 
