@@ -168,6 +168,19 @@ def test_pack_strided_and_unaligned_rows(fmt, typ):
         same_bytes(gpu_pack(x, fmt), plain_pack(x.double().cpu().numpy(), fmt))
 
 
+@pytest.mark.parametrize("typ", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_pack_from_every_start(typ, transposed):
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    buf = torch.randn(4096, generator=gen, device="cuda").to(TYPES[typ])
+    buf[0] = buf[-1] = math.nan  # (outside of what the views hold)
+    for start in range(1, 10):
+        for rows, K, ld in ((1, 47, 47), (5, 96, 96), (5, 100, 101), (7, 129, 130), (3, 260, 263)):
+            shape, strides = ((rows, K), (ld, 1)) if not transposed else ((K // 8, rows), (1, ld))
+            x = buf.as_strided(shape, strides, start)
+            same_bytes(gpu_pack(x, "mx"), plain_pack(x.double().cpu().numpy(), "mx"))
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_pack_special_values(fmt):
     x = np.zeros((16, 64), np.float32)
