@@ -536,6 +536,23 @@ def test_route_ties_masks_and_specials(typ, T, E):
             check_route(x, k, normalize)
 
 
+@pytest.mark.parametrize("typ", ["bf16", "f16"])
+@pytest.mark.parametrize("T,E,k", [(65, 5, 3), (127, 40, 8), (67, 64, 1), (66, 66, 7), (129, 128, 2), (190, 201, 8),
+                                   (259, 256, 5)])
+def test_route_of_several_blocks(typ, T, E, k):
+    gen = torch.Generator(device="cuda").manual_seed(T * E)
+    for scale in (1, 200):                         # ties everywhere, and hardly any
+        x = (torch.randint(-2 * scale, 2 * scale + 1, (T, E), generator=gen, device="cuda") / scale).to(TYPES[typ])
+        x[torch.rand((T, E), generator=gen, device="cuda") < 0.2] = -math.inf
+        x[torch.rand((T, E), generator=gen, device="cuda") < 0.05] = math.nan
+        x[-1] = -math.inf
+        x[-2] = math.nan
+        x[-3, 1:] = -math.inf
+        x[-3, 0] = torch.finfo(TYPES[typ]).min
+        for normalize in (True, False):
+            check_route(x, k, normalize)
+
+
 def test_route_infinite_logit_gives_nan_weights():
     x = torch.zeros((2, 8), device="cuda")
     x[0, 3] = math.inf
