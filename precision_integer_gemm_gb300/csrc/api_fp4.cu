@@ -51,7 +51,7 @@ static int gemm_checked(const Fp4Call &c, bool grouped, cudaStream_t stream)
     if (c.experts > kFp4MaxExperts || int64_t(c.experts) * c.N > 0x7FFFFFFF - 512 || c.rows > 0x7FFFFFFF - 512)
         return kUnsupportedShape;
     // tile numbers stay within int (tiles of 16 rows by 128 columns)
-    if ((int64_t(c.rows) / 16 + c.experts) * ((int64_t(c.N) + 127) / 128) > 0x3FFFFFFF) return kUnsupportedShape;
+    if ((int64_t(c.rows) / 16 + c.experts) * ((int64_t(c.N) + 127) / 128) > kFp4MaxTiles) return kUnsupportedShape;
     if (c.K > IGEMM_FP4_MAX_K) return kOverflowBound;
     if (!aligned(c.C, type_bytes(c.c_type)) || !aligned(c.alpha, 4) || !aligned(c.offsets, 4)) return kMisaligned;
     if (c.K == 0) {

@@ -42,6 +42,7 @@
 namespace igemm {
 
 constexpr int kFp4MaxExperts = 1024;
+constexpr int kFp4MaxTiles = 0x3FFFFFFF;  // of one call
 
 enum Fp4OutType : int { kOutF32 = 0, kOutBf16 = 1, kOutF16 = 2 };
 
@@ -435,6 +436,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         // running tile counts of the groups (the offsets may come from the kernel before)
         if (prm.offsets) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
+            // (groups that overlap against the rules could have more tiles than an int
+            // holds: those past kFp4MaxTiles are left out)
             int run = 0;
             for (int e0 = 0; e0 < prm.experts; e0 += 32) {
                 const int e = e0 + lane;
@@ -444,16 +447,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                     g.z = min(max(__ldg(prm.offsets + e + 1), g.y), prm.rows) - g.y;
                     g.w = (g.z + prm.qt - 1) / prm.qt;
                 }
-                const int tiles = g.w * prm.p_tiles;
+                const int tiles = g.w * prm.p_tiles;  // at most kFp4MaxTiles
                 int incl = tiles;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const int o = __shfl_up_sync(0xffffffffu, incl, d);
-                    if (lane >= d) incl += o;
+                    if (lane >= d) incl = min(incl + o, kFp4MaxTiles);
                 }
-                g.x = run + incl - tiles;
+                const int before = __shfl_up_sync(0xffffffffu, incl, 1);
+                g.x = min(run + (lane > 0 ? before : 0), kFp4MaxTiles);
                 if (e < prm.experts) groups[e] = g;
-                run += __shfl_sync(0xffffffffu, incl, 31);
+                run = min(run + __shfl_sync(0xffffffffu, incl, 31), kFp4MaxTiles);
             }
             if (lane == 0) *total_slot = run;
         } else if (lane == 0) {

@@ -372,6 +372,42 @@ def test_calls_back_to_back_see_each_other():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T", [7, 200])
+def test_layer_in_a_graph(T):
+    # routing, gathered packing, a grouped product and the sum, captured once and replayed on new values
+    E, k, N, K = 16, 4, 256, 512
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    logits, x = torch.empty((T, E), device="cuda"), torch.empty((T, K), device="cuda")
+    b, sb, _ = operand("mx", E * N, K, 3)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    experts, weights, slots = torch.empty((T, k), **i32), torch.empty((T, k), device="cuda"), torch.empty((T, k), **i32)
+    offsets, tokens = torch.empty(E + 1, **i32), torch.empty(T * k, **i32)
+    a = torch.empty((T * k, pig.fp4_code_bytes(K)), dtype=torch.uint8, device="cuda")
+    sa = torch.empty((T * k, pig.mxfp4_scale_pitch(K)), dtype=torch.uint8, device="cuda")
+    y, out = torch.empty((T * k, N), device="cuda"), torch.empty((T, N), device="cuda")
+
+    def layer():
+        pig.igemm_moe_route(logits, experts, weights, offsets, tokens, slots, T, E, k)
+        pig.pack_mxfp4(x, a, sa, T * k, K, index=tokens)
+        pig.igemm_mxfp4_grouped(a, b, sa, sb, offsets, y, T * k, E, N, K)
+        pig.igemm_moe_combine(y, slots, weights, out, T, k, N)
+
+    logits.normal_(generator=gen), x.normal_(generator=gen)
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    for _ in range(3):
+        logits.normal_(generator=gen), x.normal_(generator=gen)
+        out.fill_(math.nan)
+        graph.replay()
+        got = out.clone()
+        layer()
+        assert bool(torch.isfinite(got).all()) and torch.equal(got, out)
+    assert pig.igemm_last_status() == 0
+
+
 def test_timing_events_around_a_product():
     A, SFA, a = operand("nv", 8, 256, 1)
     B, SFB, b = operand("nv", 64, 256, 2)
