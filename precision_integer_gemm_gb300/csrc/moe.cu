@@ -8,8 +8,10 @@
 // reduction for the lowest expert that holds the value.  A token chooses an expert
 // at most once, so the tokens of a block of kTB that chose expert e are one bit
 // mask, and a pair's place among its expert's is the number of bits below its
-// own: the sort is stable and needs no ordered atomics.  One block does the whole
-// job for up to kTB tokens; more tokens take three launches (choice and counts
+// own: the sort is stable and needs no ordered atomics.  A cluster of up to 8 blocks
+// does the whole job for up to 512 tokens, its blocks reading each other's masks in
+// shared memory (calls of 128 x 256 bfloat16, 8 choices: 12.2 us in three launches
+// and a workspace, 7.6 in one); more tokens take three launches (choice and counts
 // per block, a scan over the blocks per expert, places), and 16-bit logits of up to
 // 256 experts then go four tokens to a warp (moe_choose4_kernel).  Bound by
 // instructions and by the launches: 17.5 us at 16384 x 256 bfloat16, 8 choices, whose
@@ -23,11 +25,16 @@
 #include "launch.cuh"
 #include "moe.cuh"
 #include "overlap.cuh"
+#include "ptx.cuh"
 
 namespace igemm {
 
-constexpr int kTB = 64;           // tokens per block: two mask words
-constexpr int kMaxExperts = 1024;
+constexpr int kTB = 64;           // most tokens per block: two mask words
+// blocks that one cluster can hold; up to so many do the whole job in one launch
+constexpr int kClusterBlocks = 8;
+// a block of one cluster takes as many tokens at least (64 x 1024 float32, 8 choices:
+// 14.8 us against 28.9 in one block of 64; 16 x 64: 6.1 us with 16 or more, 6.9 with 8)
+constexpr int kFewTokens = 16;
 constexpr int kRouteThreads = 512;
 constexpr int kChooseThreads = 1024;
 constexpr int kChoose4Threads = 32 * kTB / 4;
@@ -41,9 +48,10 @@ struct RouteParams {
     int *experts;
     float *weights;
     int *offsets, *tokens, *slots;
-    int *counts;  // [E][blocks], then exclusive prefixes; null when one block does it all
+    int *counts;  // [E][blocks], then exclusive prefixes; null when one cluster does it all
     int *totals;  // [E]
     int T, E, k, blocks;
+    int tb;       // tokens per block
     int normalize;
 };
 
@@ -94,8 +102,8 @@ __device__ __forceinline__ void route_scan(int *first, int E, F count)
 __device__ __forceinline__ void route_place(const RouteParams &p, const uint2 *mask, const int *first,
                                             const int *experts)
 {
-    const int t0 = blockIdx.x * kTB;
-    const int n = min(kTB, p.T - t0) * p.k;
+    const int t0 = blockIdx.x * p.tb;
+    const int n = min(p.tb, p.T - t0) * p.k;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         const int e = experts[i], t = i / p.k;
         int pos = -1;
@@ -109,7 +117,7 @@ __device__ __forceinline__ void route_place(const RouteParams &p, const uint2 *m
     }
 }
 
-// Choice and weights of kTB tokens; their masks; one block: everything.
+// Choice and weights of a block's tokens; their masks; one cluster: everything.
 // VPL: logits per lane (E <= 32 VPL); VEC: lane's logits in runs of V (16 bytes at
 // most), loaded together.
 template <class T, int VPL, bool VEC>
@@ -120,15 +128,16 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
     struct alignas(V * sizeof(T)) Run {
         T v[V];
     };
-    extern __shared__ uint2 mask[];  // [E], then (one block) first[E + 1], experts[kTB * k]
+    extern __shared__ uint2 mask[];  // [E], then (one cluster) first[E + 1], start[E], experts[kTB * k]
     overlap_begin();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *first = reinterpret_cast<int *>(mask + p.E);
-    int *chosen = first + p.E + 1;
+    int *start = first + p.E + 1;
+    int *chosen = start + p.E;
     for (int e = threadIdx.x; e < p.E; e += kChooseThreads) mask[e] = make_uint2(0, 0);
     __syncthreads();
-    const int t0 = blockIdx.x * kTB;
-    for (int i = warp; i < kTB && t0 + i < p.T; i += kChooseThreads / 32) {
+    const int t0 = blockIdx.x * p.tb;
+    for (int i = warp; i < p.tb && t0 + i < p.T; i += kChooseThreads / 32) {
         const int64_t t = t0 + i;
         const T *row = static_cast<const T *>(p.logits) + t * p.E;
         uint32_t key[VPL];  // of expert 32 V (j / V) + V lane + j % V
@@ -232,11 +241,32 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
             p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = __popc(mask[e].x) + __popc(mask[e].y);
         return;
     }
-    if (warp == 0) route_scan(first, p.E, [&](int e) { return __popc(mask[e].x) + __popc(mask[e].y); });
+    // the pairs of each expert in every block and in those before this one
+    const int blocks = gridDim.x;
+    if (blocks > 1) cluster_sync_all();
+    for (int e = threadIdx.x; e < p.E; e += kChooseThreads) {
+        const uint32_t at = smem_u32(mask + e);
+        int all = 0, below = 0;
+        for (int b = 0; b < blocks; ++b) {
+            const uint2 m = blocks > 1 ? ld_cluster_v2(cluster_map(at, b)) : mask[e];
+            const int n = __popc(m.x) + __popc(m.y);
+            all += n;
+            below += b < static_cast<int>(blockIdx.x) ? n : 0;
+        }
+        first[e] = all;
+        start[e] = below;
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e <= p.E; e += kChooseThreads) p.offsets[e] = first[e];
-    for (int i = first[p.E] + threadIdx.x; i < p.T * p.k; i += kChooseThreads) p.tokens[i] = -1;
-    route_place(p, mask, first, chosen);
+    if (warp == 0) route_scan(first, p.E, [&](int e) { return first[e]; });
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kChooseThreads) start[e] += first[e];
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= p.E; e += kChooseThreads) p.offsets[e] = first[e];
+    for (int i = first[p.E] + blockIdx.x * kChooseThreads + threadIdx.x; i < p.T * p.k; i += blocks * kChooseThreads)
+        p.tokens[i] = -1;
+    __syncthreads();
+    route_place(p, mask, start, chosen);
+    if (blocks > 1) cluster_sync_all();  // no block leaves while another may read its masks
 }
 
 // The larger eight of a descending list and one in ascending places, in descending
@@ -277,7 +307,7 @@ __global__ void __launch_bounds__(kChoose4Threads) moe_choose4_kernel(const Rout
     for (int e = threadIdx.x; e < p.E; e += kChoose4Threads) mask[e] = make_uint2(0, 0);
     __syncthreads();
     const int i0 = 4 * warp;  // within the block
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTB + i0;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTB + i0;  // (many tokens: p.tb is kTB)
     Run run[4][VPL / V];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -453,11 +483,14 @@ static int launch_choose_vpl(const RouteParams &p, int smem, cudaStream_t stream
     // (routing of 16384 x 256 bfloat16, 8 choices: 21.7 -> 17.5 us; 65536 x 128: 41.5 ->
     // 29.8; no case was slower)
     if constexpr (sizeof(T) == 2 && VPL <= 8)
-        if (p.blocks > 1 && p.k <= 8)
+        if (p.counts && p.k <= 8)
             return launch_overlapped(vec ? moe_choose4_kernel<T, VPL, true> : moe_choose4_kernel<T, VPL, false>,
                                      dim3(p.blocks), dim3(kChoose4Threads), smem, stream, p);
-    return launch_overlapped(vec ? moe_choose_kernel<T, VPL, true> : moe_choose_kernel<T, VPL, false>, dim3(p.blocks),
-                             dim3(kChooseThreads), smem, stream, p);
+    const auto kernel = vec ? moe_choose_kernel<T, VPL, true> : moe_choose_kernel<T, VPL, false>;
+    if (p.counts) return launch_overlapped(kernel, dim3(p.blocks), dim3(kChooseThreads), smem, stream, p);
+    int cluster = 1;
+    while (cluster < p.blocks) cluster *= 2;  // (blocks without tokens fill it up)
+    return launch_overlapped_clusters(kernel, dim3(cluster), cluster, dim3(kChooseThreads), smem, stream, p);
 }
 
 template <class T>
@@ -483,21 +516,24 @@ int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
     p.E = c.E;
     p.k = c.k;
     p.normalize = c.normalize ? 1 : 0;
-    p.blocks = (c.T + kTB - 1) / kTB;
+    // up to 512 tokens spread over the blocks of a cluster
+    const bool one = c.T <= kClusterBlocks * kTB;
+    p.tb = one ? std::max(kFewTokens, (c.T + kClusterBlocks - 1) / kClusterBlocks) : kTB;
+    p.blocks = (c.T + p.tb - 1) / p.tb;
     void *ws = nullptr;
-    if (p.blocks > 1) {
+    if (!one) {
         const size_t counts = size_t(c.E) * p.blocks * 4;
         if (workspace_alloc(&ws, counts + size_t(c.E) * 4, stream) != kOk) return kCudaError;
         p.counts = static_cast<int *>(ws);
         p.totals = reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + counts);
     }
-    const int smem = c.E * 8 + (c.E + 1) * 4 + (p.blocks > 1 ? 0 : kTB * c.k * 4);
+    const int smem = c.E * 8 + (c.E + 1) * 4 + (one ? c.E * 4 + kTB * c.k * 4 : 0);
     int rc = c.x_type == 0   ? launch_choose<float>(p, smem, stream)
              : c.x_type == 1 ? launch_choose<__nv_bfloat16>(p, smem, stream)
                              : launch_choose<__half>(p, smem, stream);
-    if (rc == kOk && p.blocks > 1)
+    if (rc == kOk && !one)
         rc = launch_overlapped(moe_scan_kernel, dim3((c.E + 3) / 4), dim3(128), 0, stream, p);
-    if (rc == kOk && p.blocks > 1)
+    if (rc == kOk && !one)
         rc = launch_overlapped(moe_place_kernel, dim3(p.blocks), dim3(kRouteThreads), smem, stream, p);
     if (ws && workspace_free(ws, stream) != kOk) rc = kCudaError;
     return rc;

@@ -231,6 +231,14 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
+// Two words of another CTA of the cluster.
+__device__ __forceinline__ uint2 ld_cluster_v2(uint32_t cluster_addr)
+{
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // 16 bytes into another CTA of the cluster; they count on that CTA's mbarrier
 // `bar_cluster` when they have landed.
 __device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, const uint32_t *v, uint32_t bar_cluster)

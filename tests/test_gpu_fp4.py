@@ -574,7 +574,8 @@ def test_route_ties_masks_and_specials(typ, T, E):
 
 @pytest.mark.parametrize("typ", ["bf16", "f16"])
 @pytest.mark.parametrize("T,E,k", [(65, 5, 3), (127, 40, 8), (67, 64, 1), (66, 66, 7), (129, 128, 2), (190, 201, 8),
-                                   (259, 256, 5)])
+                                   (259, 256, 5), (512, 30, 8), (513, 5, 3), (600, 40, 8), (530, 64, 1), (1025, 66, 7),
+                                   (700, 128, 2), (514, 201, 8), (777, 256, 5)])
 def test_route_of_several_blocks(typ, T, E, k):
     gen = torch.Generator(device="cuda").manual_seed(T * E)
     for scale in (1, 200):                         # ties everywhere, and hardly any
