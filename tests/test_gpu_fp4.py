@@ -217,6 +217,24 @@ def test_pack_gathers_rows(fmt, typ):
     same_bytes(gpu_pack(x, fmt, rows=10, index=index), plain_pack(want, fmt))
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("typ,rows,source,K", [("f32", 17000, 100, 515), ("bf16", 8400, 4200, 4096),
+                                               ("f16", 140001, 7, 130)])
+def test_pack_gathers_rows_many_times(fmt, typ, rows, source, K):
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn((source, K + 3), generator=gen, device="cuda").to(TYPES[typ])[:, :K]
+    x[source // 2, 5] = math.nan
+    index = torch.randint(-2, source + 2, (rows,), generator=gen, device="cuda").int()  # some out of range
+    index[:3] = torch.tensor([-2 ** 31, 2 ** 31 - 1, source], dtype=torch.int32)
+    g = torch.tensor([0.0031], device="cuda") if fmt == "nv" else None
+    codes, scales = plain_pack(x.double().cpu().numpy(), fmt, 0.0031)
+    at = index.cpu().numpy()
+    out = (at < 0) | (at >= source)
+    at = np.where(out, 0, at)
+    want = [np.where(out[:, None], 0, a[at]) for a in (codes, scales)]
+    same_bytes(gpu_pack(x, fmt, rows=rows, index=index, g=g), want)
+
+
 def test_pack_refuses_what_it_cannot_read():
     x = torch.zeros((8, 64), device="cuda")
     c = torch.zeros((8, 32), dtype=torch.uint8, device="cuda")
