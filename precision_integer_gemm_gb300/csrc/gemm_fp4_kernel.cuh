@@ -101,7 +101,7 @@ struct Fp4Cfg {
     static constexpr int kRedBytes = kRedBufs * BN * 512;  // split k (BN <= 64): partial tiles of the cluster's CTAs
     static constexpr int kMaxStages = 16;
     static constexpr int kNumBars = 2 * kMaxStages + 3 * kMaxScaleStages + 4 + 1 + 16;
-    static constexpr int kStoreBytes = 4 * 1024;  // 16-bit C: 16 rows x 32 columns per epilogue warp
+    static constexpr int kStoreBytes = 4 * 2048;  // 16-bit C: 32 rows x 32 columns per epilogue warp
     static constexpr int kTailBytes = 8 * kNumBars + 64 + 16;  // and the groups' table, 16 bytes each
     static constexpr int kNAlign = PAIR ? 32 : 16;
     static constexpr int kWarpMma = 4, kWarpLoadP = 5, kWarpLoadQ = 6, kWarpLoadS = 7, kWarpScale = 8;
@@ -229,12 +229,13 @@ __device__ __forceinline__ void fp4_store1(const Fp4Params &prm, float v, int64_
         static_cast<__half *>(prm.C)[at] = __float2half_rn(v);
 }
 
-// 16 accumulator columns (rows of C) of the warp's 32 lanes (columns of C).
-// float32: thread = lane, its 16 columns; a store is 128 contiguous bytes of a row.
+// 32 accumulator columns (rows of C) of the warp's 32 lanes (columns of C).
+// float32: thread = lane, its columns; a store is 128 contiguous bytes of a row.
 // 16-bit: in fragment order (tmem_ld_16x256b_x2, lanes 0-15 then 16-31), turned by
-// stmatrix so that a row's 32 columns are contiguous in the warp's 1 KB of
+// stmatrix so that a row's 32 columns are contiguous in the warp's 2 KB of
 // shared memory (64-byte rows, 16-byte chunk c of row r at c ^ (r / 2 % 4)) and
-// leave with wide stores.
+// leave with wide stores.  (32 at a time, not 16: the way through shared memory is
+// latency; the last tile of 256 columns takes 4700 cycles against 5700.)
 template <bool F32>
 __device__ __forceinline__ void fp4_load16_cols(uint32_t tacc, int c, uint32_t (&v)[16])
 {
@@ -247,7 +248,7 @@ __device__ __forceinline__ void fp4_load16_cols(uint32_t tacc, int c, uint32_t (
 }
 
 template <bool F32>
-__device__ __forceinline__ void fp4_store16_cols(const Fp4Params &prm, const uint32_t (&v)[16], float alpha, int64_t m0,
+__device__ __forceinline__ void fp4_store32_cols(const Fp4Params &prm, const uint32_t (*v)[16], float alpha, int64_t m0,
                                                  int count, int n0, uint8_t *stage)
 {
     const int lane = threadIdx.x & 31;
@@ -255,56 +256,79 @@ __device__ __forceinline__ void fp4_store16_cols(const Fp4Params &prm, const uin
         if (n0 + lane < prm.N) {
             float *c = static_cast<float *>(prm.C) + m0 * prm.N + n0 + lane;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (j < count) *c = __uint_as_float(v[j]) * alpha;
+            for (int j = 0; j < 32; ++j) {
+                if (j < count) *c = __uint_as_float(v[j / 16][j % 16]) * alpha;
                 c += prm.N;
             }
         }
     } else {
         const bool bf16 = prm.c_type == kOutBf16;
-        uint32_t pk[8];  // matrix (half h, rows + 8 s, columns 8 j): pk[4 h + 2 j + s]
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float lo = __uint_as_float(v[2 * i]) * alpha, hi = __uint_as_float(v[2 * i + 1]) * alpha;
-            if (bf16) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-                pk[i] = *reinterpret_cast<const uint32_t *>(&b);
-            } else {
-                const __half2 b = __floats2half2_rn(lo, hi);
-                pk[i] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-        }
         const uint32_t base = smem_u32(stage);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = 8 * j + (lane & 7), chunk = lane >> 3;
-            stmatrix_x4_trans(base + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4), pk[2 * j], pk[2 * j + 1], pk[4 + 2 * j],
-                              pk[4 + 2 * j + 1]);
+        for (int g = 0; g < 2; ++g) {
+            uint32_t pk[8];  // matrix (half h, rows + 8 s, columns 8 j): pk[4 h + 2 j + s]
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float lo = __uint_as_float(v[g][2 * i]) * alpha, hi = __uint_as_float(v[g][2 * i + 1]) * alpha;
+                if (bf16) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+                    pk[i] = *reinterpret_cast<const uint32_t *>(&b);
+                } else {
+                    const __half2 b = __floats2half2_rn(lo, hi);
+                    pk[i] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = 16 * g + 8 * j + (lane & 7), chunk = lane >> 3;
+                stmatrix_x4_trans(base + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4), pk[2 * j], pk[2 * j + 1],
+                                  pk[4 + 2 * j], pk[4 + 2 * j + 1]);
+            }
         }
         __syncwarp();
         uint16_t *c = static_cast<uint16_t *>(prm.C) + m0 * prm.N;
         if (prm.store_bytes == 16) {  // (N is a multiple of 8)
+            uint4 q[4];
+            const int chunk = lane & 3, n = n0 + 8 * chunk;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * i + (lane >> 2), chunk = lane & 3, n = n0 + 8 * chunk;
-                const uint4 q = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
-                if (r < count && n < prm.N) *reinterpret_cast<uint4 *>(c + static_cast<int64_t>(r) * prm.N + n) = q;
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2);
+                q[i] = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2);
+                if (r < count && n < prm.N) *reinterpret_cast<uint4 *>(c + static_cast<int64_t>(r) * prm.N + n) = q[i];
             }
         } else if (prm.store_bytes == 4) {  // (N is even)
+            uint32_t q[16];
+            const int w = lane & 15, n = n0 + 2 * w;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 2 * i + (lane >> 4), w = lane & 15, n = n0 + 2 * w;
-                const uint32_t q = *reinterpret_cast<const uint32_t *>(
-                    stage + r * 64 + (((w >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (w & 3));
-                if (r < count && n < prm.N) *reinterpret_cast<uint32_t *>(c + static_cast<int64_t>(r) * prm.N + n) = q;
+            for (int i = 0; i < 16; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                q[i] = *reinterpret_cast<const uint32_t *>(stage + r * 64 + (((w >> 2) ^ ((r >> 1) & 3)) << 4) +
+                                                           4 * (w & 3));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                if (r < count && n < prm.N)
+                    *reinterpret_cast<uint32_t *>(c + static_cast<int64_t>(r) * prm.N + n) = q[i];
             }
         } else {
+            const int n = n0 + lane;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int n = n0 + lane;
-                const uint16_t q = *reinterpret_cast<const uint16_t *>(
-                    stage + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7));
-                if (r < count && n < prm.N) c[static_cast<int64_t>(r) * prm.N + n] = q;
+            for (int r0 = 0; r0 < 32; r0 += 16) {
+                uint16_t q[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int r = r0 + i;
+                    q[i] = *reinterpret_cast<const uint16_t *>(stage + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
+                                                               2 * (lane & 7));
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (r0 + i < count && n < prm.N) c[static_cast<int64_t>(r0 + i) * prm.N + n] = q[i];
             }
         }
         __syncwarp();  // read before the next columns overwrite it
@@ -329,9 +353,9 @@ __device__ __forceinline__ void fp4_store_tile(const Fp4Params &prm, const Fp4Ti
             for (int i = 0; i < 6; i += 2) tmem_ld_wait_regs(v[i], v[i + 1]);
             if (s + 96 == shared0 + Cfg::kOverlap) release();
 #pragma unroll
-            for (int i = 0; i < 6; ++i)
+            for (int i = 0; i < 6; i += 2)
                 if (s + 16 * i < x.nq)
-                    fp4_store16_cols<F32>(prm, v[i], alpha, static_cast<int64_t>(x.q0) + s + 16 * i, x.nq - s - 16 * i,
+                    fp4_store32_cols<F32>(prm, v + i, alpha, static_cast<int64_t>(x.q0) + s + 16 * i, x.nq - s - 16 * i,
                                           n0, stage);
         }
         c = ab ? Cfg::kOverlap : 0;
@@ -344,11 +368,7 @@ __device__ __forceinline__ void fp4_store_tile(const Fp4Params &prm, const Fp4Ti
         fp4_load16_cols<F32>(tacc, c + 16, v[1]);
         tmem_ld_wait_regs(v[0], v[1]);
         if (Cfg::kOverlap == 0 && c + 32 >= c_end) release();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (c + 16 * i < c_end)
-                fp4_store16_cols<F32>(prm, v[i], alpha, static_cast<int64_t>(x.q0) + c + 16 * i, c_end - c - 16 * i, n0,
-                                      stage);
+        fp4_store32_cols<F32>(prm, v, alpha, static_cast<int64_t>(x.q0) + c, c_end - c, n0, stage);
     }
 }
 
@@ -467,11 +487,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int tiles = *total_slot;
+    Fp4Tile first{};
+    if (cid < tiles) first = fp4_tile<Cfg>(prm, groups, cid, pr);
     if (csize > 1) cluster_sync_all();  // the other CTAs' barriers are initialised
     // Up to here the kernel before this one in the stream may still run.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const uint32_t tmem = *tmem_slot;
-    const int tiles = *total_slot;
     const Watchdog wd{abort_flag, prm.status, prm.limit_ns};
     // this CTA's slice of k (split k: the cluster rank's), in blocks
     const int b0 = PAIR ? 0 : min(rank * prm.blocks_per_slice, prm.blocks);
@@ -484,7 +506,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         uint32_t issued = 0, last = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
-            const Fp4Tile x = fp4_tile<Cfg>(prm, groups, t, pr);
+            const Fp4Tile x = t == cid ? first : fp4_tile<Cfg>(prm, groups, t, pr);
             // activation rows that this CTA loads (pair: half of the tile's)
             const int mine = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : x.nq;
             const bool small = q_side && Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
@@ -530,7 +552,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         uint32_t issued = 0, last = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
-            const Fp4Tile x = fp4_tile<Cfg>(prm, groups, t, pr);
+            const Fp4Tile x = t == cid ? first : fp4_tile<Cfg>(prm, groups, t, pr);
             const int py = x.e * prm.N + x.p0;
             const int q_groups = (x.nq + 127) / 128;
             const uint32_t tx = static_cast<uint32_t>((128 + q_groups * Cfg::kQScaleRows) * 16 * Cfg::kH);
@@ -568,7 +590,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             uint32_t nacc = 0, g = 0;
             bool ok = true;
             for (int t = cid; ok && t < tiles; t += ncl, ++nacc) {
-                const Fp4Tile x = fp4_tile<Cfg>(prm, groups, t, pr);
+                const Fp4Tile x = t == cid ? first : fp4_tile<Cfg>(prm, groups, t, pr);
                 const uint32_t nq = static_cast<uint32_t>((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1));
                 const uint32_t idesc = idesc_fp4(128 * Cfg::CL, nq, NV);
                 const uint32_t ab = nacc & 1u;
@@ -717,11 +739,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int quad = warp;
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        uint8_t *stage = smem + prm.off_store + quad * 1024;
+        uint8_t *stage = smem + prm.off_store + quad * 2048;
         const uint32_t empty_leader = PAIR ? cluster_map(smem_u32(acc_empty), 0u) : 0u;
         uint32_t nacc = 0;
         for (int t = cid; t < tiles; t += ncl, ++nacc) {
-            const Fp4Tile x = fp4_tile<Cfg>(prm, groups, t, pr);
+            const Fp4Tile x = t == cid ? first : fp4_tile<Cfg>(prm, groups, t, pr);
             const float alpha = prm.alpha ? __ldg(prm.alpha + x.e) : 1.0f;
             const uint32_t ab = nacc & 1u;
             const int n = x.p0 + quad * 32 + lane;
