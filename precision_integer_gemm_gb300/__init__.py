@@ -371,9 +371,10 @@ def _pack_fp4(fn, where, x, extra, codes, scales, rows, K, index, pitch, stream)
         raise ValueError(f"{where}: x has overlapping rows")
     if transposed and index is not None:
         raise ValueError(f"{where}: rows of a transposed x cannot be gathered")
-    _check(fn(x.data_ptr(), t, ld, transposed, _typed(index, "torch.int32", _n(rows), where, "index"), r, *extra,
-              _dev(codes, _n(rows) * fp4_code_bytes(K), where, "codes"),
-              _dev(scales, _n(rows) * pitch, where, "scales"), rows, K, _stream(stream)), where)
+    n = _n(rows)
+    _check(fn(x.data_ptr(), t, ld, transposed, _typed(index, "torch.int32", n, where, "index"), r, *extra,
+              _dev(codes, n * fp4_code_bytes(K), where, "codes"), _dev(scales, n * pitch, where, "scales"), rows, K,
+              _stream(stream)), where)
 
 
 def pack_mxfp4(x, codes, scales, rows: int, K: int, index=None, stream=None) -> None:
@@ -393,8 +394,9 @@ def pack_nvfp4(x, tensor_scale, codes, scales, rows: int, K: int, index=None, st
 def _fp4_args(A, B, SFA, SFB, C, M, E, N, K, pitch, where):
     kb = fp4_code_bytes(K)
     t, size = _type(C, where)
-    return ((_dev(A, _n(M, kb), where, "A"), _dev(B, _n(E, N, kb), where, "B"),
-             _dev(SFA, _n(M, pitch), where, "SFA"), _dev(SFB, _n(E, N, pitch), where, "SFB")),
+    m, n = _n(M), _n(E, N)  # (rows of A and of B)
+    return ((_dev(A, m * kb, where, "A"), _dev(B, n * kb, where, "B"),
+             _dev(SFA, m * pitch, where, "SFA"), _dev(SFB, n * pitch, where, "SFB")),
             (_dev(C, size * _n(M, N), where, "C"), t))
 
 
@@ -438,12 +440,12 @@ def igemm_moe_route(logits, experts, weights, offsets, tokens, slots, T: int, E:
     (sorted place -> token, -1 past the last), slots [T,k] (pair -> sorted place, -1), int32."""
     w = "igemm_moe_route"
     t, size = _type(logits, w)
+    pairs = _n(T, k)
     _check(load().igemm_moe_route(
-        _dev(logits, size * _n(T, E), w, "logits"), t, _typed(experts, "torch.int32", _n(T, k), w, "experts"),
-        _typed(weights, "torch.float32", _n(T, k), w, "weights"),
-        _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"),
-        _typed(tokens, "torch.int32", _n(T, k), w, "tokens"), _typed(slots, "torch.int32", _n(T, k), w, "slots"),
-        T, E, k, int(bool(normalize)), _stream(stream)), w)
+        _dev(logits, size * _n(T, E), w, "logits"), t, _typed(experts, "torch.int32", pairs, w, "experts"),
+        _typed(weights, "torch.float32", pairs, w, "weights"),
+        _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"), _typed(tokens, "torch.int32", pairs, w, "tokens"),
+        _typed(slots, "torch.int32", pairs, w, "slots"), T, E, k, 1 if normalize else 0, _stream(stream)), w)
 
 
 def igemm_moe_combine(Y, slots, weights, out, T: int, k: int, N: int, stream=None) -> None:
@@ -452,9 +454,10 @@ def igemm_moe_combine(Y, slots, weights, out, T: int, k: int, N: int, stream=Non
     t, size = _type(Y, w)
     if out.dtype != Y.dtype:
         raise ValueError(f"{w}: out must have Y's type")
+    pairs = _n(T, k)
     _check(load().igemm_moe_combine(
-        _dev(Y, size * _n(T, k, N), w, "Y"), _typed(slots, "torch.int32", _n(T, k), w, "slots"),
-        _typed(weights, "torch.float32", _n(T, k), w, "weights"), _dev(out, size * _n(T, N), w, "out"), t, T,
+        _dev(Y, size * _n(pairs, N), w, "Y"), _typed(slots, "torch.int32", pairs, w, "slots"),
+        _typed(weights, "torch.float32", pairs, w, "weights"), _dev(out, size * _n(T, N), w, "out"), t, T,
         k, N, _stream(stream)), w)
 
 

@@ -1,6 +1,7 @@
 // Host side of the 4-bit floating-point GEMM: plan and launch of
 // igemm_fp4_kernel for one format (the two formats are two translation units).
 #pragma once
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include "launch.cuh"
@@ -39,10 +40,11 @@ template <class Cfg>
 int fp4_clusters(int csize)
 {
     static std::mutex mu;
-    static int cache[64][4] = {};
+    static std::atomic<int> cache[64][4] = {};  // (a small call asks several times: no lock once known)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     const int slot = csize == 1 ? 0 : csize == 2 ? 1 : csize == 4 ? 2 : 3;
+    if (const int known = cache[dev][slot].load(std::memory_order_acquire)) return known;
     std::lock_guard<std::mutex> lock(mu);
     if (!cache[dev][slot]) {
         auto kernel = igemm_fp4_kernel<Cfg>;
@@ -82,10 +84,13 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (make_map(&mapP, kU8, c.B, p_rows, code_bytes, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
         make_map(&mapQ, kU8, c.A, c.rows, code_bytes, Cfg::kQBox, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
-        make_map(&mapQs, kU8, c.A, c.rows, code_bytes, Cfg::kQRows, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk ||
         make_map(&mapSP, kU8, c.SFB, p_rows, pitch, 128, 16 * Cfg::kH, CU_TENSOR_MAP_SWIZZLE_NONE) != kOk ||
         make_map(&mapSQ, kU8, c.SFA, c.rows, pitch, Cfg::kQScaleRows, 16 * Cfg::kH,
                  CU_TENSOR_MAP_SWIZZLE_NONE) != kOk)
+        return kCudaError;
+    if constexpr (Cfg::kQRows == Cfg::kQBox)
+        mapQs = mapQ;
+    else if (make_map(&mapQs, kU8, c.A, c.rows, code_bytes, Cfg::kQRows, 128, CU_TENSOR_MAP_SWIZZLE_128B) != kOk)
         return kCudaError;
     const Fp4Smem<Cfg> lay(Cfg::PAIR ? 1 : csize, c.offsets ? c.experts : 0);
     Fp4Params prm{};
