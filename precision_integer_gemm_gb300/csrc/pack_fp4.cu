@@ -424,37 +424,42 @@ static int launch_pack_format(const Fp4PackCall &c, cudaStream_t stream)
 }
 
 // Packed rows copied to their places: zeros where the index is out of range.  A
-// thread takes four 16-byte pieces, all in flight.  Bound by the writes to HBM.
+// thread takes one 16-byte piece of four rows, a quarter of the rows apart, all in
+// flight (four pieces in a row, each with its own division, took 64 instructions a
+// piece: 17.9 us for 32768 rows of 2304 bytes against 15.6).
 __global__ void __launch_bounds__(256) fp4_copy_rows_kernel(const uint4 *__restrict__ codes, const uint4 *__restrict__ scales,
                                                             const Fp4PackParams p)
 {
     overlap_begin();
     const uint32_t cq = p.code_bytes / 16, per_row = cq + p.pitch / 16;
-    const uint32_t items = static_cast<uint32_t>(p.rows) * per_row;  // (below 2^32 less a block's)
-    uint4 v[4];
-    uint4 *to[4];
+    const uint32_t rows = static_cast<uint32_t>(p.rows), quarter = (rows + 3) / 4;
+    const uint32_t item = blockIdx.x * 256 + threadIdx.x;  // (fits: pack_once)
+    const uint32_t row = item / per_row, j = item - row * per_row;
+    if (row >= quarter) return;
+    const bool code = j < cq;
+    const int64_t pitch = code ? cq : per_row - cq;
+    const uint4 *from = code ? codes + j : scales + (j - cq);
+    uint4 *to = code ? reinterpret_cast<uint4 *>(p.codes) + j : reinterpret_cast<uint4 *>(p.scales) + (j - cq);
+    int src[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t item = blockIdx.x * 1024 + 256 * i + threadIdx.x;
-        v[i] = make_uint4(0, 0, 0, 0);
-        to[i] = nullptr;
-        if (item < items) {
-            const uint32_t row = item / per_row, j = item - row * per_row;
-            const int src = __ldg(p.index + row);
-            const bool code = j < cq;
-            const int64_t pitch = code ? cq : per_row - cq, at = code ? j : j - cq;
-            to[i] = reinterpret_cast<uint4 *>(code ? p.codes : p.scales) + row * pitch + at;
-            if (src >= 0 && src < p.x_rows) v[i] = __ldg((code ? codes : scales) + src * pitch + at);
-        }
+        const uint32_t r = row + i * quarter;
+        src[i] = r < rows ? __ldg(p.index + r) : -1;
     }
+    uint4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (to[i]) *to[i] = v[i];
+        v[i] = src[i] >= 0 && src[i] < p.x_rows ? __ldg(from + src[i] * pitch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t r = row + i * quarter;
+        if (r < rows) to[r * pitch] = v[i];
+    }
 }
 
 // Rows that are gathered twice or more on average are packed once, into a workspace,
 // and copied from there, where that saves reading 32 MB of x at least: 32768 x 4096
-// nvfp4 rows of 4096 take 44.6 -> 25.4 us (float32 84 -> 33), and 8192 x 4096 of 4096
+// nvfp4 rows of 4096 take 45.9 -> 23.1 us (float32 84 -> 30), and 8192 x 4096 of 4096
 // 12.4 either way; with 28 MB saved the second launch and the workspace cost more
 // (4096 x 4096 of 512: 7.4 -> 9.3).
 static bool pack_once(const Fp4PackCall &c)
@@ -489,8 +494,8 @@ int launch_fp4_pack(const Fp4PackCall &c, cudaStream_t stream)
     once.scales = once.codes + code_bytes;
     int rc = launch(once);
     if (rc == kOk) {
-        const int64_t items = c.rows * (int64_t(p.code_bytes) + p.pitch) / 16;
-        rc = launch_overlapped(fp4_copy_rows_kernel, dim3(static_cast<unsigned>((items + 1023) / 1024)), dim3(256), 0,
+        const int64_t items = (int64_t(c.rows) + 3) / 4 * ((int64_t(p.code_bytes) + p.pitch) / 16);
+        rc = launch_overlapped(fp4_copy_rows_kernel, dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0,
                                stream, reinterpret_cast<const uint4 *>(once.codes),
                                reinterpret_cast<const uint4 *>(once.scales), p);
     }
