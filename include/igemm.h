@@ -449,8 +449,8 @@ IGEMM_API int igemm_nvfp4_grouped(const uint8_t *A, const uint8_t *B, const uint
  *            `index` of pack_*)
  *   slots    [T, k] int32: sorted place of each pair, -1 where experts is -1
  * E <= 1024, k <= 32, k <= E, T * k < 2^31 (IGEMM_UNSUPPORTED_SHAPE).  T == 0 or
- * k == 0 zeroes offsets.  More than 512 tokens use a workspace of about E * T / 16
- * bytes from the library's pool.
+ * k == 0 zeroes offsets.  More than 512 tokens use a workspace of at most some
+ * E * T / 16 bytes from the library's pool.
  */
 IGEMM_API int igemm_moe_route(const void *logits, int logits_type, int32_t *experts, float *weights,
                               int32_t *offsets, int32_t *tokens, int32_t *slots, int T, int E, int k, int normalize,

@@ -11,11 +11,13 @@
 // own: the sort is stable and needs no ordered atomics.  A cluster of up to 8 blocks
 // does the whole job for up to 512 tokens, its blocks reading each other's masks in
 // shared memory (calls of 128 x 256 bfloat16, 8 choices: 12.2 us in three launches
-// and a workspace, 7.6 in one); more tokens take three launches (choice and counts
-// per block, a scan over the blocks per expert, places), and 16-bit logits of up to
-// 256 experts then go four tokens to a warp (moe_choose4_kernel).  Bound by
-// instructions and by the launches: 17.5 us at 16384 x 256 bfloat16, 8 choices, whose
-// 10.5 MB are 1.6 us of HBM (alone and cold: choice 13, scan 4.5, places 7.5 us).
+// and a workspace, 7.6 in one); more tokens take two launches (choice and counts per
+// block; places, each block summing the counts of all) or, from some 2^20 words of
+// counts read in all, three (a scan over the blocks per expert between them), and
+// 16-bit logits of up to 256 experts then go four tokens to a warp
+// (moe_choose4_kernel).  Bound by instructions and by the launches: 15.6 us at 16384 x
+// 256 bfloat16, 8 choices, whose 10.5 MB are 1.6 us of HBM (alone and cold: choice 13,
+// scan 4.5, places 7.5 us).
 //
 // Combine: bound by HBM, k rows read and one written per token.
 #include <algorithm>
@@ -48,8 +50,9 @@ struct RouteParams {
     int *experts;
     float *weights;
     int *offsets, *tokens, *slots;
-    int *counts;  // [E][blocks], then exclusive prefixes; null when one cluster does it all
+    int *counts;  // [E][blocks], then exclusive prefixes (three launches)
     int *totals;  // [E]
+    uint32_t *packed_counts;  // [blocks][ceil(E / 4)], a byte an expert (two launches)
     int T, E, k, blocks;
     int tb;       // tokens per block
     int normalize;
@@ -117,6 +120,50 @@ __device__ __forceinline__ void route_place(const RouteParams &p, const uint2 *m
     }
 }
 
+// The block's pairs of each expert (at most kTB) to the launch that places them.
+__device__ __forceinline__ void route_counts(const RouteParams &p, const uint2 *mask)
+{
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        const int n = __popc(mask[e].x) + __popc(mask[e].y);
+        if (p.packed_counts)
+            reinterpret_cast<uint8_t *>(p.packed_counts + static_cast<int64_t>(blockIdx.x) * ((p.E + 3) / 4))[e] =
+                static_cast<uint8_t>(n);
+        else
+            p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = n;
+    }
+}
+
+// From every block's counts in bytes: first[e] += all pairs of expert e, start[e] +=
+// those of the blocks before this one.  A thread sums four experts over every G-th
+// block, as pairs of 16-bit sums (with two launches a thread has at most 64 blocks).
+__device__ __forceinline__ void route_sum_counts(const RouteParams &p, int *first, int *start)
+{
+    const int words = (p.E + 3) / 4, groups = min(kRouteThreads / words, 16);
+    const int g = threadIdx.x / words, w = threadIdx.x - g * words;
+    if (g >= groups) return;
+    const int here = blockIdx.x;
+    uint32_t all[2] = {0, 0}, below[2] = {0, 0};  // experts 0 and 2, 1 and 3
+#pragma unroll 8
+    for (int b = g; b < p.blocks; b += groups) {
+        const uint32_t n = p.packed_counts[static_cast<int64_t>(b) * words + w];
+        const uint32_t even = n & 0x00FF00FFu, odd = n >> 8 & 0x00FF00FFu;
+        all[0] += even;
+        all[1] += odd;
+        if (b < here) {
+            below[0] += even;
+            below[1] += odd;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = 4 * w + i;
+        if (e < p.E) {
+            atomicAdd(&first[e], static_cast<int>(all[i & 1] >> (16 * (i >> 1)) & 0xFFFFu));
+            atomicAdd(&start[e], static_cast<int>(below[i & 1] >> (16 * (i >> 1)) & 0xFFFFu));
+        }
+    }
+}
+
 // Choice and weights of a block's tokens; their masks; one cluster: everything.
 // VPL: logits per lane (E <= 32 VPL); VEC: lane's logits in runs of V (16 bytes at
 // most), loaded together.
@@ -129,8 +176,9 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
         T v[V];
     };
     extern __shared__ uint2 mask[];  // [E], then (one cluster) first[E + 1], start[E], experts[kTB * k]
-    overlap_begin();
+    overlap_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool one_cluster = !p.counts && !p.packed_counts;
     int *first = reinterpret_cast<int *>(mask + p.E);
     int *start = first + p.E + 1;
     int *chosen = start + p.E;
@@ -231,14 +279,14 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
         if (lane < p.k) {
             p.experts[t * p.k + lane] = my_e;
             p.weights[t * p.k + lane] = my_e >= 0 ? __fdiv_rn(my_w, sum) : 0.0f;
-            if (!p.counts) chosen[i * p.k + lane] = my_e;
+            if (one_cluster) chosen[i * p.k + lane] = my_e;
             if (my_e >= 0) atomicOr(i < 32 ? &mask[my_e].x : &mask[my_e].y, 1u << (i & 31));
         }
     }
+    overlap_release();
     __syncthreads();
-    if (p.counts) {
-        for (int e = threadIdx.x; e < p.E; e += kChooseThreads)
-            p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = __popc(mask[e].x) + __popc(mask[e].y);
+    if (!one_cluster) {
+        route_counts(p, mask);
         return;
     }
     // the pairs of each expert in every block and in those before this one
@@ -302,7 +350,7 @@ __global__ void __launch_bounds__(kChoose4Threads) moe_choose4_kernel(const Rout
         T v[V];
     };
     extern __shared__ uint2 mask[];  // [E]
-    overlap_begin();
+    overlap_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < p.E; e += kChoose4Threads) mask[e] = make_uint2(0, 0);
     __syncthreads();
@@ -405,9 +453,9 @@ __global__ void __launch_bounds__(kChoose4Threads) moe_choose4_kernel(const Rout
         p.weights[t * p.k + c] = e >= 0 ? __fdiv_rn(w, all) : 0.0f;
         if (e >= 0) atomicOr(i < 32 ? &mask[e].x : &mask[e].y, 1u << (i & 31));
     }
+    overlap_release();
     __syncthreads();
-    for (int x = threadIdx.x; x < p.E; x += kChoose4Threads)
-        p.counts[static_cast<int64_t>(x) * p.blocks + blockIdx.x] = __popc(mask[x].x) + __popc(mask[x].y);
+    route_counts(p, mask);
 }
 
 // A warp per expert: its counts per block become running sums, 8 blocks a lane.
@@ -443,35 +491,44 @@ __global__ void __launch_bounds__(128) moe_scan_kernel(const RouteParams p)
 
 __global__ void __launch_bounds__(kRouteThreads) moe_place_kernel(const RouteParams p)
 {
-    extern __shared__ uint2 mask[];  // [E], then first[E + 1]
+    extern __shared__ uint2 mask[];  // [E], then first[E + 1], start[E]
     int *first = reinterpret_cast<int *>(mask + p.E);
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = make_uint2(0, 0);
-    // the scan's sums; the choices come from the kernel before the scan, which the
-    // scan waited for
+    int *start = first + p.E + 1;
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+        mask[e] = make_uint2(0, 0);
+        first[e] = start[e] = 0;
+    }
+    // the counts; with a scan between, the choices come from the kernel before it,
+    // which the scan waited for
     overlap_begin();
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) first[e] = p.totals[e];
     __syncthreads();
-    if (threadIdx.x < 32) route_scan(first, p.E, [&](int e) { return first[e]; });
-    __syncthreads();
-    const int t0 = blockIdx.x * kTB;
-    const int n = min(kTB, p.T - t0) * p.k;
+    const int t0 = blockIdx.x * p.tb;
+    const int n = min(p.tb, p.T - t0) * p.k;
     const int *experts = p.experts + static_cast<int64_t>(t0) * p.k;
     for (int i = threadIdx.x; i < n; i += kRouteThreads) {
         const int e = experts[i], t = i / p.k;
         if (e >= 0) atomicOr(t < 32 ? &mask[e].x : &mask[e].y, 1u << (t & 31));
     }
-    const int routed = first[p.E];
+    if (p.packed_counts) {
+        route_sum_counts(p, first, start);
+    } else {
+        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+            first[e] = p.totals[e];
+            start[e] = p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) route_scan(first, p.E, [&](int e) { return first[e]; });
+    __syncthreads();
     const int64_t pairs = static_cast<int64_t>(p.T) * p.k;
-    for (int64_t i = routed + static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x; i < pairs;
+    for (int64_t i = first[p.E] + static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x; i < pairs;
          i += static_cast<int64_t>(gridDim.x) * kRouteThreads)
         p.tokens[i] = -1;
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = first[e];
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) start[e] += first[e];
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
-        first[e] += p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
-    __syncthreads();
-    route_place(p, mask, first, experts);
+    route_place(p, mask, start, experts);
 }
 
 template <class T, int VPL>
@@ -483,11 +540,12 @@ static int launch_choose_vpl(const RouteParams &p, int smem, cudaStream_t stream
     // (routing of 16384 x 256 bfloat16, 8 choices: 21.7 -> 17.5 us; 65536 x 128: 41.5 ->
     // 29.8; no case was slower)
     if constexpr (sizeof(T) == 2 && VPL <= 8)
-        if (p.counts && p.k <= 8)
+        if (p.T > kClusterBlocks * kTB && p.k <= 8)
             return launch_overlapped(vec ? moe_choose4_kernel<T, VPL, true> : moe_choose4_kernel<T, VPL, false>,
                                      dim3(p.blocks), dim3(kChoose4Threads), smem, stream, p);
     const auto kernel = vec ? moe_choose_kernel<T, VPL, true> : moe_choose_kernel<T, VPL, false>;
-    if (p.counts) return launch_overlapped(kernel, dim3(p.blocks), dim3(kChooseThreads), smem, stream, p);
+    if (p.T > kClusterBlocks * kTB)
+        return launch_overlapped(kernel, dim3(p.blocks), dim3(kChooseThreads), smem, stream, p);
     int cluster = 1;
     while (cluster < p.blocks) cluster *= 2;  // (blocks without tokens fill it up)
     return launch_overlapped_clusters(kernel, dim3(cluster), cluster, dim3(kChooseThreads), smem, stream, p);
@@ -520,18 +578,27 @@ int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
     const bool one = c.T <= kClusterBlocks * kTB;
     p.tb = one ? std::max(kFewTokens, (c.T + kClusterBlocks - 1) / kClusterBlocks) : kTB;
     p.blocks = (c.T + p.tb - 1) / p.tb;
+    // the places can sum every block's counts themselves, without a scan, while all of
+    // them together read no more than 4 MB (us, two launches against three: 4096 x 256
+    // bfloat16 8.0 to 9.0, 16384 x 64 8.3 to 8.7; 16384 x 256 14.1 to 12.8)
+    const int words = (c.E + 3) / 4;
+    const bool two = !one && int64_t(p.blocks) * p.blocks * words <= int64_t(1) << 20;
     void *ws = nullptr;
     if (!one) {
-        const size_t counts = size_t(c.E) * p.blocks * 4;
-        if (workspace_alloc(&ws, counts + size_t(c.E) * 4, stream) != kOk) return kCudaError;
-        p.counts = static_cast<int *>(ws);
-        p.totals = reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + counts);
+        const size_t counts = two ? size_t(words) * p.blocks * 4 : size_t(c.E) * p.blocks * 4;
+        if (workspace_alloc(&ws, counts + (two ? 0 : size_t(c.E) * 4), stream) != kOk) return kCudaError;
+        if (two) {
+            p.packed_counts = static_cast<uint32_t *>(ws);
+        } else {
+            p.counts = static_cast<int *>(ws);
+            p.totals = reinterpret_cast<int *>(static_cast<uint8_t *>(ws) + counts);
+        }
     }
-    const int smem = c.E * 8 + (c.E + 1) * 4 + (one ? c.E * 4 + kTB * c.k * 4 : 0);
+    const int smem = c.E * 8 + (c.E + 1) * 4 + c.E * 4 + (one ? kTB * c.k * 4 : 0);
     int rc = c.x_type == 0   ? launch_choose<float>(p, smem, stream)
              : c.x_type == 1 ? launch_choose<__nv_bfloat16>(p, smem, stream)
                              : launch_choose<__half>(p, smem, stream);
-    if (rc == kOk && !one)
+    if (rc == kOk && p.counts)
         rc = launch_overlapped(moe_scan_kernel, dim3((c.E + 3) / 4), dim3(128), 0, stream, p);
     if (rc == kOk && !one)
         rc = launch_overlapped(moe_place_kernel, dim3(p.blocks), dim3(kRouteThreads), smem, stream, p);
@@ -562,7 +629,7 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const T *__restrict__ 
                                                           int Tn, int k, int N)
 {
     using Run = MoeRun<T, PER>;
-    overlap_begin();
+    overlap_wait();
     int64_t t;
     int n;
     if constexpr (RUNS == 1) {
@@ -621,6 +688,7 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const T *__restrict__ 
         for (int i = 0; i < PER; ++i) moe_out(&o.v[i], acc[r][i]);
         *reinterpret_cast<Run *>(out + t * N + nr) = o;
     }
+    overlap_release();
 }
 
 template <class T, int PER>

@@ -230,7 +230,7 @@ struct Fp4Raw {
 template <bool NV, class T, bool VEC>
 __global__ void __launch_bounds__(256, VEC ? 5 : 4) pack_fp4_rows_kernel(const T *__restrict__ x, const Fp4PackParams p)
 {
-    overlap_begin();
+    overlap_wait();
     const int k = (blockIdx.y * blockDim.x + threadIdx.x) * 16;
     const bool in_row = k < 2 * p.code_bytes;
     const bool last = k / 8 + 2 == p.code_bytes / 4;  // of the row: it writes the padding
@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(256, VEC ? 5 : 4) pack_fp4_rows_kernel(const T
         if (last)
             for (int b = (p.K + (NV ? 15 : 31)) / (NV ? 16 : 32); b < p.pitch; ++b) scales[b] = 0;
     }
+    overlap_release();
 }
 
 // Transposed x [K, rows]: a CTA takes 32 R rows (R a lane, so loads run along x's
@@ -292,7 +293,7 @@ template <bool NV, class T, int R>
 __global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__restrict__ x, const Fp4PackParams p)
 {
     static_assert(R == 1 || sizeof(T) == 2, "pairs of 16-bit values");
-    overlap_begin();
+    overlap_wait();
     constexpr int kPerWarp = NV ? 2 : 1;  // scale bytes
     constexpr int kRows = 32 * R;
     __shared__ uint4 codes[kRows][9];     // (row pitch 144 bytes: no bank conflicts)
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__res
         const int r = i / (8 * kPerWarp), b = i % (8 * kPerWarp), at = blockIdx.y * 8 * kPerWarp + b;
         if (r0 + r < p.rows && at < p.pitch) p.scales[(r0 + r) * p.pitch + at] = scales[r][b];
     }
+    overlap_release();
     // (mx: 256 k are half of 16 scale bytes) zeros from here up to the pitch
     if (blockIdx.y == gridDim.y - 1 && threadIdx.x < kRows && r0 + threadIdx.x < p.rows)
         for (int b = (blockIdx.y + 1) * 8 * kPerWarp; b < p.pitch; ++b) p.scales[(r0 + threadIdx.x) * p.pitch + b] = 0;
@@ -430,12 +432,12 @@ static int launch_pack_format(const Fp4PackCall &c, cudaStream_t stream)
 __global__ void __launch_bounds__(256) fp4_copy_rows_kernel(const uint4 *__restrict__ codes, const uint4 *__restrict__ scales,
                                                             const Fp4PackParams p)
 {
-    overlap_begin();
+    overlap_wait();
     const uint32_t cq = p.code_bytes / 16, per_row = cq + p.pitch / 16;
     const uint32_t rows = static_cast<uint32_t>(p.rows), quarter = (rows + 3) / 4;
     const uint32_t item = blockIdx.x * 256 + threadIdx.x;  // (fits: pack_once)
     const uint32_t row = item / per_row, j = item - row * per_row;
-    if (row >= quarter) return;
+    if (row >= quarter) return;  // (an exit counts as a release)
     const bool code = j < cq;
     const int64_t pitch = code ? cq : per_row - cq;
     const uint4 *from = code ? codes + j : scales + (j - cq);
@@ -455,6 +457,7 @@ __global__ void __launch_bounds__(256) fp4_copy_rows_kernel(const uint4 *__restr
         const uint32_t r = row + i * quarter;
         if (r < rows) to[r * pitch] = v[i];
     }
+    overlap_release();
 }
 
 // Rows that are gathered twice or more on average are packed once, into a workspace,

@@ -608,6 +608,14 @@ def test_route_of_several_blocks(typ, T, E, k):
             check_route(x, k, normalize)
 
 
+@pytest.mark.parametrize("typ,T,E,k", [("bf16", 32769, 256, 2), ("f32", 16500, 1000, 3), ("f16", 20000, 3, 2)])
+def test_route_of_many_tokens(typ, T, E, k):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn((T, E), generator=gen, device="cuda").to(TYPES[typ])
+    x[torch.rand(T, generator=gen, device="cuda") < 0.1] = -math.inf
+    check_route(x, k, True)
+
+
 def test_route_infinite_logit_gives_nan_weights():
     x = torch.zeros((2, 8), device="cuda")
     x[0, 3] = math.inf
