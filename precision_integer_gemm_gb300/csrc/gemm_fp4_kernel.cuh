@@ -60,6 +60,7 @@ struct Fp4Params {
     int group_p;           // tiles run in groups of group_p weight tiles (fastest) by every activation tile
     int cs;                // CTAs of a cluster that split k (1: none; a power of two, 4 cs <= BN)
     int blocks_per_slice;
+    int prefetch;          // single CTAs: stages of weights that go to L2 ahead of the kernel's turn
     int code_stages, scale_stages;  // ring slots: 256 k of codes, 512 k of scales
     int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
     int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
@@ -488,6 +489,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int tiles = *total_slot;
     Fp4Tile first{};
     if (cid < tiles) first = fp4_tile<Cfg>(prm, groups, cid, pr);
+    if constexpr (!PAIR) {
+        // The weights that fill the ring first go to L2 while the kernel before this one
+        // ends.  (It may be the one that writes them: L2 then holds what it wrote, and
+        // the loads below come after its end.)
+        if (warp == 3 && prm.prefetch > 0 && cid < tiles && elect_one()) {
+            const int k0 = 2 * rank * prm.blocks_per_slice;
+#pragma unroll 1
+            for (int k = k0; k < min(2 * prm.blocks, k0 + prm.prefetch); ++k)
+                tma_prefetch_2d(&mapP, k * 128, first.e * prm.N + first.p0);
+        }
+    }
     if (csize > 1) cluster_sync_all();  // the other CTAs' barriers are initialised
     // Up to here the kernel before this one in the stream may still run.
     asm volatile("griddepcontrol.wait;" ::: "memory");
