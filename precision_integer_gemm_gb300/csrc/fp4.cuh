@@ -28,6 +28,7 @@ struct Fp4Plan {
     int cs;        // CTAs that split k
     int qt;        // activation rows per tile
     int group_p;   // weight tiles per group of the tile order
+    double groups;  // expected groups with any rows
 };
 
 // The kernel, tile and split for a call; max_clusters(bn, pair, csize) says how

@@ -111,8 +111,9 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     prm.blocks_per_slice = (prm.blocks + plan.cs - 1) / plan.cs;
     // weights of 32 MB and more, whose first ring is a small part of what a CTA reads (us
     // without and with: 16 x 28672 x 8192 24.1 to 22.7, 16 x 8192 x 8192 10.0 to 9.5; 16 x
-    // 4096 x 4096 6.2 to 6.5, 512 x 8192 x 8192 on pairs 16.9 to 17.5)
-    prm.prefetch = !Cfg::PAIR && !c.offsets && p_rows * code_bytes >= uint64_t(1) << 25
+    // 4096 x 4096 6.2 to 6.5, 512 x 8192 x 8192 on pairs 16.9 to 17.5; 32 rows over 64
+    // experts of 4096 x 4096 29.4 to 28.4)
+    prm.prefetch = !Cfg::PAIR && plan.groups * c.N * code_bytes >= 33554432.0
                        ? std::min(lay.code_stages, 2 * prm.blocks_per_slice)
                        : 0;
     prm.code_stages = lay.code_stages;

@@ -123,31 +123,13 @@ struct Fp4Tile {
 // of activations.
 using Fp4Group = int4;
 
-// Tile t: group by binary search over the first tiles, then the grouped order of
-// its weight and activation tiles.
+// Tile r of a group: the grouped order of its weight and activation tiles.
 template <class Cfg>
-__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Params &prm, const Fp4Group *groups, int t, int rank)
+__device__ __forceinline__ Fp4Tile fp4_tile_of(const Fp4Params &prm, int e, int begin, int count, int q_tiles, int r,
+                                               int rank)
 {
     Fp4Tile x;
-    int begin = 0, count = prm.rows, r = t;
-    x.e = 0;
-    int q_tiles = 0;
-    if (prm.offsets) {
-        int lo = 0, hi = prm.experts;  // groups[lo].x <= t, t below every later group's
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (groups[mid].x <= t) lo = mid;
-            else hi = mid;
-        }
-        const Fp4Group g = groups[lo];
-        x.e = lo;
-        r = t - g.x;
-        begin = g.y;
-        count = g.z;
-        q_tiles = g.w;
-    } else {
-        q_tiles = (count + prm.qt - 1) / prm.qt;
-    }
+    x.e = e;
     const int per_group = prm.group_p * q_tiles;
     const int grp = r / per_group;
     const int first = grp * prm.group_p;
@@ -161,6 +143,70 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Params &prm, const Fp4Group
     x.q0 = begin + qi * per;
     x.nq = min(count - qi * per, per);
     return x;
+}
+
+// Tile t: group by binary search over the first tiles.
+template <class Cfg>
+__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Params &prm, const Fp4Group *groups, int t, int rank)
+{
+    int begin = 0, count = prm.rows, r = t;
+    int e = 0;
+    int q_tiles = 0;
+    if (prm.offsets) {
+        int lo = 0, hi = prm.experts;  // groups[lo].x <= t, t below every later group's
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (groups[mid].x <= t) lo = mid;
+            else hi = mid;
+        }
+        const Fp4Group g = groups[lo];
+        e = lo;
+        r = t - g.x;
+        begin = g.y;
+        count = g.z;
+        q_tiles = g.w;
+    } else {
+        q_tiles = (count + prm.qt - 1) / prm.qt;
+    }
+    return fp4_tile_of<Cfg>(prm, e, begin, count, q_tiles, r, rank);
+}
+
+// One warp, 32 groups from e0: this lane's group, with its first tile after `run`
+// others; `run` moves past them.  (Groups that overlap against the rules could have
+// more tiles than an int holds: those past kFp4MaxTiles are left out.)
+__device__ __forceinline__ Fp4Group fp4_groups32(const Fp4Params &prm, int e0, int &run)
+{
+    const int lane = threadIdx.x & 31, e = e0 + lane;
+    Fp4Group g = make_int4(0, 0, 0, 0);
+    if (e < prm.experts) {
+        g.y = min(max(__ldcg(prm.offsets + e), 0), prm.rows);
+        g.z = min(max(__ldcg(prm.offsets + e + 1), g.y), prm.rows) - g.y;
+        g.w = (g.z + prm.qt - 1) / prm.qt;
+    }
+    int incl = g.w * prm.p_tiles;  // at most kFp4MaxTiles
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl = min(incl + o, kFp4MaxTiles);
+    }
+    const int before = __shfl_up_sync(0xffffffffu, incl, 1);
+    g.x = min(run + (lane > 0 ? before : 0), kFp4MaxTiles);
+    run = min(run + __shfl_sync(0xffffffffu, incl, 31), kFp4MaxTiles);
+    return g;
+}
+
+// The weights of tile x that fill the ring first go to L2 while the kernel before
+// this one ends.  (It may be the one that writes them: L2 then holds what it wrote,
+// and the loads come after its end.)
+__device__ __forceinline__ void fp4_prefetch(const Fp4Params &prm, const CUtensorMap *map, const Fp4Tile &x, int rank)
+{
+    if (elect_one()) {
+        const int k0 = 2 * rank * prm.blocks_per_slice;
+#pragma unroll 1
+        for (int k = k0; k < min(2 * prm.blocks, k0 + prm.prefetch); ++k)
+            tma_prefetch_2d(map, k * 128, x.e * prm.N + x.p0);
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ bool fp4_warp_wait(uint64_t *bar, uint32_t parity, const Watchdog &wd)
@@ -454,34 +500,31 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         // running tile counts of the groups (the offsets may come from the kernel before)
         if (prm.offsets) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            // (groups that overlap against the rules could have more tiles than an int
-            // holds: those past kFp4MaxTiles are left out)
             int run = 0;
             for (int e0 = 0; e0 < prm.experts; e0 += 32) {
-                const int e = e0 + lane;
-                Fp4Group g = make_int4(0, 0, 0, 0);
-                if (e < prm.experts) {
-                    g.y = min(max(__ldg(prm.offsets + e), 0), prm.rows);
-                    g.z = min(max(__ldg(prm.offsets + e + 1), g.y), prm.rows) - g.y;
-                    g.w = (g.z + prm.qt - 1) / prm.qt;
-                }
-                const int tiles = g.w * prm.p_tiles;  // at most kFp4MaxTiles
-                int incl = tiles;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, incl, d);
-                    if (lane >= d) incl = min(incl + o, kFp4MaxTiles);
-                }
-                const int before = __shfl_up_sync(0xffffffffu, incl, 1);
-                g.x = min(run + (lane > 0 ? before : 0), kFp4MaxTiles);
-                if (e < prm.experts) groups[e] = g;
-                run = min(run + __shfl_sync(0xffffffffu, incl, 31), kFp4MaxTiles);
+                const Fp4Group g = fp4_groups32(prm, e0, run);
+                if (e0 + lane < prm.experts) groups[e0 + lane] = g;
             }
             if (lane == 0) *total_slot = run;
         } else if (lane == 0) {
             *total_slot = (prm.rows + prm.qt - 1) / prm.qt * prm.p_tiles;
         }
     }
+    if constexpr (!PAIR)
+        if (warp == 3 && prm.prefetch > 0 && prm.offsets) {
+            // the first tile by the offsets as they are now: if the kernel before is the
+            // one that writes them, only the prefetch misses
+            int run = 0;
+            for (int e0 = 0; e0 < prm.experts && run <= cid; e0 += 32) {
+                const Fp4Group g = fp4_groups32(prm, e0, run);
+                const uint32_t mine = __ballot_sync(0xffffffffu, g.x <= cid && cid - g.x < g.w * prm.p_tiles);
+                if (mine) {
+                    const int from = 31 - __clz(static_cast<int>(mine));
+                    const int r = cid - __shfl_sync(0xffffffffu, g.x, from), q_tiles = __shfl_sync(0xffffffffu, g.w, from);
+                    fp4_prefetch(prm, &mapP, fp4_tile_of<Cfg>(prm, e0 + from, 0, 1, q_tiles, r, 0), rank);
+                }
+            }
+        }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -489,17 +532,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int tiles = *total_slot;
     Fp4Tile first{};
     if (cid < tiles) first = fp4_tile<Cfg>(prm, groups, cid, pr);
-    if constexpr (!PAIR) {
-        // The weights that fill the ring first go to L2 while the kernel before this one
-        // ends.  (It may be the one that writes them: L2 then holds what it wrote, and
-        // the loads below come after its end.)
-        if (warp == 3 && prm.prefetch > 0 && cid < tiles && elect_one()) {
-            const int k0 = 2 * rank * prm.blocks_per_slice;
-#pragma unroll 1
-            for (int k = k0; k < min(2 * prm.blocks, k0 + prm.prefetch); ++k)
-                tma_prefetch_2d(&mapP, k * 128, first.e * prm.N + first.p0);
-        }
-    }
+    if constexpr (!PAIR)
+        if (warp == 3 && prm.prefetch > 0 && !prm.offsets && cid < tiles) fp4_prefetch(prm, &mapP, first, rank);
     if (csize > 1) cluster_sync_all();  // the other CTAs' barriers are initialised
     // Up to here the kernel before this one in the stream may still run.
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -42,7 +42,7 @@ int fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *pla
                             (cs == 1 ? 0.0 : bn == 64 ? 3.0 : 2.0);
         if (best < 0 || cost < best) {
             best = cost;
-            *plan = Fp4Plan{bn, pair, cs, qt, 1};
+            *plan = Fp4Plan{bn, pair, cs, qt, 1, groups};
         }
         return true;
     };
