@@ -60,6 +60,7 @@ struct Fp4Params {
     int group_p;           // tiles run in groups of group_p weight tiles (fastest) by every activation tile
     int cs;                // CTAs of a cluster that split k (1: none; a power of two, 4 cs <= BN)
     int blocks_per_slice;
+    int stream;            // single CTAs: the weights leave L2 first
     int prefetch;          // single CTAs: stages of weights that go to L2 ahead of the kernel's turn
     int code_stages, scale_stages;  // ring slots: 256 k of codes, 512 k of scales
     int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
@@ -546,6 +547,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         // ------------------------------------------------------------ codes
         const bool q_side = warp == Cfg::kWarpLoadQ;
         Fp4Ring cr(prm.code_stages);
+        const bool stream = !PAIR && !q_side && prm.stream;
+        const uint64_t evict_first = l2_policy_evict_first();
         uint32_t issued = 0, last = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles; t += ncl) {
@@ -575,7 +578,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         if (two) tma_load_2d_pair(to + Cfg::kQRows * 128, map, bar, k * 128, y + Cfg::kQRows);
                     } else {
                         mbar_arrive_expect_tx(&full[cr.slot], tx);
-                        tma_load_2d(to, map, &full[cr.slot], k * 128, y);
+                        // (a hint only where it says something: evict_normal for all loads
+                        // took 1 x 4096 x 14336 from 7.3 to 8.4 us)
+                        if (stream) tma_load_2d_hint(to, map, &full[cr.slot], k * 128, y, evict_first);
+                        else tma_load_2d(to, map, &full[cr.slot], k * 128, y);
                         if (two) tma_load_2d(to + Cfg::kQRows * 128, map, &full[cr.slot], k * 128, y + Cfg::kQRows);
                     }
                 }
