@@ -109,12 +109,12 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     prm.group_p = plan.group_p;
     prm.cs = plan.cs;
     prm.blocks_per_slice = (prm.blocks + plan.cs - 1) / plan.cs;
-    // weights that are too many to be in L2 at the next call leave it first, before what
-    // other kernels left there (from 48 MB: 32 rows over 64 experts of 4096 x 4096 27.9 to
-    // 25.1 us, 16 x 28672 x 8192 23.8 to 21.7; 33 MB used again and again, 16 x 8192 x
-    // 8192, took 9.7 instead of 8.9)
+    // weights from 24 MB on leave L2 first, before what other kernels left there (us
+    // without and with: 32 rows over 64 experts of 4096 x 4096 27.9 to 25.1, 16 x 28672 x
+    // 8192 23.8 to 21.7, 64 x 14336 x 4096 8.8 to 8.5; the same weights again and again
+    // out of L2, 16 x 8192 x 8192 8.9 to 9.6)
     const double weights = plan.groups * c.N * code_bytes;
-    prm.stream = !Cfg::PAIR && weights >= 48.0 * (1 << 20);
+    prm.stream = !Cfg::PAIR && weights >= 24.0 * (1 << 20);
     // weights of 32 MB and more, whose first ring is a small part of what a CTA reads (us
     // without and with: 16 x 28672 x 8192 24.1 to 22.7, 16 x 8192 x 8192 10.0 to 9.5; 16 x
     // 4096 x 4096 6.2 to 6.5, 512 x 8192 x 8192 on pairs 16.9 to 17.5; 32 rows over 64
