@@ -10,7 +10,8 @@ namespace igemm {
 // us in 128 x 16), or HBM's 6.3 MB a microsecond shared by the SMs (on CTA pairs:
 // those that read different weights), plus what a tile costs besides (1 us; 3.2 us
 // on CTA pairs).
-// A split of k adds 2 us (3 us for 64 activation rows; with 128 it never paid).
+// A split of k adds 2 us (4 us for 64 activation rows: 64 x 8192 x 8192 12.2 us
+// split, 10.1 whole; with 128 it never paid).
 // Against the fastest of all choices on 85 shapes (activations 1 .. 2048, weights
 // 128 x 65536 .. 28672 x 8192) the choice is within 15 %, mostly within 4 %; with one
 // width per number of activations and a split wherever SMs were idle, 128 x 1024 x
@@ -39,7 +40,7 @@ int fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *pla
         const double readers = std::min(tiles, double(clusters)) * (pair ? 2 / q_tiles : cs);
         const double block = std::max(bytes / 90e3, readers * 128 * (256 + scale_bytes) / 6.3e6);
         const double cost = std::ceil(tiles / clusters) * (per * block + (pair ? 3.2 : 1.0)) +
-                            (cs == 1 ? 0.0 : bn == 64 ? 3.0 : 2.0);
+                            (cs == 1 ? 0.0 : bn == 64 ? 4.0 : 2.0);
         if (best < 0 || cost < best) {
             best = cost;
             *plan = Fp4Plan{bn, pair, cs, qt, 1, groups};
