@@ -204,7 +204,7 @@ __device__ __forceinline__ void fp4_prefetch(const Fp4Params &prm, const CUtenso
     if (elect_one()) {
         const int k0 = 2 * rank * prm.blocks_per_slice;
 #pragma unroll 1
-        for (int k = k0; k < min(2 * prm.blocks, k0 + prm.prefetch); ++k)
+        for (int k = k0; k < min((prm.k_steps + 3) / 4, k0 + prm.prefetch); ++k)
             tma_prefetch_2d(map, k * 128, x.e * prm.N + x.p0);
     }
     __syncwarp();

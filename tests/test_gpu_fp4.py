@@ -482,6 +482,44 @@ def test_grouped_product_narrow_tiles(n):
     check_product(C[n:], a[n:], b[2], 544, "f32")
 
 
+# weights of more than 32 MB, asked for ahead of the kernel's turn
+@pytest.mark.parametrize("fmt,M,N,K", [("mx", 5, 16500, 4196), ("nv", 40, 9001, 8256), ("mx", 100, 66001, 1090)])
+def test_product_of_large_ragged_weights(fmt, M, N, K):
+    A, SA, a = operand(fmt, M, K, 21)
+    B, SB, b = operand(fmt, N, K, 22)
+    for _ in range(2):
+        C = torch.full((M, N), math.nan, device="cuda")
+        product(fmt, A, B, SA, SB, C, M, N, K)
+        check_product(C, a, b, K, "f32")
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_grouped_product_of_large_weights_right_after_routing(fmt):
+    # the kernel that writes the offsets is the one before; they hold anything until then
+    T, E, k, N, K = 12, 8, 2, 8200, 1100
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    B, SB, b = operand(fmt, E * N, K, 23)
+    b = b.view(E, N, -1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    experts, weights, slots = torch.empty((T, k), **i32), torch.empty((T, k), device="cuda"), torch.empty((T, k), **i32)
+    offsets, tokens = torch.empty(E + 1, **i32), torch.empty(T * k, **i32)
+    A, SA, a = operand(fmt, T * k, K, 24)
+    for fill in (0, -5, 2 ** 31 - 1, -2 ** 31, 11):
+        logits = torch.randn((T, E), generator=gen, device="cuda")
+        C = torch.full((T * k, N), math.nan, device="cuda")
+        offsets.fill_(fill)
+        pig.igemm_moe_route(logits, experts, weights, offsets, tokens, slots, T, E, k)
+        if fmt == "mx":
+            pig.igemm_mxfp4_grouped(A, B, SA, SB, offsets, C, T * k, E, N, K)
+        else:
+            pig.igemm_nvfp4_grouped(A, B, SA, SB, offsets, None, C, T * k, E, N, K)
+        ends = offsets.tolist()
+        assert ends == sorted(ends) and ends[-1] == T * k
+        for e in range(E):
+            if ends[e] < ends[e + 1]:
+                check_product(C[ends[e]:ends[e + 1]], a[ends[e]:ends[e + 1]], b[e], K, "f32")
+
+
 def test_grouped_product_alpha_per_expert():
     alpha = torch.tensor([0.5, -2.0, 3e-3], device="cuda")
     C, a, b = grouped("nv", [40, 9, 100], 300, 320, "f32", alpha=alpha)
