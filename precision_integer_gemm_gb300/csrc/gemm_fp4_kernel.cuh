@@ -29,6 +29,11 @@
 // 1024.  So a block has one joint wait for its 8 MMAs, and weights, activations and
 // scales each have a loading warp (one warp for all three took 1500 cycles a block).
 //
+// Few rows are bound by HBM: 16 x 28672 x 8192 nv takes 21.4 us, 6.2 TB/s (launch, first
+// stage and tail beside it).  Many rows are bound by the tensor core and its operands:
+// 8192^3 mx takes 155 us alone, 7.1 PFLOP/s, 1200 cycles a block where the MMAs take
+// 1024; back to back the power cap makes it 170 us.
+//
 // Warps 0-3 epilogue, 4 MMA issue, 5 weight loads, 6 activation loads, 7 scale loads,
 // 8 and up scales.  Persistent CTAs (or CTA pairs, or clusters that split k).  Every
 // wait is bounded.
