@@ -536,7 +536,7 @@ static int launch_choose_vpl(const RouteParams &p, int smem, cudaStream_t stream
 {
     constexpr int V = VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
     const bool vec = p.E % V == 0 && reinterpret_cast<uintptr_t>(p.logits) % (V * sizeof(T)) == 0;
-    // 16-bit logits of up to 256 experts, up to 8 choices and tokens for several blocks
+    // 16-bit logits of up to 256 experts, up to 8 choices and more tokens than a cluster's
     // (routing of 16384 x 256 bfloat16, 8 choices: 21.7 -> 17.5 us; 65536 x 128: 41.5 ->
     // 29.8; no case was slower)
     if constexpr (sizeof(T) == 2 && VPL <= 8)
