@@ -185,8 +185,8 @@ __device__ __forceinline__ Fp4Group fp4_groups32(const Fp4Params &prm, int e0, i
     const int lane = threadIdx.x & 31, e = e0 + lane;
     Fp4Group g = make_int4(0, 0, 0, 0);
     if (e < prm.experts) {
-        g.y = min(max(__ldcg(prm.offsets + e), 0), prm.rows);
-        g.z = min(max(__ldcg(prm.offsets + e + 1), g.y), prm.rows) - g.y;
+        g.y = min(max(ld_relaxed_s32(prm.offsets + e), 0), prm.rows);
+        g.z = min(max(ld_relaxed_s32(prm.offsets + e + 1), g.y), prm.rows) - g.y;
         g.w = (g.z + prm.qt - 1) / prm.qt;
     }
     int incl = g.w * prm.p_tiles;  // at most kFp4MaxTiles
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         uint32_t nacc = 0;
         for (int t = cid; t < tiles; t += ncl, ++nacc) {
             const Fp4Tile x = t == cid ? first : fp4_tile<Cfg>(prm, groups, t, pr);
-            const float alpha = prm.alpha ? __ldg(prm.alpha + x.e) : 1.0f;
+            const float alpha = prm.alpha ? prm.alpha[x.e] : 1.0f;
             const uint32_t ab = nacc & 1u;
             const int n = x.p0 + quad * 32 + lane;
             const uint32_t tacc = trow + ab * Cfg::kAcc1;

@@ -621,12 +621,13 @@ struct alignas(PER * sizeof(T)) MoeRun {
 // in the order of the choices.  Rows of whole 16- or 8-byte runs: one run, threads
 // laid over tokens and columns alike (4096 tokens x 8 bfloat16 rows of 4096: 48 us,
 // 0.93 of the copy rate).  Other rows: a block of threads per token and 128 RUNS PER
-// columns, so that the choices are read once for several narrow loads (rows of
-// 4095: 147 -> 72 us; of 4092, in 8-byte runs, that form took 66 us against 53).
+// columns, so that the choices are read once for several narrow loads (rows of 4095:
+// 147 -> 72 us; of 4092, in 8-byte runs, that form took 66 us against 53).  Those loads
+// are volatile, so all of them go out before the first sum (with plain ones rows of 4095
+// take 71 us against 63, of 4094 103 against 43, of 4092 59 against 49).
 template <class T, int PER, int RUNS>
-__global__ void __launch_bounds__(128) moe_combine_kernel(const T *__restrict__ Y, const int *__restrict__ slots,
-                                                          const float *__restrict__ weights, T *__restrict__ out,
-                                                          int Tn, int k, int N)
+__global__ void __launch_bounds__(128) moe_combine_kernel(const T *Y, const int *slots, const float *weights, T *out, int Tn,
+                                                          int k, int N)
 {
     using Run = MoeRun<T, PER>;
     overlap_wait();
@@ -655,9 +656,9 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const T *__restrict__ 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t at = t * k + j0 + j;
-            const int64_t s = j0 + j < k ? __ldg(slots + at) : -1;
+            const int64_t s = j0 + j < k ? slots[at] : -1;
             const bool live = s >= 0 && s < rows;
-            w[j] = live ? __ldg(weights + at) : 0.0f;
+            w[j] = live ? weights[at] : 0.0f;
 #pragma unroll
             for (int r = 0; r < RUNS; ++r) {
 #pragma unroll
@@ -666,9 +667,9 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const T *__restrict__ 
                 if (live && nr < N) {
                     const T *from = Y + s * N + nr;
                     if constexpr (sizeof(Run) == 16)
-                        *reinterpret_cast<uint4 *>(&v[j][r]) = __ldcs(reinterpret_cast<const uint4 *>(from));
+                        *reinterpret_cast<uint4 *>(&v[j][r]) = ld_stream_v4(from);
                     else
-                        v[j][r] = *reinterpret_cast<const Run *>(from);
+                        ld_once(v[j][r], from);
                 }
             }
         }

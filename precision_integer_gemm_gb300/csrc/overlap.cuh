@@ -22,6 +22,12 @@ __device__ __forceinline__ void overlap_begin()
 __device__ __forceinline__ void overlap_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void overlap_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// What such a kernel reads may be written until the wait returns, and the kernel's
+// life begins before that.  So it reads global memory with plain loads, or with the
+// volatile ones of ptx.cuh, and its pointers are not restrict: a read-only (.nc) load
+// promises memory that nobody writes during the kernel's life, and the compiler may
+// move one above the wait.
+
 // ... in clusters of `cluster` CTAs.
 template <class... Params, class... Args>
 int launch_overlapped_clusters(void (*kernel)(Params...), dim3 grid, int cluster, dim3 block, int smem,

@@ -16,6 +16,7 @@
 #include "launch.cuh"
 #include "fp4.cuh"
 #include "overlap.cuh"
+#include "ptx.cuh"
 
 namespace igemm {
 
@@ -164,7 +165,9 @@ struct Fp4Raw {
             if constexpr (!VEC) shift = static_cast<uint32_t>(at - first);
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(first) + i);
+                // (!VEC: volatile, 16384 x 8191 float32 100 us against 105 with plain loads)
+                const uint4 *piece = reinterpret_cast<const uint4 *>(first) + i;
+                const uint4 q = VEC ? *piece : ld_v4(piece);
                 w[4 * i] = q.x;
                 w[4 * i + 1] = q.y;
                 w[4 * i + 2] = q.z;
@@ -228,13 +231,13 @@ struct Fp4Raw {
 // the index after that in flight.  Bound by HBM where the rows are read once (16384 x
 // 8192: bfloat16 56 us, 6.0 TB/s; float32 90 us, 6.8 TB/s).
 template <bool NV, class T, bool VEC>
-__global__ void __launch_bounds__(256, VEC ? 5 : 4) pack_fp4_rows_kernel(const T *__restrict__ x, const Fp4PackParams p)
+__global__ void __launch_bounds__(256, VEC ? 5 : 4) pack_fp4_rows_kernel(const T *x, const Fp4PackParams p)
 {
     overlap_wait();
     const int k = (blockIdx.y * blockDim.x + threadIdx.x) * 16;
     const bool in_row = k < 2 * p.code_bytes;
     const bool last = k / 8 + 2 == p.code_bytes / 4;  // of the row: it writes the padding
-    const float g = NV && p.g ? __ldg(p.g) : 1.0f;
+    const float g = NV && p.g ? *p.g : 1.0f;
     __shared__ Fp4Factors<NV> factors;
     factors.fill(g);
     const float g6 = 6.0f * g;
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(256, VEC ? 5 : 4) pack_fp4_rows_kernel(const T
     const uint32_t rows = static_cast<uint32_t>(p.rows);
     const auto source = [&](uint32_t r) {
         if (r >= rows) return -1;
-        const int s = p.index ? __ldg(p.index + r) : static_cast<int>(r);
+        const int s = p.index ? p.index[r] : static_cast<int>(r);
         return s < p.x_rows ? s : -1;
     };
     Fp4Raw<T, VEC> raw;
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(256, VEC ? 5 : 4) pack_fp4_rows_kernel(const T
 // go through shared memory to leave as runs of 128 bytes.  Bound by HBM (28672 x 8192
 // float32: 158 us, 6.7 TB/s).
 template <bool NV, class T, int R>
-__global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__restrict__ x, const Fp4PackParams p)
+__global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *x, const Fp4PackParams p)
 {
     static_assert(R == 1 || sizeof(T) == 2, "pairs of 16-bit values");
     overlap_wait();
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *__res
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows;
     const int k0 = blockIdx.y * 256, k = k0 + 32 * warp;
-    const float g = NV && p.g ? __ldg(p.g) : 1.0f;
+    const float g = NV && p.g ? *p.g : 1.0f;
     factors.fill(g);
     const float g6 = 6.0f * g;
     float v[R][32];
@@ -428,9 +431,10 @@ static int launch_pack_format(const Fp4PackCall &c, cudaStream_t stream)
 // Packed rows copied to their places: zeros where the index is out of range.  A
 // thread takes one 16-byte piece of four rows, a quarter of the rows apart, all in
 // flight (four pieces in a row, each with its own division, took 64 instructions a
-// piece: 17.9 us for 32768 rows of 2304 bytes against 15.6).
-__global__ void __launch_bounds__(256) fp4_copy_rows_kernel(const uint4 *__restrict__ codes, const uint4 *__restrict__ scales,
-                                                            const Fp4PackParams p)
+// piece: 17.9 us for 32768 rows of 2304 bytes against 15.6).  (The index is read for
+// every quarter, the last row's where there is none: a branch around each of these loads
+// takes the whole call from 22.8 to 24.1 us.)
+__global__ void __launch_bounds__(256) fp4_copy_rows_kernel(const uint4 *codes, const uint4 *scales, const Fp4PackParams p)
 {
     overlap_wait();
     const uint32_t cq = p.code_bytes / 16, per_row = cq + p.pitch / 16;
@@ -444,14 +448,13 @@ __global__ void __launch_bounds__(256) fp4_copy_rows_kernel(const uint4 *__restr
     uint4 *to = code ? reinterpret_cast<uint4 *>(p.codes) + j : reinterpret_cast<uint4 *>(p.scales) + (j - cq);
     int src[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t r = row + i * quarter;
-        src[i] = r < rows ? __ldg(p.index + r) : -1;
-    }
+    for (int i = 0; i < 4; ++i) src[i] = p.index[min(row + i * quarter, rows - 1)];
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = src[i] >= 0 && src[i] < p.x_rows ? __ldg(from + src[i] * pitch) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (src[i] >= 0 && src[i] < p.x_rows) v[i] = from[src[i] * pitch];
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t r = row + i * quarter;
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(256) fp4_copy_rows_kernel(const uint4 *__restr
 
 // Rows that are gathered twice or more on average are packed once, into a workspace,
 // and copied from there, where that saves reading 32 MB of x at least: 32768 x 4096
-// nvfp4 rows of 4096 take 45.9 -> 23.1 us (float32 84 -> 30), and 8192 x 4096 of 4096
+// nvfp4 rows of 4096 take 45.9 -> 22.8 us (float32 84 -> 30), and 8192 x 4096 of 4096
 // 12.4 either way; with 28 MB saved the second launch and the workspace cost more
 // (4096 x 4096 of 512: 7.4 -> 9.3).
 static bool pack_once(const Fp4PackCall &c)

@@ -299,6 +299,44 @@ __device__ __forceinline__ bool wait_bounded_cluster(uint64_t *bar, uint32_t par
     }
 }
 
+// A word that another kernel may be writing: the L2's value, never a line that this
+// SM's L1 already holds.
+__device__ __forceinline__ int ld_relaxed_s32(const int *p)
+{
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// Global loads that stay behind a griddepcontrol.wait and in the order written (all are
+// volatile): 16 bytes; 16 bytes that nobody reads again; a T of 8, 4 or 2 bytes that no
+// other thread of this SM wants.
+__device__ __forceinline__ uint4 ld_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_stream_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+template <class T>
+__device__ __forceinline__ void ld_once(T &to, const void *p)
+{
+    static_assert(sizeof(T) == 8 || sizeof(T) == 4 || sizeof(T) == 2, "one load");
+    if constexpr (sizeof(T) == 8) {
+        uint2 &v = reinterpret_cast<uint2 &>(to);
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    } else if constexpr (sizeof(T) == 4) {
+        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(reinterpret_cast<uint32_t &>(to)) : "l"(p));
+    } else {
+        asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(reinterpret_cast<uint16_t &>(to)) : "l"(p));
+    }
+}
+
 // The box at (x, y) to L2.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, int y)
 {
