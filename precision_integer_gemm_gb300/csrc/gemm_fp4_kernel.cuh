@@ -109,7 +109,8 @@ struct Fp4Cfg {
     static constexpr int kMaxStages = 16;
     static constexpr int kNumBars = 2 * kMaxStages + 3 * kMaxScaleStages + 4 + 1 + 16;
     static constexpr int kStoreBytes = 4 * 2048;  // 16-bit C: 32 rows x 32 columns per epilogue warp
-    static constexpr int kTailBytes = 8 * kNumBars + 64 + 16;  // and the groups' table, 16 bytes each
+    static constexpr int kNoticeBytes = PAIR ? 16 * kMaxScaleStages : 0;
+    static constexpr int kTailBytes = 8 * kNumBars + 64 + 16 + kNoticeBytes;  // and the groups' table, 16 bytes each
     static constexpr int kNAlign = PAIR ? 32 : 16;
     static constexpr int kWarpMma = 4, kWarpLoadP = 5, kWarpLoadQ = 6, kWarpLoadS = 7, kWarpScale = 8;
     static constexpr int kThreads = 32 * (kWarpScale + 1 + kQGroups);
@@ -221,13 +222,17 @@ __device__ __forceinline__ bool fp4_warp_wait(uint64_t *bar, uint32_t parity, co
     return __all_sync(0xffffffffu, ok);
 }
 
-// Three barriers (their tests overlap when they are already complete).
+// Three barriers (their tests overlap when they are already complete).  PAIR: the third
+// acquires at cluster scope, for what threads of the odd CTA wrote.
+template <bool PAIR>
 __device__ __forceinline__ bool fp4_warp_wait3(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb, uint64_t *c,
                                                uint32_t pc, const Watchdog &wd)
 {
-    const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb), rc = mbar_try_wait(c, pc);
+    const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+    const bool rc = PAIR ? mbar_try_wait_cluster(c, pc) : mbar_try_wait(c, pc);
     if (__all_sync(0xffffffffu, ra && rb && rc)) return true;
-    const bool ok = wait_bounded(a, pa, wd) && wait_bounded(b, pb, wd) && wait_bounded(c, pc, wd);
+    const bool ok = wait_bounded(a, pa, wd) && wait_bounded(b, pb, wd) &&
+                    (PAIR ? wait_bounded_cluster(c, pc, wd) : wait_bounded(c, pc, wd));
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -443,7 +448,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint64_t *empty = full + Cfg::kMaxStages;       // [stages] codes consumed (MMA commit)
     uint64_t *sf_raw = empty + Cfg::kMaxStages;     // [scale stages] scale rows landed
     uint64_t *sf_full = sf_raw + Cfg::kMaxScaleStages;    // [scale stages] ... turned (scale warps; even CTA of a pair:
-                                                          // and the odd CTA's, its relay)
+                                                          // and the odd CTA's, its relay's copy)
     uint64_t *sf_empty = sf_full + Cfg::kMaxScaleStages;  // [scale stages] consumed (MMA commit)
     uint64_t *acc_full = sf_empty + Cfg::kMaxScaleStages; // [2] accumulator complete (commit)
     uint64_t *acc_empty = acc_full + 2;             // [2] accumulator (its overlap) read by the epilogue warps
@@ -453,7 +458,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *total_slot = reinterpret_cast<int *>(tmem_slot + 2);
-    Fp4Group *groups = reinterpret_cast<Fp4Group *>(smem + ((prm.off_bars + 8 * Cfg::kNumBars + 64 + 15) & ~15));
+    uint8_t *notices = smem + ((prm.off_bars + 8 * Cfg::kNumBars + 64 + 15) & ~15);  // [scale stages][16], never read
+    Fp4Group *groups = reinterpret_cast<Fp4Group *>(notices + Cfg::kNoticeBytes);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -472,7 +478,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         if (lane < prm.scale_stages) {
             mbar_init(&sf_raw[lane], 1);
             mbar_init(&sf_empty[lane], 1);
-            mbar_init(&sf_full[lane], 1 + Cfg::kQGroups + (PAIR && leader ? 1 : 0));
+            mbar_init(&sf_full[lane], 1 + Cfg::kQGroups);
         }
         if (lane < 2) {
             mbar_init(&acc_full[lane], 1);
@@ -642,6 +648,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(codes));
             const uint64_t sdesc0 = sdesc_rows16(smem_u32(scales));
             uint32_t nacc = 0, g = 0;
+            const uint32_t slots = (1u << prm.scale_stages) - 1u;
             bool ok = true;
             for (int t = cid; ok && t < tiles; t += ncl, ++nacc) {
                 const Fp4Tile x = t == cid ? first : fp4_tile<Cfg>(prm, groups, t, pr);
@@ -651,15 +658,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 const uint32_t d_tmem = tmem + ab * Cfg::kAcc1;
                 if constexpr (Cfg::kOverlap > 0) {
                     // the tile before has left the columns that both accumulators use
-                    if (nacc > 0 && !fp4_warp_wait(&acc_empty[ab ^ 1u], ((nacc - 1u) >> 1) & 1u, wd)) break;
+                    ok = nacc == 0 || fp4_warp_wait(&acc_empty[ab ^ 1u], ((nacc - 1u) >> 1) & 1u, wd);
                 } else {
-                    if (!fp4_warp_wait(&acc_empty[ab], ((nacc >> 1) & 1u) ^ 1u, wd)) break;
+                    ok = fp4_warp_wait(&acc_empty[ab], ((nacc >> 1) & 1u) ^ 1u, wd);
                 }
+                if (!ok) break;
                 for (int b = b0; b < b1; ++b, ++g) {
                     const Fp4Ring c0 = cr;
                     cr.next();
-                    if (!fp4_warp_wait3(&full[c0.slot], c0.phase, &full[cr.slot], cr.phase, &sf_full[fr.slot], fr.phase,
-                                        wd)) {
+                    if (!fp4_warp_wait3<PAIR>(&full[c0.slot], c0.phase, &full[cr.slot], cr.phase, &sf_full[fr.slot],
+                                              fr.phase, wd)) {
                         ok = false;
                         break;
                     }
@@ -729,18 +737,32 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 else
                     mma_commit(mma_drain);
             }
+            // gave up: the odd CTA's notices of the blocks ahead may be on their way here
+            if (PAIR && !ok) {
+                const uint32_t behind = (1u << fr.slot) - 1u;  // slots whose next phase is the other one
+                fp4_drain(sf_full, slots, fr.phase ? slots & ~behind : behind, globaltimer_ns(), prm.limit_ns);
+            }
+            __syncwarp();
         } else {
-            // relay of the odd CTA: its scales of each block, in order, to the even CTA's
-            // MMA warp (an arrival from the warps that wrote them took about 1100
-            // cycles, their release to the other CTA; this warp wrote nothing)
-            const uint32_t peer = cluster_map(smem_u32(sf_full), 0u);
+            // relay of the odd CTA: each block whose scales are turned is announced to the
+            // even CTA's MMA warp by copying 16 bytes of them there.  What the scale warps wrote
+            // comes before this warp's wait, so before the copy (which reads it, through the
+            // proxy of tcgen05.cp), so before the copy's completion, a release at cluster
+            // scope that the MMA warp acquires.  An arrival with .release.cluster says the same
+            // with a fence of its own, 1100 cycles and more: 8192^3 mx 240 us by one warp, 168
+            // by two, 163 with copies; 512 x 8192 x 8192 26.7, 19.3 and 17.3.
+            const uint32_t peer = cluster_map(smem_u32(sf_full), 0u), notice = cluster_map(smem_u32(notices), 0u);
             Fp4Ring fr(prm.scale_stages);
             bool ok = true;
             for (int t = cid; ok && t < tiles; t += ncl) {
                 for (int b = b0; b < b1; ++b) {
                     ok = fp4_warp_wait(&sf_full[fr.slot], fr.phase, wd);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_peer(peer + 8u * static_cast<uint32_t>(fr.slot));
+                    if (elect_one())
+                        bulk_copy_to_cta(notice + 16u * static_cast<uint32_t>(fr.slot),
+                                         scales + fr.slot * Cfg::kScaleStage, 16,
+                                         peer + 8u * static_cast<uint32_t>(fr.slot));
+                    __syncwarp();
                     fr.next();
                 }
             }
@@ -785,7 +807,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 }
                 fence_proxy_async_smem();  // read next by tcgen05.cp
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sf_full[fr.slot]);
+                if (lane == 0) {
+                    if (PAIR && leader && group == 0)
+                        mbar_arrive_expect_tx(&sf_full[fr.slot], 16);  // the odd CTA's notice
+                    else
+                        mbar_arrive(&sf_full[fr.slot]);
+                }
                 fr.next();
             }
         }
@@ -856,8 +883,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         if (c + j < c1) fp4_store1(prm, s[j] * alpha, static_cast<int64_t>(x.q0) + rank * per + c + j, n);
                 }
                 __syncwarp();
-                if (lane < cs && lane != rank)
-                    mbar_arrive_peer(cluster_map(smem_u32(&red_empty[bar]), static_cast<uint32_t>(lane)));
+                // read: the other CTAs may write again, where a later tile does (the release at
+                // cluster scope is a fence: 16 x 28672 x 8192 mxfp4 20.3 us, 20.6 with one after
+                // the last tile too)
+                if (t + static_cast<int64_t>(Cfg::kRedBufs) * ncl < tiles && lane < cs && lane != rank)
+                    mbar_arrive_remote(cluster_map(smem_u32(&red_empty[bar]), static_cast<uint32_t>(lane)));
                 continue;
             }
             const int n0 = x.p0 + quad * 32;

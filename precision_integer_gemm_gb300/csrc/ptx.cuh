@@ -281,6 +281,19 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
     return ok != 0;
 }
 
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // wait_bounded for a barrier whose arrivals come from other CTAs of the
 // cluster (their writes before the arrival are visible after it).
 __device__ __forceinline__ bool wait_bounded_cluster(uint64_t *bar, uint32_t parity, const Watchdog &wd)
@@ -335,6 +348,18 @@ __device__ __forceinline__ void ld_once(T &to, const void *p)
     } else {
         asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(reinterpret_cast<uint16_t &>(to)) : "l"(p));
     }
+}
+
+// `bytes` (a multiple of 16) of this CTA's shared memory into another CTA of the
+// cluster; they count on that CTA's mbarrier `bar_cluster`, and their completion
+// releases at cluster scope what came before the copy.
+__device__ __forceinline__ void bulk_copy_to_cta(uint32_t cluster_addr, const void *from, uint32_t bytes,
+                                                 uint32_t bar_cluster)
+{
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     cluster_addr),
+                 "r"(smem_u32(from)), "r"(bytes), "r"(bar_cluster)
+                 : "memory");
 }
 
 // The box at (x, y) to L2.

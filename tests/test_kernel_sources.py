@@ -22,3 +22,17 @@ def test_kernels_set_up_early_make_no_read_only_loads(name):
     assert "griddepcontrol.wait" in code or "overlap" in code or name == "gemm_fp4.cuh"
     for word in ("__ldg", "__ldcg", "__ldcs", "__restrict__", "ld.global.nc"):
         assert word not in code, word
+
+
+def test_hand_overs_between_the_ctas_of_a_4_bit_product():
+    # mbar_arrive_peer does not release at cluster scope: it may only hand over tensor memory that was read, never
+    # shared memory that threads wrote (a pair's scales) or read (the partials of a split k)
+    code = code_of("gemm_fp4_kernel.cuh")
+    targets = re.findall(r"mbar_arrive_peer\(([^;]*)\);", code)
+    assert targets and all(t.startswith("empty_leader") for t in targets), targets
+    assert re.search(r"mbar_arrive_remote\(cluster_map\(smem_u32\(&red_empty", code)
+    # ... and what waits for them acquires at cluster scope
+    assert re.search(r"PAIR \? mbar_try_wait_cluster\(c, pc\)", code) and "wait_bounded_cluster(c, pc, wd)" in code
+    assert re.search(r"fp4_warp_wait3<PAIR>\([^;]*&sf_full\[", code)
+    waits = re.findall(r"(\w+)\(&red_(?:empty|full)\[bar\], rph", code)
+    assert len(waits) == 2 and set(waits) == {"fp4_warp_wait_cluster"}
