@@ -120,6 +120,8 @@ struct SsCfg {
     // converts the stages of the ring slots s with s % 2 == b (ST even)
     static constexpr int kConvSets = kPackedP ? 2 : 0;
     static constexpr int kConvPerStage = kKB;  // converter sets that arrive on a stage's conv barrier
+    static constexpr int kOffNotice = kOffMisc + 16;  // packed P on pairs: [ST][16], never read
+    static_assert(16 + 16 * ST_ <= 128, "notices");
     static constexpr int kOffPSum = kOffMisc + 128;  // packed P: [2][128] row sums of a unit's codes
     static constexpr int kSmemBytes = kOffPSum + (kPackedP ? 2 * 128 * 4 : 0) + 1024;  // + alignment slack
     // MMA issuing threads (lane 0 of warp 4 and, for two, of warp 6), taking
@@ -283,13 +285,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 {
     constexpr int ST = Cfg::ST, QA = Cfg::QA;
     constexpr bool kPair = Cfg::CL == 2;
+    constexpr bool kNotice = kPair && Cfg::kPackedP;  // threads write a CTA's operand: see the relay
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *stages = smem + Cfg::kOffStages;
     uint8_t *cstage = smem + Cfg::kOffCStage;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBars);
     uint64_t *full = bars;              // [ST] this CTA's part of a stage landed (1 arrival + tx)
-    uint64_t *pfull = full + ST;        // [ST] pair: the odd CTA's part landed (relay, even CTA only)
+    // [ST] pair: the odd CTA's part landed (even CTA only; its relay's arrival, or with
+    // kNotice its copy of 16 bytes, that the MMA thread expects)
+    uint64_t *pfull = full + ST;
     uint64_t *empty = pfull + ST;       // [ST] stage consumed (MMA commit)
     uint64_t *acc_full = empty + ST;    // [2] accumulator complete (commit)
     uint64_t *acc_empty = acc_full + 2; // [2] accumulator drained (the epilogue warps of the pair)
@@ -454,7 +459,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 const uint32_t ab = nacc % Cfg::kAccBufs;
                 const uint32_t aph = (nacc / Cfg::kAccBufs) & 1u;
                 const uint32_t d_tmem = tmem + ab * Cfg::kAccCols;
-                if (!wait_bounded(&acc_empty[ab], aph ^ 1u, wd)) break;
+                if (!wait_bounded(&acc_empty[ab], aph ^ 1u, wd)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const int nst = (x.nkb + Cfg::kKB - 1) / Cfg::kKB;
                 for (int j = 0; j < nst; ++j, ++g) {
@@ -462,11 +470,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                     if (s % Cfg::kMmaIssuers != jm) continue;
                     const uint32_t ph = (g / ST) & 1u;
                     // this CTA's stage landed (packed P: and converted), and the odd CTA's
-                    if (!wait_bounded(Cfg::kPackedP ? &conv[s] : &full[s], ph, wd) ||
-                        (kPair && !wait_bounded(&pfull[s], ph, wd))) {
-                        ok = false;
-                        break;
+                    ok = wait_bounded(Cfg::kPackedP ? &conv[s] : &full[s], ph, wd);
+                    if constexpr (kNotice) {
+                        mbar_arrive_expect_tx(&pfull[s], 16);
+                        ok = ok && (mbar_try_wait_cluster(&pfull[s], ph) || wait_bounded_cluster(&pfull[s], ph, wd));
+                    } else if constexpr (kPair) {
+                        ok = ok && wait_bounded(&pfull[s], ph, wd);
                     }
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t a_base = smem_u32(stages + s * Cfg::kStage);
                     const uint32_t b_base = a_base + Cfg::kStageA;
@@ -506,10 +517,24 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 mma_commit_pair(mma_drain);
             else
                 mma_commit(mma_drain);
+            // gave up: the odd CTA's notices of the stages ahead may be on their way here
+            if (kNotice && !ok) {
+                const uint64_t t0 = globaltimer_ns();
+                for (uint32_t n = g; n < g + ST; ++n)
+                    while (!mbar_try_wait(&pfull[n % ST], (n / ST) & 1u) && globaltimer_ns() - t0 < prm.limit_ns) {
+                    }
+            }
         } else if (kPair && !leader && warp == 4 && lane == 0) {
             // -------------------------------------------------------- relay (odd CTA of a pair)
-            // each stage of this CTA that landed, in order, to the even CTA's MMA thread
+            // each stage of this CTA that landed, in order, to the even CTA's MMA thread.
+            // Packed P: the codes were written by threads, so their hand-over has to release
+            // at cluster scope.  16 bytes of them are copied there: the codes come before
+            // this thread's wait, so before the copy (it reads them, through the MMA's
+            // proxy), so before its completion, which releases at cluster scope.  (An arrival
+            // with .release.cluster waits for a fence at every stage: W4A8 512 x 28672 x 8192
+            // 339 us against 148.)
             const uint32_t pfull_remote = cluster_map(smem_u32(pfull), 0u);
+            const uint32_t notice_remote = cluster_map(smem_u32(smem + Cfg::kOffNotice), 0u);
             uint32_t g = 0;
             bool ok = true;
             const int n_dp = ss_dp_units(prm, cid, ncl), n_units = ss_units(prm, cid, ncl);
@@ -522,7 +547,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         ok = false;
                         break;
                     }
-                    mbar_arrive_peer(pfull_remote + 8u * static_cast<uint32_t>(s));
+                    if constexpr (kNotice)
+                        bulk_copy_to_cta(notice_remote + 16u * static_cast<uint32_t>(s), stages + s * Cfg::kStage, 16,
+                                         pfull_remote + 8u * static_cast<uint32_t>(s));
+                    else
+                        mbar_arrive_peer(pfull_remote + 8u * static_cast<uint32_t>(s));
                 }
             }
         }

@@ -36,3 +36,16 @@ def test_hand_overs_between_the_ctas_of_a_4_bit_product():
     assert re.search(r"fp4_warp_wait3<PAIR>\([^;]*&sf_full\[", code)
     waits = re.findall(r"(\w+)\(&red_(?:empty|full)\[bar\], rph", code)
     assert len(waits) == 2 and set(waits) == {"fp4_warp_wait_cluster"}
+
+
+def test_hand_overs_between_the_ctas_of_a_pair():
+    # the same in the integer GEMMs' kernel: where the operand comes from TMA its relay may arrive without cluster
+    # scope, where threads wrote it (packed weights) it sends a notice that the MMA threads acquire at cluster scope
+    code = code_of("gemm_ss_kernel.cuh")
+    peers = [m.start() for m in re.finditer(r"mbar_arrive_peer\(", code)]
+    assert len(peers) == 2
+    relay = [p for p in peers if code[p:].startswith("mbar_arrive_peer(pfull_remote")]
+    assert len(relay) == 1 and re.search(r"if constexpr \(kNotice\)\s+bulk_copy_to_cta\([^;]*;\s+else\s+$",
+                                         code[:relay[0]])
+    assert re.search(r"kNotice\) \{\s+mbar_arrive_expect_tx\(&pfull\[s\], 16\);[^}]*wait_bounded_cluster\(&pfull\[s\]", code)
+    assert "kNotice = kPair && Cfg::kPackedP" in code
