@@ -678,17 +678,18 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             // load waits about a microsecond behind the operand stream; one per
             // chunk serialised the epilogue): this thread's P row sum, and the Q
             // tile's sums spread over the lanes (lane l holds entries kQPer * l ..),
-            // read back by shuffles.
+            // read back by shuffles.  (Plain loads: the preparation pass writes the sums
+            // while this kernel is already set up.)
             constexpr int kQPer = Cfg::QA / 32;  // 8 (int4 x int4) or 4 (W4A8)
             int sp = 0;
             int4 qs0 = make_int4(0, 0, 0, 0), qs1 = qs0;
             if constexpr (!Cfg::kFloat) {
                 if (first) {
-                    if constexpr (!Cfg::kPackedP) sp = __ldg(prm.sumP + min(x.p0 + p, prm.p_rows - 1));
+                    if constexpr (!Cfg::kPackedP) sp = prm.sumP[min(x.p0 + p, prm.p_rows - 1)];
                     // (the sums arrays are padded past the last row by more than a tile)
                     const int4 *sq = reinterpret_cast<const int4 *>(prm.sumQ + x.q0) + (kQPer / 4) * lane;
-                    qs0 = __ldg(sq);
-                    if constexpr (kQPer == 8) qs1 = __ldg(sq + 1);
+                    qs0 = sq[0];
+                    if constexpr (kQPer == 8) qs1 = sq[1];
                 }
             }
             const uint32_t ab = nacc % Cfg::kAccBufs;

@@ -49,3 +49,11 @@ def test_hand_overs_between_the_ctas_of_a_pair():
                                          code[:relay[0]])
     assert re.search(r"kNotice\) \{\s+mbar_arrive_expect_tx\(&pfull\[s\], 16\);[^}]*wait_bounded_cluster\(&pfull\[s\]", code)
     assert "kNotice = kPair && Cfg::kPackedP" in code
+
+
+def test_row_sums_of_the_preparation_pass_are_not_read_through_read_only_loads():
+    # that pass and the GEMM overlap, as above (the operands' bytes themselves come by TMA)
+    code = code_of("gemm_ss_kernel.cuh")
+    assert "prm.sumP" in code and "prm.sumQ" in code
+    for word in ("__ldg", "__restrict__", "ld.global.nc"):
+        assert word not in code, word
