@@ -822,7 +822,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         uint8_t *stage = smem + prm.off_store + quad * 2048;
         const uint32_t empty_leader = PAIR ? cluster_map(smem_u32(acc_empty), 0u) : 0u;
-        uint32_t nacc = 0;
+        uint32_t nacc = 0, armed = 0;  // armed: split k, tiles whose partials this warp expects
+        bool ok = true;
         for (int t = cid; t < tiles; t += ncl, ++nacc) {
             const Fp4Tile x = t == cid ? first : fp4_tile<Cfg>(prm, groups, t, pr);
             const float alpha = prm.alpha ? prm.alpha[x.e] : 1.0f;
@@ -839,7 +840,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         mbar_arrive_peer(empty_leader + 8u * ab);
                 }
             };
-            if (!fp4_warp_wait(&acc_full[ab], (nacc >> 1) & 1u, wd)) break;
+            ok = fp4_warp_wait(&acc_full[ab], (nacc >> 1) & 1u, wd);
+            if (!ok) break;
             tc_fence_after();
             if (cs > 1) {
                 // split k: every CTA sends its partial of columns r BN / cs .. to CTA r of the
@@ -849,7 +851,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 const uint32_t rb = nacc % Cfg::kRedBufs, rph = (nacc / Cfg::kRedBufs) & 1u, bar = rb * 4 + quad;
                 uint4 *buf = reinterpret_cast<uint4 *>(red) + rb * (BN * 32) + quad * 32 + lane;
                 if (lane == 0) mbar_arrive_expect_tx(&red_full[bar], static_cast<uint32_t>((cs - 1) * per * 128));
-                if (!fp4_warp_wait_cluster(&red_empty[bar], rph ^ 1u, wd)) break;
+                ++armed;
+                ok = fp4_warp_wait_cluster(&red_empty[bar], rph ^ 1u, wd);
+                if (!ok) break;
 #pragma unroll 1
                 for (int c0 = 0; c0 < BN; c0 += 16) {
                     uint32_t v[16];
@@ -867,7 +871,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                     }
                 }
                 release();
-                if (!fp4_warp_wait_cluster(&red_full[bar], rph, wd)) break;
+                ok = fp4_warp_wait_cluster(&red_full[bar], rph, wd);
+                if (!ok) break;
                 const int c1 = min(per, x.nq - rank * per);
                 for (int c = 0; c < c1; c += 4) {
                     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -895,6 +900,18 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 fp4_store_tile<Cfg, true>(prm, x, tacc, ab, alpha, n0, stage, release);
             else
                 fp4_store_tile<Cfg, false>(prm, x, tacc, ab, alpha, n0, stage, release);
+        }
+        // gave up: another CTA's partials of this tile, and of the next with two buffers,
+        // may be on their way here
+        if (cs > 1 && !ok) {
+            const uint64_t t0 = globaltimer_ns();
+            for (uint32_t n = nacc; n < nacc + Cfg::kRedBufs; ++n) {
+                uint64_t *bar = &red_full[n % Cfg::kRedBufs * 4 + quad];
+                if (lane == 0 && n >= armed)
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>((cs - 1) * (BN / cs) * 128));
+                while (!mbar_try_wait(bar, (n / Cfg::kRedBufs) & 1u) && globaltimer_ns() - t0 < prm.limit_ns) {
+                }
+            }
         }
     }
 

@@ -57,3 +57,14 @@ def test_row_sums_of_the_preparation_pass_are_not_read_through_read_only_loads()
     assert "prm.sumP" in code and "prm.sumQ" in code
     for word in ("__ldg", "__restrict__", "ld.global.nc"):
         assert word not in code, word
+
+
+def test_a_split_k_that_gave_up_waits_for_the_partials_on_their_way():
+    # a CTA may not leave while another one's st.async may still land in its shared memory: every way out of the
+    # epilogue's loop by an expired wait ends in a bounded wait for what the other CTAs send
+    code = code_of("gemm_fp4_kernel.cuh")
+    epilogue = code[code.index("const uint32_t empty_leader"):code.index("griddepcontrol.launch_dependents")]
+    assert "st_async_v4" in epilogue and not re.search(r"wait\w*\([^;]*\)\) break;", epilogue)
+    assert epilogue.count("if (!ok) break;") == 3
+    drain = epilogue[epilogue.index("if (cs > 1 && !ok)"):]
+    assert "&red_full[" in drain and re.search(r"while \(!mbar_try_wait\([^;]*globaltimer_ns\(\) - t0 < prm.limit_ns", drain)
