@@ -32,8 +32,9 @@ struct Fp4Plan {
 };
 
 // The kernel, tile and split for a call; max_clusters(bn, pair, csize) says how
-// many clusters of a kernel fit at once.
-int fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *plan);
+// many clusters of a kernel fit at once (0: none, and the plan does without it).
+// False if not even a single CTA fits.
+bool fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *plan);
 
 int launch_fp4_mx(const Fp4Call &c, cudaStream_t stream);
 int launch_fp4_nv(const Fp4Call &c, cudaStream_t stream);

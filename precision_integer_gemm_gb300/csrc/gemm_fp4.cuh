@@ -34,25 +34,24 @@ struct Fp4Smem {
     }
 };
 
-// Clusters of `csize` CTAs of igemm_fp4_kernel<Cfg> that can be resident at once
-// (asked once per device and size); sets the kernel's shared-memory limit.
+// Clusters of `csize` CTAs of igemm_fp4_kernel<Cfg> that can be resident at once, 0 if
+// none fits (asked once per device and size); sets the kernel's shared-memory limit.
 template <class Cfg>
 int fp4_clusters(int csize)
 {
     static std::mutex mu;
-    static std::atomic<int> cache[64][4] = {};  // (a small call asks several times: no lock once known)
+    // one more than the clusters (a small call asks several times: no lock once known)
+    static std::atomic<int> cache[64][4] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     const int slot = csize == 1 ? 0 : csize == 2 ? 1 : csize == 4 ? 2 : 3;
-    if (const int known = cache[dev][slot].load(std::memory_order_acquire)) return known;
+    if (const int known = cache[dev][slot].load(std::memory_order_acquire)) return known - 1;
     std::lock_guard<std::mutex> lock(mu);
     if (!cache[dev][slot]) {
         auto kernel = igemm_fp4_kernel<Cfg>;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
-            return 0;
-        if (csize == 1) {
-            cache[dev][slot] = sm_count();
-        } else {
+        int n = sm_count();
+        cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (rc == cudaSuccess && csize > 1) {
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -64,12 +63,15 @@ int fp4_clusters(int csize)
             cfg.dynamicSmemBytes = 227 * 1024;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) return 0;
-            cache[dev][slot] = n;
+            rc = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
         }
+        if (rc != cudaSuccess) {
+            cudaGetLastError();  // (the launch of another kernel is not to report it)
+            return 0;
+        }
+        cache[dev][slot].store(std::max(n, 0) + 1, std::memory_order_release);
     }
-    return cache[dev][slot];
+    return cache[dev][slot] - 1;
 }
 
 template <class Cfg>
@@ -185,8 +187,7 @@ template <bool NV>
 int launch_fp4_format(const Fp4Call &c, cudaStream_t stream)
 {
     Fp4Plan plan;
-    const int rc = fp4_plan(c, fp4_max_clusters<NV>, &plan);
-    if (rc != kOk) return rc;
+    if (!fp4_plan(c, fp4_max_clusters<NV>, &plan)) return kCudaError;
     if (plan.pair) return launch_fp4_cfg<Fp4Cfg<NV, 256, true>>(c, plan, stream);
     switch (plan.bn) {
     case 16: return launch_fp4_cfg<Fp4Cfg<NV, 16, false>>(c, plan, stream);

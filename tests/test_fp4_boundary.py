@@ -123,3 +123,22 @@ class FakeLogits:
 
     def data_ptr(self):
         return FAKE
+
+
+def test_plan_without_the_clusters_that_do_not_fit(tmp_path):
+    import os
+    import shutil
+    import subprocess
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    csrc, cuda = os.path.join(root, "precision_integer_gemm_gb300", "csrc"), "/usr/local/cuda/include"
+    if not shutil.which("g++") or not os.path.isdir(cuda):
+        pytest.skip("g++ or the CUDA headers are missing")
+    exe = str(tmp_path / "fp4_plan_check")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", csrc, "-I", cuda, "-x", "c++",
+                        os.path.join(root, "tests", "c", "fp4_plan_check.cpp"), os.path.join(csrc, "fp4_plan.cu"),
+                        "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout[:2000]
+    assert r.stdout.startswith("fp4 plan ok")
