@@ -55,9 +55,10 @@ bool fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *pl
     }
     if (typical > 128) {
         // one group: as many equal tiles as fill the last wave best
-        const int least = c.offsets ? 1 : (c.rows + 255) / 256;
-        for (int n = least; n <= (c.offsets ? 1 : least + 2); ++n)
-            consider(256, true, 1, c.offsets ? 256 : std::min(256, ((c.rows + n - 1) / n + 31) / 32 * 32));
+        const int64_t least = c.offsets ? 1 : (int64_t(c.rows) + 255) / 256;
+        for (int64_t n = least; n <= (c.offsets ? 1 : least + 2); ++n)
+            consider(256, true, 1,
+                     c.offsets ? 256 : static_cast<int>(std::min<int64_t>(256, ((c.rows + n - 1) / n + 31) / 32 * 32)));
     }
     if (best < 0) consider(128, false, 1, 128);  // (no pairs, and more rows than the loop above takes)
     if (best < 0) return false;

@@ -146,7 +146,9 @@ __device__ __forceinline__ Fp4Tile fp4_tile_of(const Fp4Params &prm, int e, int 
     x.p0 = ((first + r - qi * gsize) * Cfg::CL + rank) * 128;
     // equal tiles (of whole MMA columns): a short last one would load its weights
     // for little
-    const int per = ((count + q_tiles - 1) / q_tiles + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1);
+    // (unsigned: rows and tiles together may pass 2^31)
+    const int per = static_cast<int>((static_cast<uint32_t>(count) + q_tiles - 1) / q_tiles + Cfg::kNAlign - 1) &
+                    ~(Cfg::kNAlign - 1);
     x.q0 = begin + qi * per;
     x.nq = min(count - qi * per, per);
     return x;

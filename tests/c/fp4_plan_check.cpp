@@ -50,6 +50,17 @@ int main()
                                     check(per * (p.cs - 1) < blocks, "empty slice", c);
                                     check(p.qt > 0 && p.qt <= p.bn && p.group_p >= 1, "tiles", c);
                                 }
+    // as many rows as an int holds less the margin that the entry points keep
+    g_singles = 152, g_clusters = 36, g_pairs = 76;
+    for (int rows : {0x7FFFFFFF - 512, 0x7FFFFFFF - (1 << 22), 0x7FFFFFFF - (1 << 23), 2000000000})
+        for (int experts : {0, 1, 7, 1024}) {
+            Fp4Call c{};
+            c.rows = rows, c.N = 1, c.K = 32;
+            c.experts = experts ? experts : 1;
+            c.offsets = experts ? &some_offsets : nullptr;
+            Fp4Plan p{};
+            check(fp4_plan(c, fit, &p) && p.pair && p.qt >= 224 && p.qt <= 256, "most rows", c);
+        }
     if (failures) return 1;
     std::printf("fp4 plan ok: %d plans\n", plans);
     return 0;
