@@ -632,19 +632,20 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const T *Y, const int 
     using Run = MoeRun<T, PER>;
     overlap_wait();
     int64_t t;
-    int n;
+    uint32_t n;  // (unsigned: a row's last threads may lie past 2^31)
     if constexpr (RUNS == 1) {
         const uint32_t per_row = static_cast<uint32_t>(N / PER);
         const uint64_t item = static_cast<uint64_t>(blockIdx.x) * 128 + threadIdx.x;
         t = static_cast<int64_t>(item / per_row);
         if (t >= Tn) return;
-        n = static_cast<int>(item - static_cast<uint64_t>(t) * per_row) * PER;
+        n = static_cast<uint32_t>(item - static_cast<uint64_t>(t) * per_row) * PER;
     } else {
-        const uint32_t chunks = static_cast<uint32_t>((N + 128 * RUNS * PER - 1) / (128 * RUNS * PER));
+        const uint32_t chunks = (static_cast<uint32_t>(N) + 128 * RUNS * PER - 1) / (128 * RUNS * PER);
         t = blockIdx.x / chunks;
-        n = static_cast<int>(blockIdx.x - static_cast<uint32_t>(t) * chunks) * (128 * RUNS * PER) + threadIdx.x * PER;
+        n = (blockIdx.x - static_cast<uint32_t>(t) * chunks) * (128 * RUNS * PER) + threadIdx.x * PER;
     }
     const int64_t rows = static_cast<int64_t>(Tn) * k;
+    const uint32_t width = static_cast<uint32_t>(N);
     float acc[RUNS][PER];
 #pragma unroll
     for (int r = 0; r < RUNS; ++r)
@@ -663,8 +664,8 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const T *Y, const int 
             for (int r = 0; r < RUNS; ++r) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) v[j][r].v[i] = T(0.0f);
-                const int nr = n + r * (128 * PER);
-                if (live && nr < N) {
+                const uint32_t nr = n + r * (128 * PER);
+                if (live && nr < width) {
                     const T *from = Y + s * N + nr;
                     if constexpr (sizeof(Run) == 16)
                         *reinterpret_cast<uint4 *>(&v[j][r]) = ld_stream_v4(from);
@@ -682,8 +683,8 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const T *Y, const int 
     }
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-        const int nr = n + r * (128 * PER);
-        if (nr >= N) break;
+        const uint32_t nr = n + r * (128 * PER);
+        if (nr >= width) break;
         Run o;
 #pragma unroll
         for (int i = 0; i < PER; ++i) moe_out(&o.v[i], acc[r][i]);

@@ -67,3 +67,25 @@ def test_product_of_nearly_2_to_31_rows(groups):
     want = torch.einsum("rk,rnk->rn", mx_values(A[rows], SA[rows]), b)
     assert torch.equal(C[rows].double(), want)
     assert bool((buf[M * N:] == -777).all())
+
+
+@pytest.mark.parametrize("N,start", [(2 ** 31 - 101, 0), (2 ** 31 - 2, 0), (2 ** 31 - 2, 1)])
+def test_combine_of_rows_of_nearly_2_to_31(N, start):
+    # two tokens of two rows, neither a multiple of a wide load; `start`: off 4 bytes
+    needs(30)
+    T, k = 2, 2
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    Y = torch.empty((T * k * N + start,), dtype=torch.bfloat16, device="cuda")
+    Y.random_(-64, 64, generator=gen)
+    Y = Y[start:].view(T * k, N)
+    slots = torch.tensor([[3, 0], [1, 2]], dtype=torch.int32, device="cuda")
+    weights = torch.tensor([[0.5, -2.0], [1.0, 0.25]], device="cuda")
+    buf = torch.full((T * N + 4096,), -777.0, dtype=torch.bfloat16, device="cuda")
+    pig.igemm_moe_combine(Y, slots, weights, buf[:T * N].view(T, N), T, k, N)
+    for t in range(T):
+        for at in range(0, N, 1 << 28):
+            part = slice(at, min(at + (1 << 28), N))
+            # small integers times powers of two: the float32 sum is exact, one rounding to bfloat16
+            want = Y[slots[t, 0], part].float() * weights[t, 0] + Y[slots[t, 1], part].float() * weights[t, 1]
+            assert torch.equal(buf[t * N + part.start:t * N + part.stop], want.bfloat16())
+    assert bool((buf[T * N:] == -777).all())
