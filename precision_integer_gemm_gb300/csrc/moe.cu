@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kChooseThreads) moe_choose_kernel(const RouteP
     for (int e = threadIdx.x; e < p.E; e += kChooseThreads) mask[e] = make_uint2(0, 0);
     __syncthreads();
     const int t0 = blockIdx.x * p.tb;
-    for (int i = warp; i < p.tb && t0 + i < p.T; i += kChooseThreads / 32) {
+    const int mine = min(p.tb, p.T - t0);  // (t0 + tb may pass 2^31)
+    for (int i = warp; i < mine; i += kChooseThreads / 32) {
         const int64_t t = t0 + i;
         const T *row = static_cast<const T *>(p.logits) + t * p.E;
         uint32_t key[VPL];  // of expert 32 V (j / V) + V lane + j % V
@@ -577,7 +578,7 @@ int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
     // up to 512 tokens spread over the blocks of a cluster
     const bool one = c.T <= kClusterBlocks * kTB;
     p.tb = one ? std::max(kFewTokens, (c.T + kClusterBlocks - 1) / kClusterBlocks) : kTB;
-    p.blocks = (c.T + p.tb - 1) / p.tb;
+    p.blocks = static_cast<int>((int64_t(c.T) + p.tb - 1) / p.tb);
     // the places can sum every block's counts themselves, without a scan, while all of
     // them together read no more than 4 MB (us, two launches against three: 4096 x 256
     // bfloat16 8.0 to 9.0, 16384 x 64 8.3 to 8.7; 16384 x 256 14.1 to 12.8)

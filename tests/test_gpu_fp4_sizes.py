@@ -89,3 +89,28 @@ def test_combine_of_rows_of_nearly_2_to_31(N, start):
             want = Y[slots[t, 0], part].float() * weights[t, 0] + Y[slots[t, 1], part].float() * weights[t, 1]
             assert torch.equal(buf[t * N + part.start:t * N + part.stop], want.bfloat16())
     assert bool((buf[T * N:] == -777).all())
+
+
+@pytest.mark.parametrize("typ", [torch.bfloat16, torch.float32])
+def test_route_of_2_to_31_tokens_but_one(typ):
+    needs(90)
+    T, E, k = 2 ** 31 - 1, 2, 1
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.empty((T, E), dtype=typ, device="cuda")
+    logits.random_(-8, 8, generator=gen)  # ties too
+    i32 = dict(dtype=torch.int32, device="cuda")
+    experts, slots, weights = torch.empty((T, k), **i32), torch.empty((T, k), **i32), torch.empty((T, k), device="cuda")
+    offsets, tokens = torch.empty((E + 1,), **i32), torch.empty((T * k,), **i32)
+    pig.igemm_moe_route(logits, experts, weights, offsets, tokens, slots, T, E, k)
+    second = 0
+    for at in range(0, T, 1 << 27):
+        part = slice(at, min(at + (1 << 27), T))
+        want = (logits[part, 1] > logits[part, 0]).int()  # a tie: the lower expert
+        assert torch.equal(experts[part, 0], want) and bool((weights[part] == 1).all())
+        # the place holds the token, and lies behind the places of the same expert's earlier tokens
+        place = slots[part, 0].long()
+        assert torch.equal(tokens[place].long(), torch.arange(part.start, part.stop, device="cuda"))
+        mask = want.bool()
+        assert bool((place[mask].diff() == 1).all()) and bool((place[~mask].diff() == 1).all())
+        second += int(want.sum())
+    assert offsets.tolist() == [0, T - second, T]
