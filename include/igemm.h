@@ -28,7 +28,9 @@
  * waits for the pass (griddepcontrol.wait) before it reads or writes what the
  * pass touches.  The kernels of the 4-bit floating-point and mixture-of-experts
  * operators are launched that way behind whatever precedes them in the stream,
- * and wait for its end before they touch memory.
+ * and wait for its end before they touch memory, but for one hint: products of
+ * 32 MB of weights and more read `offsets` (clamped) and ask L2 for their first
+ * weights ahead of that wait, as both are then.  Results do not depend on it.
  *
  * Operand formats
  *   Packed int4 matrix [rows, K/2] bytes, row-major: byte j of a row holds
@@ -275,7 +277,10 @@ IGEMM_API int pack_int4(const int8_t *logical, uint8_t *packed, int64_t rows, in
  * launches one kernel, or two: the preparation pass and the GEMM (prepared
  * codes), the zeroing of C and the GEMM (skinny shapes whose K slices are
  * summed with atomics), the scale transpose and the GEMM (block-scaled fp8);
- * a 4-bit operator one, igemm_moe_route of more than 64 tokens three.
+ * a 4-bit operator one, but igemm_moe_route two or three above 512 tokens (three
+ * where the counts that its blocks would all read pass 4 MB: with
+ * b = ceil(T / 64) blocks, 4 b b ceil(E / 4) bytes), and pack_mxfp4 or pack_nvfp4
+ * two where rows are packed once and copied (as stated there).
  * The split K of the other paths adds a memset, which is not a kernel.
  */
 IGEMM_API uint64_t igemm_kernels_launched(void);

@@ -121,3 +121,41 @@ def test_layer_after_layer(fmt, T, E, k, steps):
         return out
 
     same_with_waits(chain)
+
+
+def route_buffers(T, E, k):
+    return (torch.empty((T, k), **I32), torch.empty((T, k), device="cuda"), torch.empty((E + 1,), **I32),
+            torch.empty((T * k,), **I32), torch.empty((T, k), **I32))
+
+
+def test_kernels_launched_by_each_operator():
+    def launched(call):
+        before = pig.igemm_kernels_launched()
+        call()
+        return pig.igemm_kernels_launched() - before
+
+    # routing: one up to 512 tokens, two while 4 ceil(T / 64)^2 ceil(E / 4) bytes are at most 4 MB, three above
+    for T, E, want in [(0, 8, 0), (1, 8, 1), (65, 8, 1), (512, 8, 1), (513, 8, 2), (16384, 64, 2), (16384, 65, 3),
+                       (16385, 64, 3), (4096, 1024, 2), (4097, 1024, 3)]:
+        logits = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+        assert launched(lambda: pig.igemm_moe_route(logits, *route_buffers(T, E, 2), T, E, 2)) == want, (T, E)
+    # packing: two where rows are gathered twice or more on average and that saves reading 32 MB
+    for rows, source, K, want in [(4, 4, 64, 1), (8192, 4096, 4096, 2), (8192, 4096, 4095, 1), (8193, 4096, 4096, 2),
+                                  (16384, 8192, 2048, 2), (16383, 8192, 4096, 1), (0, 4, 64, 0)]:
+        x = torch.zeros((source, K), dtype=torch.bfloat16, device="cuda")
+        codes = torch.empty((rows, pig.fp4_code_bytes(K)), **U8)
+        scales = torch.empty((rows, pig.mxfp4_scale_pitch(K)), **U8)
+        index = torch.zeros((rows,), **I32)
+        assert launched(lambda: pig.pack_mxfp4(x, codes, scales, rows, K, index=index)) == want, (rows, source, K)
+    # a product one, whatever its kernel, and so the sum
+    for M in (1, 40, 300):
+        A, SA = packed("mx", torch.zeros((M, 1024), device="cuda"))
+        C = torch.empty((M, M), device="cuda")
+        off = torch.tensor([0, M], **I32)
+        assert launched(lambda: pig.igemm_mxfp4(A, A, SA, SA, C, M, M, 1024)) == 1
+        assert launched(lambda: pig.igemm_mxfp4_grouped(A, A, SA, SA, off, C, M, 1, M, 1024)) == 1
+        slots = torch.zeros((M, 1), **I32)
+        assert launched(lambda: pig.igemm_moe_combine(C, slots, torch.ones((M, 1), device="cuda"), torch.empty_like(C), M,
+                                                      1, M)) == 1
+    torch.cuda.synchronize()
+    assert pig.igemm_last_status() == 0
