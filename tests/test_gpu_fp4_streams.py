@@ -159,3 +159,81 @@ def test_kernels_launched_by_each_operator():
                                                       1, M)) == 1
     torch.cuda.synchronize()
     assert pig.igemm_last_status() == 0
+
+
+# routing in two launches and in three, and gathered packing through its workspace: every call that allocates
+@pytest.mark.parametrize("fmt,T,E,k,K", [("mx", 600, 40, 8, 256), ("nv", 8192, 64, 4, 1024), ("mx", 16400, 68, 3, 768)])
+def test_workspaces_in_a_graph(fmt, T, E, k, K):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    logits, x = torch.empty((T, E), device="cuda"), torch.empty((T, K), device="cuda")
+    route = route_buffers(T, E, k)
+    tokens, slots, weights = route[3], route[4], route[1]
+    a = torch.empty((T * k, pig.fp4_code_bytes(K)), **U8)
+    sa = torch.empty((T * k, (pig.mxfp4_scale_pitch if fmt == "mx" else pig.nvfp4_scale_pitch)(K)), **U8)
+    N = 64
+    B, SB = packed(fmt, torch.randn((E * N, K), generator=gen, device="cuda") * 0.1)
+    y, out = torch.empty((T * k, N), device="cuda"), torch.empty((T, N), device="cuda")
+
+    def layer():
+        pig.igemm_moe_route(logits, *route, T, E, k)
+        pack(fmt, x, a, sa, T * k, K, index=tokens)
+        if fmt == "mx":
+            pig.igemm_mxfp4_grouped(a, B, sa, SB, route[2], y, T * k, E, N, K)
+        else:
+            pig.igemm_nvfp4_grouped(a, B, sa, SB, route[2], None, y, T * k, E, N, K)
+        pig.igemm_moe_combine(y, slots, weights, out, T, k, N)
+
+    before = pig.igemm_kernels_launched()
+    logits.normal_(generator=gen), x.normal_(generator=gen)
+    layer()
+    assert pig.igemm_kernels_launched() - before == 2 + (2 if T * E < 16400 * 68 else 3) + (2 if T > 600 else 1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    for _ in range(4):
+        logits.normal_(generator=gen), x.normal_(generator=gen)
+        out.fill_(float("nan"))
+        graph.replay()
+        graph.replay()  # right behind itself, on the same workspaces
+        got = [t.clone() for t in (out, a, sa, *route)]
+        layer()  # and a call of its own right behind the graph
+        assert bool(torch.isfinite(got[0]).all())
+        for g, w in zip(got, (out, a, sa, *route)):
+            assert torch.equal(g, w)
+    assert pig.igemm_last_status() == 0
+
+
+def test_calls_on_two_streams():
+    # routing and gathered packing through the pool's workspaces, products and sums, on two streams at once
+    fmt, T, E, k, K, N, steps = "mx", 16384, 68, 3, 1024, 128, 12
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    B, SB = packed(fmt, torch.randn((E * N, K), generator=gen, device="cuda") * 0.1)
+    logits = torch.randn((2, steps, T, E), generator=gen, device="cuda")
+    x = torch.randn((2, T, K), generator=gen, device="cuda")
+    work = [(route_buffers(T, E, k), packed(fmt, torch.zeros((T * k, K), device="cuda")),
+             torch.empty((T * k, N), device="cuda")) for _ in range(2)]
+    out = torch.empty((2, steps, T, N), device="cuda")
+
+    def step(i, s):
+        route, (a, sa), y = work[i]
+        pig.igemm_moe_route(logits[i, s], *route, T, E, k)
+        pack(fmt, x[i], a, sa, T * k, K, index=route[3])
+        pig.igemm_mxfp4_grouped(a, B, sa, SB, route[2], y, T * k, E, N, K)
+        pig.igemm_moe_combine(y, route[4], route[1], out[i, s], T, k, N)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for s in range(steps):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                step(i, s)
+    torch.cuda.synchronize()
+    together = out.clone()
+    out.fill_(float("nan"))
+    for s in range(steps):
+        for i in range(2):
+            step(i, s)
+            torch.cuda.synchronize()
+    assert bool(torch.isfinite(together).all()) and torch.equal(together, out)
+    assert pig.igemm_last_status() == 0
