@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 #include "launch.cuh"
 #include "fp4.cuh"
+#include "igemm.h"
 #include "overlap.cuh"
 #include "ptx.cuh"
 
@@ -371,13 +372,14 @@ __global__ void __launch_bounds__(256) pack_fp4_transposed_kernel(const T *x, co
         for (int b = (blockIdx.y + 1) * 8 * kPerWarp; b < p.pitch; ++b) p.scales[(r0 + threadIdx.x) * p.pitch + b] = 0;
 }
 
+static_assert(IGEMM_FP4_MAX_K / 256 <= 65535, "the k axis fits in grid.y (256 k a block at least)");
+
 template <bool NV, class T>
 static int launch_pack_type(const Fp4PackCall &c, const Fp4PackParams &p, cudaStream_t stream)
 {
     const T *x = static_cast<const T *>(c.x);
     if (c.transposed) {
         const int by = (c.K + 255) / 256;
-        if (by > 65535) return kUnsupportedShape;
         const auto launch = [&](auto kernel, int rows) {
             return launch_overlapped(kernel, dim3(static_cast<unsigned>((int64_t(c.rows) + rows - 1) / rows), by),
                                      dim3(256), 0, stream, x, p);
@@ -397,7 +399,6 @@ static int launch_pack_type(const Fp4PackCall &c, const Fp4PackParams &p, cudaSt
         if (items <= 16)
             for (bx = 2; bx < items;) bx *= 2;
         const int by = std::max(1, 256 / bx);
-        if (chunks > 65535) return kUnsupportedShape;
         // blocks that are resident at once, fewer where the rows give one each
         const int64_t full = std::max<int64_t>(1, int64_t(sm_count()) * (vec ? 5 : 4) * std::max(1, 256 / (bx * by)) / chunks);
         const int64_t gx = std::min((int64_t(c.rows) + by - 1) / by, full);

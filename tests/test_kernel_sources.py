@@ -68,3 +68,9 @@ def test_a_split_k_that_gave_up_waits_for_the_partials_on_their_way():
     assert epilogue.count("if (!ok) break;") == 3
     drain = epilogue[epilogue.index("if (cs > 1 && !ok)"):]
     assert "&red_full[" in drain and re.search(r"while \(!mbar_try_wait\([^;]*globaltimer_ns\(\) - t0 < prm.limit_ns", drain)
+
+
+def test_pack_has_no_limit_that_no_call_reaches():
+    # K is at most IGEMM_FP4_MAX_K, so the k axis always fits in a grid's second dimension
+    code = code_of("pack_fp4.cu")
+    assert "65535) return" not in code and re.search(r"static_assert\(IGEMM_FP4_MAX_K[^;]*65535", code)
