@@ -32,7 +32,11 @@ class MoeFp4:
         self.down, self.g2 = self._pack_weights(down)
 
     def _tensor_scale(self, x):
-        return (x.abs().amax().float() / (6 * 448)).clamp(min=1e-30).view(1) if self.fmt == "nv" else None
+        if self.fmt != "nv":
+            return None
+        if x.numel() == 0:
+            return torch.ones((1,), device=x.device)
+        return (x.abs().amax().float() / (6 * 448)).clamp(min=1e-30).view(1)
 
     def _pack_weights(self, w):
         g = self._tensor_scale(w)

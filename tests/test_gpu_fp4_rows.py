@@ -48,3 +48,20 @@ def test_combine_rows_of_every_width_and_start(typ, shift):
             bound = bound + half * (exact.abs() + bound) * 1.01 + tiny
             assert bool(((out.double() - exact).abs() <= bound).all()), (T, k, N)
             assert bool((buf[:shift[1]] == -777).all()) and bool((buf[shift[1] + T * N:] == -777).all()), (T, k, N)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_moe_layer_of_no_tokens(fmt):
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    try:
+        import moe_fp4
+    finally:
+        sys.path.pop(0)
+    router, gate_up, down = (torch.randn(s, device="cuda") for s in ((4, 64), (4, 2 * 96, 64), (4, 64, 96)))
+    layer = moe_fp4.MoeFp4(router, gate_up, down, 2, fmt)
+    out = layer(torch.empty((0, 64), device="cuda"))
+    assert out.shape == (0, 64) and out.dtype == torch.float32
+    assert pig.igemm_last_status() == 0
