@@ -396,7 +396,8 @@ typedef enum igemm_type { IGEMM_F32 = 0, IGEMM_BF16 = 1, IGEMM_F16 = 2 } igemm_t
  *           index[r] is outside [0, x_rows) (not with transposed:
  *           IGEMM_UNSUPPORTED_SHAPE); null needs x_rows >= rows.  Where rows >= 2
  *           x_rows and that saves reading 32 MB, x is packed once into a workspace
- *           from the library's pool (the bytes of x_rows packed rows) and copied
+ *           from the library's pool (the bytes of x_rows packed rows) and copied,
+ *           or, if there is no room for it, row by row as otherwise
  * rows == 0 or K == 0 is a no-op.
  */
 IGEMM_API int pack_mxfp4(const void *x, int x_type, int64_t ld, int transposed, const int32_t *index, int x_rows,

@@ -493,7 +493,10 @@ int launch_fp4_pack(const Fp4PackCall &c, cudaStream_t stream)
     p.pitch = fp4_scale_pitch(c.K, c.nv);
     const size_t code_bytes = size_t(c.x_rows) * p.code_bytes;
     void *ws = nullptr;
-    if (workspace_alloc(&ws, code_bytes + size_t(c.x_rows) * p.pitch, stream) != kOk) return kCudaError;
+    if (workspace_alloc(&ws, code_bytes + size_t(c.x_rows) * p.pitch, stream) != kOk) {
+        cudaGetLastError();  // no room for it: row by row
+        return launch(c);
+    }
     Fp4PackCall once = c;
     once.index = nullptr;
     once.rows = c.x_rows;

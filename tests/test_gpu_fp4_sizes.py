@@ -114,3 +114,26 @@ def test_route_of_2_to_31_tokens_but_one(typ):
         assert bool((place[mask].diff() == 1).all()) and bool((place[~mask].diff() == 1).all())
         second += int(want.sum())
     assert offsets.tolist() == [0, T - second, T]
+
+
+def test_gathered_packing_without_room_for_its_workspace():
+    needs(8)
+    source, rows, K = 1 << 18, 1 << 19, 4096  # a workspace of 570 MB
+    x = torch.randint(-8, 8, (source, K), device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    index = torch.randint(0, source, (rows,), device="cuda", dtype=torch.int32)
+    codes = torch.full((2, rows, K // 2), 0xA5, dtype=torch.uint8, device="cuda")
+    scales = torch.full((2, rows, pig.mxfp4_scale_pitch(K)), 0xA5, dtype=torch.uint8, device="cuda")
+    # the reference: fewer rows a call, which never takes a workspace
+    for at in range(0, rows, source // 2):
+        part = slice(at, at + source // 2)
+        pig.pack_mxfp4(x, codes[0, part], scales[0, part], source // 2, K, index=index[part])
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    rest = torch.cuda.mem_get_info()[0] - (256 << 20)
+    filler = torch.empty((rest,), dtype=torch.uint8, device="cuda")
+    try:
+        pig.pack_mxfp4(x, codes[1], scales[1], rows, K, index=index)
+        torch.cuda.synchronize()
+    finally:
+        del filler
+    assert torch.equal(codes[0], codes[1]) and torch.equal(scales[0], scales[1])
