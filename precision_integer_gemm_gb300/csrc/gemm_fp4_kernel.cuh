@@ -117,6 +117,7 @@ struct Fp4Cfg {
     static_assert(kQBox % 8 == 0 && kStage % 1024 == 0, "1024-byte aligned operand tiles");
     static_assert(kTmemUse <= 512 && kOverlap >= 0 && kOverlap % 96 == 0, "TMEM budget");
     static_assert(!PAIR || BN == 256, "the pair form is built for 256 activation rows");
+    static_assert(2 * 4 * 8 * 16 <= kStoreBytes, "notices of a split k");
 };
 
 struct Fp4Tile {
@@ -457,11 +458,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint64_t *mma_drain = acc_empty + 2;
     uint64_t *red_full = mma_drain + 1;             // [2][4] split k: the other CTAs' partials of this warp's part landed
     uint64_t *red_empty = red_full + 8;             // [2][4] ... and the other CTAs have read what this warp sent
+                                                    // (their notices)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Cfg::kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *total_slot = reinterpret_cast<int *>(tmem_slot + 2);
-    uint8_t *notices = smem + ((prm.off_bars + 8 * Cfg::kNumBars + 64 + 15) & ~15);  // [scale stages][16], never read
-    Fp4Group *groups = reinterpret_cast<Fp4Group *>(notices + Cfg::kNoticeBytes);
+    // 16 bytes for each notice of another CTA, never read: pairs [scale stages]; split k
+    // [2][4][8 CTAs], in the epilogue's staging, which it does not use
+    uint8_t *tail = smem + ((prm.off_bars + 8 * Cfg::kNumBars + 64 + 15) & ~15);
+    uint8_t *notices = PAIR ? tail : smem + prm.off_store;
+    Fp4Group *groups = reinterpret_cast<Fp4Group *>(tail + Cfg::kNoticeBytes);
+    const uint8_t *fixed = smem + ((prm.off_bars + 8 * Cfg::kNumBars + 15) & ~15);  // 16 bytes that stay as they are
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
         if (cs > 1 && lane < 8) {
             mbar_init(&red_full[lane], 1);
-            mbar_init(&red_empty[lane], cs - 1);
+            mbar_init(&red_empty[lane], 1);
         }
         if (lane == 0) {
             mbar_init(mma_drain, 1);
@@ -890,11 +896,17 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         if (c + j < c1) fp4_store1(prm, s[j] * alpha, static_cast<int64_t>(x.q0) + rank * per + c + j, n);
                 }
                 __syncwarp();
-                // read: the other CTAs may write again, where a later tile does (the release at
-                // cluster scope is a fence: 16 x 28672 x 8192 mxfp4 20.3 us, 20.6 with one after
-                // the last tile too)
-                if (t + static_cast<int64_t>(Cfg::kRedBufs) * ncl < tiles && lane < cs && lane != rank)
-                    mbar_arrive_remote(cluster_map(smem_u32(&red_empty[bar]), static_cast<uint32_t>(lane)));
+                // read: the other CTAs may write again, where a later tile does.  Each is sent 16
+                // bytes (no matter which): this warp's reads come before that copy, so before its
+                // completion, a release at cluster scope, as with the pairs' relay.  (Arrivals
+                // with .release.cluster wait for a fence: 64 x 28672 x 8192 mxfp4 25.1 us, 23.2
+                // with copies.)
+                if (t + static_cast<int64_t>(Cfg::kRedBufs) * ncl < tiles) {
+                    if (lane == 0) mbar_arrive_expect_tx(&red_empty[bar], 16u * (cs - 1));
+                    if (lane < cs && lane != rank)
+                        bulk_copy_to_cta(cluster_map(smem_u32(notices + 16 * (8 * bar + rank)), lane), fixed, 16,
+                                         cluster_map(smem_u32(&red_empty[bar]), lane));
+                }
                 continue;
             }
             const int n0 = x.p0 + quad * 32;
@@ -904,9 +916,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 fp4_store_tile<Cfg, false>(prm, x, tacc, ab, alpha, n0, stage, release);
         }
         // gave up: another CTA's partials of this tile, and of the next with two buffers,
-        // may be on their way here
+        // may be on their way here, and its notices of the tiles before
         if (cs > 1 && !ok) {
             const uint64_t t0 = globaltimer_ns();
+            for (uint32_t n = nacc > Cfg::kRedBufs ? nacc - Cfg::kRedBufs : 0u; n <= nacc; ++n)
+                while (!mbar_try_wait(&red_empty[n % Cfg::kRedBufs * 4 + quad], (n / Cfg::kRedBufs) & 1u) &&
+                       globaltimer_ns() - t0 < prm.limit_ns) {
+                }
             for (uint32_t n = nacc; n < nacc + Cfg::kRedBufs; ++n) {
                 uint64_t *bar = &red_full[n % Cfg::kRedBufs * 4 + quad];
                 if (lane == 0 && n >= armed)

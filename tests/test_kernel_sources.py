@@ -30,7 +30,7 @@ def test_hand_overs_between_the_ctas_of_a_4_bit_product():
     code = code_of("gemm_fp4_kernel.cuh")
     targets = re.findall(r"mbar_arrive_peer\(([^;]*)\);", code)
     assert targets and all(t.startswith("empty_leader") for t in targets), targets
-    assert re.search(r"mbar_arrive_remote\(cluster_map\(smem_u32\(&red_empty", code)
+    assert re.search(r"(mbar_arrive_remote|bulk_copy_to_cta)\([^;]*smem_u32\(&red_empty", code)
     # ... and what waits for them acquires at cluster scope
     assert re.search(r"PAIR \? mbar_try_wait_cluster\(c, pc\)", code) and "wait_bounded_cluster(c, pc, wd)" in code
     assert re.search(r"fp4_warp_wait3<PAIR>\([^;]*&sf_full\[", code)
