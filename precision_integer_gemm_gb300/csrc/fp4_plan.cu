@@ -11,12 +11,13 @@ namespace igemm {
 // us in 128 x 16), or HBM's 6.3 MB a microsecond shared by the SMs (on CTA pairs:
 // those that read different weights), plus what a tile costs besides (1 us; 3.2 us
 // on CTA pairs).
-// A split of k adds 2 us (4 us for 64 activation rows: 64 x 8192 x 8192 12.2 us
-// split, 10.1 whole; with 128 it never paid).
-// Against the fastest of all choices on 85 shapes (activations 1 .. 2048, weights
-// 128 x 65536 .. 28672 x 8192) the choice is within 15 %, mostly within 4 %; with one
-// width per number of activations and a split wherever SMs were idle, 128 x 1024 x
-// 1024 took 12.7 us against 8 and 128 x 128 x 65536 took 38 us against 13.
+// A split of k adds 2 us (4 us for 64 activation rows: 64 x 8192 x 8192 12.0 us
+// split, 10.3 whole; with 128 it never paid).
+// Against the fastest of all choices on 90 shapes (activations 1 .. 2048, weights
+// 128 x 65536 .. 28672 x 8192) the choice is within 3 % on 79, within 12 % on 85, and
+// 16 to 22 % behind on five: a single token through 4096 x 4096 that two CTAs should
+// split, 40 and 64 rows through 28672 x 8192 that nobody should, 200 x 4096 x 14336
+// and 2048 x 128 x 65536 that do not belong on CTA pairs.
 bool fp4_plan(const Fp4Call &c, int (*max_clusters)(int, bool, int), Fp4Plan *plan)
 {
     const int blocks = (c.K + 511) / 512;

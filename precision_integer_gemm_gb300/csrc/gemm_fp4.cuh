@@ -112,15 +112,15 @@ int launch_fp4_cfg(const Fp4Call &c, const Fp4Plan &plan, cudaStream_t stream)
     prm.cs = plan.cs;
     prm.blocks_per_slice = (prm.blocks + plan.cs - 1) / plan.cs;
     // weights from 24 MB on leave L2 first, before what other kernels left there (us
-    // without and with: 32 rows over 64 experts of 4096 x 4096 27.9 to 25.1, 16 x 28672 x
-    // 8192 23.8 to 21.7, 64 x 14336 x 4096 8.8 to 8.5; the same weights again and again
-    // out of L2, 16 x 8192 x 8192 8.9 to 9.6)
+    // without and with: 32 rows over 64 experts of 4096 x 4096 39.2 to 36.1, 16 x 28672 x
+    // 8192 nvfp4 24.0 to 21.7, mxfp4 23.0 to 20.2; weights that L2 holds from call to call,
+    // 64 x 14336 x 4096 7.6 to 7.9)
     const double weights = plan.groups * c.N * code_bytes;
     prm.stream = !Cfg::PAIR && weights >= 24.0 * (1 << 20);
     // weights of 32 MB and more, whose first ring is a small part of what a CTA reads (us
-    // without and with: 16 x 28672 x 8192 24.1 to 22.7, 16 x 8192 x 8192 10.0 to 9.5; 16 x
-    // 4096 x 4096 6.2 to 6.5, 512 x 8192 x 8192 on pairs 16.9 to 17.5; 32 rows over 64
-    // experts of 4096 x 4096 29.4 to 28.4)
+    // without and with: 16 x 28672 x 8192 mxfp4 22.5 to 20.2, nvfp4 21.8 to 21.7, 32 rows
+    // over 64 experts of 4096 x 4096 37.9 to 36.1; with this hint and the one above for
+    // smaller weights, 16 x 4096 x 4096 5.7 to 6.2, 1 x 4096 x 14336 8.1 to 8.8)
     prm.prefetch = !Cfg::PAIR && weights >= 32.0 * (1 << 20)
                        ? std::min(lay.code_stages, 2 * prm.blocks_per_slice)
                        : 0;

@@ -29,10 +29,10 @@
 // 1024.  So a block has one joint wait for its 8 MMAs, and weights, activations and
 // scales each have a loading warp (one warp for all three took 1500 cycles a block).
 //
-// Few rows are bound by HBM: 16 x 28672 x 8192 nv takes 21.4 us, 6.2 TB/s (launch, first
+// Few rows are bound by HBM: 16 x 28672 x 8192 nv takes 21.5 us, 6.2 TB/s (launch, first
 // stage and tail beside it).  Many rows are bound by the tensor core and its operands:
 // 8192^3 mx takes 155 us alone, 7.1 PFLOP/s, 1200 cycles a block where the MMAs take
-// 1024; back to back the power cap makes it 170 us.
+// 1024; back to back the power cap makes it 171 to 176 us.
 //
 // Warps 0-3 epilogue, 4 MMA issue, 5 weight loads, 6 activation loads, 7 scale loads,
 // 8 and up scales.  Persistent CTAs (or CTA pairs, or clusters that split k).  Every
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             // proxy of tcgen05.cp), so before the copy's completion, a release at cluster
             // scope that the MMA warp acquires.  An arrival with .release.cluster says the same
             // with a fence of its own, 1100 cycles and more: 8192^3 mx 240 us by one warp, 168
-            // by two, 163 with copies; 512 x 8192 x 8192 26.7, 19.3 and 17.3.
+            // by two, 163 with copies (the three in turn); 512 x 8192 x 8192 26.7, 19.3, 17.3.
             const uint32_t peer = cluster_map(smem_u32(sf_full), 0u), notice = cluster_map(smem_u32(notices), 0u);
             Fp4Ring fr(prm.scale_stages);
             bool ok = true;
@@ -936,8 +936,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     // ---------------------------------------------------------------- teardown
     // The next kernel may be set up on SMs that this one has left; it waits for the end
     // of this grid before it touches memory.  (Let in from the start, its blocks settle on
-    // the SMs that happen to have room: 128 x 4096 x 4096 back to back 6.8 us against 6.4,
-    // a mixture-of-experts layer of 8 tokens 56 against 54.)
+    // the SMs that happen to have room: 128 x 4096 x 4096 back to back 6.8 us against 6.5,
+    // a mixture-of-experts layer of 8 tokens 52.5 against 49.)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();

@@ -10,12 +10,12 @@
 // mask, and a pair's place among its expert's is the number of bits below its
 // own: the sort is stable and needs no ordered atomics.  A cluster of up to 8 blocks
 // does the whole job for up to 512 tokens, its blocks reading each other's masks in
-// shared memory (calls of 128 x 256 bfloat16, 8 choices: 12.2 us in three launches
-// and a workspace, 7.6 in one); more tokens take two launches (choice and counts per
+// shared memory (128 x 256 bfloat16, 8 choices: 5.9 us, where three launches and a
+// workspace made a call 4.6 us longer); more tokens take two launches (choice and counts per
 // block; places, each block summing the counts of all) or, from some 2^20 words of
 // counts read in all, three (a scan over the blocks per expert between them), and
 // 16-bit logits of up to 256 experts then go four tokens to a warp
-// (moe_choose4_kernel).  Bound by instructions and by the launches: 15.6 us at 16384 x
+// (moe_choose4_kernel).  Bound by instructions and by the launches: 15.5 us at 16384 x
 // 256 bfloat16, 8 choices, whose 10.5 MB are 1.6 us of HBM (alone and cold: choice 13,
 // scan 4.5, places 7.5 us).
 //
@@ -34,8 +34,8 @@ namespace igemm {
 constexpr int kTB = 64;           // most tokens per block: two mask words
 // blocks that one cluster can hold; up to so many do the whole job in one launch
 constexpr int kClusterBlocks = 8;
-// a block of one cluster takes as many tokens at least (64 x 1024 float32, 8 choices:
-// 14.8 us against 28.9 in one block of 64; 16 x 64: 6.1 us with 16 or more, 6.9 with 8)
+// a block of one cluster takes as many tokens at least (16 x 64 bfloat16, 4 choices: 3.0
+// us, 4.2 with 8; 64 x 1024 float32, 8 choices: 11.4 us, 10.7 with 8 and 25.7 with 64)
 constexpr int kFewTokens = 16;
 constexpr int kRouteThreads = 512;
 constexpr int kChooseThreads = 1024;
@@ -341,7 +341,7 @@ __device__ __forceinline__ void route_merge8(uint32_t (&a)[8], const uint32_t (&
 // such lists pairwise, halving the tokens that a lane holds (16 lanes apart: two
 // tokens each, 8 apart: one), so that eight lanes end with the eight largest of one
 // token and lane c of them keeps choice c.  About 400 instructions a token against
-// 640 with one token per warp and a reduction per choice.
+// 640 with one token per warp and a reduction per choice (times: launch_choose_vpl).
 template <class T, int VPL, bool VEC>
 __global__ void __launch_bounds__(kChoose4Threads) moe_choose4_kernel(const RouteParams p)
 {
@@ -538,8 +538,8 @@ static int launch_choose_vpl(const RouteParams &p, int smem, cudaStream_t stream
     constexpr int V = VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
     const bool vec = p.E % V == 0 && reinterpret_cast<uintptr_t>(p.logits) % (V * sizeof(T)) == 0;
     // 16-bit logits of up to 256 experts, up to 8 choices and more tokens than a cluster's
-    // (routing of 16384 x 256 bfloat16, 8 choices: 21.7 -> 17.5 us; 65536 x 128: 41.5 ->
-    // 29.8; no case was slower)
+    // (routing with 8 choices, a token a warp and four: 16384 x 256 bfloat16 20.1 and 15.4
+    // us, 65536 x 128 37.5 and 25.5, 8192 x 64 10.4 and 6.6)
     if constexpr (sizeof(T) == 2 && VPL <= 8)
         if (p.T > kClusterBlocks * kTB && p.k <= 8)
             return launch_overlapped(vec ? moe_choose4_kernel<T, VPL, true> : moe_choose4_kernel<T, VPL, false>,
@@ -580,8 +580,8 @@ int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream)
     p.tb = one ? std::max(kFewTokens, (c.T + kClusterBlocks - 1) / kClusterBlocks) : kTB;
     p.blocks = static_cast<int>((int64_t(c.T) + p.tb - 1) / p.tb);
     // the places can sum every block's counts themselves, without a scan, while all of
-    // them together read no more than 4 MB (us, two launches against three: 4096 x 256
-    // bfloat16 8.0 to 9.0, 16384 x 64 8.3 to 8.7; 16384 x 256 14.1 to 12.8)
+    // them together read no more than 4 MB (us, two launches and three: 4096 x 256 bfloat16
+    // 8.2 and 10.3, 16384 x 64 9.1 and 10.8; 16384 x 256 18.7 and 15.4)
     const int words = (c.E + 3) / 4;
     const bool two = !one && int64_t(p.blocks) * p.blocks * words <= int64_t(1) << 20;
     void *ws = nullptr;
@@ -623,9 +623,10 @@ struct alignas(PER * sizeof(T)) MoeRun {
 // laid over tokens and columns alike (4096 tokens x 8 bfloat16 rows of 4096: 48 us,
 // 0.93 of the copy rate).  Other rows: a block of threads per token and 128 RUNS PER
 // columns, so that the choices are read once for several narrow loads (rows of 4095:
-// 147 -> 72 us; of 4092, in 8-byte runs, that form took 66 us against 53).  Those loads
-// are volatile, so all of them go out before the first sum (with plain ones rows of 4095
-// take 71 us against 63, of 4094 103 against 43, of 4092 59 against 49).
+// 61 us, 147 with a thread per value).  In 8-byte runs that form takes 43 us for rows of
+// 4092, where one run takes 49, but 11.9 against 2.5 for rows of 68.  The narrow loads are
+// volatile, so all of them go out before the first sum (with plain ones rows of 4095
+// took 71 us, of 4094 103 instead of 43, of 4092 59).
 template <class T, int PER, int RUNS>
 __global__ void __launch_bounds__(128) moe_combine_kernel(const T *Y, const int *slots, const float *weights, T *out, int Tn,
                                                           int k, int N)

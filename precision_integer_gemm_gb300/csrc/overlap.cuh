@@ -17,8 +17,8 @@ __device__ __forceinline__ void overlap_begin()
 // The two halves apart: a kernel that fills the SMs lets the next one in only towards
 // its end, so that the next one's blocks spread over all SMs instead of settling where
 // there happens to be room (back to back, us, from the start against at the end:
-// routing of 8192 x 64 bfloat16 12.1 to 6.5, packing of 128 x 4096 float32 2.9 to 2.0,
-// combining 256 x 8 rows of 4096 5.0 to 3.5).
+// routing of 8192 x 64 bfloat16 12.1 to 6.6, packing of 128 x 4096 float32 2.5 to 1.8,
+// combining 256 x 8 rows of 4096 6.0 to 4.0).
 __device__ __forceinline__ void overlap_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void overlap_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

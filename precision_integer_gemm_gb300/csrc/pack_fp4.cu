@@ -384,7 +384,7 @@ static int launch_pack_type(const Fp4PackCall &c, const Fp4PackParams &p, cudaSt
             return launch_overlapped(kernel, dim3(static_cast<unsigned>((int64_t(c.rows) + rows - 1) / rows), by),
                                      dim3(256), 0, stream, x, p);
         };
-        // pairs where every row of x starts on 4 bytes (16384 x 8192 bfloat16: 69 -> 57 us)
+        // pairs where every row of x starts on 4 bytes (16384 x 8192 bfloat16: 69 -> 56 us)
         if constexpr (sizeof(T) == 2)
             if (reinterpret_cast<uintptr_t>(x) % 4 == 0 && c.ld % 2 == 0)
                 return launch(pack_fp4_transposed_kernel<NV, T, 2>, 64);
@@ -466,9 +466,9 @@ __global__ void __launch_bounds__(256) fp4_copy_rows_kernel(const uint4 *codes, 
 
 // Rows that are gathered twice or more on average are packed once, into a workspace,
 // and copied from there, where that saves reading 32 MB of x at least: 32768 x 4096
-// nvfp4 rows of 4096 take 45.9 -> 22.8 us (float32 84 -> 30), and 8192 x 4096 of 4096
-// 12.4 either way; with 28 MB saved the second launch and the workspace cost more
-// (4096 x 4096 of 512: 7.4 -> 9.3).
+// nvfp4 rows of 4096 take 45.0 -> 23.0 us (float32 84 -> 30), and 8192 x 4096 of 4096
+// 13.5 -> 13.1; with 28 MB saved the GPU would still gain (4096 x 4096 of 512: 7.2 -> 5.3
+// us), but a loop of calls is slower (7.4 -> 9.3) for a second launch and a workspace.
 static bool pack_once(const Fp4PackCall &c)
 {
     const int64_t pieces = fp4_code_bytes(c.K) / 16 + fp4_scale_pitch(c.K, c.nv) / 16;
