@@ -621,7 +621,7 @@ struct alignas(PER * sizeof(T)) MoeRun {
 // A thread per RUNS runs of PER columns of a token, four rows in flight; float32 sums
 // in the order of the choices.  Rows of whole 16- or 8-byte runs: one run, threads
 // laid over tokens and columns alike (4096 tokens x 8 bfloat16 rows of 4096: 48 us,
-// 0.93 of the copy rate).  Other rows: a block of threads per token and 128 RUNS PER
+// 0.92 of the copy rate).  Other rows: a block of threads per token and 128 RUNS PER
 // columns, so that the choices are read once for several narrow loads (rows of 4095:
 // 61 us, 147 with a thread per value).  In 8-byte runs that form takes 43 us for rows of
 // 4092, where one run takes 49, but 11.9 against 2.5 for rows of 68.  The narrow loads are
