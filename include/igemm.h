@@ -415,7 +415,8 @@ IGEMM_API int pack_nvfp4(const void *x, int x_type, int64_t ld, int transposed, 
  *           tensor scales
  *   C       [M, N] of c_type, row-major, naturally aligned; every element written
  * A NaN scale makes its row (column) of C NaN.  M == 0 or N == 0 is a no-op,
- * K == 0 zeroes C.
+ * K == 0 zeroes C.  M and N are below 2^31 - 512, ceil(M / 16) ceil(N / 128) below
+ * 2^30 (IGEMM_UNSUPPORTED_SHAPE).
  */
 IGEMM_API int igemm_mxfp4(const uint8_t *A, const uint8_t *B, const uint8_t *SFA, const uint8_t *SFB, void *C,
                           int c_type, int M, int N, int K, cudaStream_t stream);
@@ -431,8 +432,8 @@ IGEMM_API int igemm_nvfp4(const uint8_t *A, const uint8_t *B, const uint8_t *SFA
  *            start is empty
  *   alpha    nvfp4: [E] float32, or null for 1
  *   C        [rows, N]; rows of no group are left as they were
- * E <= 1024 and E * N < 2^31 - 512 (IGEMM_UNSUPPORTED_SHAPE, as K == 0 is);
- * rows, N or E of 0 is a no-op.
+ * E <= 1024, rows and E * N < 2^31 - 512, (rows / 16 + E) ceil(N / 128) < 2^30
+ * (IGEMM_UNSUPPORTED_SHAPE, as K == 0 is); rows, N or E of 0 is a no-op.
  */
 IGEMM_API int igemm_mxfp4_grouped(const uint8_t *A, const uint8_t *B, const uint8_t *SFA, const uint8_t *SFB,
                                   const int32_t *offsets, void *C, int c_type, int rows, int E, int N, int K,
@@ -466,7 +467,8 @@ IGEMM_API int igemm_moe_route(const void *logits, int logits_type, int32_t *expe
  * out[t,:] = sum_j weights[t,j] * Y[slots[t,j],:], float32 sums in the order of j,
  * rounded once; slots outside [0, T * k) add nothing.
  *   Y [T * k, N], out [T, N] of `type` (device, naturally aligned); slots, weights
- *   [T, k] as igemm_moe_route writes them; k <= 32 (IGEMM_UNSUPPORTED_SHAPE)
+ *   [T, k] as igemm_moe_route writes them; k <= 32, T * k < 2^31
+ *   (IGEMM_UNSUPPORTED_SHAPE)
  * T == 0 or N == 0 is a no-op, k == 0 zeroes out.
  */
 IGEMM_API int igemm_moe_combine(const void *Y, const int32_t *slots, const float *weights, void *out, int type, int T,
