@@ -75,7 +75,7 @@ typedef enum igemm_status {
     IGEMM_INVALID_ARGUMENT = 1,  /* null pointer for a non-empty operand, negative size */
     IGEMM_UNSUPPORTED_SHAPE = 2, /* K % 32 != 0 (GEMM); odd K (pack_int4); the limits stated at the 4-bit operators */
     IGEMM_MISALIGNED = 3,        /* a base address is not 16-byte aligned (4-bit operators: as stated there) */
-    IGEMM_OVERFLOW_BOUND = 4,    /* K above the int32 bound (33554431 int4 x int4, 2097151 W4A8) or IGEMM_FP4_MAX_K */
+    IGEMM_OVERFLOW_BOUND = 4,    /* K above the int32 bound (33554431 int4 x int4, 2097151 W4A8), IGEMM_FP4_MAX_K or IGEMM_BSFP8_MAX_K */
     IGEMM_CUDA_ERROR = 5,        /* tensor-map encoding, memset or launch failed */
     IGEMM_DEVICE_TIMEOUT = 6,    /* a kernel's bounded wait expired (see igemm_last_status) */
     IGEMM_WORKSPACE_LIMIT = 7    /* i4i4_gemm_noalloc: the problem needs more than its fixed workspace */
@@ -473,6 +473,69 @@ IGEMM_API int igemm_moe_route(const void *logits, int logits_type, int32_t *expe
  */
 IGEMM_API int igemm_moe_combine(const void *Y, const int32_t *slots, const float *weights, void *out, int type, int T,
                                 int k, int N, cudaStream_t stream);
+
+/*
+ * Block-scaled fp8 with one float32 scale per 128 k of an activation row and one per
+ * 128 x 128 tile of a weight matrix: packing, the product, and the product grouped by
+ * expert (fp8_blockscaled_gemm is the form with a scale per row of both operands).
+ *
+ * Operand format.  A matrix of `rows` rows of K values is held as
+ *   codes  [rows, 16 * ceil(K/16)] bytes, row-major; packing zeroes the bytes past K,
+ *          products ignore them
+ *   scales [ceil(rows/tile_rows), 4 * ceil(K/512)] float32, row-major: one per tile_rows
+ *          rows (1: activations; 128: weights) and 128 k; packing zeroes the entries
+ *          past the last block, products ignore them
+ * both 16-byte aligned (IGEMM_MISALIGNED otherwise).  `format` is an igemm_fp8.
+ * K <= IGEMM_BSFP8_MAX_K (IGEMM_OVERFLOW_BOUND); any K, whole blocks or not.  Where
+ * K is a multiple of 512, codes and scales of tile_rows 1 are also what
+ * fp8_blockscaled_gemm takes.
+ */
+typedef enum igemm_fp8 { IGEMM_E4M3 = 0, IGEMM_E5M2 = 1 } igemm_fp8;
+#define IGEMM_BSFP8_MAX_K (1 << 22)
+
+/*
+ * Quantise x into codes and scales: s = max(max |x| / F, 2^-126) over the block (F = 448
+ * for e4m3, 57344 for e5m2), codes fp8(x * (1 / s)); every operation float32, rounded to
+ * nearest, ties to even, saturating.  A block that holds a NaN or an infinity gets a NaN
+ * scale and zero codes.
+ *   x, x_type, ld, transposed, index, x_rows   as for pack_mxfp4; index only with
+ *           tile_rows 1 and not with transposed (IGEMM_UNSUPPORTED_SHAPE)
+ *   tile_rows  1 or 128 (IGEMM_UNSUPPORTED_SHAPE otherwise); the last tile of rows may be
+ *           short
+ * rows == 0 or K == 0 is a no-op.
+ */
+IGEMM_API int pack_bsfp8(const void *x, int x_type, int64_t ld, int transposed, const int32_t *index, int x_rows,
+                         int tile_rows, int format, uint8_t *codes, float *scales, int rows, int K,
+                         cudaStream_t stream);
+
+/*
+ * C[m,n] = sum_kb SFA[m,kb] * SFB[n/128,kb] * sum_{k in block kb} a[m,k] * b[n,k], a block's
+ * sum from the tensor core in float32, scaled and added in float32 in block order (a
+ * long K may be cut into up to four parts whose sums are added in order; repeated calls
+ * give the same bits) and rounded once to c_type.
+ *   A, SFA  codes and scales (tile_rows 1) of M rows of K; B, SFB (tile_rows 128) of N
+ *           rows (device)
+ *   C       [M, N] of c_type (igemm_type), row-major, naturally aligned; every element
+ *           written
+ * A NaN scale makes its row (its 128 columns) of C NaN.  M == 0 or N == 0 is a no-op, K ==
+ * 0 zeroes C.  M and N are below 2^31 - 512, ceil(M / 16) ceil(N / 128) below 2^30
+ * (IGEMM_UNSUPPORTED_SHAPE).
+ */
+IGEMM_API int igemm_bsfp8(const uint8_t *A, const uint8_t *B, const float *SFA, const float *SFB, void *C, int c_type,
+                          int format, int M, int N, int K, cudaStream_t stream);
+
+/*
+ * The same product grouped by expert: rows offsets[e] .. offsets[e+1] - 1 of A times the
+ * transpose of B[e], for e = 0 .. E-1.
+ *   A, SFA   codes and scales of `rows` rows; B [E, N, ...]; SFB [E, ceil(N/128), ...]
+ *   offsets  [E + 1] int32 and C [rows, N] as for igemm_mxfp4_grouped; rows of no group
+ *            are left as they were
+ * E <= 1024, rows and E * N < 2^31 - 512, (rows / 16 + E) ceil(N / 128) < 2^30
+ * (IGEMM_UNSUPPORTED_SHAPE, as K == 0 is); rows, N or E of 0 is a no-op.
+ */
+IGEMM_API int igemm_bsfp8_grouped(const uint8_t *A, const uint8_t *B, const float *SFA, const float *SFB,
+                                  const int32_t *offsets, void *C, int c_type, int format, int rows, int E, int N, int K,
+                                  cudaStream_t stream);
 
 /* Static, human-readable text for an igemm_status value. */
 IGEMM_API const char *igemm_strerror(int code);

@@ -27,6 +27,7 @@ __all__ = [
     "pack_mxfp4", "pack_nvfp4", "igemm_mxfp4", "igemm_nvfp4",
     "igemm_mxfp4_grouped", "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine",
     "fp4_code_bytes", "mxfp4_scale_pitch", "nvfp4_scale_pitch",
+    "pack_bsfp8", "igemm_bsfp8", "igemm_bsfp8_grouped", "bsfp8_code_bytes", "bsfp8_scale_pitch",
     "EXPORTED_SYMBOLS", "LIB_PATH", "build_library",
 ]
 
@@ -36,7 +37,8 @@ EXPORTED_SYMBOLS = ("i4i4_gemm", "i4i4_gemm_noalloc", "w4a8_gemm", "i4i4_gemm_ho
                     "igemm_watchdog_selftest", "igemm_kernels_launched",
                     "igemm_time_next_gemm", "igemm_skinny_plan", "igemm_ss_plan", "igemm_route",
                     "pack_mxfp4", "pack_nvfp4", "igemm_mxfp4", "igemm_nvfp4", "igemm_mxfp4_grouped",
-                    "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine")
+                    "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine",
+                    "pack_bsfp8", "igemm_bsfp8", "igemm_bsfp8_grouped")
 
 IGEMM_OK = 0
 IGEMM_INVALID_ARGUMENT = 1
@@ -117,8 +119,12 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.igemm_nvfp4_grouped.argtypes = [p, p, p, p, p, p, p, i, i, i, i, i, p]
     lib.igemm_moe_route.argtypes = [p, i, p, p, p, p, p, i, i, i, i, p]
     lib.igemm_moe_combine.argtypes = [p, p, p, p, i, i, i, i, p]
+    lib.pack_bsfp8.argtypes = [p, i, i64, i, p, i, i, i, p, p, i, i, p]
+    lib.igemm_bsfp8.argtypes = [p, p, p, p, p, i, i, i, i, i, p]
+    lib.igemm_bsfp8_grouped.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, p]
     for name in ("pack_mxfp4", "pack_nvfp4", "igemm_mxfp4", "igemm_nvfp4", "igemm_mxfp4_grouped",
-                 "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine"):
+                 "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine", "pack_bsfp8", "igemm_bsfp8",
+                 "igemm_bsfp8_grouped"):
         getattr(lib, name).restype = i
     lib.igemm_watchdog_selftest.argtypes = [ctypes.c_uint32, p]
     lib.igemm_watchdog_selftest.restype = i
@@ -353,7 +359,8 @@ def _typed(x, dtype: str, count: int, where: str, name: str):
     return _dev(x, 4 * count, where, name)
 
 
-def _pack_fp4(fn, where, x, extra, codes, scales, rows, K, index, pitch, stream):
+def _pack_operand(where, x, rows, K, index):
+    """(type, leading dimension, transposed, rows) of the matrix x that `rows` rows of K are packed from."""
     t, _ = _type(x, where)
     if not x.is_cuda or x.dim() != 2:
         raise ValueError(f"{where}: x must be a CUDA matrix")
@@ -371,6 +378,11 @@ def _pack_fp4(fn, where, x, extra, codes, scales, rows, K, index, pitch, stream)
         raise ValueError(f"{where}: x has overlapping rows")
     if transposed and index is not None:
         raise ValueError(f"{where}: rows of a transposed x cannot be gathered")
+    return t, ld, transposed, r
+
+
+def _pack_fp4(fn, where, x, extra, codes, scales, rows, K, index, pitch, stream):
+    t, ld, transposed, r = _pack_operand(where, x, rows, K, index)
     n = _n(rows)
     _check(fn(x.data_ptr(), t, ld, transposed, _typed(index, "torch.int32", n, where, "index"), r, *extra,
               _dev(codes, n * fp4_code_bytes(K), where, "codes"), _dev(scales, n * pitch, where, "scales"), rows, K,
@@ -459,6 +471,70 @@ def igemm_moe_combine(Y, slots, weights, out, T: int, k: int, N: int, stream=Non
         _dev(Y, size * _n(pairs, N), w, "Y"), _typed(slots, "torch.int32", pairs, w, "slots"),
         _typed(weights, "torch.float32", pairs, w, "weights"), _dev(out, size * _n(T, N), w, "out"), t, T,
         k, N, _stream(stream)), w)
+
+
+# ---------------------------------------------------------------- block-scaled fp8
+FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
+
+
+def bsfp8_code_bytes(K: int) -> int:
+    """Bytes of a row of K fp8 codes (whole 16-byte units)."""
+    return -(-K // 16) * 16
+
+
+def bsfp8_scale_pitch(K: int) -> int:
+    """float32 scales of a row of K values: one per 128 k, rounded up to four."""
+    return -(-K // 512) * 4
+
+
+def _fp8_format(format: str, where: str) -> int:
+    f = FP8_FORMATS.get(format)
+    if f is None:
+        raise ValueError(f"{where}: format must be 'e4m3' or 'e5m2', not {format!r}")
+    return f
+
+
+def pack_bsfp8(x, codes, scales, rows: int, K: int, tile_rows: int = 1, format: str = "e4m3", index=None,
+               stream=None) -> None:
+    """codes [rows, bsfp8_code_bytes(K)] (a byte each), scales [ceil(rows/tile_rows), bsfp8_scale_pitch(K)] (float32) =
+    x quantised to fp8 with one scale per tile_rows (1: activations, 128: weights) x 128 k.  x and index as for
+    pack_mxfp4 (index with tile_rows 1 only)."""
+    w = "pack_bsfp8"
+    t, ld, transposed, r = _pack_operand(w, x, rows, K, index)
+    n = _n(rows)
+    tiles = n if tile_rows == 1 else -(-n // 128)
+    _check(load().pack_bsfp8(x.data_ptr(), t, ld, transposed, _typed(index, "torch.int32", n, w, "index"), r, tile_rows,
+                             _fp8_format(format, w), _dev(codes, n * bsfp8_code_bytes(K), w, "codes"),
+                             _typed(scales, "torch.float32", tiles * bsfp8_scale_pitch(K), w, "scales"), rows, K,
+                             _stream(stream)), w)
+
+
+def _bsfp8_args(A, B, SFA, SFB, C, M, E, N, K, where):
+    kb, pitch = bsfp8_code_bytes(K), bsfp8_scale_pitch(K)
+    t, size = _type(C, where)
+    m = _n(M)
+    return ((_dev(A, m * kb, where, "A"), _dev(B, _n(E, N) * kb, where, "B"),
+             _typed(SFA, "torch.float32", m * pitch, where, "SFA"),
+             _typed(SFB, "torch.float32", _n(E, -(-N // 128)) * pitch, where, "SFB")),
+            (_dev(C, size * _n(M, N), where, "C"), t))
+
+
+def igemm_bsfp8(A, B, SFA, SFB, C, M: int, N: int, K: int, format: str = "e4m3", stream=None) -> None:
+    """C[M,N] (float32, bfloat16 or float16) = A . B^T of block-scaled fp8 matrices: A as pack_bsfp8 writes it with
+    tile_rows 1, B with tile_rows 128."""
+    w = "igemm_bsfp8"
+    ops, c = _bsfp8_args(A, B, SFA, SFB, C, M, 1, N, K, w)
+    _check(load().igemm_bsfp8(*ops, *c, _fp8_format(format, w), M, N, K, _stream(stream)), w)
+
+
+def igemm_bsfp8_grouped(A, B, SFA, SFB, offsets, C, rows: int, E: int, N: int, K: int, format: str = "e4m3",
+                        stream=None) -> None:
+    """Rows offsets[e] .. offsets[e+1]-1 of C [rows, N] = those rows of A times the transpose of B[e] (B [E, N, ...], SFB
+    [E, ceil(N/128), ...]); offsets: int32 [E+1] on the device.  Rows of no group are left as they were."""
+    w = "igemm_bsfp8_grouped"
+    ops, c = _bsfp8_args(A, B, SFA, SFB, C, rows, E, N, K, w)
+    _check(load().igemm_bsfp8_grouped(*ops, _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"), *c,
+                                      _fp8_format(format, w), rows, E, N, K, _stream(stream)), w)
 
 
 def igemm_strerror(code: int) -> str:

@@ -85,13 +85,13 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_tiled()
 }
 
 int make_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t rows, uint64_t cols,
-             uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle)
+             uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle, uint64_t pitch)
 {
     auto fn = encode_tiled();
     if (!fn) return kCudaError;
     const uint64_t esize = (dtype == CU_TENSOR_MAP_DATA_TYPE_INT32 || dtype == CU_TENSOR_MAP_DATA_TYPE_FLOAT32) ? 4 : 1;
     const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {cols * esize};
+    const cuuint64_t strides[1] = {pitch ? pitch : cols * esize};
     const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, dtype, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -1,0 +1,729 @@
+// Block-scaled fp8 GEMM, dense or grouped by expert:
+//
+//   C[m,n] = sum_kb sa[m,kb] sb[n/128,kb] sum_{k in block kb} a[m,k] b[n,k]
+//
+// with fp8 codes (both operands e4m3 or both e5m2), float32 scales per row and 128 k
+// of A and per 128 x 128 tile of B, float32 accumulation.  The scales are any float32
+// values, which the tensor core's own block scaling (powers of two) cannot take, so
+// the tensor core writes a block's partial sums to one of PB buffers in tensor memory
+// and the CUDA cores add it, times its scale, to totals in registers: 32 FMAs per
+// output and 4096 k beside the MMAs, as f32x2 pairs.
+//
+// The weights B are the MMA's M side (128 rows per CTA) and the activations its N
+// side, so that one kernel serves a single token (N = 16) and a prompt (N = 256 on a
+// CTA pair) and the N of a ragged last tile is set per tile.  A scale then belongs to a
+// column of the partial.  Loaded in fragment order (16x256b) a thread holds four
+// rows of each of its columns, so that 16 bytes of scales serve 16 values; in the plain
+// order (a lane a row) they would serve four, 1024 cycles of shared memory a block
+// beside the 512 of its MMAs.
+//
+// Full tiles of a CTA pair turn the operands round (256 activations on the M side, 256
+// weight rows on the N side): a lane's scale is then one number per block.
+//
+// Warps 0 .. EW-1 epilogue (four or eight), then two that issue MMAs (alternate blocks: a
+// thread that waits after issuing resumes only when its MMAs are done), one that loads
+// codes, one for the scales.  Persistent CTAs (or CTA pairs, or clusters that split k).
+// Every wait is bounded.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include "ptx.cuh"
+#include "bsfp8.cuh"
+#include "gemm_fp4_kernel.cuh"  // groups of rows, stores of a tile
+
+namespace igemm {
+
+struct Bsfp8Params {
+    void *C;               // [rows, N] row-major
+    int c_type;            // Fp4OutType
+    const int *offsets;    // [experts + 1] rows of each group, or null: one group of all rows
+    int rows, N, experts;
+    int blocks;            // of 128 k: ceil(K / 128)
+    int qt;                // activation rows per tile (Cfg::BN)
+    int p_tiles;           // tiles of 128 weight rows (pair: of 256)
+    int n_blocks;          // rows of scales per expert: ceil(N / 128)
+    int group_p;           // tiles run in groups of group_p weight tiles (fastest) by every activation tile
+    int cs;                // CTAs of a cluster that split k (1, 2 or 4)
+    int slice;             // blocks of 128 k per CTA of such a cluster (a multiple of 4)
+    int stream;            // single CTAs: the weights leave L2 first
+    int format;            // 0 e4m3, 1 e5m2
+    int turned;            // CTA pairs: full tiles with the activations on the M side
+    int stages;            // ring slots of codes, even
+    int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
+    int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
+    int *status;
+    unsigned long long limit_ns;
+};
+
+template <int BN_, bool PAIR_>
+struct Bsfp8Cfg {
+    static constexpr int BN = BN_;                     // most activation rows per tile
+    static constexpr bool PAIR = PAIR_;
+    static constexpr int CL = PAIR ? 2 : 1;
+    static constexpr int kParts = BN >= 64 ? 2 : 1;    // epilogue warps per TMEM lane quadrant
+    static constexpr int PC = BN / kParts;             // columns of each
+    static constexpr int EW = 4 * kParts;
+    static constexpr int PB = PAIR ? 2 : 4;            // partial buffers of BN columns in TMEM
+    static constexpr int kQBox = BN / CL;              // activation rows this CTA loads
+    // a tile with few activation rows loads them in one or two boxes of a quarter of the
+    // full box
+    static constexpr int kQRows = BN >= 128 ? kQBox / 4 : kQBox;
+    static constexpr int kBoxP = 128 * 128;            // bytes of a block
+    static constexpr int kBoxQ = kQBox * 128;
+    static constexpr int kStage = kBoxP + kBoxQ;
+    // four blocks' scales: BN rows of 16 bytes (turned: [4][BN]), then CL rows of the weights'
+    static constexpr int kScaleStage = BN * 16 + 128;
+    static constexpr int SS = PAIR ? 3 : BN == 128 ? 4 : 8;  // ring slots of scales
+    static constexpr int kTmemCols = PB * BN;
+    static constexpr int kRedBytes = BN <= 128 ? BN * 512 : 0;  // split k: the cluster's partials of this CTA's part
+    static constexpr int kStoreBytes = EW * 2048;      // 16-bit C: 32 rows x 32 columns per epilogue warp
+    static constexpr int kMaxStages = 16;
+    static constexpr int kNumBars = 2 * kMaxStages + 3 * SS + 2 * PB + 2 + 2 * EW;
+    static constexpr int kBarBytes = (8 * kNumBars + 15) & ~15;
+    static constexpr int kTailBytes = kBarBytes + 32;  // and the groups' table, 16 bytes each
+    static constexpr int kNAlign = PAIR ? 32 : 16;
+    static constexpr int kWarpMma = EW, kWarpLoad = EW + 2, kWarpScale = EW + 3;
+    static constexpr int kThreads = 32 * (EW + 4);
+    static_assert(kStage % 1024 == 0 && kScaleStage % 128 == 0, "aligned operand tiles");
+    static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
+    static_assert(PB % 2 == 0, "a buffer belongs to one of the two issuing warps");
+    static_assert(!PAIR || BN == 256, "the pair form is built for 256 activation rows");
+    static_assert(PC % 16 == 0, "whole loads");
+    static_assert(EW * 8 * 16 <= kStoreBytes, "notices of a split k");
+};
+
+// Tile t: group by binary search over the first tiles; whole tiles of qt activation rows
+// and a remainder, in the grouped order of weight and activation tiles.
+template <class Cfg>
+__device__ __forceinline__ Fp4Tile bsfp8_tile(const Bsfp8Params &prm, const Fp4Group *groups, int t, int rank)
+{
+    int begin = 0, count = prm.rows, r = t, e = 0, q_tiles;
+    if (prm.offsets) {
+        int lo = 0, hi = prm.experts;  // groups[lo].x <= t, t below every later group's
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (groups[mid].x <= t) lo = mid;
+            else hi = mid;
+        }
+        const Fp4Group g = groups[lo];
+        e = lo;
+        r = t - g.x;
+        begin = g.y;
+        count = g.z;
+        q_tiles = g.w;
+    } else {
+        q_tiles = (count + prm.qt - 1) / prm.qt;
+    }
+    Fp4Tile x;
+    x.e = e;
+    const int per_group = prm.group_p * q_tiles;
+    const int grp = r / per_group;
+    const int first = grp * prm.group_p;
+    const int gsize = min(prm.p_tiles - first, prm.group_p);
+    r -= grp * per_group;
+    const int qi = r / gsize;
+    x.p0 = ((first + r - qi * gsize) * Cfg::CL + rank) * 128;
+    x.q0 = begin + qi * prm.qt;
+    x.nq = min(count - qi * prm.qt, prm.qt);
+    return x;
+}
+
+// totals (a pair) += v * s
+__device__ __forceinline__ void bsfp8_fma2(unsigned long long &t, uint32_t v0, uint32_t v1, float s0, float s1)
+{
+    asm("{\n\t.reg .b64 v, s;\n\t"
+        "mov.b64 v, {%1, %2};\n\t"
+        "mov.b64 s, {%3, %4};\n\t"
+        "fma.rn.f32x2 %0, v, s, %0;\n\t}"
+        : "+l"(t)
+        : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
+}
+__device__ __forceinline__ uint32_t bsfp8_lo(unsigned long long t) { return static_cast<uint32_t>(t); }
+__device__ __forceinline__ uint32_t bsfp8_hi(unsigned long long t) { return static_cast<uint32_t>(t >> 32); }
+
+// 16 bytes of scales: the columns of 16 in the order of the fragments (columns 2 q, 2 q +
+// 1, 8 + 2 q, 9 + 2 q at 4 q).
+__device__ __forceinline__ int bsfp8_place(int column)
+{
+    return (column & ~15) + ((column >> 1) & 3) * 4 + ((column >> 3) & 1) * 2 + (column & 1);
+}
+
+template <int R>
+__device__ __forceinline__ void bsfp8_regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void bsfp8_regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// Two barriers (their tests overlap when they are already complete).
+__device__ __forceinline__ bool bsfp8_warp_wait2(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb, const Watchdog &wd)
+{
+    const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+    if (__all_sync(0xffffffffu, ra && rb)) return true;
+    const bool ok = wait_bounded(a, pa, wd) && wait_bounded(b, pb, wd);
+    return __all_sync(0xffffffffu, ok);
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::kThreads, 1)
+    igemm_bsfp8_kernel(const __grid_constant__ CUtensorMap mapP, const __grid_constant__ CUtensorMap mapQ,
+                       const __grid_constant__ CUtensorMap mapQs, const __grid_constant__ CUtensorMap mapSP,
+                       const __grid_constant__ CUtensorMap mapSQ, const Bsfp8Params prm)
+{
+    constexpr bool PAIR = Cfg::PAIR;
+    constexpr int BN = Cfg::BN, PB = Cfg::PB, SS = Cfg::SS, EW = Cfg::EW, PC = Cfg::PC;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *codes = smem;
+    uint8_t *scales = smem + prm.off_scales;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + prm.off_bars);
+    uint64_t *full = bars;                        // [stages] codes landed (pair: both CTAs', in the even CTA)
+    uint64_t *empty = full + Cfg::kMaxStages;     // [stages] consumed (MMA commit)
+    uint64_t *s_raw = empty + Cfg::kMaxStages;    // [SS] scale rows landed
+    uint64_t *s_full = s_raw + SS;                // [SS] ... turned (scale warp)
+    uint64_t *s_empty = s_full + SS;              // [SS] read (epilogue warps)
+    uint64_t *p_full = s_empty + SS;              // [PB] a block's partial complete (commit)
+    uint64_t *p_empty = p_full + PB;              // [PB] ... read by the epilogue warps (pair: both CTAs', in the even CTA)
+    uint64_t *mma_drain = p_empty + PB;           // [2]
+    uint64_t *red_full = mma_drain + 2;           // [EW] split k: the other CTAs' partials for this warp landed
+    uint64_t *red_empty = red_full + EW;          // [EW] ... and the other CTAs have read what this warp sent
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + prm.off_bars + Cfg::kBarBytes);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *total_slot = reinterpret_cast<int *>(tmem_slot + 2);
+    uint8_t *fixed = reinterpret_cast<uint8_t *>(tmem_slot) + 16;  // 16 bytes that stay as they are
+    Fp4Group *groups = reinterpret_cast<Fp4Group *>(smem + prm.off_bars + Cfg::kTailBytes);
+    // split k: 16 bytes for each notice of another CTA, never read ([EW][4 CTAs], in the
+    // staging of stores, which it does not use)
+    uint8_t *notices = smem + prm.off_store;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int cs = PAIR ? 1 : prm.cs;
+    const int csize = PAIR ? 2 : cs;
+    const int rank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int pr = PAIR ? rank : 0;  // half of the pair's tile
+    const int cid = blockIdx.x / csize, ncl = gridDim.x / csize;
+    const bool leader = !PAIR || rank == 0;
+
+    if (warp == Cfg::kWarpLoad) {
+        if (lane < prm.stages) {
+            mbar_init(&full[lane], 1);
+            mbar_init(&empty[lane], 1);
+        }
+        if (lane < SS) {
+            mbar_init(&s_raw[lane], 1);
+            mbar_init(&s_full[lane], 1);
+            mbar_init(&s_empty[lane], EW);
+        }
+        if (lane < PB) {
+            mbar_init(&p_full[lane], 1);
+            mbar_init(&p_empty[lane], EW * Cfg::CL);
+        }
+        if (lane < 2) mbar_init(&mma_drain[lane], 1);
+        if (cs > 1 && lane < EW) {
+            mbar_init(&red_full[lane], 1);
+            mbar_init(&red_empty[lane], 1);
+        }
+        if (lane == 0) {
+            *abort_flag = 0;
+            tma_prefetch_map(&mapP);
+            tma_prefetch_map(&mapQ);
+            if (Cfg::kQRows < Cfg::kQBox) tma_prefetch_map(&mapQs);
+            tma_prefetch_map(&mapSP);
+            tma_prefetch_map(&mapSQ);
+        }
+        fence_mbar_init();
+    }
+    if (warp == Cfg::kWarpMma) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(tmem_slot, Cfg::kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, Cfg::kTmemCols);
+            tmem_relinquish();
+        }
+    }
+    if (warp == 0) {
+        if (prm.offsets) {
+            // running tile counts of the groups (the offsets may come from the kernel before)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int run = 0;
+            for (int e0 = 0; e0 < prm.experts; e0 += 32) {
+                const Fp4Group g = fp4_groups32(prm, e0, run);
+                if (e0 + lane < prm.experts) groups[e0 + lane] = g;
+            }
+            if (lane == 0) *total_slot = run;
+        } else if (lane == 0) {
+            *total_slot = (prm.rows + prm.qt - 1) / prm.qt * prm.p_tiles;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int tiles = *total_slot;
+    if (csize > 1) cluster_sync_all();  // the other CTAs' barriers are initialised
+    // Up to here the kernel before this one in the stream may still run.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Watchdog wd{abort_flag, prm.status, prm.limit_ns};
+    // this CTA's slice of k, in blocks (split k: the cluster rank's)
+    const int b0 = PAIR ? 0 : min(rank * prm.slice, prm.blocks);
+    const int b1 = PAIR ? prm.blocks : min(b0 + prm.slice, prm.blocks);
+
+    if (warp >= EW) {
+        // (of 168 registers a thread at the launch: 256 x 216 + 128 x 72 = 384 x 168)
+        if constexpr (PAIR) bsfp8_regs_dec<72>();
+        if (warp == Cfg::kWarpLoad) {
+            // -------------------------------------------------------- codes
+            Fp4Ring cr(prm.stages);
+            const bool stream = !PAIR && prm.stream;
+            const uint64_t evict_first = l2_policy_evict_first();
+            uint32_t issued = 0, last = 0;
+            bool ok = true;
+            for (int t = cid; ok && t < tiles; t += ncl) {
+                const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
+                // activation rows that this CTA loads (pair: half of the tile's)
+                const int mine = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : x.nq;
+                const bool small = Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
+                const bool two = small && mine > Cfg::kQRows;
+                const int py = x.e * prm.N + x.p0, qy = x.q0 + pr * mine;
+                const uint32_t tx = static_cast<uint32_t>(Cfg::kBoxP +
+                                                          (!small ? Cfg::kBoxQ : (two ? 2 : 1) * Cfg::kQRows * 128));
+                const CUtensorMap *mq = small ? &mapQs : &mapQ;
+#pragma unroll 1
+                for (int b = b0; b < b1; ++b) {
+                    if (!fp4_warp_wait(&empty[cr.slot], cr.phase ^ 1u, wd)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        uint8_t *to = codes + cr.slot * Cfg::kStage, *tq = to + Cfg::kBoxP;
+                        if constexpr (PAIR) {
+                            // both CTAs' bytes count on the even CTA's barrier
+                            if (leader) mbar_arrive_expect_tx(&full[cr.slot], 2 * tx);
+                            const uint32_t bar = cluster_map(smem_u32(&full[cr.slot]), 0u);
+                            tma_load_2d_pair(to, &mapP, bar, b * 128, py);
+                            tma_load_2d_pair(tq, mq, bar, b * 128, qy);
+                            if (two) tma_load_2d_pair(tq + Cfg::kQRows * 128, mq, bar, b * 128, qy + Cfg::kQRows);
+                        } else {
+                            mbar_arrive_expect_tx(&full[cr.slot], tx);
+                            if (stream) tma_load_2d_hint(to, &mapP, &full[cr.slot], b * 128, py, evict_first);
+                            else tma_load_2d(to, &mapP, &full[cr.slot], b * 128, py);
+                            tma_load_2d(tq, mq, &full[cr.slot], b * 128, qy);
+                            if (two) tma_load_2d(tq + Cfg::kQRows * 128, mq, &full[cr.slot], b * 128, qy + Cfg::kQRows);
+                        }
+                    }
+                    __syncwarp();
+                    issued |= 1u << cr.slot;
+                    last = (last & ~(1u << cr.slot)) | (cr.phase << cr.slot);
+                    cr.next();
+                }
+            }
+            // never leave with copies in flight, nor with an MMA commit on its way here
+            const uint64_t t0 = globaltimer_ns();
+            if (leader) fp4_drain(full, issued, last, t0, prm.limit_ns);
+            fp4_drain(empty, issued, last, t0, prm.limit_ns);
+        } else if (warp == Cfg::kWarpScale) {
+            // -------------------------------------------------------- scales
+            // Four blocks at a time.  The loads run SS - 1 groups of blocks ahead of the
+            // turning, so that the slot of the next one is that of the group before, which
+            // the epilogue leaves while it has the turned one still to do.
+            Fp4Ring lr(SS), sr(SS);
+            uint32_t issued = 0, last = 0;
+            bool ok = true;
+            int lt = cid, lb = b0;  // next to load
+            const auto load = [&] {
+                const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, lt, pr);
+                ok = fp4_warp_wait(&s_empty[lr.slot], lr.phase ^ 1u, wd);
+                if (!ok) return;
+                if (elect_one()) {
+                    uint8_t *to = scales + lr.slot * Cfg::kScaleStage;
+                    mbar_arrive_expect_tx(&s_raw[lr.slot], BN * 16 + Cfg::CL * 16);
+                    tma_load_2d(to, &mapSQ, &s_raw[lr.slot], lb * 4, x.q0);
+                    tma_load_2d(to + BN * 16, &mapSP, &s_raw[lr.slot], lb * 4,
+                                x.e * prm.n_blocks + (x.p0 / 128 - pr));
+                }
+                __syncwarp();
+                issued |= 1u << lr.slot;
+                last = (last & ~(1u << lr.slot)) | (lr.phase << lr.slot);
+                lr.next();
+                lb += 4;
+                if (lb >= b1) {
+                    lb = b0;
+                    lt += ncl;
+                }
+            };
+            if (b0 < b1) {
+                for (int i = 0; i < SS - 1 && ok && lt < tiles; ++i) load();
+                for (int t = cid; ok && t < tiles; t += ncl) {
+                    const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
+                    const bool lanes = PAIR && prm.turned && x.nq == BN;
+                    for (int b = b0; ok && b < b1; b += 4) {
+                        ok = fp4_warp_wait(&s_raw[sr.slot], sr.phase, wd);
+                        if (!ok) break;
+                        if (!lanes) {
+                            // [BN][4] to [4][BN], times the weights' scale
+                            float4 *raw = reinterpret_cast<float4 *>(scales + sr.slot * Cfg::kScaleStage);
+                            float *to = reinterpret_cast<float *>(raw);
+                            const float4 sb = raw[BN + pr];
+                            constexpr int R = (BN + 31) / 32;
+                            float4 v[R];
+#pragma unroll
+                            for (int i = 0; i < R; ++i)
+                                if (32 * i + lane < BN) v[i] = raw[32 * i + lane];
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < R; ++i)
+                                if (32 * i + lane < BN) {
+                                    const int at = bsfp8_place(32 * i + lane);
+                                    to[at] = v[i].x * sb.x;
+                                    to[BN + at] = v[i].y * sb.y;
+                                    to[2 * BN + at] = v[i].z * sb.z;
+                                    to[3 * BN + at] = v[i].w * sb.w;
+                                }
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_full[sr.slot]);
+                        sr.next();
+                        if (lt < tiles) load();
+                    }
+                }
+            }
+            const uint64_t t0 = globaltimer_ns();
+            fp4_drain(s_raw, issued, last, t0, prm.limit_ns);
+        } else if (leader) {
+            // -------------------------------------------------------- MMA issuers
+            const int me = warp - Cfg::kWarpMma;
+            const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(codes));
+            const uint32_t fmt = static_cast<uint32_t>(prm.format);
+            Fp4Ring cr(prm.stages);
+            uint32_t g = 0;
+            bool ok = true;
+            for (int t = cid; ok && t < tiles; t += ncl) {
+                const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
+                const uint32_t nq = static_cast<uint32_t>((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1));
+                const bool lanes = PAIR && prm.turned && x.nq == BN;
+                const uint32_t idesc = idesc_f8_f32(128 * Cfg::CL, nq, fmt);
+                for (int b = b0; b < b1; ++b, ++g) {
+                    if (static_cast<int>(g & 1u) == me) {
+                        const uint32_t pb = g % PB;
+                        if (!bsfp8_warp_wait2(&p_empty[pb], ((g / PB) & 1u) ^ 1u, &full[cr.slot], cr.phase, wd)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t p0 = desc0 + static_cast<uint64_t>(cr.slot * (Cfg::kStage >> 4));
+                            const uint64_t q0 = p0 + static_cast<uint64_t>(Cfg::kBoxP >> 4);
+                            const uint64_t da = lanes ? q0 : p0, db = lanes ? p0 : q0;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if constexpr (PAIR)
+                                    mma_f8f6f4_pair(tmem + pb * BN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
+                                else
+                                    mma_f8f6f4(tmem + pb * BN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
+                            }
+                            if constexpr (PAIR) {
+                                mma_commit_pair_multicast(&empty[cr.slot], 0x3);
+                                mma_commit_pair_multicast(&p_full[pb], 0x3);
+                            } else {
+                                mma_commit(&empty[cr.slot]);
+                                mma_commit(&p_full[pb]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    cr.next();
+                }
+            }
+            if (elect_one()) {
+                if constexpr (PAIR) mma_commit_pair(&mma_drain[me]);
+                else mma_commit(&mma_drain[me]);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        if constexpr (PAIR) bsfp8_regs_inc<216>();
+        const int quad = warp & 3, part = warp >> 2;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * PC;
+        uint8_t *stage = smem + prm.off_store + warp * 2048;
+        const uint32_t empty_leader = PAIR ? cluster_map(smem_u32(p_empty), 0u) : 0u;
+        const int q4 = lane & 3;
+        Fp4Ring sr(SS);
+        uint32_t g = 0, n = 0, armed = 0;  // armed: split k, tiles whose partials this warp expects
+        bool ok = true;
+        for (int t = cid; t < tiles; t += ncl, ++n) {
+            const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
+            const bool lanes = PAIR && prm.turned && x.nq == BN;
+            // the tile's columns of this warp
+            const int cols = min(x.nq - part * PC, PC);
+            unsigned long long tot[PC / 2];
+#pragma unroll
+            for (int i = 0; i < PC / 2; ++i) tot[i] = 0ull;
+#pragma unroll 1
+            for (int b = b0; b < b1; ++b, ++g) {
+                const uint32_t pb = g % PB;
+                if ((b & 3) == 0) {
+                    ok = fp4_warp_wait(&s_full[sr.slot], sr.phase, wd);
+                    if (!ok) break;
+                }
+                ok = fp4_warp_wait(&p_full[pb], (g / PB) & 1u, wd);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t tacc = trow + pb * BN;
+                const auto release = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) mbar_arrive(&p_empty[pb]);
+                        else mbar_arrive_peer(empty_leader + 8u * pb);
+                    }
+                };
+                const float *sc = reinterpret_cast<const float *>(scales + sr.slot * Cfg::kScaleStage);
+                if (!lanes) {
+                    // 32 columns of fragments at a time, the next ones in flight
+                    constexpr int kChunk = PC < 32 ? 16 : 32, kChunks = PC / kChunk;
+                    const int chunks = (cols + kChunk - 1) / kChunk;
+                    const float4 *s4 = reinterpret_cast<const float4 *>(sc + (b & 3) * BN + part * PC) + q4;
+                    uint32_t v[2][kChunk];
+                    const auto load = [&](int i, uint32_t(&to)[kChunk]) {
+                        if constexpr (kChunk == 32) {
+                            tmem_ld_16x256b_x4(tacc + 32 * i, to);
+                            tmem_ld_16x256b_x4(tacc + (16u << 16) + 32 * i, to + 16);
+                        } else {
+                            tmem_ld_16x256b_x2(tacc + 16 * i, to);
+                            tmem_ld_16x256b_x2(tacc + (16u << 16) + 16 * i, to + 8);
+                        }
+                    };
+                    if (chunks > 0) {
+                        load(0, v[0]);
+                        tmem_ld_wait_regs(v[0]);
+                    } else {
+                        release();
+                    }
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        if (i < chunks) {
+                            if (i + 1 < chunks) load(i + 1, v[(i + 1) & 1]);
+                            else release();
+                            // register of (16 columns c, lanes h of 16, octet o of these, column octet j,
+                            // b): 8 c + 4 j + 2 o + b of lanes h
+#pragma unroll
+                            for (int c = 0; c < kChunk / 16; ++c) {
+                                const float4 s = s4[(i * (kChunk / 16) + c) * 4];
+                                unsigned long long *to = tot + 8 * (i * (kChunk / 16) + c);
+                                const uint32_t(&w)[kChunk] = v[i & 1];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                    for (int o = 0; o < 2; ++o) {
+                                        const int at = h * (kChunk / 2) + 8 * c + 2 * o;
+                                        bsfp8_fma2(to[4 * h + o], w[at], w[at + 1], s.x, s.y);
+                                        bsfp8_fma2(to[4 * h + 2 + o], w[at + 4], w[at + 5], s.z, s.w);
+                                    }
+                            }
+                            if (i + 1 < chunks) tmem_ld_wait_regs(v[(i + 1) & 1]);
+                        }
+                    }
+                } else if constexpr (PAIR) {
+                    // a lane an activation row, the part's 128 columns one block of weight rows
+                    const float s = sc[(rank * 128 + quad * 32 + lane) * 4 + (b & 3)] * sc[(BN + part) * 4 + (b & 3)];
+                    uint32_t v[2][32];
+                    tmem_ld_32x32b_x32(tacc, v[0]);
+                    tmem_ld_wait_regs(v[0]);
+#pragma unroll
+                    for (int i = 0; i < PC / 32; ++i) {
+                        if (i + 1 < PC / 32) tmem_ld_32x32b_x32(tacc + 32 * (i + 1), v[(i + 1) & 1]);
+                        else release();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            bsfp8_fma2(tot[16 * i + j], v[i & 1][2 * j], v[i & 1][2 * j + 1], s, s);
+                        if (i + 1 < PC / 32) tmem_ld_wait_regs(v[(i + 1) & 1]);
+                    }
+                }
+                if ((b & 3) == 3 || b == b1 - 1) {
+                    fence_proxy_async_smem();  // read before the next copies overwrite them
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[sr.slot]);
+                    sr.next();
+                }
+            }
+            if (!ok) break;
+            const int n0 = x.p0 + quad * 32;
+            if (cs > 1) {
+                // split k: CTA r adds the parts of row octets r .. of the cluster's CTAs in
+                // rank order (fixed, whatever arrives first).  An octet's 16 columns are 16
+                // bytes a lane, at [sender][warp][(16 columns, octet of the owner)][lane].
+                const int per = 4 / cs;               // octets of an owner
+                constexpr int C16 = PC / 16;
+                const int units = C16 * per;
+                uint4 *buf = reinterpret_cast<uint4 *>(smem + prm.off_red) + lane;
+                const uint32_t ph = n & 1u;
+                if (lane == 0) mbar_arrive_expect_tx(&red_full[warp], static_cast<uint32_t>((cs - 1) * units * 512));
+                ++armed;
+                ok = fp4_warp_wait_cluster(&red_empty[warp], ph ^ 1u, wd);
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < C16; ++c)
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) {
+                        const int owner = o / per;
+                        const unsigned long long *from = tot + 8 * c + 4 * (o >> 1) + (o & 1);
+                        const uint32_t v[4] = {bsfp8_lo(from[0]), bsfp8_hi(from[0]), bsfp8_lo(from[2]), bsfp8_hi(from[2])};
+                        if (owner != rank) {
+                            const uint4 *to = buf + ((rank * EW + warp) * units + c * per + o % per) * 32;
+                            st_async_v4(cluster_map(smem_u32(to), static_cast<uint32_t>(owner)), v,
+                                        cluster_map(smem_u32(&red_full[warp]), static_cast<uint32_t>(owner)));
+                        }
+                    }
+                ok = fp4_warp_wait_cluster(&red_full[warp], ph, wd);
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < C16; ++c)
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) {
+                        if (o / per != rank) continue;
+                        const unsigned long long *own = tot + 8 * c + 4 * (o >> 1) + (o & 1);
+                        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int r = 0; r < cs; ++r) {
+                            const uint4 v = r == rank ? make_uint4(bsfp8_lo(own[0]), bsfp8_hi(own[0]), bsfp8_lo(own[2]),
+                                                                   bsfp8_hi(own[2]))
+                                                      : buf[((r * EW + warp) * units + c * per + o % per) * 32];
+                            s[0] += __uint_as_float(v.x);
+                            s[1] += __uint_as_float(v.y);
+                            s[2] += __uint_as_float(v.z);
+                            s[3] += __uint_as_float(v.w);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int col = 16 * c + 8 * (j >> 1) + 2 * q4 + (j & 1);
+                            if (col < cols)
+                                fp4_store1(prm, s[j], static_cast<int64_t>(x.q0) + part * PC + col,
+                                           n0 + 8 * o + (lane >> 2));
+                        }
+                    }
+                __syncwarp();
+                // read: the other CTAs may write again, where a later tile does.  Each is sent
+                // 16 bytes (no matter which): this warp's reads come before that copy, so before
+                // its completion, a release at cluster scope.
+                if (t + ncl < tiles) {
+                    if (lane == 0) mbar_arrive_expect_tx(&red_empty[warp], 16u * (cs - 1));
+                    if (lane < cs && lane != rank)
+                        bulk_copy_to_cta(cluster_map(smem_u32(notices + 16 * (4 * warp + rank)), lane), fixed, 16,
+                                         cluster_map(smem_u32(&red_empty[warp]), lane));
+                }
+                continue;
+            }
+            if (PAIR && lanes) {
+                // a lane's row of 128 columns (rows of C start on 16 bytes)
+                const int c0 = x.p0 - 128 * pr + part * PC;
+                const int64_t m = static_cast<int64_t>(x.q0) + rank * 128 + quad * 32 + lane;
+                if (prm.c_type == kOutF32) {
+                    float *to = static_cast<float *>(prm.C) + m * prm.N + c0;
+#pragma unroll
+                    for (int j = 0; j < PC / 4; ++j)
+                        if (c0 + 4 * j < prm.N)
+                            *reinterpret_cast<uint4 *>(to + 4 * j) =
+                                make_uint4(bsfp8_lo(tot[2 * j]), bsfp8_hi(tot[2 * j]), bsfp8_lo(tot[2 * j + 1]),
+                                           bsfp8_hi(tot[2 * j + 1]));
+                } else {
+                    uint16_t *to = static_cast<uint16_t *>(prm.C) + m * prm.N + c0;
+                    const bool bf16 = prm.c_type == kOutBf16;
+#pragma unroll
+                    for (int j = 0; j < PC / 8; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float lo = __uint_as_float(bsfp8_lo(tot[4 * j + i]));
+                            const float hi = __uint_as_float(bsfp8_hi(tot[4 * j + i]));
+                            if (bf16) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                            } else {
+                                const __half2 h = __floats2half2_rn(lo, hi);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                        }
+                        if (c0 + 8 * j < prm.N)
+                            *reinterpret_cast<uint4 *>(to + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else if (prm.c_type == kOutF32) {
+                // (a store: eight columns of C of each of four rows)
+                float *to = static_cast<float *>(prm.C) + (static_cast<int64_t>(x.q0) + part * PC + 2 * q4) * prm.N + n0 +
+                            (lane >> 2);
+#pragma unroll
+                for (int c = 0; c < PC / 8; ++c)
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) {
+                        const unsigned long long v = tot[8 * (c >> 1) + 4 * (o >> 1) + 2 * (c & 1) + (o & 1)];
+                        const int col = 8 * c + 2 * q4;
+                        if (n0 + 8 * o + (lane >> 2) < prm.N) {
+                            float *at = to + static_cast<int64_t>(8 * c) * prm.N + 8 * o;
+                            if (col < cols) at[0] = __uint_as_float(bsfp8_lo(v));
+                            if (col + 1 < cols) at[prm.N] = __uint_as_float(bsfp8_hi(v));
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int c = 0; c < PC; c += 32) {
+                    if (c < cols) {
+                        uint32_t v[2][16];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                // (fragments: lanes 0-15 and 16-31, column octet, row octet)
+                                const int from = c / 2 + 8 * i + j;
+                                const bool there = c + 16 * i < PC;
+                                const unsigned long long w = there ? tot[there ? from : 0] : 0ull;
+                                v[i][2 * j] = bsfp8_lo(w);
+                                v[i][2 * j + 1] = bsfp8_hi(w);
+                            }
+                        fp4_store32_cols<false>(prm, v, 1.0f, static_cast<int64_t>(x.q0) + part * PC + c, cols - c, n0,
+                                                stage);
+                    }
+                }
+            }
+        }
+        // gave up: another CTA's partials may be on their way here, and its notices
+        if (cs > 1 && !ok) {
+            const uint64_t t0 = globaltimer_ns();
+            const auto drain = [&](uint64_t *bar, uint32_t parity) {
+                while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < prm.limit_ns) {
+                }
+            };
+            if (n > 0) drain(&red_empty[warp], (n - 1) & 1u);
+            if (lane == 0 && n >= armed)
+                mbar_arrive_expect_tx(&red_full[warp], static_cast<uint32_t>((cs - 1) * (PC / 16) * (4 / cs) * 512));
+            drain(&red_full[warp], n & 1u);
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    // The next kernel may be set up on SMs that this one has left; it waits for the end
+    // of this grid before it touches memory.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    if (warp == Cfg::kWarpMma) {
+        if (leader && lane == 0) fp4_drain(mma_drain, 3u, 0u, globaltimer_ns(), prm.limit_ns);
+        __syncwarp();
+    }
+    // no CTA of a cluster frees TMEM or leaves while another may still reach it
+    if (csize > 1) cluster_sync_all();
+    if (warp == Cfg::kWarpMma) {
+        tc_fence_after();
+        if constexpr (PAIR)
+            tmem_dealloc_pair(tmem, Cfg::kTmemCols);
+        else
+            tmem_dealloc(tmem, Cfg::kTmemCols);
+    }
+}
+
+}  // namespace igemm

@@ -184,7 +184,8 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Params &prm, const Fp4Group
 // One warp, 32 groups from e0: this lane's group, with its first tile after `run`
 // others; `run` moves past them.  (Groups that overlap against the rules could have
 // more tiles than an int holds: those past kFp4MaxTiles are left out.)
-__device__ __forceinline__ Fp4Group fp4_groups32(const Fp4Params &prm, int e0, int &run)
+template <class Params>
+__device__ __forceinline__ Fp4Group fp4_groups32(const Params &prm, int e0, int &run)
 {
     const int lane = threadIdx.x & 31, e = e0 + lane;
     Fp4Group g = make_int4(0, 0, 0, 0);
@@ -278,7 +279,8 @@ __device__ __forceinline__ uint32_t fp4_keep(uint32_t v, int left)
 }
 
 // One value of C.
-__device__ __forceinline__ void fp4_store1(const Fp4Params &prm, float v, int64_t m, int n)
+template <class Params>
+__device__ __forceinline__ void fp4_store1(const Params &prm, float v, int64_t m, int n)
 {
     if (n >= prm.N) return;
     const int64_t at = m * prm.N + n;
@@ -308,8 +310,8 @@ __device__ __forceinline__ void fp4_load16_cols(uint32_t tacc, int c, uint32_t (
     }
 }
 
-template <bool F32>
-__device__ __forceinline__ void fp4_store32_cols(const Fp4Params &prm, const uint32_t (*v)[16], float alpha, int64_t m0,
+template <bool F32, class Params>
+__device__ __forceinline__ void fp4_store32_cols(const Params &prm, const uint32_t (*v)[16], float alpha, int64_t m0,
                                                  int count, int n0, uint8_t *stage)
 {
     const int lane = threadIdx.x & 31;

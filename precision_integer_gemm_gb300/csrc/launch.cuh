@@ -26,8 +26,9 @@ enum Status : int {
 
 // 2-D tiled tensor map over a row-major matrix [rows, cols] of `dtype`
 // (UINT8 or INT32), box [box_rows, box_cols]; out-of-bounds reads are zero.
+// `pitch`: bytes from row to row (0: rows without gaps).
 int make_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, uint64_t rows, uint64_t cols,
-             uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle);
+             uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle, uint64_t pitch = 0);
 
 // Device status word of the current device (address of a file-scope
 // __device__ int, fetched once per device).
