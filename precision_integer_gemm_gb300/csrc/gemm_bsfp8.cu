@@ -18,8 +18,8 @@ struct Bsfp8Smem {
         const int red = cs > 1 ? Cfg::kRedBytes : 0;
         const int tail = Cfg::kTailBytes + 16 * experts;
         const int left = kLimit - red - Cfg::kStoreBytes - Cfg::SS * Cfg::kScaleStage - tail;
-        // (even: a slot belongs to one of the two issuing warps)
-        stages = std::min(left / Cfg::kStage, static_cast<int>(Cfg::kMaxStages)) & ~1;
+        // (single CTAs: even, a slot belongs to one of the two issuing warps)
+        stages = std::min(left / Cfg::kStage, static_cast<int>(Cfg::kMaxStages)) & ~(Cfg::PAIR ? 0 : 1);
         off_scales = stages * Cfg::kStage;
         off_red = off_scales + Cfg::SS * Cfg::kScaleStage;
         off_store = off_red + red;
@@ -127,6 +127,7 @@ static int launch_bsfp8_cfg(const Bsfp8Call &c, const Bsfp8Plan &plan, cudaStrea
     prm.off_bars = lay.off_bars;
     prm.status = device_status_word();
     prm.limit_ns = watchdog_limit_ns();
+    prm.limit_ns32 = static_cast<uint32_t>(std::min<unsigned long long>(prm.limit_ns, 4000000000ull));
     if (!prm.status) return kCudaError;
     const int64_t q_tiles = (int64_t(c.rows) + Cfg::BN - 1) / Cfg::BN + (c.offsets ? std::min(c.rows, c.experts) - 1 : 0);
     const int64_t tiles = q_tiles * prm.p_tiles;  // grouped: at most

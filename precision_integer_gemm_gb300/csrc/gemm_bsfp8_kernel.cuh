@@ -26,6 +26,7 @@
 // Every wait is bounded.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include "ptx.cuh"
 #include "bsfp8.cuh"
@@ -53,6 +54,7 @@ struct Bsfp8Params {
     int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
     int *status;
     unsigned long long limit_ns;
+    uint32_t limit_ns32;   // the same, at most 4 s
 };
 
 template <int BN_, bool PAIR_>
@@ -60,10 +62,16 @@ struct Bsfp8Cfg {
     static constexpr int BN = BN_;                     // most activation rows per tile
     static constexpr bool PAIR = PAIR_;
     static constexpr int CL = PAIR ? 2 : 1;
+    // a block's partial sums are one accumulator of UN columns, or (pairs) two that are
+    // multiplied, handed over and read apart
+    static constexpr int kUnits = PAIR ? 2 : 1;
+    static constexpr int UN = BN / kUnits;
+    static constexpr int PB = 4;                       // accumulators in TMEM: blocks in turn
+    static constexpr int kTurns = PB / kUnits;
     static constexpr int kParts = BN >= 64 ? 2 : 1;    // epilogue warps per TMEM lane quadrant
-    static constexpr int PC = BN / kParts;             // columns of each
+    static constexpr int CU = UN / kParts;             // most columns of an accumulator for each
+    static constexpr int PC = kUnits * CU;             // ... of a tile
     static constexpr int EW = 4 * kParts;
-    static constexpr int PB = PAIR ? 2 : 4;            // partial buffers of BN columns in TMEM
     static constexpr int kQBox = BN / CL;              // activation rows this CTA loads
     // a tile with few activation rows loads them in one or two boxes of a quarter of the
     // full box
@@ -74,22 +82,30 @@ struct Bsfp8Cfg {
     // four blocks' scales: BN rows of 16 bytes (turned: [4][BN]), then CL rows of the weights'
     static constexpr int kScaleStage = BN * 16 + 128;
     static constexpr int SS = PAIR ? 3 : BN == 128 ? 4 : 8;  // ring slots of scales
-    static constexpr int kTmemCols = PB * BN;
+    static constexpr int kTmemCols = PB * UN;
     static constexpr int kRedBytes = BN <= 128 ? BN * 512 : 0;  // split k: the cluster's partials of this CTA's part
     static constexpr int kStoreBytes = EW * 2048;      // 16-bit C: 32 rows x 32 columns per epilogue warp
     static constexpr int kMaxStages = 16;
     static constexpr int kNumBars = 2 * kMaxStages + 3 * SS + 2 * PB + 2 + 2 * EW;
     static constexpr int kBarBytes = (8 * kNumBars + 15) & ~15;
     static constexpr int kTailBytes = kBarBytes + 32;  // and the groups' table, 16 bytes each
-    static constexpr int kNAlign = PAIR ? 32 : 16;
     static constexpr int kWarpMma = EW, kWarpLoad = EW + 2, kWarpScale = EW + 3;
     static constexpr int kThreads = 32 * (EW + 4);
     static_assert(kStage % 1024 == 0 && kScaleStage % 128 == 0, "aligned operand tiles");
     static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
-    static_assert(PB % 2 == 0, "a buffer belongs to one of the two issuing warps");
+    static_assert(kTurns % 2 == 0, "an accumulator belongs to one of the two issuing warps");
     static_assert(!PAIR || BN == 256, "the pair form is built for 256 activation rows");
-    static_assert(PC % 16 == 0, "whole loads");
+    static_assert(CU % 16 == 0, "whole loads");
     static_assert(EW * 8 * 16 <= kStoreBytes, "notices of a split k");
+
+    // A tile's accumulators, their columns (whole MMA columns that the epilogue's parts
+    // share evenly in 16s) and each part's columns of one.
+    __device__ static int units(int nq) { return kUnits == 2 && nq > UN ? 2 : 1; }
+    __device__ static int columns(int nq)
+    {
+        const int step = 16 * kParts, n = units(nq) == 2 ? (nq + 1) / 2 : nq;
+        return (n + step - 1) / step * step;
+    }
 };
 
 // Tile t: group by binary search over the first tiles; whole tiles of qt activation rows
@@ -128,19 +144,20 @@ __device__ __forceinline__ Fp4Tile bsfp8_tile(const Bsfp8Params &prm, const Fp4G
     return x;
 }
 
-// totals (a pair) += v * s
-__device__ __forceinline__ void bsfp8_fma2(unsigned long long &t, uint32_t v0, uint32_t v1, float s0, float s1)
+__device__ __forceinline__ unsigned long long bsfp8_pair(float lo, float hi)
 {
-    asm("{\n\t.reg .b64 v, s;\n\t"
-        "mov.b64 v, {%1, %2};\n\t"
-        "mov.b64 s, {%3, %4};\n\t"
-        "fma.rn.f32x2 %0, v, s, %0;\n\t}"
-        : "+l"(t)
-        : "r"(v0), "r"(v1), "f"(s0), "f"(s1));
+    unsigned long long p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
 }
-__device__ __forceinline__ uint32_t bsfp8_lo(unsigned long long t) { return static_cast<uint32_t>(t); }
-__device__ __forceinline__ uint32_t bsfp8_hi(unsigned long long t) { return static_cast<uint32_t>(t >> 32); }
-
+using F2 = float2;
+__device__ __forceinline__ void bsfp8_fma2(F2 &t, uint32_t v0, uint32_t v1, F2 s)
+{
+    t = __ffma2_rn(make_float2(__uint_as_float(v0), __uint_as_float(v1)), s, t);
+}
+__device__ __forceinline__ uint32_t bsfp8_lo(F2 t) { return __float_as_uint(t.x); }
+__device__ __forceinline__ uint32_t bsfp8_hi(F2 t) { return __float_as_uint(t.y); }
+__device__ __forceinline__ F2 bsfp8_f2(float a, float b) { return make_float2(a, b); }
 // 16 bytes of scales: the columns of 16 in the order of the fragments (columns 2 q, 2 q +
 // 1, 8 + 2 q, 9 + 2 q at 4 q).
 __device__ __forceinline__ int bsfp8_place(int column)
@@ -159,6 +176,40 @@ __device__ __forceinline__ void bsfp8_regs_dec()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// fp4_warp_wait for the loop that sets the pace: by addresses, and the way taken when the
+// barrier is not there yet needs few registers.
+__device__ __forceinline__ uint32_t bsfp8_there(uint32_t bar, uint32_t parity)
+{
+    uint32_t there;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(there)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return there;
+}
+__device__ __forceinline__ bool bsfp8_wait(uint32_t bar, uint32_t parity, uint32_t abort_at, const Bsfp8Params &prm)
+{
+    if (__all_sync(0xffffffffu, bsfp8_there(bar, parity))) return true;
+    uint32_t start;  // (microseconds of a clock that wraps: 32 bits of it are enough)
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(start));
+#pragma unroll 1
+    for (;;) {
+        if (__all_sync(0xffffffffu, bsfp8_there(bar, parity))) return true;
+        uint32_t now, aborted;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(aborted) : "r"(abort_at) : "memory");
+        const bool late = now - start > prm.limit_ns32;
+        if (__any_sync(0xffffffffu, late && !aborted)) {
+            asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_at), "r"(1) : "memory");
+            atomicCAS(prm.status, 0, kStatusTimeout);
+        }
+        if (__any_sync(0xffffffffu, late || aborted)) return false;
+    }
+}
+
 // Two barriers (their tests overlap when they are already complete).
 __device__ __forceinline__ bool bsfp8_warp_wait2(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb, const Watchdog &wd)
 {
@@ -175,7 +226,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                        const __grid_constant__ CUtensorMap mapSQ, const Bsfp8Params prm)
 {
     constexpr bool PAIR = Cfg::PAIR;
-    constexpr int BN = Cfg::BN, PB = Cfg::PB, SS = Cfg::SS, EW = Cfg::EW, PC = Cfg::PC;
+    constexpr int BN = Cfg::BN, PB = Cfg::PB, SS = Cfg::SS, EW = Cfg::EW, CU = Cfg::CU, PC = Cfg::PC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *codes = smem;
@@ -186,7 +237,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint64_t *s_raw = empty + Cfg::kMaxStages;    // [SS] scale rows landed
     uint64_t *s_full = s_raw + SS;                // [SS] ... turned (scale warp)
     uint64_t *s_empty = s_full + SS;              // [SS] read (epilogue warps)
-    uint64_t *p_full = s_empty + SS;              // [PB] a block's partial complete (commit)
+    uint64_t *p_full = s_empty + SS;              // [PB] an accumulator complete (commit)
     uint64_t *p_empty = p_full + PB;              // [PB] ... read by the epilogue warps (pair: both CTAs', in the even CTA)
     uint64_t *mma_drain = p_empty + PB;           // [2]
     uint64_t *red_full = mma_drain + 2;           // [EW] split k: the other CTAs' partials for this warp landed
@@ -212,7 +263,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     if (warp == Cfg::kWarpLoad) {
         if (lane < prm.stages) {
             mbar_init(&full[lane], 1);
-            mbar_init(&empty[lane], 1);
+            mbar_init(&empty[lane], Cfg::kUnits);  // (pairs: both issuing warps' MMAs)
         }
         if (lane < SS) {
             mbar_init(&s_raw[lane], 1);
@@ -275,8 +326,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int b1 = PAIR ? prm.blocks : min(b0 + prm.slice, prm.blocks);
 
     if (warp >= EW) {
-        // (of 168 registers a thread at the launch: 256 x 216 + 128 x 72 = 384 x 168)
-        if constexpr (PAIR) bsfp8_regs_dec<72>();
+        // (of 168 registers a thread at the launch: 256 x 224 + 128 x 56 = 384 x 168)
+        if constexpr (PAIR) bsfp8_regs_dec<56>();
         if (warp == Cfg::kWarpLoad) {
             // -------------------------------------------------------- codes
             Fp4Ring cr(prm.stages);
@@ -287,7 +338,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             for (int t = cid; ok && t < tiles; t += ncl) {
                 const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
                 // activation rows that this CTA loads (pair: half of the tile's)
-                const int mine = PAIR ? ((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1)) / 2 : x.nq;
+                const int mine = PAIR ? Cfg::units(x.nq) * Cfg::columns(x.nq) / 2 : x.nq;
                 const bool small = Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
                 const bool two = small && mine > Cfg::kQRows;
                 const int py = x.e * prm.N + x.p0, qy = x.q0 + pr * mine;
@@ -340,6 +391,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, lt, pr);
                 ok = fp4_warp_wait(&s_empty[lr.slot], lr.phase ^ 1u, wd);
                 if (!ok) return;
+                fence_proxy_async_smem();  // this warp's earlier writes of turned scales come before the copies
+                __syncwarp();
                 if (elect_one()) {
                     uint8_t *to = scales + lr.slot * Cfg::kScaleStage;
                     mbar_arrive_expect_tx(&s_raw[lr.slot], BN * 16 + Cfg::CL * 16);
@@ -397,21 +450,26 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             fp4_drain(s_raw, issued, last, t0, prm.limit_ns);
         } else if (leader) {
             // -------------------------------------------------------- MMA issuers
+            // A block each in turn, or (pairs) an accumulator of every block each.
             const int me = warp - Cfg::kWarpMma;
             const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(codes));
             const uint32_t fmt = static_cast<uint32_t>(prm.format);
             Fp4Ring cr(prm.stages);
-            uint32_t g = 0;
+            uint32_t phases = 0;  // of the accumulators' turns
             bool ok = true;
             for (int t = cid; ok && t < tiles; t += ncl) {
                 const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
-                const uint32_t nq = static_cast<uint32_t>((x.nq + Cfg::kNAlign - 1) & ~(Cfg::kNAlign - 1));
                 const bool lanes = PAIR && prm.turned && x.nq == BN;
-                const uint32_t idesc = idesc_f8_f32(128 * Cfg::CL, nq, fmt);
-                for (int b = b0; b < b1; ++b, ++g) {
-                    if (static_cast<int>(g & 1u) == me) {
-                        const uint32_t pb = g % PB;
-                        if (!bsfp8_warp_wait2(&p_empty[pb], ((g / PB) & 1u) ^ 1u, &full[cr.slot], cr.phase, wd)) {
+                const int nu = Cfg::units(x.nq), cols = Cfg::columns(x.nq);
+                const uint32_t idesc = idesc_f8_f32(128 * Cfg::CL, static_cast<uint32_t>(cols), fmt);
+                // the second accumulator: the other half of each CTA's rows on the N side
+                const uint64_t half = PAIR ? static_cast<uint64_t>(me * (cols / 2 * 128 >> 4)) : 0;
+                for (int b = b0; b < b1; ++b) {
+                    const uint32_t turn = b % Cfg::kTurns, phase = phases >> turn & 1u;
+                    phases ^= 1u << turn;
+                    if (PAIR || (b & 1) == me) {
+                        const uint32_t pb = PAIR ? 2u * turn + me : turn;
+                        if (!bsfp8_warp_wait2(&p_empty[pb], phase ^ 1u, &full[cr.slot], cr.phase, wd)) {
                             ok = false;
                             break;
                         }
@@ -419,20 +477,22 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         if (elect_one()) {
                             const uint64_t p0 = desc0 + static_cast<uint64_t>(cr.slot * (Cfg::kStage >> 4));
                             const uint64_t q0 = p0 + static_cast<uint64_t>(Cfg::kBoxP >> 4);
-                            const uint64_t da = lanes ? q0 : p0, db = lanes ? p0 : q0;
+                            const uint64_t da = lanes ? q0 : p0, db = (lanes ? p0 : q0) + half;
+                            if (!PAIR || me < nu) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                if constexpr (PAIR)
-                                    mma_f8f6f4_pair(tmem + pb * BN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
-                                else
-                                    mma_f8f6f4(tmem + pb * BN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
+                                for (int q = 0; q < 4; ++q) {
+                                    if constexpr (PAIR)
+                                        mma_f8f6f4_pair(tmem + pb * Cfg::UN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
+                                    else
+                                        mma_f8f6f4(tmem + pb * Cfg::UN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
+                                }
                             }
                             if constexpr (PAIR) {
-                                mma_commit_pair_multicast(&empty[cr.slot], 0x3);
                                 mma_commit_pair_multicast(&p_full[pb], 0x3);
+                                mma_commit_pair_multicast(&empty[cr.slot], 0x3);
                             } else {
-                                mma_commit(&empty[cr.slot]);
                                 mma_commit(&p_full[pb]);
+                                mma_commit(&empty[cr.slot]);
                             }
                         }
                         __syncwarp();
@@ -448,111 +508,159 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        if constexpr (PAIR) bsfp8_regs_inc<216>();
+        if constexpr (PAIR) bsfp8_regs_inc<224>();
         const int quad = warp & 3, part = warp >> 2;
-        const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * PC;
+        const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         uint8_t *stage = smem + prm.off_store + warp * 2048;
-        const uint32_t empty_leader = PAIR ? cluster_map(smem_u32(p_empty), 0u) : 0u;
+        // (the even CTA's; single CTAs: their own)
+        const uint32_t empty_leader = csize > 1 ? cluster_map(smem_u32(p_empty), PAIR ? 0u : rank) : smem_u32(p_empty);
+        const uint32_t abort_at = smem_u32(const_cast<int *>(abort_flag)), p_full_at = smem_u32(p_full), s_full_at = smem_u32(s_full);
         const int q4 = lane & 3;
         Fp4Ring sr(SS);
-        uint32_t g = 0, n = 0, armed = 0;  // armed: split k, tiles whose partials this warp expects
+        uint32_t phases = 0;         // of the accumulators' turns
+        uint32_t n = 0, armed = 0;  // armed: split k, tiles whose partials this warp expects
         bool ok = true;
         for (int t = cid; t < tiles; t += ncl, ++n) {
             const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
             const bool lanes = PAIR && prm.turned && x.nq == BN;
-            // the tile's columns of this warp
-            const int cols = min(x.nq - part * PC, PC);
-            unsigned long long tot[PC / 2];
+            // this warp's columns of an accumulator, and of the tile from c0 on
+            const int nu = Cfg::units(x.nq), cu = Cfg::columns(x.nq) / Cfg::kParts, c0 = part * nu * cu;
+            const int cols = min(x.nq - c0, nu * cu);
+            const uint32_t tpart = trow + part * cu;
+            // The blocks of the tile, an accumulator at a time: load(address, chunk, to) brings
+            // W of its columns of this warp to registers, add(begin(scales, block), h, chunk, from)
+            // adds them, while the other warp of the SM's quarter loads.  Four blocks (a slot of
+            // scales) are straight code: a branch costs as much as a load.  (A CTA that gives up
+            // runs on without waiting: an exit costs registers and moves.)
+            const auto blocks = [&](auto all_units, auto load, auto begin, auto add) {
+                constexpr int W = CU, kChunks = CU / W;
+                const int count = decltype(all_units)::value ? Cfg::kUnits : nu;
+                const auto block = [&](const float *slot, int j) {
+                    const auto sc = begin(slot, j);
+                    const uint32_t turn = j % Cfg::kTurns, phase = phases >> turn & 1u;
+                    phases ^= 1u << turn;
+                    bool early = false;
 #pragma unroll
-            for (int i = 0; i < PC / 2; ++i) tot[i] = 0ull;
-#pragma unroll 1
-            for (int b = b0; b < b1; ++b, ++g) {
-                const uint32_t pb = g % PB;
-                if ((b & 3) == 0) {
-                    ok = fp4_warp_wait(&s_full[sr.slot], sr.phase, wd);
-                    if (!ok) break;
-                }
-                ok = fp4_warp_wait(&p_full[pb], (g / PB) & 1u, wd);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t tacc = trow + pb * BN;
-                const auto release = [&] {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader) mbar_arrive(&p_empty[pb]);
-                        else mbar_arrive_peer(empty_leader + 8u * pb);
+                    for (int h = 0; h < Cfg::kUnits; ++h) {
+                        const uint32_t pb = turn * Cfg::kUnits + h;
+                        if (h < count) {
+                            if (h == 0 || !early) ok &= bsfp8_wait(p_full_at + 8 * pb, phase, abort_at, prm);
+                            tc_fence_after();
+#pragma unroll
+                            for (int i = 0; i < kChunks; ++i) {
+                                uint32_t v[W];
+                                load(tpart + pb * Cfg::UN, i, v);
+                                if (h + 1 < count) early = bsfp8_there(p_full_at + 8 * (pb + 1), phase);
+                                tmem_ld_wait_regs(v);
+                                if (i + 1 == kChunks) {
+                                    tc_fence_before();
+                                    if (lane == 0) mbar_arrive_peer(empty_leader + 8 * pb);
+                                }
+                                add(sc, h, i, v);
+                                if (h + 1 < count) early = __all_sync(0xffffffffu, early);
+                            }
+                        } else if (lane == 0) {
+                            mbar_arrive_peer(empty_leader + 8 * pb);  // (not used)
+                        }
                     }
                 };
-                const float *sc = reinterpret_cast<const float *>(scales + sr.slot * Cfg::kScaleStage);
-                if (!lanes) {
-                    // 32 columns of fragments at a time, the next ones in flight
-                    constexpr int kChunk = PC < 32 ? 16 : 32, kChunks = PC / kChunk;
-                    const int chunks = (cols + kChunk - 1) / kChunk;
-                    const float4 *s4 = reinterpret_cast<const float4 *>(sc + (b & 3) * BN + part * PC) + q4;
-                    uint32_t v[2][kChunk];
-                    const auto load = [&](int i, uint32_t(&to)[kChunk]) {
-                        if constexpr (kChunk == 32) {
-                            tmem_ld_16x256b_x4(tacc + 32 * i, to);
-                            tmem_ld_16x256b_x4(tacc + (16u << 16) + 32 * i, to + 16);
-                        } else {
-                            tmem_ld_16x256b_x2(tacc + 16 * i, to);
-                            tmem_ld_16x256b_x2(tacc + (16u << 16) + 16 * i, to + 8);
-                        }
-                    };
-                    if (chunks > 0) {
-                        load(0, v[0]);
-                        tmem_ld_wait_regs(v[0]);
-                    } else {
-                        release();
+#pragma unroll 1
+                for (int b = b0; b < b1; b += 4) {
+                    ok &= bsfp8_wait(s_full_at + 8 * sr.slot, sr.phase, abort_at, prm);
+                    const float *slot = reinterpret_cast<const float *>(scales + sr.slot * Cfg::kScaleStage);
+                    const int some = min(4, b1 - b);
+#pragma unroll 1
+                    for (int j = 0; j < some; j += 2) {
+                        block(slot, j);
+                        if (j + 1 < some) block(slot, j + 1);
                     }
-#pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        if (i < chunks) {
-                            if (i + 1 < chunks) load(i + 1, v[(i + 1) & 1]);
-                            else release();
-                            // register of (16 columns c, lanes h of 16, octet o of these, column octet j,
-                            // b): 8 c + 4 j + 2 o + b of lanes h
-#pragma unroll
-                            for (int c = 0; c < kChunk / 16; ++c) {
-                                const float4 s = s4[(i * (kChunk / 16) + c) * 4];
-                                unsigned long long *to = tot + 8 * (i * (kChunk / 16) + c);
-                                const uint32_t(&w)[kChunk] = v[i & 1];
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                    for (int o = 0; o < 2; ++o) {
-                                        const int at = h * (kChunk / 2) + 8 * c + 2 * o;
-                                        bsfp8_fma2(to[4 * h + o], w[at], w[at + 1], s.x, s.y);
-                                        bsfp8_fma2(to[4 * h + 2 + o], w[at + 4], w[at + 5], s.z, s.w);
-                                    }
-                            }
-                            if (i + 1 < chunks) tmem_ld_wait_regs(v[(i + 1) & 1]);
-                        }
-                    }
-                } else if constexpr (PAIR) {
-                    // a lane an activation row, the part's 128 columns one block of weight rows
-                    const float s = sc[(rank * 128 + quad * 32 + lane) * 4 + (b & 3)] * sc[(BN + part) * 4 + (b & 3)];
-                    uint32_t v[2][32];
-                    tmem_ld_32x32b_x32(tacc, v[0]);
-                    tmem_ld_wait_regs(v[0]);
-#pragma unroll
-                    for (int i = 0; i < PC / 32; ++i) {
-                        if (i + 1 < PC / 32) tmem_ld_32x32b_x32(tacc + 32 * (i + 1), v[(i + 1) & 1]);
-                        else release();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            bsfp8_fma2(tot[16 * i + j], v[i & 1][2 * j], v[i & 1][2 * j + 1], s, s);
-                        if (i + 1 < PC / 32) tmem_ld_wait_regs(v[(i + 1) & 1]);
-                    }
-                }
-                if ((b & 3) == 3 || b == b1 - 1) {
-                    fence_proxy_async_smem();  // read before the next copies overwrite them
-                    __syncwarp();
+                    __syncwarp();  // (read; what the scale warp wrote there it orders before its copies itself)
                     if (lane == 0) mbar_arrive(&s_empty[sr.slot]);
                     sr.next();
                 }
+            };
+            if constexpr (PAIR) if (lanes) {
+                // a lane an activation row, the part's columns one block of weight rows
+                F2 tot[PC / 2];
+#pragma unroll
+                for (int i = 0; i < PC / 2; ++i) tot[i] = make_float2(0.0f, 0.0f);
+                const auto load = [&](uint32_t at, int i, uint32_t(&to)[64]) { tmem_ld_32x32b_x64(at, to); };
+                const auto begin = [&](const float *sc, int kb) {
+                    const float s = sc[(rank * 128 + quad * 32 + lane) * 4 + kb] * sc[(BN + part) * 4 + kb];
+                    return bsfp8_f2(s, s);
+                };
+                const auto add = [&](F2 ss, int h, int i, const uint32_t(&w)[64]) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) bsfp8_fma2(tot[h * (CU / 2) + j], w[2 * j], w[2 * j + 1], ss);
+                };
+                blocks(std::true_type(), load, begin, add);
+                if (!ok) break;
+                // a lane's row of 128 columns (rows of C start on 16 bytes)
+                const int nb = x.p0 - 128 * pr + part * 128;
+                const int64_t m = static_cast<int64_t>(x.q0) + rank * 128 + quad * 32 + lane;
+                if (prm.c_type == kOutF32) {
+                    float *to = static_cast<float *>(prm.C) + m * prm.N + nb;
+#pragma unroll
+                    for (int j = 0; j < PC / 4; ++j)
+                        if (nb + 4 * j < prm.N)
+                            *reinterpret_cast<uint4 *>(to + 4 * j) =
+                                make_uint4(bsfp8_lo(tot[2 * j]), bsfp8_hi(tot[2 * j]), bsfp8_lo(tot[2 * j + 1]),
+                                           bsfp8_hi(tot[2 * j + 1]));
+                } else {
+                    uint16_t *to = static_cast<uint16_t *>(prm.C) + m * prm.N + nb;
+                    const bool bf16 = prm.c_type == kOutBf16;
+#pragma unroll
+                    for (int j = 0; j < PC / 8; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float lo = __uint_as_float(bsfp8_lo(tot[4 * j + i]));
+                            const float hi = __uint_as_float(bsfp8_hi(tot[4 * j + i]));
+                            if (bf16) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                            } else {
+                                const __half2 h = __floats2half2_rn(lo, hi);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                        }
+                        if (nb + 8 * j < prm.N)
+                            *reinterpret_cast<uint4 *>(to + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                continue;
             }
+            // 16 columns of fragments at a time.  Pairs of totals: 16 columns (8 i), lanes
+            // 0-15 and 16-31 (4 e), column octet (2 j), row octet (o).
+            F2 tot[PC / 2];
+#pragma unroll
+            for (int i = 0; i < PC / 2; ++i) tot[i] = make_float2(0.0f, 0.0f);
+            constexpr int W = CU;
+            const auto load = [&](uint32_t at, int i, uint32_t(&to)[W]) {
+#pragma unroll
+                for (int c = 0; c < W / 16; ++c) {
+                    tmem_ld_16x256b_x2(at + 16 * c, to + 16 * c);
+                    tmem_ld_16x256b_x2(at + (16u << 16) + 16 * c, to + 16 * c + 8);
+                }
+            };
+            const auto begin = [&](const float *sc, int kb) { return sc + kb * BN + c0 + 4 * q4; };
+            const auto add = [&](const float *sc, int h, int i, const uint32_t(&v)[W]) {
+#pragma unroll
+                for (int c = 0; c < W / 16; ++c) {
+                    const float4 s = *reinterpret_cast<const float4 *>(sc + h * cu + W * i + 16 * c);
+                    const F2 s01 = bsfp8_f2(s.x, s.y), s23 = bsfp8_f2(s.z, s.w);
+                    F2 *to = tot + h * (CU / 2) + W / 2 * i + 8 * c;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            const int at = e * 8 + 16 * c + 2 * o;
+                            bsfp8_fma2(to[4 * e + o], v[at], v[at + 1], s01);
+                            bsfp8_fma2(to[4 * e + 2 + o], v[at + 4], v[at + 5], s23);
+                        }
+                }
+            };
+            blocks(std::false_type(), load, begin, add);
             if (!ok) break;
             const int n0 = x.p0 + quad * 32;
             if (cs > 1) {
@@ -573,7 +681,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
                     for (int o = 0; o < 4; ++o) {
                         const int owner = o / per;
-                        const unsigned long long *from = tot + 8 * c + 4 * (o >> 1) + (o & 1);
+                        const F2 *from = tot + 8 * c + 4 * (o >> 1) + (o & 1);
                         const uint32_t v[4] = {bsfp8_lo(from[0]), bsfp8_hi(from[0]), bsfp8_lo(from[2]), bsfp8_hi(from[2])};
                         if (owner != rank) {
                             const uint4 *to = buf + ((rank * EW + warp) * units + c * per + o % per) * 32;
@@ -588,7 +696,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
                     for (int o = 0; o < 4; ++o) {
                         if (o / per != rank) continue;
-                        const unsigned long long *own = tot + 8 * c + 4 * (o >> 1) + (o & 1);
+                        const F2 *own = tot + 8 * c + 4 * (o >> 1) + (o & 1);
                         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                         for (int r = 0; r < cs; ++r) {
                             const uint4 v = r == rank ? make_uint4(bsfp8_lo(own[0]), bsfp8_hi(own[0]), bsfp8_lo(own[2]),
@@ -603,7 +711,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         for (int j = 0; j < 4; ++j) {
                             const int col = 16 * c + 8 * (j >> 1) + 2 * q4 + (j & 1);
                             if (col < cols)
-                                fp4_store1(prm, s[j], static_cast<int64_t>(x.q0) + part * PC + col,
+                                fp4_store1(prm, s[j], static_cast<int64_t>(x.q0) + c0 + col,
                                            n0 + 8 * o + (lane >> 2));
                         }
                     }
@@ -619,60 +727,29 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 }
                 continue;
             }
-            if (PAIR && lanes) {
-                // a lane's row of 128 columns (rows of C start on 16 bytes)
-                const int c0 = x.p0 - 128 * pr + part * PC;
-                const int64_t m = static_cast<int64_t>(x.q0) + rank * 128 + quad * 32 + lane;
-                if (prm.c_type == kOutF32) {
-                    float *to = static_cast<float *>(prm.C) + m * prm.N + c0;
-#pragma unroll
-                    for (int j = 0; j < PC / 4; ++j)
-                        if (c0 + 4 * j < prm.N)
-                            *reinterpret_cast<uint4 *>(to + 4 * j) =
-                                make_uint4(bsfp8_lo(tot[2 * j]), bsfp8_hi(tot[2 * j]), bsfp8_lo(tot[2 * j + 1]),
-                                           bsfp8_hi(tot[2 * j + 1]));
-                } else {
-                    uint16_t *to = static_cast<uint16_t *>(prm.C) + m * prm.N + c0;
-                    const bool bf16 = prm.c_type == kOutBf16;
-#pragma unroll
-                    for (int j = 0; j < PC / 8; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float lo = __uint_as_float(bsfp8_lo(tot[4 * j + i]));
-                            const float hi = __uint_as_float(bsfp8_hi(tot[4 * j + i]));
-                            if (bf16) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                            } else {
-                                const __half2 h = __floats2half2_rn(lo, hi);
-                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                            }
-                        }
-                        if (c0 + 8 * j < prm.N)
-                            *reinterpret_cast<uint4 *>(to + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-            } else if (prm.c_type == kOutF32) {
+            if (prm.c_type == kOutF32) {
                 // (a store: eight columns of C of each of four rows)
-                float *to = static_cast<float *>(prm.C) + (static_cast<int64_t>(x.q0) + part * PC + 2 * q4) * prm.N + n0 +
+                float *to = static_cast<float *>(prm.C) + (static_cast<int64_t>(x.q0) + c0 + 2 * q4) * prm.N + n0 +
                             (lane >> 2);
 #pragma unroll
-                for (int c = 0; c < PC / 8; ++c)
+                for (int c = 0; c < PC / 8; ++c) {
+                    const int in = 8 * (c % (CU / 8)), col = c / (CU / 8) * cu + in;  // in its accumulator, in the tile
+                    if (in >= cu) continue;
 #pragma unroll
                     for (int o = 0; o < 4; ++o) {
-                        const unsigned long long v = tot[8 * (c >> 1) + 4 * (o >> 1) + 2 * (c & 1) + (o & 1)];
-                        const int col = 8 * c + 2 * q4;
+                        const F2 v = tot[8 * (c >> 1) + 4 * (o >> 1) + 2 * (c & 1) + (o & 1)];
                         if (n0 + 8 * o + (lane >> 2) < prm.N) {
-                            float *at = to + static_cast<int64_t>(8 * c) * prm.N + 8 * o;
-                            if (col < cols) at[0] = __uint_as_float(bsfp8_lo(v));
-                            if (col + 1 < cols) at[prm.N] = __uint_as_float(bsfp8_hi(v));
+                            float *at = to + static_cast<int64_t>(col) * prm.N + 8 * o;
+                            if (col + 2 * q4 < cols) at[0] = __uint_as_float(bsfp8_lo(v));
+                            if (col + 2 * q4 + 1 < cols) at[prm.N] = __uint_as_float(bsfp8_hi(v));
                         }
                     }
+                }
             } else {
 #pragma unroll
                 for (int c = 0; c < PC; c += 32) {
-                    if (c < cols) {
+                    const int in = c % CU, col = c / CU * cu + in;
+                    if (in < cu && col < cols) {
                         uint32_t v[2][16];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -681,12 +758,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                                 // (fragments: lanes 0-15 and 16-31, column octet, row octet)
                                 const int from = c / 2 + 8 * i + j;
                                 const bool there = c + 16 * i < PC;
-                                const unsigned long long w = there ? tot[there ? from : 0] : 0ull;
+                                const F2 w = there ? tot[there ? from : 0] : make_float2(0.0f, 0.0f);
                                 v[i][2 * j] = bsfp8_lo(w);
                                 v[i][2 * j + 1] = bsfp8_hi(w);
                             }
-                        fp4_store32_cols<false>(prm, v, 1.0f, static_cast<int64_t>(x.q0) + part * PC + c, cols - c, n0,
-                                                stage);
+                        fp4_store32_cols<false>(prm, v, 1.0f, static_cast<int64_t>(x.q0) + c0 + col,
+                                                min(cu - in, cols - col), n0, stage);
                     }
                 }
             }

@@ -114,10 +114,10 @@ def test_kernels_set_up_early_make_no_read_only_loads(name):
 
 
 def test_hand_overs_between_the_ctas_of_a_product():
-    # mbar_arrive_peer does not release at cluster scope: it may only hand over tensor memory that was read
+    # what threads wrote or read goes to another CTA with a release at cluster scope, never by mbar_arrive_peer
     code = code_of("gemm_bsfp8_kernel.cuh")
     targets = re.findall(r"mbar_arrive_peer\(([^;]*)\);", code)
-    assert targets and all(t.startswith("empty_leader") for t in targets), targets
+    assert targets and all(t.startswith("empty_leader") for t in targets), targets  # (tensor memory that was read)
     assert re.search(r"bulk_copy_to_cta\([^;]*smem_u32\(&red_empty", code)
     waits = re.findall(r"(\w+)\(&red_(?:empty|full)\[warp\], ph", code)
     assert len(waits) == 2 and set(waits) == {"fp4_warp_wait_cluster"}
