@@ -277,7 +277,8 @@ IGEMM_API int pack_int4(const int8_t *logical, uint8_t *packed, int64_t rows, in
  * launches one kernel, or two: the preparation pass and the GEMM (prepared
  * codes), the zeroing of C and the GEMM (skinny shapes whose K slices are
  * summed with atomics), the scale transpose and the GEMM (block-scaled fp8);
- * a 4-bit operator one, but igemm_moe_route two or three above 512 tokens (three
+ * a 4-bit or block-scaled fp8 operator with 128 x 128 scales one, but igemm_moe_route (and
+ * igemm_moe_route_scored) two or three above 512 tokens (three
  * where the counts that its blocks would all read pass 4 MB: with
  * b = ceil(T / 64) blocks, 4 b b ceil(E / 4) bytes), and pack_mxfp4 or pack_nvfp4
  * two where rows are packed once and copied (as stated there).
@@ -462,6 +463,46 @@ IGEMM_API int igemm_nvfp4_grouped(const uint8_t *A, const uint8_t *B, const uint
 IGEMM_API int igemm_moe_route(const void *logits, int logits_type, int32_t *experts, float *weights,
                               int32_t *offsets, int32_t *tokens, int32_t *slots, int T, int E, int k, int normalize,
                               cudaStream_t stream);
+
+/*
+ * Routing by scores: s = softmax(logits) or sigmoid(logits) over the E experts of a token,
+ * c = s + bias; the experts form `groups` equal runs, a group's score is the sum of its
+ * group_top (1 or 2) largest c (of one where only one can be chosen); chosen are the k
+ * largest c among the group_k groups of the highest scores.
+ *   logits   [T, E] of logits_type (device); -inf and NaN are never chosen, nor is a c that is
+ *            NaN or -inf; with softmax a row with +inf has no scores and chooses nothing
+ *   bias     [E] float32 (device), or null for 0: for the choice only
+ *   score    an igemm_score
+ *   experts, offsets, tokens, slots   as igemm_moe_route writes them, experts by falling c
+ *   weights  [T, k] float32: scale * s, over the sum of the chosen s with normalize != 0; 0
+ *            where experts is -1
+ * The choice is that of the scores in 64 bits, equal ones the lowest expert (group) first;
+ * without a bias experts are compared by their logits, whose order is that of the scores.
+ * E <= 1024, k <= 32, groups <= 32, E a multiple of groups, 1 <= group_k <= groups, group_top
+ * 1 or 2, k <= group_k E / groups, T * k < 2^31 (IGEMM_UNSUPPORTED_SHAPE).  T == 0 or k == 0
+ * zeroes offsets.  Launches and workspace as for igemm_moe_route.
+ */
+typedef enum igemm_score { IGEMM_SOFTMAX = 0, IGEMM_SIGMOID = 1 } igemm_score;
+IGEMM_API int igemm_moe_route_scored(const void *logits, int logits_type, const float *bias, int32_t *experts,
+                                     float *weights, int32_t *offsets, int32_t *tokens, int32_t *slots, int T, int E, int k,
+                                     int score, int groups, int group_k, int group_top, int normalize, float scale,
+                                     cudaStream_t stream);
+
+/*
+ * Its gradient: that of the logits for that of the weights (the choice has none, nor the
+ * bias).  Arguments as for igemm_moe_route_scored.
+ *   logits    [T, E], experts [T, k] (device), read only; experts outside [0, E), and those
+ *             whose logit is -inf or NaN, have no weight; one that a token names twice gets
+ *             the sum
+ *   dweights  [T, k] float32 (device), read only
+ *   dlogits   [T, E] of logits_type (device), written: every element, 0 where the weights do
+ *             not depend on it
+ * float32 arithmetic in a fixed order, rounded once.  E <= 1024, k <= 32, T * k < 2^31
+ * (IGEMM_UNSUPPORTED_SHAPE).  T == 0 or E == 0 is a no-op; k == 0 zeroes dlogits.
+ */
+IGEMM_API int igemm_moe_route_scored_grad(const void *logits, int logits_type, const int32_t *experts,
+                                          const float *dweights, void *dlogits, int T, int E, int k, int score,
+                                          int normalize, float scale, cudaStream_t stream);
 
 /*
  * out[t,:] = sum_j weights[t,j] * Y[slots[t,j],:], float32 sums in the order of j,

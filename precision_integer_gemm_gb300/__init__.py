@@ -28,6 +28,7 @@ __all__ = [
     "igemm_mxfp4_grouped", "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine",
     "fp4_code_bytes", "mxfp4_scale_pitch", "nvfp4_scale_pitch",
     "pack_bsfp8", "igemm_bsfp8", "igemm_bsfp8_grouped", "bsfp8_code_bytes", "bsfp8_scale_pitch",
+    "igemm_moe_route_scored", "igemm_moe_route_scored_grad",
     "EXPORTED_SYMBOLS", "LIB_PATH", "build_library",
 ]
 
@@ -38,7 +39,8 @@ EXPORTED_SYMBOLS = ("i4i4_gemm", "i4i4_gemm_noalloc", "w4a8_gemm", "i4i4_gemm_ho
                     "igemm_time_next_gemm", "igemm_skinny_plan", "igemm_ss_plan", "igemm_route",
                     "pack_mxfp4", "pack_nvfp4", "igemm_mxfp4", "igemm_nvfp4", "igemm_mxfp4_grouped",
                     "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine",
-                    "pack_bsfp8", "igemm_bsfp8", "igemm_bsfp8_grouped")
+                    "pack_bsfp8", "igemm_bsfp8", "igemm_bsfp8_grouped", "igemm_moe_route_scored",
+                    "igemm_moe_route_scored_grad")
 
 IGEMM_OK = 0
 IGEMM_INVALID_ARGUMENT = 1
@@ -122,9 +124,12 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.pack_bsfp8.argtypes = [p, i, i64, i, p, i, i, i, p, p, i, i, p]
     lib.igemm_bsfp8.argtypes = [p, p, p, p, p, i, i, i, i, i, p]
     lib.igemm_bsfp8_grouped.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, p]
+    f = ctypes.c_float
+    lib.igemm_moe_route_scored.argtypes = [p, i, p, p, p, p, p, p, i, i, i, i, i, i, i, i, f, p]
+    lib.igemm_moe_route_scored_grad.argtypes = [p, i, p, p, p, i, i, i, i, i, f, p]
     for name in ("pack_mxfp4", "pack_nvfp4", "igemm_mxfp4", "igemm_nvfp4", "igemm_mxfp4_grouped",
                  "igemm_nvfp4_grouped", "igemm_moe_route", "igemm_moe_combine", "pack_bsfp8", "igemm_bsfp8",
-                 "igemm_bsfp8_grouped"):
+                 "igemm_bsfp8_grouped", "igemm_moe_route_scored", "igemm_moe_route_scored_grad"):
         getattr(lib, name).restype = i
     lib.igemm_watchdog_selftest.argtypes = [ctypes.c_uint32, p]
     lib.igemm_watchdog_selftest.restype = i
@@ -458,6 +463,48 @@ def igemm_moe_route(logits, experts, weights, offsets, tokens, slots, T: int, E:
         _typed(weights, "torch.float32", pairs, w, "weights"),
         _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"), _typed(tokens, "torch.int32", pairs, w, "tokens"),
         _typed(slots, "torch.int32", pairs, w, "slots"), T, E, k, 1 if normalize else 0, _stream(stream)), w)
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score: str, where: str) -> int:
+    s = SCORES.get(score)
+    if s is None:
+        raise ValueError(f"{where}: score must be 'softmax' or 'sigmoid', not {score!r}")
+    return s
+
+
+def igemm_moe_route_scored(logits, bias, experts, weights, offsets, tokens, slots, T: int, E: int, k: int,
+                           score: str = "softmax", groups: int = 1, group_k: int = 1, group_top: int = 1,
+                           normalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """igemm_moe_route by scores: softmax or sigmoid of logits [T,E] plus bias (float32 [E], None: 0; for the choice
+    only), the group_k best of `groups` equal runs of experts (by the sum of their group_top largest), the k best
+    experts in them; weights = scale * score, over the sum of the chosen scores (normalize)."""
+    w = "igemm_moe_route_scored"
+    t, size = _type(logits, w)
+    pairs = _n(T, k)
+    _check(load().igemm_moe_route_scored(
+        _dev(logits, size * _n(T, E), w, "logits"), t, _typed(bias, "torch.float32", _n(E), w, "bias"),
+        _typed(experts, "torch.int32", pairs, w, "experts"), _typed(weights, "torch.float32", pairs, w, "weights"),
+        _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"), _typed(tokens, "torch.int32", pairs, w, "tokens"),
+        _typed(slots, "torch.int32", pairs, w, "slots"), T, E, k, _score(score, w), groups, group_k, group_top,
+        1 if normalize else 0, scale, _stream(stream)), w)
+
+
+def igemm_moe_route_scored_grad(logits, experts, dweights, dlogits, T: int, E: int, k: int, score: str = "softmax",
+                                normalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """dlogits [T,E] (of logits' type) = gradient of the logits for dweights [T,k] (float32), that of the weights which
+    igemm_moe_route_scored gave the choices experts [T,k] with the same score, normalize and scale."""
+    w = "igemm_moe_route_scored_grad"
+    t, size = _type(logits, w)
+    if dlogits.dtype != logits.dtype:
+        raise ValueError(f"{w}: dlogits must have logits' type")
+    pairs = _n(T, k)
+    _check(load().igemm_moe_route_scored_grad(
+        _dev(logits, size * _n(T, E), w, "logits"), t, _typed(experts, "torch.int32", pairs, w, "experts"),
+        _typed(dweights, "torch.float32", pairs, w, "dweights"), _dev(dlogits, size * _n(T, E), w, "dlogits"), T, E, k,
+        _score(score, w), 1 if normalize else 0, scale, _stream(stream)), w)
 
 
 def igemm_moe_combine(Y, slots, weights, out, T: int, k: int, N: int, stream=None) -> None:

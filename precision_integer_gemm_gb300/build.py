@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libigemm.so")
 SOURCES = ["api.cu", "prep.cu", "gemm_i4i4.cu", "gemm_small.cu", "gemm_w4a8.cu", "gemm_fp8.cu", "gemm_bs.cu", "host.cu",
            "api_fp4.cu", "fp4_plan.cu", "pack_fp4.cu", "gemm_fp4_mx.cu", "gemm_fp4_nv.cu", "moe.cu",
-           "api_bsfp8.cu", "bsfp8_plan.cu", "pack_bsfp8.cu", "gemm_bsfp8.cu"]
+           "api_bsfp8.cu", "bsfp8_plan.cu", "pack_bsfp8.cu", "gemm_bsfp8.cu", "moe_scored.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -109,6 +109,51 @@ extern "C" int igemm_moe_route(const void *logits, int logits_type, int32_t *exp
                             stream);
 }
 
+static bool known_score(int score) { return score == IGEMM_SOFTMAX || score == IGEMM_SIGMOID; }
+
+extern "C" int igemm_moe_route_scored(const void *logits, int logits_type, const float *bias, int32_t *experts,
+                                      float *weights, int32_t *offsets, int32_t *tokens, int32_t *slots, int T, int E,
+                                      int k, int score, int groups, int group_k, int group_top, int normalize,
+                                      float scale, cudaStream_t stream)
+{
+    if (T < 0 || E < 0 || k < 0 || !known_type(logits_type) || !known_score(score)) return kInvalidArgument;
+    if (!offsets) return kInvalidArgument;
+    if (!aligned(offsets, 4)) return kMisaligned;
+    if (E > kFp4MaxExperts || k > 32 || k > E || int64_t(T) * k > 0x7FFFFFFF) return kUnsupportedShape;
+    if (groups < 1 || groups > 32 || E % groups != 0 || group_k < 1 || group_k > groups || group_top < 1 ||
+        group_top > 2 || k > group_k * (E / groups))
+        return kUnsupportedShape;
+    if (T == 0 || k == 0)
+        return cudaMemsetAsync(offsets, 0, size_t(E + 1) * 4, stream) == cudaSuccess ? kOk : kCudaError;
+    if (!logits || !experts || !weights || !tokens || !slots) return kInvalidArgument;
+    if (!aligned(logits, type_bytes(logits_type)) || !aligned(bias, 4) || !aligned(experts, 4) ||
+        !aligned(weights, 4) || !aligned(tokens, 4) || !aligned(slots, 4))
+        return kMisaligned;
+    return launch_moe_route_scored(
+        {{logits, logits_type, experts, weights, offsets, tokens, slots, T, E, k, normalize != 0},
+         bias, score, groups, group_k, group_top, scale},
+        stream);
+}
+
+extern "C" int igemm_moe_route_scored_grad(const void *logits, int logits_type, const int32_t *experts,
+                                           const float *dweights, void *dlogits, int T, int E, int k, int score,
+                                           int normalize, float scale, cudaStream_t stream)
+{
+    if (T < 0 || E < 0 || k < 0 || !known_type(logits_type) || !known_score(score)) return kInvalidArgument;
+    if (T == 0 || E == 0) return kOk;
+    if (!dlogits) return kInvalidArgument;
+    if (E > kFp4MaxExperts || k > 32 || int64_t(T) * k > 0x7FFFFFFF) return kUnsupportedShape;
+    if (!aligned(dlogits, type_bytes(logits_type))) return kMisaligned;
+    if (k == 0)
+        return cudaMemsetAsync(dlogits, 0, size_t(T) * size_t(E) * type_bytes(logits_type), stream) == cudaSuccess
+                   ? kOk
+                   : kCudaError;
+    if (!logits || !experts || !dweights) return kInvalidArgument;
+    if (!aligned(logits, type_bytes(logits_type)) || !aligned(experts, 4) || !aligned(dweights, 4)) return kMisaligned;
+    return launch_moe_route_scored_grad(
+        {logits, logits_type, experts, dweights, dlogits, T, E, k, score, normalize != 0, scale}, stream);
+}
+
 extern "C" int igemm_moe_combine(const void *Y, const int32_t *slots, const float *weights, void *out, int type, int T,
                                  int k, int N, cudaStream_t stream)
 {

@@ -18,6 +18,29 @@ struct MoeRouteCall {
 };
 int launch_moe_route(const MoeRouteCall &c, cudaStream_t stream);
 
+// Routing by scores: softmax or sigmoid, a bias for the choice, groups of experts.
+struct MoeScoredCall {
+    MoeRouteCall route;
+    const float *bias;  // [E] or null
+    int score;          // 0 softmax, 1 sigmoid
+    int groups, group_k, group_top;
+    float scale;
+};
+int launch_moe_route_scored(const MoeScoredCall &c, cudaStream_t stream);
+
+// Gradient of the logits [T, E] for that of the weights.
+struct MoeScoredGradCall {
+    const void *logits;
+    int x_type;
+    const int *experts;     // [T, k]
+    const float *dweights;  // [T, k]
+    void *dlogits;          // [T, E] of type x_type
+    int T, E, k, score;
+    bool normalize;
+    float scale;
+};
+int launch_moe_route_scored_grad(const MoeScoredGradCall &c, cudaStream_t stream);
+
 struct MoeCombineCall {
     const void *Y;  // [T * k, N] of type x_type
     int x_type;

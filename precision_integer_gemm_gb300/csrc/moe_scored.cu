@@ -1,0 +1,564 @@
+// Routing by scores and its gradient.
+//
+//   s = softmax(x) or 1 / (1 + e^-x) over the E experts of a token, c = s + bias; a group's
+//   score is the sum of its one or two largest c; the choice is the k largest c among the
+//   experts of the best groups, the weight scale * s, over the sum of the chosen s where
+//   they are renormalised.
+//
+// The choice is that of the definition in 64 bits, ties to the lowest expert: a token's c
+// are computed in 32 bits, and where two that decide (neighbours among the chosen, the
+// last of them and the best one left, the last group taken and the best one left) are
+// nearer than the rounding could be, the token is done again in 64 bits (some tokens in a
+// thousand, 2 us each on a warp).  Without a bias the scores are in the order of the
+// logits, which are compared as they are.
+//
+// A warp per token, a lane E / 32 neighbouring experts, so that a group is a run of lanes
+// and the first lane with the largest value holds the lowest expert.  From the choices to
+// the sorted pairs everything is as without scores (moe_route.cuh).
+#include <algorithm>
+#include <math_constants.h>
+#include "launch.cuh"
+#include "moe.cuh"
+#include "moe_route.cuh"
+#include "overlap.cuh"
+#include "ptx.cuh"
+
+namespace igemm {
+
+constexpr int kScoredThreads = 512;
+
+struct ScoredParams {
+    RouteParams r;
+    const float *bias;
+    int sigmoid;
+    int groups, per, group_k, two;  // per: experts of a group; two: its two largest count
+    float scale;
+};
+
+__device__ __forceinline__ float scored_sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+
+// The logit as it counts: NaN is -inf.
+template <class T>
+__device__ __forceinline__ float scored_logit(const T *row, int e)
+{
+    const float v = moe_float(row[e]);
+    return v != v ? -CUDART_INF_F : v;
+}
+
+// a1 >= a2: the two largest so far; v another.
+template <class F>
+__device__ __forceinline__ void scored_two(F &a1, F &a2, F v)
+{
+    a2 = v > a1 ? a1 : v > a2 ? v : a2;
+    a1 = v > a1 ? v : a1;
+}
+
+// The sum of a group's largest, or of its two largest where there are two.
+template <class F>
+__device__ __forceinline__ F scored_group(F a1, F a2, bool two)
+{
+    return two && a2 > F(-CUDART_INF_F) ? a1 + a2 : a1;
+}
+
+// Bit g: group g is taken; lane g holds its score (-inf: nothing to choose).
+template <class F>
+__device__ __forceinline__ uint32_t scored_groups(F score, int groups, int group_k)
+{
+    const int lane = threadIdx.x & 31;
+    int rank = 0;
+    for (int g = 0; g < groups; ++g) {
+        const F other = __shfl_sync(0xffffffffu, score, g);
+        rank += other > score || (other == score && g < lane) ? 1 : 0;
+    }
+    return __ballot_sync(0xffffffffu, lane < groups && rank < group_k && score > F(-CUDART_INF_F));
+}
+
+// The choice in 64 bits: lane c's expert, -1 where none is left.
+template <class T, int VPL>
+__device__ __noinline__ int scored_choose_64(const ScoredParams &p, const T *row)
+{
+    const int lane = threadIdx.x & 31, e0 = lane * VPL;
+    const double none = -CUDART_INF;
+    double c[VPL], s[VPL];
+    double sum = 0.0;
+    float m = -CUDART_INF_F;
+    for (int j = 0; j < VPL; ++j) {
+        const float x = e0 + j < p.r.E ? scored_logit(row, e0 + j) : -CUDART_INF_F;
+        c[j] = x;
+        m = fmaxf(m, x);
+    }
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int j = 0; j < VPL; ++j) {
+        s[j] = c[j] == none ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-c[j])) : exp(c[j] - static_cast<double>(m));
+        sum += s[j];
+    }
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    for (int j = 0; j < VPL; ++j) {
+        if (!p.sigmoid) s[j] /= sum;
+        if (p.bias && c[j] > none) {
+            const double v = s[j] + static_cast<double>(p.bias[e0 + j]);
+            c[j] = v > none ? v : none;  // (not NaN)
+            s[j] = c[j];
+        }
+    }
+    if (p.groups > 1) {
+        double score = none;
+        for (int g = 0; g < p.groups; ++g) {
+            double a1 = none, a2 = none;
+            for (int j = 0; j < VPL; ++j)
+                if (c[j] > none && (e0 + j) / p.per == g) scored_two(a1, a2, p.two && !p.bias ? s[j] : c[j]);
+            for (int d = 16; d; d >>= 1) {
+                const double b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
+                scored_two(a1, a2, b1);
+                scored_two(a1, a2, b2);
+            }
+            if (lane == g) score = a1 > none ? scored_group(a1, a2, p.two) : none;
+        }
+        const uint32_t taken = scored_groups(score, p.groups, p.group_k);
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j < p.r.E && !(taken >> ((e0 + j) / p.per) & 1u)) c[j] = none;
+    }
+    int mine = -1;
+    for (int i = 0; i < p.r.k; ++i) {
+        double best = none;
+        int e = 0x7FFFFFFF;
+        for (int j = 0; j < VPL; ++j)
+            if (c[j] > best) {
+                best = c[j];
+                e = e0 + j;
+            }
+        for (int d = 16; d; d >>= 1) {
+            const double b = __shfl_xor_sync(0xffffffffu, best, d);
+            const int f = __shfl_xor_sync(0xffffffffu, e, d);
+            if (b > best || (b == best && f < e)) {
+                best = b;
+                e = f;
+            }
+        }
+        if (!(best > none)) break;
+        if (lane == i) mine = e;
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j == e) c[j] = none;
+    }
+    return mine;
+}
+
+// Choice and weights of a block's tokens; their masks; one cluster: everything.
+// VPL: experts per lane (E <= 32 VPL); VEC: a lane's logits in runs of V (16 bytes at most),
+// loaded together.
+template <class T, int VPL, bool VEC>
+__global__ void __launch_bounds__(kScoredThreads) moe_choose_scored_kernel(const ScoredParams sp)
+{
+    constexpr int V = !VEC ? 1 : VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
+    struct alignas(V * sizeof(T)) Run {
+        T v[V];
+    };
+    constexpr float kNone = -__builtin_huge_valf();
+    const RouteParams &p = sp.r;
+    extern __shared__ uint2 mask[];  // [E], then (one cluster) first[E + 1], start[E], experts[kTB * k]
+    overlap_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * VPL;
+    const bool one_cluster = !p.counts && !p.packed_counts;
+    int *first = reinterpret_cast<int *>(mask + p.E);
+    int *start = first + p.E + 1;
+    int *chosen = start + p.E;
+    for (int e = threadIdx.x; e < p.E; e += kScoredThreads) mask[e] = make_uint2(0, 0);
+    float bias[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) bias[j] = sp.bias && e0 + j < p.E ? sp.bias[e0 + j] : 0.0f;
+    __syncthreads();
+    const int t0 = blockIdx.x * p.tb;
+    const int mine = min(p.tb, p.T - t0);  // (t0 + tb may pass 2^31)
+    const bool grouped = sp.groups > 1;
+    // groups of whole lanes, a power of two of them
+    const int lanes = sp.per / VPL;
+    const bool runs = sp.per % VPL == 0 && (lanes & (lanes - 1)) == 0;
+    const bool scores = sp.bias || (grouped && sp.two);  // every expert's is needed
+    for (int i = warp; i < mine; i += kScoredThreads / 32) {
+        const int64_t t = t0 + i;
+        const T *row = static_cast<const T *>(p.logits) + t * p.E;
+        float c[VPL], s[VPL];
+        float m = kNone;
+#pragma unroll
+        for (int j = 0; j < VPL; j += V) {
+            Run run;
+            const bool there = e0 + j < p.E;  // (VEC: E is a multiple of V)
+            if (there) run = *reinterpret_cast<const Run *>(row + e0 + j);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float v = there ? moe_float(run.v[q]) : kNone;
+                c[j + q] = v != v ? kNone : v + 0.0f;
+                m = fmaxf(m, c[j + q]);
+            }
+        }
+        // softmax: the largest logit and the sum over all experts; a row with +inf has no scores
+        float sum = 1.0f;
+        if (!sp.sigmoid) {
+            m = route_value(__reduce_max_sync(0xffffffffu, route_key(m)));
+            if (!(m < CUDART_INF_F)) {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) c[j] = kNone;
+            }
+            if (scores || !p.normalize) {
+                sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    s[j] = c[j] > kNone ? expf(c[j] - m) : 0.0f;
+                    sum += s[j];
+                }
+#pragma unroll
+                for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            }
+        }
+        // error of one c below: at sigmoids 2^-21 (1 + |c|), at softmax 2^-17 of the largest score
+        // (their sum takes VPL + 5 roundings) and the sum's rounding
+        float slack = 0x1p-20f;
+        if (scores) {
+            const float inv = __fdiv_rn(1.0f, sum);
+            if (!sp.sigmoid) slack = 0x1p-16f * inv;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                s[j] = !(c[j] > kNone) ? 0.0f : sp.sigmoid ? scored_sigmoid(c[j]) : s[j] * inv;
+                if (sp.bias && c[j] > kNone) {
+                    const float v = s[j] + bias[j];
+                    c[j] = v > kNone ? v : kNone;  // (not NaN)
+                }
+            }
+        }
+        bool near = false;
+        if (grouped) {
+            float score = kNone;  // of group `lane`
+            if (runs) {
+                float a1 = kNone, a2 = kNone;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (c[j] > kNone) scored_two(a1, a2, sp.two && !sp.bias ? s[j] : c[j]);
+                for (int d = 1; d < lanes; d <<= 1) {
+                    const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
+                    scored_two(a1, a2, b1);
+                    scored_two(a1, a2, b2);
+                }
+                const float mine_score = scored_group(a1, a2, sp.two);
+                score = __shfl_sync(0xffffffffu, mine_score, (lane * lanes) & 31);
+                if (lane >= sp.groups) score = kNone;
+            } else {
+                for (int g = 0; g < sp.groups; ++g) {
+                    float a1 = kNone, a2 = kNone;
+                    const int from = g * sp.per - e0, to = from + sp.per;
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j)
+                        if (j >= from && j < to && c[j] > kNone) scored_two(a1, a2, sp.two && !sp.bias ? s[j] : c[j]);
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) {
+                        const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
+                        scored_two(a1, a2, b1);
+                        scored_two(a1, a2, b2);
+                    }
+                    if (lane == g) score = scored_group(a1, a2, sp.two);
+                }
+            }
+            const uint32_t taken = scored_groups(score, sp.groups, sp.group_k);
+            if (scores) {
+                // the last group taken and the best one left
+                const bool in = taken >> lane & 1u;
+                const float least = route_value(__reduce_min_sync(0xffffffffu, in ? route_key(score) : 0xFF800000u));
+                const float most = route_value(__reduce_max_sync(0xffffffffu, in ? kKeyNone : route_key(score)));
+                if (most > kNone)
+                    near = !(least - most > 2.0f * (sp.sigmoid ? slack * (1.0f + fabsf(least)) : slack + 0x1p-22f * fabsf(least)));
+            }
+            int g = e0 / sp.per, left = (g + 1) * sp.per - e0;  // experts until the next group
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                if (left == 0) {
+                    ++g;
+                    left = sp.per;
+                }
+                --left;
+                if (g >= 32 || !(taken >> g & 1u)) c[j] = kNone;
+            }
+        }
+        uint32_t key[VPL], local = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            key[j] = route_key(c[j]);
+            local = max(local, key[j]);
+        }
+        // lane n keeps choice n
+        int my_e = -1;
+        uint32_t my_key = kKeyNone, top = __reduce_max_sync(0xffffffffu, local);
+        for (int n = 0; n < p.k; ++n) {
+            if (top <= kKeyNone) break;  // nothing is left
+            const int owner = __ffs(__ballot_sync(0xffffffffu, local == top)) - 1;
+            int at = 0;
+            if (lane == owner) {
+                local = 0;
+                bool found = false;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    const bool it = !found && key[j] == top;
+                    if (it) {
+                        at = j;
+                        key[j] = 0u;
+                    }
+                    found |= it;
+                    local = max(local, key[j]);
+                }
+            }
+            const int e = owner * VPL + __shfl_sync(0xffffffffu, at, owner);
+            if (lane == n) {
+                my_e = e;
+                my_key = top;
+            }
+            top = __reduce_max_sync(0xffffffffu, local);
+        }
+        float x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
+        if (sp.bias) {
+            // neighbours nearer than the rounding, but for those that are equal in both parts
+            const float b = my_e >= 0 ? sp.bias[my_e] : 0.0f, v = route_value(my_key);
+            const auto margin = [&](float of) {
+                return sp.sigmoid ? slack * (1.0f + fabsf(of)) : slack + 0x1p-22f * fabsf(of);
+            };
+            const int e2 = __shfl_down_sync(0xffffffffu, my_e, 1);
+            const float x2 = __shfl_down_sync(0xffffffffu, x, 1), b2 = __shfl_down_sync(0xffffffffu, b, 1);
+            const float v2 = __shfl_down_sync(0xffffffffu, v, 1);
+            const bool pair = my_e >= 0 && lane + 1 < p.k && e2 >= 0;
+            near |= __any_sync(0xffffffffu, pair && !(v - v2 > margin(v)) && !(x == x2 && b == b2));
+            // the last one and those left
+            const float vk = __shfl_sync(0xffffffffu, v, p.k - 1), xk = __shfl_sync(0xffffffffu, x, p.k - 1);
+            const float bk = __shfl_sync(0xffffffffu, b, p.k - 1);
+            if (top > kKeyNone && !(vk - route_value(top) > margin(vk))) {
+                bool other = false;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j)
+                    if (key[j] > kKeyNone && !(vk - route_value(key[j]) > margin(vk)))
+                        other |= !(scored_logit(row, e0 + j) == xk && bias[j] == bk);
+                near |= __any_sync(0xffffffffu, other);
+            }
+        }
+        if (near) {
+            my_e = scored_choose_64<T, VPL>(sp, row);
+            x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
+        }
+        // The weight before the scale.  Renormalised ones need no score that could underflow:
+        // softmax from the largest chosen logit, sigmoids times e^-min(0, that).
+        float w = 0.0f, total = sum;
+        if (p.normalize) {
+            const float most = route_value(__reduce_max_sync(0xffffffffu, route_key(x)));
+            if (my_e >= 0) {
+                if (!sp.sigmoid) w = expf(x - most);
+                else if (x > 0.0f) w = scored_sigmoid(x);
+                else w = __fdiv_rn(expf(x - fminf(most, 0.0f)), 1.0f + expf(x));
+            }
+            total = w;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        } else if (my_e >= 0) {
+            w = sp.sigmoid ? scored_sigmoid(x) : expf(x - m);
+        }
+        if (lane < p.k) {
+            p.experts[t * p.k + lane] = my_e;
+            p.weights[t * p.k + lane] = my_e >= 0 ? sp.scale * __fdiv_rn(w, total) : 0.0f;
+            if (one_cluster) chosen[i * p.k + lane] = my_e;
+            if (my_e >= 0) atomicOr(i < 32 ? &mask[my_e].x : &mask[my_e].y, 1u << (i & 31));
+        }
+    }
+    overlap_release();
+    __syncthreads();
+    if (!one_cluster) {
+        route_counts(p, mask);
+        return;
+    }
+    route_finish<kScoredThreads>(p, mask, first, start, chosen);
+}
+
+template <class T, int VPL>
+static int launch_scored_vpl(const ScoredParams &p, int smem, cudaStream_t stream)
+{
+    constexpr int V = VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
+    const bool vec = p.r.E % V == 0 && reinterpret_cast<uintptr_t>(p.r.logits) % (V * sizeof(T)) == 0;
+    const auto kernel = vec ? moe_choose_scored_kernel<T, VPL, true> : moe_choose_scored_kernel<T, VPL, false>;
+    if (p.r.T > kClusterBlocks * kTB)
+        return launch_overlapped(kernel, dim3(p.r.blocks), dim3(kScoredThreads), smem, stream, p);
+    int cluster = 1;
+    while (cluster < p.r.blocks) cluster *= 2;  // (blocks without tokens fill it up)
+    return launch_overlapped_clusters(kernel, dim3(cluster), cluster, dim3(kScoredThreads), smem, stream, p);
+}
+
+template <class T>
+static int launch_scored(const ScoredParams &p, int smem, cudaStream_t stream)
+{
+    if (p.r.E <= 64) return launch_scored_vpl<T, 2>(p, smem, stream);
+    if (p.r.E <= 128) return launch_scored_vpl<T, 4>(p, smem, stream);
+    if (p.r.E <= 256) return launch_scored_vpl<T, 8>(p, smem, stream);
+    if (p.r.E <= 512) return launch_scored_vpl<T, 16>(p, smem, stream);
+    return launch_scored_vpl<T, 32>(p, smem, stream);
+}
+
+int launch_moe_route_scored(const MoeScoredCall &c, cudaStream_t stream)
+{
+    RouteParams p{};
+    p.logits = c.route.logits;
+    p.experts = c.route.experts;
+    p.weights = c.route.weights;
+    p.offsets = c.route.offsets;
+    p.tokens = c.route.tokens;
+    p.slots = c.route.slots;
+    p.T = c.route.T;
+    p.E = c.route.E;
+    p.k = c.route.k;
+    p.normalize = c.route.normalize ? 1 : 0;
+    return route_launch(p, stream, [&](const RouteParams &q, int smem) {
+        const ScoredParams sp{q, c.bias, c.score == 1, c.groups, q.E / c.groups, c.group_k, c.group_top == 2, c.scale};
+        return c.route.x_type == 0   ? launch_scored<float>(sp, smem, stream)
+               : c.route.x_type == 1 ? launch_scored<__nv_bfloat16>(sp, smem, stream)
+                                     : launch_scored<__half>(sp, smem, stream);
+    });
+}
+
+// ---------------------------------------------------------------- gradient
+__device__ __forceinline__ void scored_out(float *o, float v) { *o = v; }
+__device__ __forceinline__ void scored_out(__nv_bfloat16 *o, float v) { *o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void scored_out(__half *o, float v) { *o = __float2half_rn(v); }
+
+// With u the weights before the scale and g their gradient:
+//   renormalised  dx_i = scale u_i (g_i - sum_j g_j u_j), times sigmoid(-x_i) for sigmoids
+//   sigmoids      dx_i = scale u_i sigmoid(-x_i) g_i
+//   softmax       dx_e = scale (sum of the g of e's pairs, times u_e, - p_e sum_j g_j u_j)
+// A warp per token: lane j the pair j, then the row (zeros, or the last line's second part)
+// in runs of V, then the chosen logits' own values over it.  Bound by HBM: the row is
+// written, and read where every logit has a gradient.
+template <class T, int V>
+__global__ void __launch_bounds__(256) moe_scored_grad_kernel(const T *logits, const int *experts, const float *dweights,
+                                                              T *dlogits, int Tn, int E, int k, int sigmoid, int normalize,
+                                                              float scale)
+{
+    struct alignas(V * sizeof(T)) Run {
+        T v[V];
+    };
+    constexpr float kNone = -__builtin_huge_valf();
+    overlap_wait();
+    const int lane = threadIdx.x & 31;
+    const bool dense = !sigmoid && !normalize;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < Tn; t += step) {
+        const T *row = logits + t * E;
+        T *out = dlogits + t * E;
+        int e = lane < k ? experts[t * k + lane] : -1;
+        float g = lane < k ? dweights[t * k + lane] : 0.0f;
+        float x = e >= 0 && e < E ? scored_logit(row, e) : kNone;
+        if (!(x > kNone)) {  // no choice, or one that has no weight
+            e = -1;
+            g = 0.0f;
+        }
+        float m = 0.0f, inv = 0.0f;
+        if (dense) {
+            // the row's largest and the sum, a lane's running ones joined
+            m = kNone;
+            float sum = 0.0f;
+            for (int i = lane * V; i < E; i += 32 * V) {
+                const Run run = *reinterpret_cast<const Run *>(row + i);
+                float v[V], most = m;
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    v[q] = moe_float(run.v[q]);
+                    if (v[q] != v[q]) v[q] = kNone;
+                    most = fmaxf(most, v[q]);
+                }
+                if (most > kNone) {
+                    sum = m > kNone ? sum * expf(m - most) : 0.0f;
+#pragma unroll
+                    for (int q = 0; q < V; ++q) sum += expf(v[q] - most);
+                    m = most;
+                }
+            }
+            const float most = route_value(__reduce_max_sync(0xffffffffu, route_key(m)));
+            sum = m > kNone ? sum * expf(m - most) : 0.0f;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            m = most;
+            if (m > kNone && m < CUDART_INF_F) {
+                inv = __fdiv_rn(1.0f, sum);
+            } else {  // no scores: nothing was chosen
+                e = -1;
+                g = 0.0f;
+            }
+        }
+        // u of the pair, and how much of its score's gradient reaches the logit
+        float u = 0.0f, part = 1.0f;
+        if (sigmoid) part = e >= 0 ? scored_sigmoid(-x) : 0.0f;
+        if (normalize) {
+            const float most = route_value(__reduce_max_sync(0xffffffffu, route_key(e >= 0 ? x : kNone)));
+            if (e >= 0) {
+                if (!sigmoid) u = expf(x - most);
+                else if (x > 0.0f) u = scored_sigmoid(x);
+                else u = __fdiv_rn(expf(x - fminf(most, 0.0f)), 1.0f + expf(x));
+            }
+            float total = u;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+            if (e >= 0) u = __fdiv_rn(u, total);
+        } else if (e >= 0) {
+            u = sigmoid ? scored_sigmoid(x) : expf(x - m) * inv;
+        }
+        float mean = 0.0f;
+        if (!sigmoid || normalize) {
+            mean = g * u;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, d);
+        }
+        float d = scale * u * part * (g - (normalize ? mean : 0.0f));
+        // an expert twice in a token: the first of its pairs writes the sum
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && (same & (same - 1))) {
+            float all = 0.0f;
+            for (int j = 0; j < k; ++j) {
+                const float o = __shfl_sync(same, d, j);
+                if (same >> j & 1u) all += o;
+            }
+            d = all;
+        }
+        if (dense) d -= scale * u * mean;
+        const float of_row = scale * mean;
+        for (int i = lane * V; i < E; i += 32 * V) {
+            Run run;
+            if (dense && inv > 0.0f) {
+                const Run in = *reinterpret_cast<const Run *>(row + i);
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    const float v = moe_float(in.v[q]);
+                    scored_out(&run.v[q], v > kNone ? -(expf(v - m) * inv) * of_row : 0.0f);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < V; ++q) scored_out(&run.v[q], 0.0f);
+            }
+            *reinterpret_cast<Run *>(out + i) = run;
+        }
+        __syncwarp();  // the row before the values of the chosen ones
+        if (e >= 0 && lane == __ffs(same) - 1) scored_out(out + e, d);
+    }
+    overlap_release();
+}
+
+template <class T, int V>
+static int launch_grad(const MoeScoredGradCall &c, cudaStream_t stream)
+{
+    const uintptr_t at = reinterpret_cast<uintptr_t>(c.logits) | reinterpret_cast<uintptr_t>(c.dlogits);
+    if constexpr (V > 1)
+        if (at % (V * sizeof(T)) != 0 || c.E % V != 0) return launch_grad<T, V / 2>(c, stream);
+    const int64_t blocks = std::min<int64_t>((int64_t(c.T) + 7) / 8, int64_t(sm_count()) * 8);
+    return launch_overlapped(moe_scored_grad_kernel<T, V>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                             static_cast<const T *>(c.logits), c.experts, c.dweights, static_cast<T *>(c.dlogits), c.T, c.E,
+                             c.k, c.score == 1 ? 1 : 0, c.normalize ? 1 : 0, c.scale);
+}
+
+int launch_moe_route_scored_grad(const MoeScoredGradCall &c, cudaStream_t stream)
+{
+    switch (c.x_type) {
+    case 0: return launch_grad<float, 4>(c, stream);
+    case 1: return launch_grad<__nv_bfloat16, 8>(c, stream);
+    default: return launch_grad<__half, 8>(c, stream);
+    }
+}
+
+}  // namespace igemm
