@@ -280,8 +280,8 @@ IGEMM_API int pack_int4(const int8_t *logical, uint8_t *packed, int64_t rows, in
  * a 4-bit or block-scaled fp8 operator with 128 x 128 scales one, but igemm_moe_route (and
  * igemm_moe_route_scored) two or three above 512 tokens (three
  * where the counts that its blocks would all read pass 4 MB: with
- * b = ceil(T / 64) blocks, 4 b b ceil(E / 4) bytes), and pack_mxfp4 or pack_nvfp4
- * two where rows are packed once and copied (as stated there).
+ * b = ceil(T / 64) blocks, 4 b b ceil(E / 4) bytes), and pack_mxfp4, pack_nvfp4 or
+ * pack_bsfp8 two where rows are packed once and copied (as stated there).
  * The split K of the other paths adds a memset, which is not a kernel.
  */
 IGEMM_API uint64_t igemm_kernels_launched(void);
@@ -539,8 +539,8 @@ typedef enum igemm_fp8 { IGEMM_E4M3 = 0, IGEMM_E5M2 = 1 } igemm_fp8;
  * for e4m3, 57344 for e5m2), codes fp8(x * (1 / s)); every operation float32, rounded to
  * nearest, ties to even, saturating.  A block that holds a NaN or an infinity gets a NaN
  * scale and zero codes.
- *   x, x_type, ld, transposed, index, x_rows   as for pack_mxfp4; index only with
- *           tile_rows 1 and not with transposed (IGEMM_UNSUPPORTED_SHAPE)
+ *   x, x_type, ld, transposed, index, x_rows   as for pack_mxfp4, its workspace too; index only
+ *           with tile_rows 1 and not with transposed (IGEMM_UNSUPPORTED_SHAPE)
  *   tile_rows  1 or 128 (IGEMM_UNSUPPORTED_SHAPE otherwise); the last tile of rows may be
  *           short
  * rows == 0 or K == 0 is a no-op.

@@ -136,13 +136,14 @@ int launch_route_scan(const RouteParams &p, cudaStream_t stream);
 int launch_route_place(const RouteParams &p, int smem, cudaStream_t stream);
 
 // The launches of a routing: choose(p, smem) launches the choice of experts, on the
-// blocks of one cluster (p.counts and p.packed_counts null) or on many.
+// blocks of one cluster (p.counts and p.packed_counts null) or on many, of `tb` tokens
+// (at most kTB).
 template <class Choose>
-int route_launch(RouteParams p, cudaStream_t stream, Choose choose)
+int route_launch(RouteParams p, cudaStream_t stream, Choose choose, int tb = kTB)
 {
     // up to 512 tokens spread over the blocks of a cluster
     const bool one = p.T <= kClusterBlocks * kTB;
-    p.tb = one ? std::max(kFewTokens, (p.T + kClusterBlocks - 1) / kClusterBlocks) : kTB;
+    p.tb = one ? std::max(kFewTokens, (p.T + kClusterBlocks - 1) / kClusterBlocks) : tb;
     p.blocks = static_cast<int>((int64_t(p.T) + p.tb - 1) / p.tb);
     // the places can sum every block's counts themselves, without a scan, while all of
     // them together read no more than 4 MB (us, two launches and three: 4096 x 256 bfloat16

@@ -6,11 +6,13 @@
 //   they are renormalised.
 //
 // The choice is that of the definition in 64 bits, ties to the lowest expert: a token's c
-// are computed in 32 bits, and where two that decide (neighbours among the chosen, the
-// last of them and the best one left, the last group taken and the best one left) are
-// nearer than the rounding could be, the token is done again in 64 bits (some tokens in a
-// thousand, 2 us each on a warp).  Without a bias the scores are in the order of the
-// logits, which are compared as they are.
+// are computed in 32 bits, and where two that decide are nearer than the rounding could
+// be, these alone are computed again, a lane each: neighbours among the chosen and those
+// left behind the last of them (some tokens in a thousand), the largest experts of groups
+// at the border between taken and left (one token in ten thousand).  (The 64-bit pipe is
+// slow: a token's 256 scores take a warp 40 us, one a lane 2.)  A token with more of them
+// than a warp has lanes is done again as a whole, after the block's others.  Without a bias
+// the scores are in the order of the logits, which are compared as they are.
 //
 // A warp per token, a lane E / 32 neighbouring experts, so that a group is a run of lanes
 // and the first lane with the largest value holds the lowest expert.  From the choices to
@@ -33,9 +35,25 @@ struct ScoredParams {
     int sigmoid;
     int groups, per, group_k, two;  // per: experts of a group; two: its two largest count
     float scale;
+    int vec;  // rows of whole runs
 };
 
 __device__ __forceinline__ float scored_sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+// For the choice: within 1.63 2^-22 (an exponential of 2 + 1.173 |x| ulp counts s (1 - s),
+// the sum 2^-24, the quotient 2 ulp).
+__device__ __forceinline__ float scored_sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// Order-preserving integers of 64-bit scores (comparisons of doubles are as slow as their sums).
+__device__ __forceinline__ uint64_t scored_key(double v)
+{
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return b >> 63 ? ~b : b | (uint64_t(1) << 63);
+}
+__device__ __forceinline__ double scored_value(uint64_t k)
+{
+    return __longlong_as_double(static_cast<long long>(k >> 63 ? k & ~(uint64_t(1) << 63) : ~k));
+}
+constexpr uint64_t kKey64None = 0x000FFFFFFFFFFFFFull;  // of -inf
 
 // The logit as it counts: NaN is -inf.
 template <class T>
@@ -54,15 +72,14 @@ __device__ __forceinline__ void scored_two(F &a1, F &a2, F v)
 }
 
 // The sum of a group's largest, or of its two largest where there are two.
-template <class F>
-__device__ __forceinline__ F scored_group(F a1, F a2, bool two)
+__device__ __forceinline__ float scored_group(float a1, float a2, bool two)
 {
-    return two && a2 > F(-CUDART_INF_F) ? a1 + a2 : a1;
+    return two && a2 > -CUDART_INF_F ? a1 + a2 : a1;
 }
 
-// Bit g: group g is taken; lane g holds its score (-inf: nothing to choose).
+// Bit g: group g is taken; lane g holds its score (`none`: nothing to choose).
 template <class F>
-__device__ __forceinline__ uint32_t scored_groups(F score, int groups, int group_k)
+__device__ __forceinline__ uint32_t scored_groups(F score, F none, int groups, int group_k)
 {
     const int lane = threadIdx.x & 31;
     int rank = 0;
@@ -70,57 +87,71 @@ __device__ __forceinline__ uint32_t scored_groups(F score, int groups, int group
         const F other = __shfl_sync(0xffffffffu, score, g);
         rank += other > score || (other == score && g < lane) ? 1 : 0;
     }
-    return __ballot_sync(0xffffffffu, lane < groups && rank < group_k && score > F(-CUDART_INF_F));
+    return __ballot_sync(0xffffffffu, lane < groups && rank < group_k && score > none);
 }
 
-// The choice in 64 bits: lane c's expert, -1 where none is left.
+// One expert's c in 64 bits; softmax: with the row's largest logit and sum.
+__device__ __forceinline__ double scored_c_64(const ScoredParams &p, double x, int e, double m, double sum)
+{
+    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / sum;
+    return p.bias ? s + static_cast<double>(p.bias[e]) : s;
+}
+
+// A softmax row's sum in 64 bits (m: its largest logit).
+template <class T, int VPL>
+__device__ __noinline__ double scored_sum_64(const ScoredParams &p, const T *row, float m)
+{
+    const int e0 = (threadIdx.x & 31) * VPL;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int j = 0; j < VPL; ++j)
+        if (e0 + j < p.r.E) sum += exp(static_cast<double>(scored_logit(row, e0 + j)) - static_cast<double>(m));
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    return sum;
+}
+
+// The whole choice in 64 bits: lane i's expert, -1 where none is left.
 template <class T, int VPL>
 __device__ __noinline__ int scored_choose_64(const ScoredParams &p, const T *row)
 {
     const int lane = threadIdx.x & 31, e0 = lane * VPL;
-    const double none = -CUDART_INF;
-    double c[VPL], s[VPL];
-    double sum = 0.0;
+    uint64_t c[VPL], s[VPL];  // what experts and groups are chosen by
     float m = -CUDART_INF_F;
+    for (int j = 0; j < VPL; ++j)
+        if (e0 + j < p.r.E) m = fmaxf(m, scored_logit(row, e0 + j));
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const double sum = p.sigmoid ? 1.0 : scored_sum_64<T, VPL>(p, row, m);
     for (int j = 0; j < VPL; ++j) {
         const float x = e0 + j < p.r.E ? scored_logit(row, e0 + j) : -CUDART_INF_F;
-        c[j] = x;
-        m = fmaxf(m, x);
-    }
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    for (int j = 0; j < VPL; ++j) {
-        s[j] = c[j] == none ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-c[j])) : exp(c[j] - static_cast<double>(m));
-        sum += s[j];
-    }
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    for (int j = 0; j < VPL; ++j) {
-        if (!p.sigmoid) s[j] /= sum;
-        if (p.bias && c[j] > none) {
-            const double v = s[j] + static_cast<double>(p.bias[e0 + j]);
-            c[j] = v > none ? v : none;  // (not NaN)
-            s[j] = c[j];
+        c[j] = s[j] = kKey64None;
+        if (x > -CUDART_INF_F) {
+            const double v = scored_c_64(p, x, e0 + j, m, sum);
+            const uint64_t k = v == v ? scored_key(v) : kKey64None;
+            c[j] = p.bias ? k : scored_key(x);
+            s[j] = p.bias || p.two ? k : c[j];
         }
     }
     if (p.groups > 1) {
-        double score = none;
+        uint64_t score = kKey64None;
         for (int g = 0; g < p.groups; ++g) {
-            double a1 = none, a2 = none;
+            uint64_t a1 = kKey64None, a2 = kKey64None;
             for (int j = 0; j < VPL; ++j)
-                if (c[j] > none && (e0 + j) / p.per == g) scored_two(a1, a2, p.two && !p.bias ? s[j] : c[j]);
+                if (c[j] > kKey64None && (e0 + j) / p.per == g) scored_two(a1, a2, s[j]);
             for (int d = 16; d; d >>= 1) {
-                const double b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
+                const uint64_t b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
                 scored_two(a1, a2, b1);
                 scored_two(a1, a2, b2);
             }
-            if (lane == g) score = a1 > none ? scored_group(a1, a2, p.two) : none;
+            if (lane == g)
+                score = p.two && a2 > kKey64None ? scored_key(scored_value(a1) + scored_value(a2)) : a1;
         }
-        const uint32_t taken = scored_groups(score, p.groups, p.group_k);
+        const uint32_t taken = scored_groups(score, kKey64None, p.groups, p.group_k);
         for (int j = 0; j < VPL; ++j)
-            if (e0 + j < p.r.E && !(taken >> ((e0 + j) / p.per) & 1u)) c[j] = none;
+            if (e0 + j < p.r.E && !(taken >> ((e0 + j) / p.per) & 1u)) c[j] = kKey64None;
     }
     int mine = -1;
     for (int i = 0; i < p.r.k; ++i) {
-        double best = none;
+        uint64_t best = kKey64None;
         int e = 0x7FFFFFFF;
         for (int j = 0; j < VPL; ++j)
             if (c[j] > best) {
@@ -128,28 +159,78 @@ __device__ __noinline__ int scored_choose_64(const ScoredParams &p, const T *row
                 e = e0 + j;
             }
         for (int d = 16; d; d >>= 1) {
-            const double b = __shfl_xor_sync(0xffffffffu, best, d);
+            const uint64_t b = __shfl_xor_sync(0xffffffffu, best, d);
             const int f = __shfl_xor_sync(0xffffffffu, e, d);
             if (b > best || (b == best && f < e)) {
                 best = b;
                 e = f;
             }
         }
-        if (!(best > none)) break;
+        if (best <= kKey64None) break;
         if (lane == i) mine = e;
         for (int j = 0; j < VPL; ++j)
-            if (e0 + j == e) c[j] = none;
+            if (e0 + j == e) c[j] = kKey64None;
     }
     return mine;
 }
 
-// Choice and weights of a block's tokens; their masks; one cluster: everything.
-// VPL: experts per lane (E <= 32 VPL); VEC: a lane's logits in runs of V (16 bytes at most),
-// loaded together.
-template <class T, int VPL, bool VEC>
-__global__ void __launch_bounds__(kScoredThreads) moe_choose_scored_kernel(const ScoredParams sp)
+// The first n lanes hold experts by falling c in 32 bits, among them every one that could
+// be among the k largest; the same by c in 64 bits, lanes from k on -1.
+__device__ __forceinline__ int scored_order_64(const ScoredParams &p, int e, float x, int n, double m, double sum)
 {
-    constexpr int V = !VEC ? 1 : VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
+    const int lane = threadIdx.x & 31;
+    const uint64_t key = lane < n ? scored_key(scored_c_64(p, x, e, m, sum)) : kKey64None;
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const uint64_t other = __shfl_sync(0xffffffffu, key, i);
+        const int f = __shfl_sync(0xffffffffu, e, i);
+        rank += other > key || (other == key && f < e) ? 1 : 0;
+    }
+    int mine = -1;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const int r = __shfl_sync(0xffffffffu, rank, i), f = __shfl_sync(0xffffffffu, e, i);
+        if (r == lane && lane < p.r.k) mine = f;
+    }
+    return mine;
+}
+
+// The groups of `border` may be taken or not: bit j of a lane's `cand` says that its expert j
+// may count in one of them.  The groups taken, by 64 bits; 0 where the experts are more than
+// a warp's lanes.
+template <class T, int VPL>
+__device__ __forceinline__ uint32_t scored_border_64(const ScoredParams &p, const T *row, uint32_t cand, uint32_t taken,
+                                                     uint32_t border, double m, double sum)
+{
+    const int lane = threadIdx.x & 31;
+    if (__reduce_add_sync(0xffffffffu, __popc(cand)) > 32) return 0;
+    int n = 0, mine = -1;
+#pragma unroll 1
+    for (int j = 0; j < VPL; ++j)
+        for (uint32_t lanes = __ballot_sync(0xffffffffu, cand >> j & 1u); lanes; lanes &= lanes - 1, ++n)
+            if (lane == n) mine = (__ffs(lanes) - 1) * VPL + j;
+    const uint64_t key = mine >= 0 ? scored_key(scored_c_64(p, scored_logit(row, mine), mine, m, sum)) : kKey64None;
+    uint64_t a1 = kKey64None, a2 = kKey64None;  // of group `lane`
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const uint64_t k = __shfl_sync(0xffffffffu, key, i);
+        if (__shfl_sync(0xffffffffu, mine, i) / p.per == lane) scored_two(a1, a2, k);
+    }
+    const bool open = border >> lane & 1u;
+    const uint64_t score = !open ? kKey64None
+                           : p.two && a2 > kKey64None ? scored_key(scored_value(a1) + scored_value(a2))
+                                                      : a1;
+    return (taken & ~border) | scored_groups(score, kKey64None, p.groups, __popc(taken & border));
+}
+
+// Choice and weights of a block's tokens; their masks; one cluster: everything.
+// VPL: experts per lane (E <= 32 VPL), their logits in runs of V (16 bytes at most) where rows
+// start on such.
+template <class T, int VPL>
+__global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_scored_kernel(const ScoredParams sp)
+{
+    constexpr int V = VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
     struct alignas(V * sizeof(T)) Run {
         T v[V];
     };
@@ -162,7 +243,9 @@ __global__ void __launch_bounds__(kScoredThreads) moe_choose_scored_kernel(const
     int *first = reinterpret_cast<int *>(mask + p.E);
     int *start = first + p.E + 1;
     int *chosen = start + p.E;
+    __shared__ int again[kTB], again_count;  // tokens to do again
     for (int e = threadIdx.x; e < p.E; e += kScoredThreads) mask[e] = make_uint2(0, 0);
+    if (threadIdx.x == 0) again_count = 0;
     float bias[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) bias[j] = sp.bias && e0 + j < p.E ? sp.bias[e0 + j] : 0.0f;
@@ -174,6 +257,33 @@ __global__ void __launch_bounds__(kScoredThreads) moe_choose_scored_kernel(const
     const int lanes = sp.per / VPL;
     const bool runs = sp.per % VPL == 0 && (lanes & (lanes - 1)) == 0;
     const bool scores = sp.bias || (grouped && sp.two);  // every expert's is needed
+    // The weights of token i's choice, lane n's expert my_e; m and sum: softmax over all experts.
+    const auto finish = [&](int i, const T *row, int my_e, float m, float sum) {
+        const int64_t t = t0 + i;
+        const float x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
+        // The weight before the scale.  Renormalised ones need no score that could underflow:
+        // softmax from the largest chosen logit, sigmoids times e^-min(0, that).
+        float w = 0.0f, total = sum;
+        if (p.normalize) {
+            const float most = route_value(__reduce_max_sync(0xffffffffu, route_key(x)));
+            if (my_e >= 0) {
+                if (!sp.sigmoid) w = expf(x - most);
+                else if (x > 0.0f) w = scored_sigmoid(x);
+                else w = __fdiv_rn(expf(x - fminf(most, 0.0f)), 1.0f + expf(x));
+            }
+            total = w;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        } else if (my_e >= 0) {
+            w = sp.sigmoid ? scored_sigmoid(x) : expf(x - m);
+        }
+        if (lane < p.k) {
+            p.experts[t * p.k + lane] = my_e;
+            p.weights[t * p.k + lane] = my_e >= 0 ? sp.scale * __fdiv_rn(w, total) : 0.0f;
+            if (one_cluster) chosen[i * p.k + lane] = my_e;
+            if (my_e >= 0) atomicOr(i < 32 ? &mask[my_e].x : &mask[my_e].y, 1u << (i & 31));
+        }
+    };
     for (int i = warp; i < mine; i += kScoredThreads / 32) {
         const int64_t t = t0 + i;
         const T *row = static_cast<const T *>(p.logits) + t * p.E;
@@ -182,11 +292,15 @@ __global__ void __launch_bounds__(kScoredThreads) moe_choose_scored_kernel(const
 #pragma unroll
         for (int j = 0; j < VPL; j += V) {
             Run run;
-            const bool there = e0 + j < p.E;  // (VEC: E is a multiple of V)
-            if (there) run = *reinterpret_cast<const Run *>(row + e0 + j);
+            if (sp.vec && e0 + j < p.E) {  // (E is a multiple of V)
+                run = *reinterpret_cast<const Run *>(row + e0 + j);
+            } else {
+#pragma unroll
+                for (int q = 0; q < V; ++q) run.v[q] = e0 + j + q < p.E ? row[e0 + j + q] : T(kNone);
+            }
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                const float v = there ? moe_float(run.v[q]) : kNone;
+                const float v = moe_float(run.v[q]);
                 c[j + q] = v != v ? kNone : v + 0.0f;
                 m = fmaxf(m, c[j + q]);
             }
@@ -203,22 +317,24 @@ __global__ void __launch_bounds__(kScoredThreads) moe_choose_scored_kernel(const
                 sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
-                    s[j] = c[j] > kNone ? expf(c[j] - m) : 0.0f;
+                    s[j] = !(c[j] > kNone) ? 0.0f : p.normalize ? __expf(c[j] - m) : expf(c[j] - m);
                     sum += s[j];
                 }
 #pragma unroll
                 for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             }
         }
-        // error of one c below: at sigmoids 2^-21 (1 + |c|), at softmax 2^-17 of the largest score
-        // (their sum takes VPL + 5 roundings) and the sum's rounding
-        float slack = 0x1p-20f;
+        // Two c that are farther apart than slack + 2^-22 |c| are in order: twice the error of
+        // one, of sigmoids 1.63 2^-22, of softmax 24.3 2^-23 of the largest score (an
+        // exponential's 2 + 1.173 |x - m| ulp and |x - m| 2^-24 count e^(x - m), the sum takes
+        // VPL + 5 roundings), and of the addition 2^-24 |c|.
+        float slack = 0x1.ap-21f;
         if (scores) {
             const float inv = __fdiv_rn(1.0f, sum);
-            if (!sp.sigmoid) slack = 0x1p-16f * inv;
+            if (!sp.sigmoid) slack = 0x1p-17f * inv;
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
-                s[j] = !(c[j] > kNone) ? 0.0f : sp.sigmoid ? scored_sigmoid(c[j]) : s[j] * inv;
+                s[j] = !(c[j] > kNone) ? 0.0f : sp.sigmoid ? scored_sigmoid_fast(c[j]) : s[j] * inv;
                 if (sp.bias && c[j] > kNone) {
                     const float v = s[j] + bias[j];
                     c[j] = v > kNone ? v : kNone;  // (not NaN)
@@ -257,110 +373,142 @@ __global__ void __launch_bounds__(kScoredThreads) moe_choose_scored_kernel(const
                     if (lane == g) score = scored_group(a1, a2, sp.two);
                 }
             }
-            const uint32_t taken = scored_groups(score, sp.groups, sp.group_k);
+            uint32_t taken = scored_groups(score, kNone, sp.groups, sp.group_k);
             if (scores) {
                 // the last group taken and the best one left
-                const bool in = taken >> lane & 1u;
+                const bool in = taken >> lane & 1u, some = lane < sp.groups && score > kNone;
                 const float least = route_value(__reduce_min_sync(0xffffffffu, in ? route_key(score) : 0xFF800000u));
                 const float most = route_value(__reduce_max_sync(0xffffffffu, in ? kKeyNone : route_key(score)));
-                if (most > kNone)
-                    near = !(least - most > 2.0f * (sp.sigmoid ? slack * (1.0f + fabsf(least)) : slack + 0x1p-22f * fabsf(least)));
-            }
-            int g = e0 / sp.per, left = (g + 1) * sp.per - e0;  // experts until the next group
+                const float margin = 2.0f * slack + 0x1p-21f * fabsf(least);
+                if (most > kNone && !(least - most > margin)) {
+                    const uint32_t border =
+                        __ballot_sync(0xffffffffu, some && (in ? !(score - most > margin) : !(least - score > margin)));
+                    // their experts that may be the largest, or the two largest
+                    uint32_t cand = 0;
+                    for (uint32_t open = border; open; open &= open - 1) {
+                        const int g = __ffs(open) - 1, from = g * sp.per - e0, to = from + sp.per;
+                        float a1 = kNone, a2 = kNone;
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                if (left == 0) {
-                    ++g;
-                    left = sp.per;
+                        for (int j = 0; j < VPL; ++j)
+                            if (j >= from && j < to && c[j] > kNone) scored_two(a1, a2, sp.bias ? c[j] : s[j]);
+#pragma unroll
+                        for (int d = 16; d; d >>= 1) {
+                            const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
+                            scored_two(a1, a2, b1);
+                            scored_two(a1, a2, b2);
+                        }
+                        const float least_of = sp.two ? a2 : a1;
+#pragma unroll
+                        for (int j = 0; j < VPL; ++j)
+                            if (j >= from && j < to && c[j] > kNone &&
+                                !(least_of - (sp.bias ? c[j] : s[j]) > slack + 0x1p-22f * fabsf(least_of)))
+                                cand |= 1u << j;
+                    }
+                    const double sum64 = sp.sigmoid ? 1.0 : scored_sum_64<T, VPL>(sp, row, m);
+                    taken = scored_border_64<T, VPL>(sp, row, cand, taken, border, m, sum64);
+                    near = taken == 0;
                 }
-                --left;
-                if (g >= 32 || !(taken >> g & 1u)) c[j] = kNone;
             }
-        }
-        uint32_t key[VPL], local = 0;
+            if (runs) {
+                const bool in = lane < sp.groups * lanes && (taken >> lane / lanes & 1u);
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-            key[j] = route_key(c[j]);
-            local = max(local, key[j]);
-        }
-        // lane n keeps choice n
-        int my_e = -1;
-        uint32_t my_key = kKeyNone, top = __reduce_max_sync(0xffffffffu, local);
-        for (int n = 0; n < p.k; ++n) {
-            if (top <= kKeyNone) break;  // nothing is left
-            const int owner = __ffs(__ballot_sync(0xffffffffu, local == top)) - 1;
-            int at = 0;
-            if (lane == owner) {
-                local = 0;
-                bool found = false;
+                for (int j = 0; j < VPL; ++j) c[j] = in ? c[j] : kNone;
+            } else {
+                int g = e0 / sp.per, left = (g + 1) * sp.per - e0;  // experts until the next group
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
-                    const bool it = !found && key[j] == top;
-                    if (it) {
-                        at = j;
-                        key[j] = 0u;
+                    if (left == 0) {
+                        ++g;
+                        left = sp.per;
                     }
-                    found |= it;
-                    local = max(local, key[j]);
+                    --left;
+                    if (g >= 32 || !(taken >> g & 1u)) c[j] = kNone;
                 }
             }
-            const int e = owner * VPL + __shfl_sync(0xffffffffu, at, owner);
+        }
+        // A lane's two largest that are not taken, looked for again once both are: few lanes
+        // hold more than two of a token's choices.
+        float a1 = kNone, a2 = kNone;
+        int at1 = 0, at2 = 0, held = 2;
+        uint32_t used = 0;
+        const auto look = [&] {
+            a1 = a2 = kNone;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const float v = used >> j & 1u ? kNone : c[j];
+                const bool first_of = v > a1, second = v > a2;
+                a2 = first_of ? a1 : second ? v : a2;
+                at2 = first_of ? at1 : second ? j : at2;
+                a1 = first_of ? v : a1;
+                at1 = first_of ? j : at1;
+            }
+        };
+        look();
+        // lane n keeps choice n; those left that the last one does not surely exceed join the list
+        int my_e = -1, n = 0;
+        float my_c = kNone, last = kNone;
+        uint32_t local = route_key(a1), top = __reduce_max_sync(0xffffffffu, local);
+        const auto apart = [&](float a, float b) { return a - b > slack + 0x1p-22f * fabsf(a); };
+        for (; top > kKeyNone; ++n) {
+            if (n >= p.k) {
+                if (!sp.bias) break;
+                if (n == p.k) last = __shfl_sync(0xffffffffu, my_c, p.k - 1);
+                if (apart(last, route_value(top))) break;
+                near |= n == 32;  // (more than the list holds)
+                if (n == 32) break;
+            }
+            const int owner = __ffs(__ballot_sync(0xffffffffu, local == top)) - 1;
+            const int e = owner * VPL + __shfl_sync(0xffffffffu, at1, owner);
             if (lane == n) {
                 my_e = e;
-                my_key = top;
+                my_c = route_value(top);
+            }
+            if (lane == owner) {
+                used |= 1u << at1;
+                if (--held) {
+                    a1 = a2;
+                    at1 = at2;
+                } else {
+                    look();
+                    held = 2;
+                }
+                local = route_key(a1);
             }
             top = __reduce_max_sync(0xffffffffu, local);
         }
-        float x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
         if (sp.bias) {
             // neighbours nearer than the rounding, but for those that are equal in both parts
-            const float b = my_e >= 0 ? sp.bias[my_e] : 0.0f, v = route_value(my_key);
-            const auto margin = [&](float of) {
-                return sp.sigmoid ? slack * (1.0f + fabsf(of)) : slack + 0x1p-22f * fabsf(of);
-            };
-            const int e2 = __shfl_down_sync(0xffffffffu, my_e, 1);
+            const float x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
+            const float b = my_e >= 0 ? sp.bias[my_e] : 0.0f, v = my_c;
             const float x2 = __shfl_down_sync(0xffffffffu, x, 1), b2 = __shfl_down_sync(0xffffffffu, b, 1);
             const float v2 = __shfl_down_sync(0xffffffffu, v, 1);
-            const bool pair = my_e >= 0 && lane + 1 < p.k && e2 >= 0;
-            near |= __any_sync(0xffffffffu, pair && !(v - v2 > margin(v)) && !(x == x2 && b == b2));
-            // the last one and those left
-            const float vk = __shfl_sync(0xffffffffu, v, p.k - 1), xk = __shfl_sync(0xffffffffu, x, p.k - 1);
-            const float bk = __shfl_sync(0xffffffffu, b, p.k - 1);
-            if (top > kKeyNone && !(vk - route_value(top) > margin(vk))) {
-                bool other = false;
-#pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    if (key[j] > kKeyNone && !(vk - route_value(key[j]) > margin(vk)))
-                        other |= !(scored_logit(row, e0 + j) == xk && bias[j] == bk);
-                near |= __any_sync(0xffffffffu, other);
+            const bool unsure = lane + 1 < n && !apart(v, v2) && !(x == x2 && b == b2);
+            if (__any_sync(0xffffffffu, unsure)) {
+                const double sum64 = sp.sigmoid ? 1.0 : scored_sum_64<T, VPL>(sp, row, m);
+                my_e = scored_order_64(sp, my_e, x, n, m, sum64);
             }
         }
         if (near) {
-            my_e = scored_choose_64<T, VPL>(sp, row);
-            x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
+            if (lane == 0) again[atomicAdd(&again_count, 1)] = i;
+            continue;
         }
-        // The weight before the scale.  Renormalised ones need no score that could underflow:
-        // softmax from the largest chosen logit, sigmoids times e^-min(0, that).
-        float w = 0.0f, total = sum;
-        if (p.normalize) {
-            const float most = route_value(__reduce_max_sync(0xffffffffu, route_key(x)));
-            if (my_e >= 0) {
-                if (!sp.sigmoid) w = expf(x - most);
-                else if (x > 0.0f) w = scored_sigmoid(x);
-                else w = __fdiv_rn(expf(x - fminf(most, 0.0f)), 1.0f + expf(x));
-            }
-            total = w;
+        if (lane >= p.k) my_e = -1;
+        finish(i, row, my_e, m, sum);
+    }
+    __syncthreads();
+    for (int n = warp; n < again_count; n += kScoredThreads / 32) {
+        const int i = again[n];
+        const T *row = static_cast<const T *>(p.logits) + static_cast<int64_t>(t0 + i) * p.E;
+        float m = kNone, sum = 1.0f;
+        if (!sp.sigmoid && !p.normalize) {
+            for (int e = lane; e < p.E; e += 32) m = fmaxf(m, scored_logit(row, e));
+            m = route_value(__reduce_max_sync(0xffffffffu, route_key(m)));
+            sum = 0.0f;
+            for (int e = lane; e < p.E; e += 32) sum += expf(scored_logit(row, e) - m);
 #pragma unroll
-            for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        } else if (my_e >= 0) {
-            w = sp.sigmoid ? scored_sigmoid(x) : expf(x - m);
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         }
-        if (lane < p.k) {
-            p.experts[t * p.k + lane] = my_e;
-            p.weights[t * p.k + lane] = my_e >= 0 ? sp.scale * __fdiv_rn(w, total) : 0.0f;
-            if (one_cluster) chosen[i * p.k + lane] = my_e;
-            if (my_e >= 0) atomicOr(i < 32 ? &mask[my_e].x : &mask[my_e].y, 1u << (i & 31));
-        }
+        finish(i, row, scored_choose_64<T, VPL>(sp, row), m, sum);
     }
     overlap_release();
     __syncthreads();
@@ -372,11 +520,11 @@ __global__ void __launch_bounds__(kScoredThreads) moe_choose_scored_kernel(const
 }
 
 template <class T, int VPL>
-static int launch_scored_vpl(const ScoredParams &p, int smem, cudaStream_t stream)
+static int launch_scored_vpl(ScoredParams p, int smem, cudaStream_t stream)
 {
     constexpr int V = VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
-    const bool vec = p.r.E % V == 0 && reinterpret_cast<uintptr_t>(p.r.logits) % (V * sizeof(T)) == 0;
-    const auto kernel = vec ? moe_choose_scored_kernel<T, VPL, true> : moe_choose_scored_kernel<T, VPL, false>;
+    p.vec = p.r.E % V == 0 && reinterpret_cast<uintptr_t>(p.r.logits) % (V * sizeof(T)) == 0;
+    const auto kernel = moe_choose_scored_kernel<T, VPL>;
     if (p.r.T > kClusterBlocks * kTB)
         return launch_overlapped(kernel, dim3(p.r.blocks), dim3(kScoredThreads), smem, stream, p);
     int cluster = 1;
@@ -407,12 +555,16 @@ int launch_moe_route_scored(const MoeScoredCall &c, cudaStream_t stream)
     p.E = c.route.E;
     p.k = c.route.k;
     p.normalize = c.route.normalize ? 1 : 0;
-    return route_launch(p, stream, [&](const RouteParams &q, int smem) {
-        const ScoredParams sp{q, c.bias, c.score == 1, c.groups, q.E / c.groups, c.group_k, c.group_top == 2, c.scale};
+    // blocks in whole waves of two on every SM
+    const int64_t wave = 2 * sm_count(), waves = (int64_t(p.T) + wave * kTB - 1) / (wave * kTB);
+    const int tb = std::max(16, static_cast<int>((p.T + waves * wave - 1) / std::max<int64_t>(1, waves * wave)));
+    const auto choose = [&](const RouteParams &q, int smem) {
+        const ScoredParams sp{q, c.bias, c.score == 1, c.groups, q.E / c.groups, c.group_k, c.group_top == 2, c.scale, 0};
         return c.route.x_type == 0   ? launch_scored<float>(sp, smem, stream)
                : c.route.x_type == 1 ? launch_scored<__nv_bfloat16>(sp, smem, stream)
                                      : launch_scored<__half>(sp, smem, stream);
-    });
+    };
+    return route_launch(p, stream, choose, tb);
 }
 
 // ---------------------------------------------------------------- gradient

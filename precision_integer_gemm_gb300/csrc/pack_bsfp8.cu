@@ -334,9 +334,88 @@ static int launch_pack_format(const Bsfp8PackCall &c, cudaStream_t stream)
     }
 }
 
+// Packed rows copied to their places; where the index is out of range, a row of zeros.
+// A thread takes one 16-byte piece of four rows, a quarter of the rows apart, all in flight.
+__global__ void __launch_bounds__(256) bsfp8_copy_rows_kernel(const uint4 *codes, const uint4 *scales, const Bsfp8PackParams p)
+{
+    overlap_wait();
+    const uint32_t cq = p.code_bytes / 16, per_row = cq + p.pitch / 4;
+    const uint32_t rows = static_cast<uint32_t>(p.rows), quarter = (rows + 3) / 4;
+    const uint32_t item = blockIdx.x * 256 + threadIdx.x;  // (fits: pack_once)
+    const uint32_t row = item / per_row, j = item - row * per_row;
+    if (row >= quarter) return;  // (an exit counts as a release)
+    const bool code = j < cq;
+    const int64_t pitch = code ? cq : per_row - cq;
+    const uint4 *from = code ? codes + j : scales + (j - cq);
+    uint4 *to = code ? reinterpret_cast<uint4 *>(p.codes) + j : reinterpret_cast<uint4 *>(p.scales) + (j - cq);
+    uint4 zeros = make_uint4(0, 0, 0, 0);
+    if (!code) {  // (the scale of a block of zeros, 2^-126)
+        const int left = (p.K + 127) / 128 - 4 * static_cast<int>(j - cq);
+        constexpr uint32_t kLeast = 0x00800000u;
+        zeros = make_uint4(left > 0 ? kLeast : 0, left > 1 ? kLeast : 0, left > 2 ? kLeast : 0, left > 3 ? kLeast : 0);
+    }
+    int src[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) src[i] = p.index[min(row + i * quarter, rows - 1)];
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = zeros;
+        if (src[i] >= 0 && src[i] < p.x_rows) v[i] = from[src[i] * pitch];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t r = row + i * quarter;
+        if (r < rows) to[r * pitch] = v[i];
+    }
+    overlap_release();
+}
+
+// Rows that are gathered twice or more on average are packed once, into a workspace,
+// and copied from there, where that saves reading 32 MB of x at least.
+static bool pack_once(const Bsfp8PackCall &c)
+{
+    const int64_t pieces = bsfp8_code_bytes(c.K) / 16 + bsfp8_scale_pitch(c.K) / 4;
+    const int64_t saved = (int64_t(c.rows) - c.x_rows) * c.K * (c.x_type == 0 ? 4 : 2);
+    return c.index && c.x_rows > 0 && c.rows / 2 >= c.x_rows && saved >= int64_t(1) << 25 &&
+           c.rows * pieces <= 0xFFFFFFFFll - 1024;
+}
+
 int launch_bsfp8_pack(const Bsfp8PackCall &c, cudaStream_t stream)
 {
-    return c.format == 0 ? launch_pack_format<0>(c, stream) : launch_pack_format<1>(c, stream);
+    const auto launch = [&](const Bsfp8PackCall &call) {
+        return call.format == 0 ? launch_pack_format<0>(call, stream) : launch_pack_format<1>(call, stream);
+    };
+    if (!pack_once(c)) return launch(c);
+    Bsfp8PackParams p{};
+    p.index = c.index;
+    p.codes = c.codes;
+    p.scales = c.scales;
+    p.x_rows = c.x_rows;
+    p.rows = c.rows;
+    p.K = c.K;
+    p.code_bytes = bsfp8_code_bytes(c.K);
+    p.pitch = bsfp8_scale_pitch(c.K);
+    const size_t code_bytes = size_t(c.x_rows) * p.code_bytes;
+    void *ws = nullptr;
+    if (workspace_alloc(&ws, code_bytes + size_t(c.x_rows) * p.pitch * 4, stream) != kOk) {
+        cudaGetLastError();  // no room for it: row by row
+        return launch(c);
+    }
+    Bsfp8PackCall once = c;
+    once.index = nullptr;
+    once.rows = c.x_rows;
+    once.codes = static_cast<uint8_t *>(ws);
+    once.scales = reinterpret_cast<float *>(once.codes + code_bytes);
+    int rc = launch(once);
+    if (rc == kOk) {
+        const int64_t items = (int64_t(c.rows) + 3) / 4 * (int64_t(p.code_bytes) / 16 + p.pitch / 4);
+        rc = launch_overlapped(bsfp8_copy_rows_kernel, dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0,
+                               stream, reinterpret_cast<const uint4 *>(once.codes),
+                               reinterpret_cast<const uint4 *>(once.scales), p);
+    }
+    if (workspace_free(ws, stream) != kOk) rc = kCudaError;
+    return rc;
 }
 
 }  // namespace igemm
