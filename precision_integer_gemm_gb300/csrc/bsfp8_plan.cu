@@ -5,10 +5,14 @@
 
 namespace igemm {
 
-// Kernel, tile and split by estimated time in microseconds.  A wave of tiles takes
-// groups of 512 k times the time of a group on an SM: what its bytes take from L2 (100
-// KB a microsecond) or from HBM (6.3 MB a microsecond shared by the SMs), or what its
-// MMAs and their promotion take; plus what a tile costs besides.
+// Kernel, tile and split by estimated time in microseconds: 4.5 for the start, then every
+// wave of tiles its groups of 512 k and what a tile costs besides.  A group takes an SM
+// 0.83 with tiles of 16 activations, 0.86 with 32, 0.92 with 64, 1.47 with 128, a CTA pair
+// 1.6 (up to 128) or 1.8, or what HBM takes to bring the weights of all SMs at work, 6.3 MB
+// a microsecond.  A split of k over two or four CTAs adds up to 2.7, with 64 activations
+// or more to every wave (7 with 128).  (4096 x 4096 weights and 16 activations: 11.3 whole, 8.7 on two, 8.3 on
+// four; 64: 12.1, 10.7, 9.9; 128 activations as two tiles of 64: 12.3, as one 16.0; 8192 x
+// 8192: 256 activations as two tiles of 128 28, on pairs 34.7; 768: 76 and 68.)
 bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Plan *plan)
 {
     const int steps = (c.K + 511) / 512;
@@ -28,11 +32,17 @@ bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Pl
         const double q_tiles = c.offsets && typical > bn ? typical / bn + 0.5 : std::ceil(typical / bn);
         const double rows = std::min(typical / q_tiles, double(bn));
         const double tiles = p_tiles * q_tiles * groups;
-        const double bytes = (128 + (pair ? rows / 2 : rows)) * 512;
-        const double readers = std::min(tiles, double(clusters)) * (pair ? 2 / q_tiles : cs);
-        const double compute = pair ? 1.25 * rows / 256 : bn == 128 ? 1.1 : bn == 64 ? 0.6 : 0.45;
-        const double step = std::max({bytes / 100e3, readers * 128 * 512 / 6.3e6, compute});
-        const double cost = std::ceil(tiles / clusters) * (per * step + (pair ? 2.5 : 1.0)) + (cs == 1 ? 0.0 : 2.0);
+        const double compute = pair ? (rows <= 128 ? 1.6 : 1.8) : bn == 128 ? 1.47 : bn == 64 ? 0.92 : bn == 32 ? 0.86 : 0.83;
+        const double split = cs == 1 ? 0.0 : bn == 128 ? 7.0 : bn == 64 ? 2.1 + 0.15 * cs : bn == 32 ? 1.8 + 0.2 * cs : 0.4 + 0.1 * cs;
+        // (a lane's row of C in narrow pieces: float32 tiles of pairs take longer to leave)
+        const double tile = !pair ? 0.5 : c.c_type == 0 ? 8.0 : 3.2;
+        // a wave of n clusters: they read the weights of n / q_tiles tiles
+        const auto wave = [&](double n) {
+            const double weights = n * (pair ? 2 : cs) / std::min(q_tiles, n) * 128 * 512;
+            return per * std::max(compute, weights / 6.3e6) + tile + (bn >= 64 ? split : 0.0);
+        };
+        const double full = std::floor(tiles / clusters), rest = tiles - full * clusters;
+        const double cost = full * wave(clusters) + (rest > 0.01 ? wave(rest) : 0.0) + (bn >= 64 ? 0.0 : split);
         if (best < 0 || cost < best) {
             best = cost;
             *plan = Bsfp8Plan{bn, pair, cs, 1, groups};

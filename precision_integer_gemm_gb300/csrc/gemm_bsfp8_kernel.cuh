@@ -48,9 +48,9 @@ struct Bsfp8Params {
     int slice;             // blocks of 128 k per CTA of such a cluster (a multiple of 4)
     int stream;            // single CTAs: the weights leave L2 first
     int format;            // 0 e4m3, 1 e5m2
-    int turned;            // CTA pairs: full tiles with the activations on the M side
+    int turned;            // CTA pairs: activations from which on a tile has them on the M side
     int stages;            // ring slots of codes, even
-    int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
+    int store_bytes;       // of C at once (16, 8, 4 or 2), as the alignment of its rows allows
     int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
     int *status;
     unsigned long long limit_ns;
@@ -106,6 +106,8 @@ struct Bsfp8Cfg {
         const int step = 16 * kParts, n = units(nq) == 2 ? (nq + 1) / 2 : nq;
         return (n + step - 1) / step * step;
     }
+    // Whether a tile's activations are on the M side.
+    __device__ static bool lanes(const Bsfp8Params &prm, int nq) { return PAIR && nq >= prm.turned; }
 };
 
 // Tile t: group by binary search over the first tiles; whole tiles of qt activation rows
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             for (int t = cid; ok && t < tiles; t += ncl) {
                 const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
                 // activation rows that this CTA loads (pair: half of the tile's)
-                const int mine = PAIR ? Cfg::units(x.nq) * Cfg::columns(x.nq) / 2 : x.nq;
+                const int mine = !PAIR ? x.nq : Cfg::lanes(prm, x.nq) ? 128 : Cfg::units(x.nq) * Cfg::columns(x.nq) / 2;
                 const bool small = Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
                 const bool two = small && mine > Cfg::kQRows;
                 const int py = x.e * prm.N + x.p0, qy = x.q0 + pr * mine;
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 for (int i = 0; i < SS - 1 && ok && lt < tiles; ++i) load();
                 for (int t = cid; ok && t < tiles; t += ncl) {
                     const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
-                    const bool lanes = PAIR && prm.turned && x.nq == BN;
+                    const bool lanes = Cfg::lanes(prm, x.nq);
                     for (int b = b0; ok && b < b1; b += 4) {
                         ok = fp4_warp_wait(&s_raw[sr.slot], sr.phase, wd);
                         if (!ok) break;
@@ -450,25 +452,34 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             fp4_drain(s_raw, issued, last, t0, prm.limit_ns);
         } else if (leader) {
             // -------------------------------------------------------- MMA issuers
-            // A block each in turn, or (pairs) an accumulator of every block each.
+            // A block each in turn; of a pair's tile with two accumulators, one of every block
+            // each (an accumulator always belongs to the same warp).
             const int me = warp - Cfg::kWarpMma;
             const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(codes));
             const uint32_t fmt = static_cast<uint32_t>(prm.format);
             Fp4Ring cr(prm.stages);
-            uint32_t phases = 0;  // of the accumulators' turns
+            uint32_t phases = 0;  // of the accumulators
             bool ok = true;
             for (int t = cid; ok && t < tiles; t += ncl) {
                 const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
-                const bool lanes = PAIR && prm.turned && x.nq == BN;
-                const int nu = Cfg::units(x.nq), cols = Cfg::columns(x.nq);
+                const bool lanes = Cfg::lanes(prm, x.nq);
+                const int nu = lanes ? Cfg::kUnits : Cfg::units(x.nq), cols = lanes ? Cfg::UN : Cfg::columns(x.nq);
                 const uint32_t idesc = idesc_f8_f32(128 * Cfg::CL, static_cast<uint32_t>(cols), fmt);
                 // the second accumulator: the other half of each CTA's rows on the N side
-                const uint64_t half = PAIR ? static_cast<uint64_t>(me * (cols / 2 * 128 >> 4)) : 0;
+                const uint64_t half = nu == 2 ? static_cast<uint64_t>(me * (cols / 2 * 128 >> 4)) : 0;
                 for (int b = b0; b < b1; ++b) {
-                    const uint32_t turn = b % Cfg::kTurns, phase = phases >> turn & 1u;
-                    phases ^= 1u << turn;
-                    if (PAIR || (b & 1) == me) {
-                        const uint32_t pb = PAIR ? 2u * turn + me : turn;
+                    const bool mine = nu == 2 || (b & 1) == me;
+                    const uint32_t pb = nu == 2 ? 2 * (b & 1) + me : b % PB;
+                    if (PAIR && !mine) {
+                        // the slot's other arrival, in its turn
+                        ok = fp4_warp_wait(&full[cr.slot], cr.phase, wd);
+                        if (!ok) break;
+                        if (elect_one()) mma_commit_pair_multicast(&empty[cr.slot], 0x3);
+                        __syncwarp();
+                    }
+                    if (mine) {
+                        const uint32_t phase = phases >> pb & 1u;
+                        phases ^= 1u << pb;
                         if (!bsfp8_warp_wait2(&p_empty[pb], phase ^ 1u, &full[cr.slot], cr.phase, wd)) {
                             ok = false;
                             break;
@@ -478,14 +489,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                             const uint64_t p0 = desc0 + static_cast<uint64_t>(cr.slot * (Cfg::kStage >> 4));
                             const uint64_t q0 = p0 + static_cast<uint64_t>(Cfg::kBoxP >> 4);
                             const uint64_t da = lanes ? q0 : p0, db = (lanes ? p0 : q0) + half;
-                            if (!PAIR || me < nu) {
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    if constexpr (PAIR)
-                                        mma_f8f6f4_pair(tmem + pb * Cfg::UN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
-                                    else
-                                        mma_f8f6f4(tmem + pb * Cfg::UN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
-                                }
+                            for (int q = 0; q < 4; ++q) {
+                                if constexpr (PAIR)
+                                    mma_f8f6f4_pair(tmem + pb * Cfg::UN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
+                                else
+                                    mma_f8f6f4(tmem + pb * Cfg::UN, da + 2 * q, db + 2 * q, idesc, q > 0 ? 1u : 0u);
                             }
                             if constexpr (PAIR) {
                                 mma_commit_pair_multicast(&p_full[pb], 0x3);
@@ -517,51 +526,41 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         const uint32_t abort_at = smem_u32(const_cast<int *>(abort_flag)), p_full_at = smem_u32(p_full), s_full_at = smem_u32(s_full);
         const int q4 = lane & 3;
         Fp4Ring sr(SS);
-        uint32_t phases = 0;         // of the accumulators' turns
+        uint32_t phases = 0;         // of the accumulators
         uint32_t n = 0, armed = 0;  // armed: split k, tiles whose partials this warp expects
         bool ok = true;
         for (int t = cid; t < tiles; t += ncl, ++n) {
             const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
-            const bool lanes = PAIR && prm.turned && x.nq == BN;
+            const bool lanes = Cfg::lanes(prm, x.nq);
             // this warp's columns of an accumulator, and of the tile from c0 on
-            const int nu = Cfg::units(x.nq), cu = Cfg::columns(x.nq) / Cfg::kParts, c0 = part * nu * cu;
+            const int nu = Cfg::units(x.nq);
+            const int cu = (lanes ? Cfg::UN : Cfg::columns(x.nq)) / Cfg::kParts, c0 = part * nu * cu;
             const int cols = min(x.nq - c0, nu * cu);
             const uint32_t tpart = trow + part * cu;
-            // The blocks of the tile, an accumulator at a time: load(address, chunk, to) brings
-            // W of its columns of this warp to registers, add(begin(scales, block), h, chunk, from)
-            // adds them, while the other warp of the SM's quarter loads.  Four blocks (a slot of
-            // scales) are straight code: a branch costs as much as a load.  (A CTA that gives up
-            // runs on without waiting: an exit costs registers and moves.)
-            const auto blocks = [&](auto all_units, auto load, auto begin, auto add) {
-                constexpr int W = CU, kChunks = CU / W;
-                const int count = decltype(all_units)::value ? Cfg::kUnits : nu;
+            // The blocks of the tile, an accumulator at a time: load(address, to) brings all its
+            // columns of this warp to registers, it is released, and add(begin(scales, block),
+            // h, from) adds them, while the other warp of the SM's quarter loads.  (A CTA that
+            // gives up runs on without waiting: an exit costs registers and moves.)
+            const auto blocks = [&](auto units, auto load, auto begin, auto add) {
+                constexpr int count = decltype(units)::value;
                 const auto block = [&](const float *slot, int j) {
                     const auto sc = begin(slot, j);
-                    const uint32_t turn = j % Cfg::kTurns, phase = phases >> turn & 1u;
-                    phases ^= 1u << turn;
                     bool early = false;
 #pragma unroll
-                    for (int h = 0; h < Cfg::kUnits; ++h) {
-                        const uint32_t pb = turn * Cfg::kUnits + h;
-                        if (h < count) {
-                            if (h == 0 || !early) ok &= bsfp8_wait(p_full_at + 8 * pb, phase, abort_at, prm);
-                            tc_fence_after();
-#pragma unroll
-                            for (int i = 0; i < kChunks; ++i) {
-                                uint32_t v[W];
-                                load(tpart + pb * Cfg::UN, i, v);
-                                if (h + 1 < count) early = bsfp8_there(p_full_at + 8 * (pb + 1), phase);
-                                tmem_ld_wait_regs(v);
-                                if (i + 1 == kChunks) {
-                                    tc_fence_before();
-                                    if (lane == 0) mbar_arrive_peer(empty_leader + 8 * pb);
-                                }
-                                add(sc, h, i, v);
-                                if (h + 1 < count) early = __all_sync(0xffffffffu, early);
-                            }
-                        } else if (lane == 0) {
-                            mbar_arrive_peer(empty_leader + 8 * pb);  // (not used)
-                        }
+                    for (int h = 0; h < count; ++h) {
+                        const uint32_t pb = count == 2 ? 2 * (j & 1) + h : j % PB, phase = phases >> pb & 1u;
+                        if (h == 0 || !early) ok &= bsfp8_wait(p_full_at + 8 * pb, phase, abort_at, prm);
+                        tc_fence_after();
+                        phases ^= 1u << pb;
+                        uint32_t v[CU];
+                        load(tpart + pb * Cfg::UN, v);
+                        // (the next one's test is on its way meanwhile)
+                        if (h + 1 < count) early = bsfp8_there(p_full_at + 8 * (pb + 1), phases >> (pb + 1) & 1u);
+                        tmem_ld_wait_regs(v);
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive_peer(empty_leader + 8 * pb);
+                        add(sc, h, v);
+                        if (h + 1 < count) early = __all_sync(0xffffffffu, early);
                     }
                 };
 #pragma unroll 1
@@ -584,48 +583,65 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 F2 tot[PC / 2];
 #pragma unroll
                 for (int i = 0; i < PC / 2; ++i) tot[i] = make_float2(0.0f, 0.0f);
-                const auto load = [&](uint32_t at, int i, uint32_t(&to)[64]) { tmem_ld_32x32b_x64(at, to); };
+                const auto load = [&](uint32_t at, uint32_t(&to)[CU]) { tmem_ld_32x32b_x64(at, to); };
                 const auto begin = [&](const float *sc, int kb) {
                     const float s = sc[(rank * 128 + quad * 32 + lane) * 4 + kb] * sc[(BN + part) * 4 + kb];
                     return bsfp8_f2(s, s);
                 };
-                const auto add = [&](F2 ss, int h, int i, const uint32_t(&w)[64]) {
+                const auto add = [&](F2 ss, int h, const uint32_t(&w)[CU]) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) bsfp8_fma2(tot[h * (CU / 2) + j], w[2 * j], w[2 * j + 1], ss);
                 };
-                blocks(std::true_type(), load, begin, add);
+                blocks(std::integral_constant<int, 2>(), load, begin, add);
                 if (!ok) break;
-                // a lane's row of 128 columns (rows of C start on 16 bytes)
-                const int nb = x.p0 - 128 * pr + part * 128;
-                const int64_t m = static_cast<int64_t>(x.q0) + rank * 128 + quad * 32 + lane;
-                if (prm.c_type == kOutF32) {
-                    float *to = static_cast<float *>(prm.C) + m * prm.N + nb;
+                // a lane's row of 128 columns
+                const int nb = x.p0 - 128 * pr + part * 128, in = rank * 128 + quad * 32 + lane;
+                if (in < x.nq) {
+                    const int64_t at = (static_cast<int64_t>(x.q0) + in) * prm.N + nb;
+                    const int left = prm.N - nb;
+                    if (prm.c_type == kOutF32) {
+                        float *to = static_cast<float *>(prm.C) + at;
+                        if (prm.store_bytes == 16) {
 #pragma unroll
-                    for (int j = 0; j < PC / 4; ++j)
-                        if (nb + 4 * j < prm.N)
-                            *reinterpret_cast<uint4 *>(to + 4 * j) =
-                                make_uint4(bsfp8_lo(tot[2 * j]), bsfp8_hi(tot[2 * j]), bsfp8_lo(tot[2 * j + 1]),
-                                           bsfp8_hi(tot[2 * j + 1]));
-                } else {
-                    uint16_t *to = static_cast<uint16_t *>(prm.C) + m * prm.N + nb;
-                    const bool bf16 = prm.c_type == kOutBf16;
+                            for (int j = 0; j < PC / 4; ++j)
+                                if (4 * j < left)
+                                    *reinterpret_cast<float4 *>(to + 4 * j) =
+                                        make_float4(tot[2 * j].x, tot[2 * j].y, tot[2 * j + 1].x, tot[2 * j + 1].y);
+                        } else if (prm.store_bytes == 8) {  // (N is even)
 #pragma unroll
-                    for (int j = 0; j < PC / 8; ++j) {
-                        uint32_t w[4];
+                            for (int j = 0; j < PC / 2; ++j)
+                                if (2 * j < left) *reinterpret_cast<float2 *>(to + 2 * j) = tot[j];
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float lo = __uint_as_float(bsfp8_lo(tot[4 * j + i]));
-                            const float hi = __uint_as_float(bsfp8_hi(tot[4 * j + i]));
-                            if (bf16) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                            } else {
-                                const __half2 h = __floats2half2_rn(lo, hi);
-                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                            for (int j = 0; j < PC / 2; ++j) {
+                                if (2 * j < left) to[2 * j] = tot[j].x;
+                                if (2 * j + 1 < left) to[2 * j + 1] = tot[j].y;
                             }
                         }
-                        if (nb + 8 * j < prm.N)
-                            *reinterpret_cast<uint4 *>(to + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+                        uint16_t *to = static_cast<uint16_t *>(prm.C) + at;
+                        const bool bf16 = prm.c_type == kOutBf16;
+#pragma unroll
+                        for (int j = 0; j < PC / 8; ++j) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (bf16) {
+                                    const __nv_bfloat162 h = __floats2bfloat162_rn(tot[4 * j + i].x, tot[4 * j + i].y);
+                                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                                } else {
+                                    const __half2 h = __floats2half2_rn(tot[4 * j + i].x, tot[4 * j + i].y);
+                                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                                }
+                            }
+                            if (prm.store_bytes == 16) {  // (N is a multiple of 8)
+                                if (8 * j < left) *reinterpret_cast<uint4 *>(to + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                            } else {  // (of 2)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (8 * j + 2 * i < left) *reinterpret_cast<uint32_t *>(to + 8 * j + 2 * i) = w[i];
+                            }
+                        }
                     }
                 }
                 continue;
@@ -635,21 +651,20 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             F2 tot[PC / 2];
 #pragma unroll
             for (int i = 0; i < PC / 2; ++i) tot[i] = make_float2(0.0f, 0.0f);
-            constexpr int W = CU;
-            const auto load = [&](uint32_t at, int i, uint32_t(&to)[W]) {
+            const auto load = [&](uint32_t at, uint32_t(&to)[CU]) {
 #pragma unroll
-                for (int c = 0; c < W / 16; ++c) {
+                for (int c = 0; c < CU / 16; ++c) {
                     tmem_ld_16x256b_x2(at + 16 * c, to + 16 * c);
                     tmem_ld_16x256b_x2(at + (16u << 16) + 16 * c, to + 16 * c + 8);
                 }
             };
             const auto begin = [&](const float *sc, int kb) { return sc + kb * BN + c0 + 4 * q4; };
-            const auto add = [&](const float *sc, int h, int i, const uint32_t(&v)[W]) {
+            const auto add = [&](const float *sc, int h, const uint32_t(&v)[CU]) {
 #pragma unroll
-                for (int c = 0; c < W / 16; ++c) {
-                    const float4 s = *reinterpret_cast<const float4 *>(sc + h * cu + W * i + 16 * c);
+                for (int c = 0; c < CU / 16; ++c) {
+                    const float4 s = *reinterpret_cast<const float4 *>(sc + h * cu + 16 * c);
                     const F2 s01 = bsfp8_f2(s.x, s.y), s23 = bsfp8_f2(s.z, s.w);
-                    F2 *to = tot + h * (CU / 2) + W / 2 * i + 8 * c;
+                    F2 *to = tot + h * (CU / 2) + 8 * c;
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -660,7 +675,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         }
                 }
             };
-            blocks(std::false_type(), load, begin, add);
+            if constexpr (PAIR) {
+                if (nu == 2) blocks(std::integral_constant<int, 2>(), load, begin, add);
+                else blocks(std::integral_constant<int, 1>(), load, begin, add);
+            } else {
+                blocks(std::integral_constant<int, 1>(), load, begin, add);
+            }
             if (!ok) break;
             const int n0 = x.p0 + quad * 32;
             if (cs > 1) {
