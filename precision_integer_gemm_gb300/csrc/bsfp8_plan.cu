@@ -21,6 +21,8 @@ bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Pl
     double groups = 1.0;
     if (c.offsets) groups = c.experts * (1.0 - std::pow(1.0 - 1.0 / c.experts, double(c.rows)));
     const double typical = std::max(1.0, c.rows / groups);
+    // where rows of C start
+    const uintptr_t rows_at = reinterpret_cast<uintptr_t>(c.C) | uintptr_t(c.N) * (c.c_type == 0 ? 4 : 2);
     double best = -1;
     const auto consider = [&](int bn, bool pair, int cs) {
         const int per = (steps + cs - 1) / cs;
@@ -34,8 +36,9 @@ bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Pl
         const double tiles = p_tiles * q_tiles * groups;
         const double compute = pair ? (rows <= 128 ? 1.6 : 1.8) : bn == 128 ? 1.47 : bn == 64 ? 0.92 : bn == 32 ? 0.86 : 0.83;
         const double split = cs == 1 ? 0.0 : bn == 128 ? 7.0 : bn == 64 ? 2.1 + 0.15 * cs : bn == 32 ? 1.8 + 0.2 * cs : 0.4 + 0.1 * cs;
-        // (a lane's row of C in narrow pieces: float32 tiles of pairs take longer to leave)
-        const double tile = !pair ? 0.5 : c.c_type == 0 ? 8.0 : 3.2;
+        // (pairs: a lane's row of C, in pieces of 16 bytes at most)
+        const bool wide = c.c_type != 0 && rows_at % 16 == 0;
+        const double tile = !pair ? 0.5 : wide ? 3.2 : 8.0;
         // a wave of n clusters: they read the weights of n / q_tiles tiles
         const auto wave = [&](double n) {
             const double weights = n * (pair ? 2 : cs) / std::min(q_tiles, n) * 128 * 512;
@@ -53,7 +56,8 @@ bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Pl
         if (typical > 16 * bn) continue;
         for (int cs = 1; cs <= 4; cs *= 2) consider(bn, false, cs);
     }
-    if (typical > 64) consider(256, true, 1);
+    // (not with rows of C that only 2-byte pieces reach, a lane a row)
+    if (typical > 64 && rows_at % 4 == 0) consider(256, true, 1);
     if (best < 0) consider(128, false, 1);  // (no pairs, and more rows than the loop above takes)
     if (best < 0) return false;
     const int64_t p_tiles = (c.N + (plan->pair ? 255 : 127)) / (plan->pair ? 256 : 128);

@@ -119,10 +119,6 @@ static int launch_bsfp8_cfg(const Bsfp8Call &c, const Bsfp8Plan &plan, cudaStrea
     const uintptr_t rows_at = reinterpret_cast<uintptr_t>(c.C) | (static_cast<uintptr_t>(c.N) * (c.c_type == kOutF32 ? 4 : 2));
     prm.store_bytes = rows_at % 16 == 0 ? 16 : rows_at % 8 == 0 ? 8 : rows_at % 4 == 0 ? 4 : 2;
     if (c.c_type != kOutF32 && prm.store_bytes == 8) prm.store_bytes = 4;
-    // from 129 activations on (144 to 224 through 8192 x 8192: 34.7 us, 44.5 with the weights
-    // on the M side); with 2-byte stores a lane a row would take longer than through shared
-    // memory
-    prm.turned = prm.store_bytes >= 4 ? 129 : 257;
     prm.stages = lay.stages;
     prm.off_scales = lay.off_scales;
     prm.off_red = lay.off_red;

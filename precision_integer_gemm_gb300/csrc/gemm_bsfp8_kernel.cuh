@@ -48,7 +48,6 @@ struct Bsfp8Params {
     int slice;             // blocks of 128 k per CTA of such a cluster (a multiple of 4)
     int stream;            // single CTAs: the weights leave L2 first
     int format;            // 0 e4m3, 1 e5m2
-    int turned;            // CTA pairs: activations from which on a tile has them on the M side
     int stages;            // ring slots of codes, even
     int store_bytes;       // of C at once (16, 8, 4 or 2), as the alignment of its rows allows
     int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
@@ -95,19 +94,14 @@ struct Bsfp8Cfg {
     static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
     static_assert(kTurns % 2 == 0, "an accumulator belongs to one of the two issuing warps");
     static_assert(!PAIR || BN == 256, "the pair form is built for 256 activation rows");
-    static_assert(CU % 16 == 0, "whole loads");
+    static_assert(CU == 16 || CU == 32 || CU == 64, "whole loads");
     static_assert(EW * 8 * 16 <= kStoreBytes, "notices of a split k");
 
-    // A tile's accumulators, their columns (whole MMA columns that the epilogue's parts
-    // share evenly in 16s) and each part's columns of one.
-    __device__ static int units(int nq) { return kUnits == 2 && nq > UN ? 2 : 1; }
-    __device__ static int columns(int nq)
-    {
-        const int step = 16 * kParts, n = units(nq) == 2 ? (nq + 1) / 2 : nq;
-        return (n + step - 1) / step * step;
-    }
-    // Whether a tile's activations are on the M side.
-    __device__ static bool lanes(const Bsfp8Params &prm, int nq) { return PAIR && nq >= prm.turned; }
+    // Whether a tile's activations are on the M side (144 to 224 of them through 8192 x 8192:
+    // 34.7 us, 44.5 on the N side): then a block has two accumulators, else one.
+    __device__ static bool lanes(int nq) { return PAIR && nq > UN; }
+    // On the N side: columns of an accumulator that the epilogue's parts share evenly in 16s.
+    __device__ static int columns(int nq) { return (nq + 16 * kParts - 1) / (16 * kParts) * (16 * kParts); }
 };
 
 // Tile t: group by binary search over the first tiles; whole tiles of qt activation rows
@@ -340,7 +334,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             for (int t = cid; ok && t < tiles; t += ncl) {
                 const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
                 // activation rows that this CTA loads (pair: half of the tile's)
-                const int mine = !PAIR ? x.nq : Cfg::lanes(prm, x.nq) ? 128 : Cfg::units(x.nq) * Cfg::columns(x.nq) / 2;
+                const int mine = !PAIR ? x.nq : Cfg::lanes(x.nq) ? 128 : Cfg::columns(x.nq) / 2;
                 const bool small = Cfg::kQRows < Cfg::kQBox && mine <= 2 * Cfg::kQRows;
                 const bool two = small && mine > Cfg::kQRows;
                 const int py = x.e * prm.N + x.p0, qy = x.q0 + pr * mine;
@@ -416,7 +410,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 for (int i = 0; i < SS - 1 && ok && lt < tiles; ++i) load();
                 for (int t = cid; ok && t < tiles; t += ncl) {
                     const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
-                    const bool lanes = Cfg::lanes(prm, x.nq);
+                    const bool lanes = Cfg::lanes(x.nq);
                     for (int b = b0; ok && b < b1; b += 4) {
                         ok = fp4_warp_wait(&s_raw[sr.slot], sr.phase, wd);
                         if (!ok) break;
@@ -462,14 +456,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             bool ok = true;
             for (int t = cid; ok && t < tiles; t += ncl) {
                 const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
-                const bool lanes = Cfg::lanes(prm, x.nq);
-                const int nu = lanes ? Cfg::kUnits : Cfg::units(x.nq), cols = lanes ? Cfg::UN : Cfg::columns(x.nq);
+                const bool lanes = Cfg::lanes(x.nq);
+                const int cols = lanes ? Cfg::UN : Cfg::columns(x.nq);
                 const uint32_t idesc = idesc_f8_f32(128 * Cfg::CL, static_cast<uint32_t>(cols), fmt);
                 // the second accumulator: the other half of each CTA's rows on the N side
-                const uint64_t half = nu == 2 ? static_cast<uint64_t>(me * (cols / 2 * 128 >> 4)) : 0;
+                const uint64_t half = lanes ? static_cast<uint64_t>(me * (64 * 128 >> 4)) : 0;
                 for (int b = b0; b < b1; ++b) {
-                    const bool mine = nu == 2 || (b & 1) == me;
-                    const uint32_t pb = nu == 2 ? 2 * (b & 1) + me : b % PB;
+                    const bool mine = lanes || (b & 1) == me;
+                    const uint32_t pb = lanes ? 2 * (b & 1) + me : b % PB;
                     if (PAIR && !mine) {
                         // the slot's other arrival, in its turn
                         ok = fp4_warp_wait(&full[cr.slot], cr.phase, wd);
@@ -531,11 +525,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         bool ok = true;
         for (int t = cid; t < tiles; t += ncl, ++n) {
             const Fp4Tile x = bsfp8_tile<Cfg>(prm, groups, t, pr);
-            const bool lanes = Cfg::lanes(prm, x.nq);
-            // this warp's columns of an accumulator, and of the tile from c0 on
-            const int nu = Cfg::units(x.nq);
-            const int cu = (lanes ? Cfg::UN : Cfg::columns(x.nq)) / Cfg::kParts, c0 = part * nu * cu;
-            const int cols = min(x.nq - c0, nu * cu);
+            const bool lanes = Cfg::lanes(x.nq);
+            // this warp's columns of an accumulator (activations on the N side: of the tile)
+            const int cu = (lanes ? Cfg::UN : Cfg::columns(x.nq)) / Cfg::kParts, c0 = part * cu;
+            const int cols = min(x.nq - c0, cu);
             const uint32_t tpart = trow + part * cu;
             // The blocks of the tile, an accumulator at a time: load(address, to) brings all its
             // columns of this warp to registers, it is released, and add(begin(scales, block),
@@ -648,39 +641,36 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             }
             // 16 columns of fragments at a time.  Pairs of totals: 16 columns (8 i), lanes
             // 0-15 and 16-31 (4 e), column octet (2 j), row octet (o).
-            F2 tot[PC / 2];
+            F2 tot[CU / 2];
 #pragma unroll
-            for (int i = 0; i < PC / 2; ++i) tot[i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < CU / 2; ++i) tot[i] = make_float2(0.0f, 0.0f);
             const auto load = [&](uint32_t at, uint32_t(&to)[CU]) {
 #pragma unroll
-                for (int c = 0; c < CU / 16; ++c) {
-                    tmem_ld_16x256b_x2(at + 16 * c, to + 16 * c);
-                    tmem_ld_16x256b_x2(at + (16u << 16) + 16 * c, to + 16 * c + 8);
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t from = at + (static_cast<uint32_t>(16 * e) << 16);
+                    if constexpr (CU == 64) tmem_ld_16x256b_x8(from, to + e * (CU / 2));
+                    else if constexpr (CU == 32) tmem_ld_16x256b_x4(from, to + e * (CU / 2));
+                    else tmem_ld_16x256b_x2(from, to + e * (CU / 2));
                 }
             };
             const auto begin = [&](const float *sc, int kb) { return sc + kb * BN + c0 + 4 * q4; };
-            const auto add = [&](const float *sc, int h, const uint32_t(&v)[CU]) {
+            const auto add = [&](const float *sc, int, const uint32_t(&v)[CU]) {
 #pragma unroll
                 for (int c = 0; c < CU / 16; ++c) {
-                    const float4 s = *reinterpret_cast<const float4 *>(sc + h * cu + 16 * c);
+                    const float4 s = *reinterpret_cast<const float4 *>(sc + 16 * c);
                     const F2 s01 = bsfp8_f2(s.x, s.y), s23 = bsfp8_f2(s.z, s.w);
-                    F2 *to = tot + h * (CU / 2) + 8 * c;
+                    F2 *to = tot + 8 * c;
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int o = 0; o < 2; ++o) {
-                            const int at = e * 8 + 16 * c + 2 * o;
+                            const int at = e * (CU / 2) + 8 * c + 2 * o;
                             bsfp8_fma2(to[4 * e + o], v[at], v[at + 1], s01);
                             bsfp8_fma2(to[4 * e + 2 + o], v[at + 4], v[at + 5], s23);
                         }
                 }
             };
-            if constexpr (PAIR) {
-                if (nu == 2) blocks(std::integral_constant<int, 2>(), load, begin, add);
-                else blocks(std::integral_constant<int, 1>(), load, begin, add);
-            } else {
-                blocks(std::integral_constant<int, 1>(), load, begin, add);
-            }
+            blocks(std::integral_constant<int, 1>(), load, begin, add);
             if (!ok) break;
             const int n0 = x.p0 + quad * 32;
             if (cs > 1) {
@@ -688,7 +678,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 // rank order (fixed, whatever arrives first).  An octet's 16 columns are 16
                 // bytes a lane, at [sender][warp][(16 columns, octet of the owner)][lane].
                 const int per = 4 / cs;               // octets of an owner
-                constexpr int C16 = PC / 16;
+                constexpr int C16 = CU / 16;
                 const int units = C16 * per;
                 uint4 *buf = reinterpret_cast<uint4 *>(smem + prm.off_red) + lane;
                 const uint32_t ph = n & 1u;
@@ -752,9 +742,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 float *to = static_cast<float *>(prm.C) + (static_cast<int64_t>(x.q0) + c0 + 2 * q4) * prm.N + n0 +
                             (lane >> 2);
 #pragma unroll
-                for (int c = 0; c < PC / 8; ++c) {
-                    const int in = 8 * (c % (CU / 8)), col = c / (CU / 8) * cu + in;  // in its accumulator, in the tile
-                    if (in >= cu) continue;
+                for (int c = 0; c < CU / 8; ++c) {
+                    const int col = 8 * c;
 #pragma unroll
                     for (int o = 0; o < 4; ++o) {
                         const F2 v = tot[8 * (c >> 1) + 4 * (o >> 1) + 2 * (c & 1) + (o & 1)];
@@ -767,9 +756,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < PC; c += 32) {
-                    const int in = c % CU, col = c / CU * cu + in;
-                    if (in < cu && col < cols) {
+                for (int c = 0; c < CU; c += 32) {
+                    if (c < cols) {
                         uint32_t v[2][16];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -777,13 +765,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                             for (int j = 0; j < 8; ++j) {
                                 // (fragments: lanes 0-15 and 16-31, column octet, row octet)
                                 const int from = c / 2 + 8 * i + j;
-                                const bool there = c + 16 * i < PC;
+                                const bool there = c + 16 * i < CU;
                                 const F2 w = there ? tot[there ? from : 0] : make_float2(0.0f, 0.0f);
                                 v[i][2 * j] = bsfp8_lo(w);
                                 v[i][2 * j + 1] = bsfp8_hi(w);
                             }
-                        fp4_store32_cols<false>(prm, v, 1.0f, static_cast<int64_t>(x.q0) + c0 + col,
-                                                min(cu - in, cols - col), n0, stage);
+                        fp4_store32_cols<false>(prm, v, 1.0f, static_cast<int64_t>(x.q0) + c0 + c, cols - c, n0, stage);
                     }
                 }
             }
@@ -797,7 +784,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             };
             if (n > 0) drain(&red_empty[warp], (n - 1) & 1u);
             if (lane == 0 && n >= armed)
-                mbar_arrive_expect_tx(&red_full[warp], static_cast<uint32_t>((cs - 1) * (PC / 16) * (4 / cs) * 512));
+                mbar_arrive_expect_tx(&red_full[warp], static_cast<uint32_t>((cs - 1) * (CU / 16) * (4 / cs) * 512));
             drain(&red_full[warp], n & 1u);
         }
     }
