@@ -50,6 +50,7 @@ struct Bsfp8Params {
     int format;            // 0 e4m3, 1 e5m2
     int stages;            // ring slots of codes, even
     int store_bytes;       // of C at once (16, 8, 4 or 2), as the alignment of its rows allows
+    int wide;              // rows of C start on 32 bytes
     int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
     int *status;
     unsigned long long limit_ns;
@@ -594,7 +595,18 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                     const int left = prm.N - nb;
                     if (prm.c_type == kOutF32) {
                         float *to = static_cast<float *>(prm.C) + at;
-                        if (prm.store_bytes == 16) {
+                        if (prm.wide) {
+#pragma unroll
+                            for (int j = 0; j < PC / 8; ++j) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    w[2 * i] = bsfp8_lo(tot[4 * j + i]);
+                                    w[2 * i + 1] = bsfp8_hi(tot[4 * j + i]);
+                                }
+                                if (8 * j < left) st_v8(to + 8 * j, w);
+                            }
+                        } else if (prm.store_bytes == 16) {
 #pragma unroll
                             for (int j = 0; j < PC / 4; ++j)
                                 if (4 * j < left)
@@ -615,24 +627,30 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                         uint16_t *to = static_cast<uint16_t *>(prm.C) + at;
                         const bool bf16 = prm.c_type == kOutBf16;
 #pragma unroll
-                        for (int j = 0; j < PC / 8; ++j) {
-                            uint32_t w[4];
+                        for (int j = 0; j < PC / 16; ++j) {
+                            uint32_t w[8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < 8; ++i) {
                                 if (bf16) {
-                                    const __nv_bfloat162 h = __floats2bfloat162_rn(tot[4 * j + i].x, tot[4 * j + i].y);
+                                    const __nv_bfloat162 h = __floats2bfloat162_rn(tot[8 * j + i].x, tot[8 * j + i].y);
                                     w[i] = *reinterpret_cast<const uint32_t *>(&h);
                                 } else {
-                                    const __half2 h = __floats2half2_rn(tot[4 * j + i].x, tot[4 * j + i].y);
+                                    const __half2 h = __floats2half2_rn(tot[8 * j + i].x, tot[8 * j + i].y);
                                     w[i] = *reinterpret_cast<const uint32_t *>(&h);
                                 }
                             }
-                            if (prm.store_bytes == 16) {  // (N is a multiple of 8)
-                                if (8 * j < left) *reinterpret_cast<uint4 *>(to + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (prm.wide) {  // (N is a multiple of 16)
+                                if (16 * j < left) st_v8(to + 16 * j, w);
+                            } else if (prm.store_bytes == 16) {  // (of 8)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (16 * j + 8 * i < left)
+                                        *reinterpret_cast<uint4 *>(to + 16 * j + 8 * i) =
+                                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                             } else {  // (of 2)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (8 * j + 2 * i < left) *reinterpret_cast<uint32_t *>(to + 8 * j + 2 * i) = w[i];
+                                for (int i = 0; i < 8; ++i)
+                                    if (16 * j + 2 * i < left) *reinterpret_cast<uint32_t *>(to + 16 * j + 2 * i) = w[i];
                             }
                         }
                     }

@@ -350,6 +350,14 @@ __device__ __forceinline__ void ld_once(T &to, const void *p)
     }
 }
 
+// 32 bytes at once (32-byte aligned).
+__device__ __forceinline__ void st_v8(void *to, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // `bytes` (a multiple of 16) of this CTA's shared memory into another CTA of the
 // cluster; they count on that CTA's mbarrier `bar_cluster`, and their completion
 // releases at cluster scope what came before the copy.
