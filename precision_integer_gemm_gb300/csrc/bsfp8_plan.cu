@@ -7,8 +7,8 @@ namespace igemm {
 
 // Kernel, tile and split by estimated time in microseconds: 4.5 for the start, then every
 // wave of tiles its groups of 512 k and what a tile costs besides.  A group takes an SM
-// 0.83 with tiles of 16 activations, 0.86 with 32, 0.92 with 64, 1.47 with 128, a CTA pair
-// 1.6 (up to 128) or 1.8, or what HBM takes to bring the weights of all SMs at work, 6.3 MB
+// 0.83 with tiles of 16 activations, 0.86 with 32, 0.92 with 64, 1.55 with 128, a CTA pair
+// 1.6 (up to 128) or 1.75, or what HBM takes to bring the weights of all SMs at work, 6.3 MB
 // a microsecond.  A split of k over two or four CTAs adds up to 2.7, with 64 activations
 // or more to every wave (7 with 128).  (4096 x 4096 weights and 16 activations: 11.3 whole, 8.7 on two, 8.3 on
 // four; 64: 12.1, 10.7, 9.9; 128 activations as two tiles of 64: 12.3, as one 16.0; 8192 x
@@ -34,11 +34,12 @@ bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Pl
         const double q_tiles = c.offsets && typical > bn ? typical / bn + 0.5 : std::ceil(typical / bn);
         const double rows = std::min(typical / q_tiles, double(bn));
         const double tiles = p_tiles * q_tiles * groups;
-        const double compute = pair ? (rows <= 128 ? 1.6 : 1.8) : bn == 128 ? 1.47 : bn == 64 ? 0.92 : bn == 32 ? 0.86 : 0.83;
+        const double compute = pair ? (rows <= 128 ? 1.6 : 1.75) : bn == 128 ? 1.55 : bn == 64 ? 0.92 : bn == 32 ? 0.86 : 0.83;
         const double split = cs == 1 ? 0.0 : bn == 128 ? 7.0 : bn == 64 ? 2.1 + 0.15 * cs : bn == 32 ? 1.8 + 0.2 * cs : 0.4 + 0.1 * cs;
-        // (pairs: a lane's row of C, in pieces of 16 bytes at most)
-        const bool wide = c.c_type != 0 && rows_at % 16 == 0;
-        const double tile = !pair ? 0.5 : wide ? 3.2 : 8.0;
+        // (pairs: a lane's row of C, straight from registers or through shared memory)
+        const double tile = pair        ? 2.4 + (c.c_type == 0 ? 0.6 : 0.0) + (rows_at % 32 == 0 ? 0.0 : 0.8)
+                            : bn == 128 ? (c.c_type == 0 ? 1.5 : 0.8)
+                                        : 0.5;
         // a wave of n clusters: they read the weights of n / q_tiles tiles
         const auto wave = [&](double n) {
             const double weights = n * (pair ? 2 : cs) / std::min(q_tiles, n) * 128 * 512;

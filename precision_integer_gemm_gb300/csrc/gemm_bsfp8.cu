@@ -117,9 +117,8 @@ static int launch_bsfp8_cfg(const Bsfp8Call &c, const Bsfp8Plan &plan, cudaStrea
     prm.stream = !Cfg::PAIR && plan.groups * c.N * double(pitch) >= 24.0 * (1 << 20);
     prm.format = c.format;
     const uintptr_t rows_at = reinterpret_cast<uintptr_t>(c.C) | (static_cast<uintptr_t>(c.N) * (c.c_type == kOutF32 ? 4 : 2));
-    prm.store_bytes = rows_at % 16 == 0 ? 16 : rows_at % 8 == 0 ? 8 : rows_at % 4 == 0 ? 4 : 2;
+    prm.store_bytes = rows_at % 16 == 0 ? 16 : rows_at % 4 == 0 ? 4 : 2;
     prm.wide = rows_at % 32 == 0;
-    if (c.c_type != kOutF32 && prm.store_bytes == 8) prm.store_bytes = 4;
     prm.stages = lay.stages;
     prm.off_scales = lay.off_scales;
     prm.off_red = lay.off_red;

@@ -49,7 +49,7 @@ struct Bsfp8Params {
     int stream;            // single CTAs: the weights leave L2 first
     int format;            // 0 e4m3, 1 e5m2
     int stages;            // ring slots of codes, even
-    int store_bytes;       // of C at once (16, 8, 4 or 2), as the alignment of its rows allows
+    int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
     int wide;              // rows of C start on 32 bytes
     int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
     int *status;
@@ -588,71 +588,66 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 };
                 blocks(std::integral_constant<int, 2>(), load, begin, add);
                 if (!ok) break;
-                // a lane's row of 128 columns
-                const int nb = x.p0 - 128 * pr + part * 128, in = rank * 128 + quad * 32 + lane;
-                if (in < x.nq) {
-                    const int64_t at = (static_cast<int64_t>(x.q0) + in) * prm.N + nb;
-                    const int left = prm.N - nb;
-                    if (prm.c_type == kOutF32) {
-                        float *to = static_cast<float *>(prm.C) + at;
-                        if (prm.wide) {
+                // A lane's row of 128 columns, 16 words at a time: as two stores of 32 bytes, or,
+                // where rows of C start elsewhere, through shared memory (64-byte rows, 16-byte
+                // chunk c of row r at c ^ (r / 2 % 4)) to leave as 64 contiguous bytes of two rows.
+                const int nb = x.p0 - 128 * pr + part * 128, r0 = rank * 128 + quad * 32;
+                const bool f32 = prm.c_type == kOutF32, bf16 = prm.c_type == kOutBf16;
+                const int row_words = f32 ? prm.N : prm.N / 2;  // (N is even)
+                const int64_t at = (static_cast<int64_t>(x.q0) + r0) * row_words + (f32 ? nb : nb / 2);
+                uint32_t *to = static_cast<uint32_t *>(prm.C) + at;
+                const int left = row_words - (f32 ? nb : nb / 2), rows = x.nq - r0;
+                const auto leave = [&](int word, const uint32_t(&w)[16]) {
+                    if (word >= left) return;  // (the same in every lane)
+                    if (prm.wide) {
+                        if (lane < rows) {
+                            uint32_t *from = to + static_cast<int64_t>(lane) * row_words + word;
+                            st_v8(from, reinterpret_cast<const uint32_t(&)[8]>(w[0]));
+                            if (word + 8 < left) st_v8(from + 8, reinterpret_cast<const uint32_t(&)[8]>(w[8]));
+                        }
+                        return;
+                    }
 #pragma unroll
-                            for (int j = 0; j < PC / 8; ++j) {
-                                uint32_t w[8];
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) =
+                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                    __syncwarp();
+                    const int c = lane & 15;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    w[2 * i] = bsfp8_lo(tot[4 * j + i]);
-                                    w[2 * i + 1] = bsfp8_hi(tot[4 * j + i]);
-                                }
-                                if (8 * j < left) st_v8(to + 8 * j, w);
-                            }
-                        } else if (prm.store_bytes == 16) {
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 2 * i + (lane >> 4);
+                        const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                            stage + r * 64 + (((c >> 2) ^ (r >> 1 & 3)) << 4) + (c & 3) * 4);
+                        if (r < rows && word + c < left) to[static_cast<int64_t>(r) * row_words + word + c] = v;
+                    }
+                    __syncwarp();  // read before the next words overwrite them
+                };
+                if (f32) {
 #pragma unroll
-                            for (int j = 0; j < PC / 4; ++j)
-                                if (4 * j < left)
-                                    *reinterpret_cast<float4 *>(to + 4 * j) =
-                                        make_float4(tot[2 * j].x, tot[2 * j].y, tot[2 * j + 1].x, tot[2 * j + 1].y);
-                        } else if (prm.store_bytes == 8) {  // (N is even)
+                    for (int j = 0; j < PC; j += 16) {
+                        uint32_t w[16];
 #pragma unroll
-                            for (int j = 0; j < PC / 2; ++j)
-                                if (2 * j < left) *reinterpret_cast<float2 *>(to + 2 * j) = tot[j];
-                        } else {
+                        for (int i = 0; i < 8; ++i) {
+                            w[2 * i] = bsfp8_lo(tot[j / 2 + i]);
+                            w[2 * i + 1] = bsfp8_hi(tot[j / 2 + i]);
+                        }
+                        leave(j, w);
+                    }
+                } else {
 #pragma unroll
-                            for (int j = 0; j < PC / 2; ++j) {
-                                if (2 * j < left) to[2 * j] = tot[j].x;
-                                if (2 * j + 1 < left) to[2 * j + 1] = tot[j].y;
+                    for (int j = 0; j < PC / 2; j += 16) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (bf16) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(tot[j + i].x, tot[j + i].y);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                            } else {
+                                const __half2 h = __floats2half2_rn(tot[j + i].x, tot[j + i].y);
+                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
                             }
                         }
-                    } else {
-                        uint16_t *to = static_cast<uint16_t *>(prm.C) + at;
-                        const bool bf16 = prm.c_type == kOutBf16;
-#pragma unroll
-                        for (int j = 0; j < PC / 16; ++j) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if (bf16) {
-                                    const __nv_bfloat162 h = __floats2bfloat162_rn(tot[8 * j + i].x, tot[8 * j + i].y);
-                                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                                } else {
-                                    const __half2 h = __floats2half2_rn(tot[8 * j + i].x, tot[8 * j + i].y);
-                                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                                }
-                            }
-                            if (prm.wide) {  // (N is a multiple of 16)
-                                if (16 * j < left) st_v8(to + 16 * j, w);
-                            } else if (prm.store_bytes == 16) {  // (of 8)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i)
-                                    if (16 * j + 8 * i < left)
-                                        *reinterpret_cast<uint4 *>(to + 16 * j + 8 * i) =
-                                            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                            } else {  // (of 2)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    if (16 * j + 2 * i < left) *reinterpret_cast<uint32_t *>(to + 16 * j + 2 * i) = w[i];
-                            }
-                        }
+                        leave(j, w);
                     }
                 }
                 continue;
