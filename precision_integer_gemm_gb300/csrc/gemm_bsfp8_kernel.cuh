@@ -666,11 +666,21 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                     else tmem_ld_16x256b_x2(from, to + e * (CU / 2));
                 }
             };
-            const auto begin = [&](const float *sc, int kb) { return sc + kb * BN + c0 + 4 * q4; };
-            const auto add = [&](const float *sc, int, const uint32_t(&v)[CU]) {
+            // (read before the wait for the partial sums)
+            struct Scales {
+                float4 of[CU / 16];
+            };
+            const auto begin = [&](const float *sc, int kb) {
+                Scales s;
+                const float *from = sc + kb * BN + c0 + 4 * q4;
+#pragma unroll
+                for (int c = 0; c < CU / 16; ++c) s.of[c] = *reinterpret_cast<const float4 *>(from + 16 * c);
+                return s;
+            };
+            const auto add = [&](const Scales &sc, int, const uint32_t(&v)[CU]) {
 #pragma unroll
                 for (int c = 0; c < CU / 16; ++c) {
-                    const float4 s = *reinterpret_cast<const float4 *>(sc + 16 * c);
+                    const float4 s = sc.of[c];
                     const F2 s01 = bsfp8_f2(s.x, s.y), s23 = bsfp8_f2(s.z, s.w);
                     F2 *to = tot + 8 * c;
 #pragma unroll
