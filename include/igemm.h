@@ -477,7 +477,8 @@ IGEMM_API int igemm_moe_route(const void *logits, int logits_type, int32_t *expe
  *   weights  [T, k] float32: scale * s, over the sum of the chosen s with normalize != 0; 0
  *            where experts is -1
  * The choice is that of the scores in 64 bits, equal ones the lowest expert (group) first;
- * without a bias experts are compared by their logits, whose order is that of the scores.
+ * without a bias (null, or E zeros) experts are compared by their logits, whose order is that
+ * of the scores, so that scores which round to the same number keep it.
  * E <= 1024, k <= 32, groups <= 32, E a multiple of groups, 1 <= group_k <= groups, group_top
  * 1 or 2, k <= group_k E / groups, T * k < 2^31 (IGEMM_UNSUPPORTED_SHAPE).  T == 0 or k == 0
  * zeroes offsets.  Launches and workspace as for igemm_moe_route.

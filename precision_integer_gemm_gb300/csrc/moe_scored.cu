@@ -12,7 +12,9 @@
 // at the border between taken and left (one token in ten thousand).  (The 64-bit pipe is
 // slow: a token's 256 scores take a warp 40 us, one a lane 2.)  A token with more of them
 // than a warp has lanes is done again as a whole, after the block's others.  Without a bias
-// the scores are in the order of the logits, which are compared as they are.
+// (none given, or zeros, as before the first step of a training) the scores are in the order
+// of the logits, which are compared as they are; a group's two largest then are those of its
+// logits, and scores are told apart by their relative error.
 //
 // A warp per token, a lane E / 32 neighbouring experts, so that a group is a run of lanes
 // and the first lane with the largest value holds the lowest expert.  From the choices to
@@ -112,7 +114,7 @@ __device__ __noinline__ double scored_sum_64(const ScoredParams &p, const T *row
 
 // The whole choice in 64 bits: lane i's expert, -1 where none is left.
 template <class T, int VPL>
-__device__ __noinline__ int scored_choose_64(const ScoredParams &p, const T *row)
+__device__ __noinline__ int scored_choose_64(const ScoredParams &p, const T *row, bool biased)
 {
     const int lane = threadIdx.x & 31, e0 = lane * VPL;
     uint64_t c[VPL], s[VPL];  // what experts and groups are chosen by
@@ -127,8 +129,8 @@ __device__ __noinline__ int scored_choose_64(const ScoredParams &p, const T *row
         if (x > -CUDART_INF_F) {
             const double v = scored_c_64(p, x, e0 + j, m, sum);
             const uint64_t k = v == v ? scored_key(v) : kKey64None;
-            c[j] = p.bias ? k : scored_key(x);
-            s[j] = p.bias || p.two ? k : c[j];
+            c[j] = biased ? k : scored_key(x);
+            s[j] = biased || p.two ? k : c[j];
         }
     }
     if (p.groups > 1) {
@@ -249,6 +251,10 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
     float bias[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) bias[j] = sp.bias && e0 + j < p.E ? sp.bias[e0 + j] : 0.0f;
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) any |= bias[j] != 0.0f;
+    const bool biased = __any_sync(0xffffffffu, any);
     __syncthreads();
     const int t0 = blockIdx.x * p.tb;
     const int mine = min(p.tb, p.T - t0);  // (t0 + tb may pass 2^31)
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
     // groups of whole lanes, a power of two of them
     const int lanes = sp.per / VPL;
     const bool runs = sp.per % VPL == 0 && (lanes & (lanes - 1)) == 0;
-    const bool scores = sp.bias || (grouped && sp.two);  // every expert's is needed
+    const bool scores = biased || (grouped && sp.two);  // every expert's is needed
     // The weights of token i's choice, lane n's expert my_e; m and sum: softmax over all experts.
     const auto finish = [&](int i, const T *row, int my_e, float m, float sum) {
         const int64_t t = t0 + i;
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 s[j] = !(c[j] > kNone) ? 0.0f : sp.sigmoid ? scored_sigmoid_fast(c[j]) : s[j] * inv;
-                if (sp.bias && c[j] > kNone) {
+                if (biased && c[j] > kNone) {
                     const float v = s[j] + bias[j];
                     c[j] = v > kNone ? v : kNone;  // (not NaN)
                 }
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
                 float a1 = kNone, a2 = kNone;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j)
-                    if (c[j] > kNone) scored_two(a1, a2, sp.two && !sp.bias ? s[j] : c[j]);
+                    if (c[j] > kNone) scored_two(a1, a2, sp.two && !biased ? s[j] : c[j]);
                 for (int d = 1; d < lanes; d <<= 1) {
                     const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
                     scored_two(a1, a2, b1);
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
                     const int from = g * sp.per - e0, to = from + sp.per;
 #pragma unroll
                     for (int j = 0; j < VPL; ++j)
-                        if (j >= from && j < to && c[j] > kNone) scored_two(a1, a2, sp.two && !sp.bias ? s[j] : c[j]);
+                        if (j >= from && j < to && c[j] > kNone) scored_two(a1, a2, sp.two && !biased ? s[j] : c[j]);
 #pragma unroll
                     for (int d = 16; d; d >>= 1) {
                         const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
@@ -379,7 +385,9 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
                 const bool in = taken >> lane & 1u, some = lane < sp.groups && score > kNone;
                 const float least = route_value(__reduce_min_sync(0xffffffffu, in ? route_key(score) : 0xFF800000u));
                 const float most = route_value(__reduce_max_sync(0xffffffffu, in ? kKeyNone : route_key(score)));
-                const float margin = 2.0f * slack + 0x1p-21f * fabsf(least);
+                // (without a bias also by relative errors: two of e^-y, y up to 84, in 143 2^-23)
+                float margin = 2.0f * slack + 0x1p-21f * fabsf(least);
+                if (!biased) margin = fminf(margin, 0x1p-14f * least + 0x1p-119f);
                 if (most > kNone && !(least - most > margin)) {
                     const uint32_t border =
                         __ballot_sync(0xffffffffu, some && (in ? !(score - most > margin) : !(least - score > margin)));
@@ -387,10 +395,27 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
                     uint32_t cand = 0;
                     for (uint32_t open = border; open; open &= open - 1) {
                         const int g = __ffs(open) - 1, from = g * sp.per - e0, to = from + sp.per;
+                        if (!biased) {
+#pragma unroll 1
+                            for (int n = 0; n < 2; ++n) {
+                                float a = kNone;
+                                int at = 0;
+#pragma unroll
+                                for (int j = 0; j < VPL; ++j)
+                                    if (j >= from && j < to && !(cand >> j & 1u) && c[j] > a) {
+                                        a = c[j];
+                                        at = j;
+                                    }
+                                const uint32_t local = route_key(a), top = __reduce_max_sync(0xffffffffu, local);
+                                if (top <= kKeyNone) break;
+                                if (lane == __ffs(__ballot_sync(0xffffffffu, local == top)) - 1) cand |= 1u << at;
+                            }
+                            continue;
+                        }
                         float a1 = kNone, a2 = kNone;
 #pragma unroll
                         for (int j = 0; j < VPL; ++j)
-                            if (j >= from && j < to && c[j] > kNone) scored_two(a1, a2, sp.bias ? c[j] : s[j]);
+                            if (j >= from && j < to && c[j] > kNone) scored_two(a1, a2, c[j]);
 #pragma unroll
                         for (int d = 16; d; d >>= 1) {
                             const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
 #pragma unroll
                         for (int j = 0; j < VPL; ++j)
                             if (j >= from && j < to && c[j] > kNone &&
-                                !(least_of - (sp.bias ? c[j] : s[j]) > slack + 0x1p-22f * fabsf(least_of)))
+                                !(least_of - c[j] > slack + 0x1p-22f * fabsf(least_of)))
                                 cand |= 1u << j;
                     }
                     const double sum64 = sp.sigmoid ? 1.0 : scored_sum_64<T, VPL>(sp, row, m);
@@ -451,7 +476,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
         const auto apart = [&](float a, float b) { return a - b > slack + 0x1p-22f * fabsf(a); };
         for (; top > kKeyNone; ++n) {
             if (n >= p.k) {
-                if (!sp.bias) break;
+                if (!biased) break;
                 if (n == p.k) last = __shfl_sync(0xffffffffu, my_c, p.k - 1);
                 if (apart(last, route_value(top))) break;
                 near |= n == 32;  // (more than the list holds)
@@ -476,7 +501,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
             }
             top = __reduce_max_sync(0xffffffffu, local);
         }
-        if (sp.bias) {
+        if (biased) {
             // neighbours nearer than the rounding, but for those that are equal in both parts
             const float x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
             const float b = my_e >= 0 ? sp.bias[my_e] : 0.0f, v = my_c;
@@ -508,7 +533,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         }
-        finish(i, row, scored_choose_64<T, VPL>(sp, row), m, sum);
+        finish(i, row, scored_choose_64<T, VPL>(sp, row, biased), m, sum);
     }
     overlap_release();
     __syncthreads();

@@ -170,6 +170,26 @@ def test_near_and_equal_scores(score):
         check(coarse.to(torch.bfloat16), b, k, score)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,group_k", [(200, 256, 8, 8, 4), (90, 160, 6, 20, 7), (70, 64, 4, 32, 9), (40, 1024, 8, 8, 2)])
+@pytest.mark.parametrize("spread", [0.0, 4.0, 16.0, 60.0])
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+def test_scores_of_very_different_size(T, E, k, groups, group_k, score, spread, typ):
+    # scores that float32 holds to few bits, not at all (60: e^-300), or as 1, and all equal ones
+    g = torch.Generator(device="cuda").manual_seed(T)
+    logits = (spread * torch.randn((T, E), generator=g, device="cuda")).to(TYPES[typ])
+    for group_top in (1, 2):
+        check(logits, None, k, score, groups, group_k, group_top)
+        with_zeros = route(logits, torch.zeros((E,), device="cuda"), k, score, groups, group_k, group_top)
+        without = route(logits, None, k, score, groups, group_k, group_top)
+        for name in without:
+            assert torch.equal(with_zeros[name], without[name])
+    bias = 0.02 * torch.randn((E,), generator=g, device="cuda")
+    check(logits, bias, k, score, groups, group_k, 2)
+    bias[1:] = 0.0  # one that is not zero: sums as they round
+    check(logits, bias, k, score, groups, group_k, 2)
+
+
 @pytest.mark.parametrize("offset", [1, 3])
 def test_logits_off_16_bytes(offset):
     T, E = 600, 128
