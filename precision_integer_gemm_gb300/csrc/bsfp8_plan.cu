@@ -1,6 +1,7 @@
 // Host only: the kernel, tile and split of a block-scaled fp8 product.
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 #include "bsfp8.cuh"
 
 namespace igemm {
@@ -10,9 +11,10 @@ namespace igemm {
 // 0.83 with tiles of 16 activations, 0.86 with 32, 0.92 with 64, 1.55 with 128, a CTA pair
 // 1.6 (up to 128) or 1.75, or what HBM takes to bring the weights of all SMs at work, 6.3 MB
 // a microsecond.  A split of k over two or four CTAs adds up to 2.7, with 64 activations
-// or more to every wave (7 with 128).  (4096 x 4096 weights and 16 activations: 11.3 whole, 8.7 on two, 8.3 on
-// four; 64: 12.1, 10.7, 9.9; 128 activations as two tiles of 64: 12.3, as one 16.0; 8192 x
-// 8192: 256 activations as two tiles of 128 28, on pairs 34.7; 768: 76 and 68.)
+// or more to every wave (7 with 128).  (4096 x 4096 weights and 16 activations: 11.3 whole,
+// 8.7 on two, 8.3 on four; 64: 12.1, 10.7, 9.9; 128 activations as two tiles of 64: 12.3,
+// as one 16.0; 8192 x 8192: 256 activations as two tiles of 128 28, on pairs 34.7; 768: 76
+// and 68.)
 bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Plan *plan)
 {
     const int steps = (c.K + 511) / 512;

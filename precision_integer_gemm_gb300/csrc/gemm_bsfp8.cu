@@ -18,8 +18,7 @@ struct Bsfp8Smem {
         const int red = cs > 1 ? Cfg::kRedBytes : 0;
         const int tail = Cfg::kTailBytes + 16 * experts;
         const int left = kLimit - red - Cfg::kStoreBytes - Cfg::SS * Cfg::kScaleStage - tail;
-        // (single CTAs: even, a slot belongs to one of the two issuing warps)
-        stages = std::min(left / Cfg::kStage, static_cast<int>(Cfg::kMaxStages)) & ~(Cfg::PAIR ? 0 : 1);
+        stages = std::min(left / Cfg::kStage, static_cast<int>(Cfg::kMaxStages));
         off_scales = stages * Cfg::kStage;
         off_red = off_scales + Cfg::SS * Cfg::kScaleStage;
         off_store = off_red + red;

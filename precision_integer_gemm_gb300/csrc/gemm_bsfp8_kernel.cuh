@@ -48,7 +48,7 @@ struct Bsfp8Params {
     int slice;             // blocks of 128 k per CTA of such a cluster (a multiple of 4)
     int stream;            // single CTAs: the weights leave L2 first
     int format;            // 0 e4m3, 1 e5m2
-    int stages;            // ring slots of codes, even
+    int stages;            // ring slots of codes
     int store_bytes;       // 16-bit C: bytes of a store (16, 4 or 2), as the alignment of its rows allows
     int wide;              // rows of C start on 32 bytes
     int off_scales, off_red, off_store, off_bars;  // shared-memory offsets after the code stages
@@ -85,7 +85,9 @@ struct Bsfp8Cfg {
     static constexpr int kTmemCols = PB * UN;
     static constexpr int kRedBytes = BN <= 128 ? BN * 512 : 0;  // split k: the cluster's partials of this CTA's part
     static constexpr int kStoreBytes = EW * 2048;      // 16-bit C: 32 rows x 32 columns per epilogue warp
-    static constexpr int kMaxStages = 16;
+    // (16 activations: 166 KB of codes on their way to an SM; 16 x 28672 x 8192 with 8, 9, 10
+    // and 11 slots 37.9, 37.6, 38.3 and 39.0 us)
+    static constexpr int kMaxStages = BN == 16 ? 9 : 16;
     static constexpr int kNumBars = 2 * kMaxStages + 3 * SS + 2 * PB + 2 + 2 * EW;
     static constexpr int kBarBytes = (8 * kNumBars + 15) & ~15;
     static constexpr int kTailBytes = kBarBytes + 32;  // and the groups' table, 16 bytes each
@@ -190,7 +192,7 @@ __device__ __forceinline__ uint32_t bsfp8_there(uint32_t bar, uint32_t parity)
 __device__ __forceinline__ bool bsfp8_wait(uint32_t bar, uint32_t parity, uint32_t abort_at, const Bsfp8Params &prm)
 {
     if (__all_sync(0xffffffffu, bsfp8_there(bar, parity))) return true;
-    uint32_t start;  // (microseconds of a clock that wraps: 32 bits of it are enough)
+    uint32_t start;  // (nanoseconds; 32 bits wrap after 4.3 s, and the limit is 4)
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(start));
 #pragma unroll 1
     for (;;) {
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint8_t *scales = smem + prm.off_scales;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + prm.off_bars);
     uint64_t *full = bars;                        // [stages] codes landed (pair: both CTAs', in the even CTA)
-    uint64_t *empty = full + Cfg::kMaxStages;     // [stages] consumed (MMA commit)
+    uint64_t *empty = full + Cfg::kMaxStages;     // [stages] consumed (MMA commit), and seen by the other issuing warp
     uint64_t *s_raw = empty + Cfg::kMaxStages;    // [SS] scale rows landed
     uint64_t *s_full = s_raw + SS;                // [SS] ... turned (scale warp)
     uint64_t *s_empty = s_full + SS;              // [SS] read (epilogue warps)
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     if (warp == Cfg::kWarpLoad) {
         if (lane < prm.stages) {
             mbar_init(&full[lane], 1);
-            mbar_init(&empty[lane], Cfg::kUnits);  // (pairs: both issuing warps' MMAs)
+            mbar_init(&empty[lane], 2);
         }
         if (lane < SS) {
             mbar_init(&s_raw[lane], 1);
@@ -465,11 +467,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 for (int b = b0; b < b1; ++b) {
                     const bool mine = lanes || (b & 1) == me;
                     const uint32_t pb = lanes ? 2 * (b & 1) + me : b % PB;
-                    if (PAIR && !mine) {
-                        // the slot's other arrival, in its turn
+                    if (!mine) {
+                        // The slot's other arrival, in its turn: both warps see every use of a slot, so
+                        // that a wait by parity is never passed by the use before.
                         ok = fp4_warp_wait(&full[cr.slot], cr.phase, wd);
                         if (!ok) break;
-                        if (elect_one()) mma_commit_pair_multicast(&empty[cr.slot], 0x3);
+                        if (elect_one()) {
+                            if constexpr (PAIR) mma_commit_pair_multicast(&empty[cr.slot], 0x3);
+                            else mbar_arrive(&empty[cr.slot]);
+                        }
                         __syncwarp();
                     }
                     if (mine) {

@@ -248,6 +248,34 @@ def test_grouped(counts, typ):
     assert bool((C[:start] == 3).all()) and bool((C[ends[-1]:] == 3).all())
 
 
+@pytest.mark.parametrize("E,each,N,K", [(1024, 70, 256, 640), (700, 20, 384, 1152), (1000, 140, 128, 896)])
+def test_grouped_many_experts(E, each, N, K):
+    # the largest tables of groups (few slots of codes), an odd number of blocks a tile, several tiles a CTA
+    g = torch.Generator(device="cuda").manual_seed(E)
+    counts = torch.randint(0, 2 * each, (E,), generator=g, device="cuda")
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).int()
+    rows = int(offsets[-1])
+    A, SFA, B, SFB = operands(rows, N, K, experts=E)
+    a, at = values(A, SFA, 1, "e4m3", K), offsets.tolist()
+    C = torch.empty((rows, N), dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        C.fill_(math.nan)
+        pig.igemm_bsfp8_grouped(A, B, SFA, SFB, offsets, C, rows, E, N, K)
+        for e in range(0, E, 37):
+            near(C[at[e]:at[e + 1]], a[at[e]:at[e + 1]], values(B[e], SFB[e], 128, "e4m3", K), K)
+
+
+@pytest.mark.parametrize("M,N,K", [(96, 4096, 640), (128, 20000, 4992), (100, 24000, 384), (16, 60000, 896)])
+def test_product_many_tiles_of_odd_blocks(M, N, K):
+    A, SFA, B, SFB = operands(M, N, K)
+    a, b = values(A, SFA, 1, "e4m3", K), values(B[0], SFB[0], 128, "e4m3", K)
+    C = torch.empty((M, N), device="cuda")
+    for _ in range(3):
+        C.fill_(math.nan)
+        pig.igemm_bsfp8(A, B[0], SFA, SFB[0], C, M, N, K)
+        near(C, a, b, K)
+
+
 def test_grouped_offsets_out_of_range():
     # clamped to the rows there are; a group whose end is not past its start is empty
     E, N, K, rows = 4, 128, 256, 50
