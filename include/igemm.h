@@ -277,11 +277,12 @@ IGEMM_API int pack_int4(const int8_t *logical, uint8_t *packed, int64_t rows, in
  * launches one kernel, or two: the preparation pass and the GEMM (prepared
  * codes), the zeroing of C and the GEMM (skinny shapes whose K slices are
  * summed with atomics), the scale transpose and the GEMM (block-scaled fp8);
- * a 4-bit or block-scaled fp8 operator with 128 x 128 scales one, but igemm_moe_route (and
- * igemm_moe_route_scored) two or three above 512 tokens (three
- * where the counts that its blocks would all read pass 4 MB: with
- * b = ceil(T / 64) blocks, 4 b b ceil(E / 4) bytes), and pack_mxfp4, pack_nvfp4 or
- * pack_bsfp8 two where rows are packed once and copied (as stated there).
+ * a 4-bit operator, or one on block-scaled fp8 with 128 x 128 scales, one, but
+ * igemm_moe_route and igemm_moe_route_scored two or three above 512 tokens (three
+ * where the counts that its blocks would all read pass 4 MB: with b blocks
+ * 4 b b ceil(E / 4) bytes; igemm_moe_route has ceil(T / 64) blocks, igemm_moe_route_scored as
+ * many or more), and pack_mxfp4, pack_nvfp4 or pack_bsfp8 two where rows are packed once
+ * and copied (as stated there).
  * The split K of the other paths adds a memset, which is not a kernel.
  */
 IGEMM_API uint64_t igemm_kernels_launched(void);
@@ -552,7 +553,8 @@ IGEMM_API int pack_bsfp8(const void *x, int x_type, int64_t ld, int transposed, 
 
 /*
  * C[m,n] = sum_kb SFA[m,kb] * SFB[n/128,kb] * sum_{k in block kb} a[m,k] * b[n,k], a block's
- * sum from the tensor core in float32, scaled and added in float32 in block order (a
+ * sum from the tensor core in float32, the product of its two scales rounded to float32, the
+ * sum times that added by one float32 fused multiply-add in block order (a
  * long K may be cut into up to four parts whose sums are added in order; repeated calls
  * give the same bits) and rounded once to c_type.
  *   A, SFA  codes and scales (tile_rows 1) of M rows of K; B, SFB (tile_rows 128) of N

@@ -19,6 +19,10 @@
 // A warp per token, a lane E / 32 neighbouring experts, so that a group is a run of lanes
 // and the first lane with the largest value holds the lowest expert.  From the choices to
 // the sorted pairs everything is as without scores (moe_route.cuh).
+//
+// Bound by instructions: 16384 x 256 float32, 8 choices, by sigmoid 24.6 us without bias or
+// groups, 30.2 with a bias, 37.1 with 8 groups by their two best as well (1414 warp
+// instructions a token, issue slots 64 % busy; reading the logits is 2.5 us).
 #include <algorithm>
 #include <math_constants.h>
 #include "launch.cuh"
@@ -602,8 +606,9 @@ __device__ __forceinline__ void scored_out(__half *o, float v) { *o = __float2ha
 //   sigmoids      dx_i = scale u_i sigmoid(-x_i) g_i
 //   softmax       dx_e = scale (sum of the g of e's pairs, times u_e, - p_e sum_j g_j u_j)
 // A warp per token: lane j the pair j, then the row (zeros, or the last line's second part)
-// in runs of V, then the chosen logits' own values over it.  Bound by HBM: the row is
-// written, and read where every logit has a gradient.
+// in runs of V, then the chosen logits' own values over it.  The row is written, and read
+// where every logit has a gradient: 16384 x 256 float32 sigmoids, renormalised, 7 us (17 MB
+// written; the host's time of a call), 10 from a cold cache.
 template <class T, int V>
 __global__ void __launch_bounds__(256) moe_scored_grad_kernel(const T *logits, const int *experts, const float *dweights,
                                                               T *dlogits, int Tn, int E, int k, int sigmoid, int normalize,
