@@ -130,3 +130,29 @@ def test_register_shares_of_the_pair_kernel():
     assert len(inc) == 1 and len(dec) == 1
     launched = re.search(r"attr\.numRegs != (\d+)\) return 0", code_of("gemm_bsfp8.cu"))
     assert 256 * int(inc[0]) + 128 * int(dec[0]) <= 384 * int(launched.group(1))
+
+
+def test_both_issuing_warps_see_every_use_of_a_slot_of_codes():
+    # a wait by parity that skips uses of a slot may be passed by an earlier one
+    code = code_of("gemm_bsfp8_kernel.cuh")
+    assert re.search(r"mbar_init\(&empty\[lane\], 2\);", code)
+    skipped = re.search(r"if \(!mine\) \{(.*?)__syncwarp\(\);", code, flags=re.S).group(1)
+    assert "fp4_warp_wait(&full[cr.slot], cr.phase, wd)" in skipped
+    assert "mma_commit_pair_multicast(&empty[cr.slot], 0x3)" in skipped and "mbar_arrive(&empty[cr.slot])" in skipped
+
+
+def test_plan_without_the_clusters_that_do_not_fit(tmp_path):
+    import shutil
+    import subprocess
+
+    root, cuda = os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "/usr/local/cuda/include"
+    if not shutil.which("g++") or not os.path.isdir(cuda):
+        pytest.skip("g++ or the CUDA headers are missing")
+    exe = str(tmp_path / "bsfp8_plan_check")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", CSRC, "-I", cuda, "-x", "c++",
+                        os.path.join(root, "tests", "c", "bsfp8_plan_check.cpp"), os.path.join(CSRC, "bsfp8_plan.cu"),
+                        "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout[:2000]
+    assert r.stdout.startswith("bsfp8 plan ok")
