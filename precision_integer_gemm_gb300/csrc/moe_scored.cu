@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
     int *start = first + p.E + 1;
     int *chosen = start + p.E;
     __shared__ int again[kTB], again_count;  // tokens to do again
+    __shared__ float2 lists[kScoredThreads / 32][32];  // a warp's candidates: c, expert
     for (int e = threadIdx.x; e < p.E; e += kScoredThreads) mask[e] = make_uint2(0, 0);
     if (threadIdx.x == 0) again_count = 0;
     float bias[VPL];
@@ -455,55 +456,107 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
                 }
             }
         }
-        // A lane's two largest that are not taken, looked for again once both are: few lanes
-        // hold more than two of a token's choices.
-        float a1 = kNone, a2 = kNone;
-        int at1 = 0, at2 = 0, held = 2;
-        uint32_t used = 0;
-        const auto look = [&] {
-            a1 = a2 = kNone;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const float v = used >> j & 1u ? kNone : c[j];
-                const bool first_of = v > a1, second = v > a2;
-                a2 = first_of ? a1 : second ? v : a2;
-                at2 = first_of ? at1 : second ? j : at2;
-                a1 = first_of ? v : a1;
-                at1 = first_of ? j : at1;
-            }
-        };
-        look();
-        // lane n keeps choice n; those left that the last one does not surely exceed join the list
+        // lane n's expert and c by falling c: the k largest and, with a bias, those left that the
+        // last of them does not surely exceed (some more do not matter)
         int my_e = -1, n = 0;
-        float my_c = kNone, last = kNone;
-        uint32_t local = route_key(a1), top = __reduce_max_sync(0xffffffffu, local);
+        float my_c = kNone;
         const auto apart = [&](float a, float b) { return a - b > slack + 0x1p-22f * fabsf(a); };
-        for (; top > kKeyNone; ++n) {
-            if (n >= p.k) {
-                if (!biased) break;
-                if (n == p.k) last = __shfl_sync(0xffffffffu, my_c, p.k - 1);
-                if (apart(last, route_value(top))) break;
-                near |= n == 32;  // (more than the list holds)
-                if (n == 32) break;
+        // The k-th largest of the lanes' largest is at most the k-th largest of all: what is
+        // not below it are the candidates, a few more than k.
+        float most = kNone;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) most = fmaxf(most, c[j]);
+        uint32_t left = route_key(most), least = 0;
+        for (int i = 0; i < p.k; ++i) {
+            least = __reduce_max_sync(0xffffffffu, left);
+            if (least <= kKeyNone) break;
+            left = left == least ? 0 : left;
+        }
+        float cut = least > kKeyNone ? route_value(least) : kNone;
+        if (biased) cut -= slack + 0x1p-22f * fabsf(cut);
+        uint32_t cand = 0;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (c[j] > kNone && !(c[j] < cut)) cand |= 1u << j;
+        int end = __popc(cand);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, end, d);
+            if (lane >= d) end += o;
+        }
+        n = __shfl_sync(0xffffffffu, end, 31);
+        if (n <= 32) {
+            float2 *list = lists[warp];
+            int at = end - __popc(cand);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (cand >> j & 1u) list[at++] = make_float2(c[j], __int_as_float(e0 + j));
+            __syncwarp();
+            const float2 own = lane < n ? list[lane] : make_float2(kNone, 0.0f);
+            int rank = 0;  // (in the order of the experts: of equal ones the first)
+            for (int i = 0; i < n; ++i) {
+                const float other = __shfl_sync(0xffffffffu, own.x, i);
+                rank += other > own.x || (other == own.x && i < lane) ? 1 : 0;
             }
-            const int owner = __ffs(__ballot_sync(0xffffffffu, local == top)) - 1;
-            const int e = owner * VPL + __shfl_sync(0xffffffffu, at1, owner);
-            if (lane == n) {
-                my_e = e;
-                my_c = route_value(top);
+            __syncwarp();
+            if (lane < n) list[rank] = own;
+            __syncwarp();
+            if (lane < n) {
+                my_c = list[lane].x;
+                my_e = __float_as_int(list[lane].y);
             }
-            if (lane == owner) {
-                used |= 1u << at1;
-                if (--held) {
-                    a1 = a2;
-                    at1 = at2;
-                } else {
-                    look();
-                    held = 2;
+            __syncwarp();  // read before the next token's
+        } else {
+            // one at a time
+            n = 0;
+            // A lane's two largest that are not taken, looked for again once both are: few lanes
+            // hold more than two of a token's choices.
+            float a1 = kNone, a2 = kNone;
+            int at1 = 0, at2 = 0, held = 2;
+            uint32_t used = 0;
+            const auto look = [&] {
+                a1 = a2 = kNone;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    const float v = used >> j & 1u ? kNone : c[j];
+                    const bool first_of = v > a1, second = v > a2;
+                    a2 = first_of ? a1 : second ? v : a2;
+                    at2 = first_of ? at1 : second ? j : at2;
+                    a1 = first_of ? v : a1;
+                    at1 = first_of ? j : at1;
                 }
-                local = route_key(a1);
+            };
+            look();
+            // lane n keeps choice n; those left that the last one does not surely exceed join the list
+            float last = kNone;
+            uint32_t local = route_key(a1), top = __reduce_max_sync(0xffffffffu, local);
+            for (; top > kKeyNone; ++n) {
+                if (n >= p.k) {
+                    if (!biased) break;
+                    if (n == p.k) last = __shfl_sync(0xffffffffu, my_c, p.k - 1);
+                    if (apart(last, route_value(top))) break;
+                    near |= n == 32;  // (more than the list holds)
+                    if (n == 32) break;
+                }
+                const int owner = __ffs(__ballot_sync(0xffffffffu, local == top)) - 1;
+                const int e = owner * VPL + __shfl_sync(0xffffffffu, at1, owner);
+                if (lane == n) {
+                    my_e = e;
+                    my_c = route_value(top);
+                }
+                if (lane == owner) {
+                    used |= 1u << at1;
+                    if (--held) {
+                        a1 = a2;
+                        at1 = at2;
+                    } else {
+                        look();
+                        held = 2;
+                    }
+                    local = route_key(a1);
+                }
+                top = __reduce_max_sync(0xffffffffu, local);
             }
-            top = __reduce_max_sync(0xffffffffu, local);
         }
         if (biased) {
             // neighbours nearer than the rounding, but for those that are equal in both parts
@@ -511,7 +564,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
             const float b = my_e >= 0 ? sp.bias[my_e] : 0.0f, v = my_c;
             const float x2 = __shfl_down_sync(0xffffffffu, x, 1), b2 = __shfl_down_sync(0xffffffffu, b, 1);
             const float v2 = __shfl_down_sync(0xffffffffu, v, 1);
-            const bool unsure = lane + 1 < n && !apart(v, v2) && !(x == x2 && b == b2);
+            const bool unsure = lane < p.k && lane + 1 < n && !apart(v, v2) && !(x == x2 && b == b2);
             if (__any_sync(0xffffffffu, unsure)) {
                 const double sum64 = sp.sigmoid ? 1.0 : scored_sum_64<T, VPL>(sp, row, m);
                 my_e = scored_order_64(sp, my_e, x, n, m, sum64);
