@@ -77,6 +77,18 @@ __device__ __forceinline__ void scored_two(F &a1, F &a2, F v)
     a1 = v > a1 ? v : a1;
 }
 
+__device__ __forceinline__ void scored_two(float &a1, float &a2, float v)
+{
+    a2 = fmaxf(a2, fminf(a1, v));
+    a1 = fmaxf(a1, v);
+}
+// ... and two others, b1 >= b2.
+__device__ __forceinline__ void scored_join(float &a1, float &a2, float b1, float b2)
+{
+    a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+    a1 = fmaxf(a1, b1);
+}
+
 // The sum of a group's largest, or of its two largest where there are two.
 __device__ __forceinline__ float scored_group(float a1, float a2, bool two)
 {
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
     };
     constexpr float kNone = -__builtin_huge_valf();
     const RouteParams &p = sp.r;
-    extern __shared__ uint2 mask[];  // [E], then (one cluster) first[E + 1], start[E], experts[kTB * k]
+    extern __shared__ uint2 mask[];  // [E], then first[E + 1], start[E], experts[kTB * k]
     overlap_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = lane * VPL;
     const bool one_cluster = !p.counts && !p.packed_counts;
@@ -250,6 +262,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
     int *start = first + p.E + 1;
     int *chosen = start + p.E;
     __shared__ int again[kTB], again_count;  // tokens to do again
+    __shared__ float2 softmax[kTB];          // a token's largest logit and sum, where weights need them
     __shared__ float2 lists[kScoredThreads / 32][32];  // a warp's candidates: c, expert
     for (int e = threadIdx.x; e < p.E; e += kScoredThreads) mask[e] = make_uint2(0, 0);
     if (threadIdx.x == 0) again_count = 0;
@@ -267,35 +280,42 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
     // groups of whole lanes, a power of two of them
     const int lanes = sp.per / VPL;
     const bool runs = sp.per % VPL == 0 && (lanes & (lanes - 1)) == 0;
+    // up to so many choices the candidates of one search mostly fit a warp's lanes
+    const bool few = p.k <= 16;
     const bool scores = biased || (grouped && sp.two);  // every expert's is needed
-    // The weights of token i's choice, lane n's expert my_e; m and sum: softmax over all experts.
-    const auto finish = [&](int i, const T *row, int my_e, float m, float sum) {
+    constexpr int kWarps = kScoredThreads / 32;
+    // The weights of the chosen of token i (the same in `per` lanes, a power of two).
+    const auto weigh = [&](int i, int per) {
+        const int q = lane & (per - 1);
         const int64_t t = t0 + i;
-        const float x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
+        const bool there = i < mine && q < p.k;
+        const int my_e = there ? chosen[i * p.k + q] : -1;
+        const float x = my_e >= 0 ? scored_logit(static_cast<const T *>(p.logits) + t * p.E, my_e) : kNone;
         // The weight before the scale.  Renormalised ones need no score that could underflow:
         // softmax from the largest chosen logit, sigmoids times e^-min(0, that).
-        float w = 0.0f, total = sum;
+        float w = 0.0f, total = i < mine ? softmax[i].y : 1.0f;
         if (p.normalize) {
-            const float most = route_value(__reduce_max_sync(0xffffffffu, route_key(x)));
+            float most = x;
+            for (int d = per / 2; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
             if (my_e >= 0) {
                 if (!sp.sigmoid) w = expf(x - most);
                 else if (x > 0.0f) w = scored_sigmoid(x);
                 else w = __fdiv_rn(expf(x - fminf(most, 0.0f)), 1.0f + expf(x));
             }
             total = w;
-#pragma unroll
-            for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+            for (int d = per / 2; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
         } else if (my_e >= 0) {
-            w = sp.sigmoid ? scored_sigmoid(x) : expf(x - m);
+            w = sp.sigmoid ? scored_sigmoid(x) : expf(x - softmax[i].x);
         }
-        if (lane < p.k) {
-            p.experts[t * p.k + lane] = my_e;
-            p.weights[t * p.k + lane] = my_e >= 0 ? sp.scale * __fdiv_rn(w, total) : 0.0f;
-            if (one_cluster) chosen[i * p.k + lane] = my_e;
+        if (there) {
+            p.experts[t * p.k + q] = my_e;
+            p.weights[t * p.k + q] = my_e >= 0 ? sp.scale * __fdiv_rn(w, total) : 0.0f;
             if (my_e >= 0) atomicOr(i < 32 ? &mask[my_e].x : &mask[my_e].y, 1u << (i & 31));
         }
     };
-    for (int i = warp; i < mine; i += kScoredThreads / 32) {
+    // a token's at once, or (more than two tokens a warp) after the last one
+    const bool at_once = p.tb <= 2 * kWarps;
+    for (int i = warp; i < mine; i += kWarps) {
         const int64_t t = t0 + i;
         const T *row = static_cast<const T *>(p.logits) + t * p.E;
         float c[VPL], s[VPL];
@@ -357,13 +377,16 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
             float score = kNone;  // of group `lane`
             if (runs) {
                 float a1 = kNone, a2 = kNone;
+                if (sp.two && !biased) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    if (c[j] > kNone) scored_two(a1, a2, sp.two && !biased ? s[j] : c[j]);
+                    for (int j = 0; j < VPL; ++j) scored_two(a1, a2, c[j] > kNone ? s[j] : kNone);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) scored_two(a1, a2, c[j]);
+                }
                 for (int d = 1; d < lanes; d <<= 1) {
                     const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
-                    scored_two(a1, a2, b1);
-                    scored_two(a1, a2, b2);
+                    scored_join(a1, a2, b1, b2);
                 }
                 const float mine_score = scored_group(a1, a2, sp.two);
                 score = __shfl_sync(0xffffffffu, mine_score, (lane * lanes) & 31);
@@ -378,8 +401,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
 #pragma unroll
                     for (int d = 16; d; d >>= 1) {
                         const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
-                        scored_two(a1, a2, b1);
-                        scored_two(a1, a2, b2);
+                        scored_join(a1, a2, b1, b2);
                     }
                     if (lane == g) score = scored_group(a1, a2, sp.two);
                 }
@@ -424,8 +446,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
 #pragma unroll
                         for (int d = 16; d; d >>= 1) {
                             const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
-                            scored_two(a1, a2, b1);
-                            scored_two(a1, a2, b2);
+                            scored_join(a1, a2, b1, b2);
                         }
                         const float least_of = sp.two ? a2 : a1;
 #pragma unroll
@@ -463,28 +484,32 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
         const auto apart = [&](float a, float b) { return a - b > slack + 0x1p-22f * fabsf(a); };
         // The k-th largest of the lanes' largest is at most the k-th largest of all: what is
         // not below it are the candidates, a few more than k.
-        float most = kNone;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) most = fmaxf(most, c[j]);
-        uint32_t left = route_key(most), least = 0;
-        for (int i = 0; i < p.k; ++i) {
-            least = __reduce_max_sync(0xffffffffu, left);
-            if (least <= kKeyNone) break;
-            left = left == least ? 0 : left;
-        }
-        float cut = least > kKeyNone ? route_value(least) : kNone;
-        if (biased) cut -= slack + 0x1p-22f * fabsf(cut);
         uint32_t cand = 0;
+        int end = 0;
+        n = 33;
+        if (few) {
+            float most = kNone;
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-            if (c[j] > kNone && !(c[j] < cut)) cand |= 1u << j;
-        int end = __popc(cand);
+            for (int j = 0; j < VPL; ++j) most = fmaxf(most, c[j]);
+            uint32_t left = route_key(most), least = 0;
+            for (int i = 0; i < p.k; ++i) {
+                least = __reduce_max_sync(0xffffffffu, left);
+                if (least <= kKeyNone) break;
+                left = left == least ? 0 : left;
+            }
+            float cut = least > kKeyNone ? route_value(least) : kNone;
+            if (biased) cut -= slack + 0x1p-22f * fabsf(cut);
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, end, d);
-            if (lane >= d) end += o;
+            for (int j = 0; j < VPL; ++j)
+                if (c[j] > kNone && !(c[j] < cut)) cand |= 1u << j;
+            end = __popc(cand);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, end, d);
+                if (lane >= d) end += o;
+            }
+            n = __shfl_sync(0xffffffffu, end, 31);
         }
-        n = __shfl_sync(0xffffffffu, end, 31);
         if (n <= 32) {
             float2 *list = lists[warp];
             int at = end - __popc(cand);
@@ -574,11 +599,15 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
             if (lane == 0) again[atomicAdd(&again_count, 1)] = i;
             continue;
         }
-        if (lane >= p.k) my_e = -1;
-        finish(i, row, my_e, m, sum);
+        if (lane < p.k) chosen[i * p.k + lane] = my_e;
+        if (lane == 0) softmax[i] = make_float2(m, sum);
+        if (at_once) {
+            __syncwarp();
+            weigh(i, 32);
+        }
     }
     __syncthreads();
-    for (int n = warp; n < again_count; n += kScoredThreads / 32) {
+    for (int n = warp; n < again_count; n += kWarps) {
         const int i = again[n];
         const T *row = static_cast<const T *>(p.logits) + static_cast<int64_t>(t0 + i) * p.E;
         float m = kNone, sum = 1.0f;
@@ -590,7 +619,17 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         }
-        finish(i, row, scored_choose_64<T, VPL>(sp, row, biased), m, sum);
+        const int my_e = scored_choose_64<T, VPL>(sp, row, biased);
+        if (lane < p.k) chosen[i * p.k + lane] = my_e;
+        if (lane == 0) softmax[i] = make_float2(m, sum);
+    }
+    __syncthreads();
+    if (!at_once || again_count) {
+        // several tokens a warp
+        int per = 1;
+        while (per < p.k) per *= 2;
+        const int tokens = 32 / per;
+        for (int i0 = warp * tokens; i0 < mine; i0 += kWarps * tokens) weigh(i0 + lane / per, per);
     }
     overlap_release();
     __syncthreads();
@@ -608,7 +647,7 @@ static int launch_scored_vpl(ScoredParams p, int smem, cudaStream_t stream)
     p.vec = p.r.E % V == 0 && reinterpret_cast<uintptr_t>(p.r.logits) % (V * sizeof(T)) == 0;
     const auto kernel = moe_choose_scored_kernel<T, VPL>;
     if (p.r.T > kClusterBlocks * kTB)
-        return launch_overlapped(kernel, dim3(p.r.blocks), dim3(kScoredThreads), smem, stream, p);
+        return launch_overlapped(kernel, dim3(p.r.blocks), dim3(kScoredThreads), smem + kTB * p.r.k * 4, stream, p);
     int cluster = 1;
     while (cluster < p.r.blocks) cluster *= 2;  // (blocks without tokens fill it up)
     return launch_overlapped_clusters(kernel, dim3(cluster), cluster, dim3(kScoredThreads), smem, stream, p);
