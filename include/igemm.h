@@ -278,11 +278,11 @@ IGEMM_API int pack_int4(const int8_t *logical, uint8_t *packed, int64_t rows, in
  * codes), the zeroing of C and the GEMM (skinny shapes whose K slices are
  * summed with atomics), the scale transpose and the GEMM (block-scaled fp8);
  * a 4-bit operator, or one on block-scaled fp8 with 128 x 128 scales, one, but
- * igemm_moe_route and igemm_moe_route_scored two or three above 512 tokens (three
- * where the counts that its blocks would all read pass 4 MB: with b blocks
- * 4 b b ceil(E / 4) bytes; igemm_moe_route has ceil(T / 64) blocks, igemm_moe_route_scored as
- * many or more), and pack_mxfp4, pack_nvfp4 or pack_bsfp8 two where rows are packed once
- * and copied (as stated there).
+ * igemm_moe_route two or three above 512 tokens and igemm_moe_route_scored above
+ * min(512, 65536 / E) (three where the counts that its blocks would all read pass 4 MB: with
+ * b blocks 4 b b ceil(E / 4) bytes; b is ceil(T / 64) for igemm_moe_route, as many or more for
+ * igemm_moe_route_scored), and pack_mxfp4, pack_nvfp4 or pack_bsfp8 two where rows are
+ * packed once and copied (as stated there).
  * The split K of the other paths adds a memset, which is not a kernel.
  */
 IGEMM_API uint64_t igemm_kernels_launched(void);
@@ -482,7 +482,8 @@ IGEMM_API int igemm_moe_route(const void *logits, int logits_type, int32_t *expe
  * of the scores, so that scores which round to the same number keep it.
  * E <= 1024, k <= 32, groups <= 32, E a multiple of groups, 1 <= group_k <= groups, group_top
  * 1 or 2, k <= group_k E / groups, T * k < 2^31 (IGEMM_UNSUPPORTED_SHAPE).  T == 0 or k == 0
- * zeroes offsets.  Launches and workspace as for igemm_moe_route.
+ * zeroes offsets.  Workspace as for
+ * igemm_moe_route, where it takes more than one launch.
  */
 typedef enum igemm_score { IGEMM_SOFTMAX = 0, IGEMM_SIGMOID = 1 } igemm_score;
 IGEMM_API int igemm_moe_route_scored(const void *logits, int logits_type, const float *bias, int32_t *experts,

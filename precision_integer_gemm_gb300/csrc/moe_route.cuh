@@ -139,10 +139,10 @@ int launch_route_place(const RouteParams &p, int smem, cudaStream_t stream);
 // blocks of one cluster (p.counts and p.packed_counts null) or on many, of `tb` tokens
 // (at most kTB).
 template <class Choose>
-int route_launch(RouteParams p, cudaStream_t stream, Choose choose, int tb = kTB)
+int route_launch(RouteParams p, cudaStream_t stream, Choose choose, int tb = kTB, int most = kClusterBlocks * kTB)
 {
-    // up to 512 tokens spread over the blocks of a cluster
-    const bool one = p.T <= kClusterBlocks * kTB;
+    // up to `most` tokens (512) spread over the blocks of a cluster
+    const bool one = p.T <= most;
     p.tb = one ? std::max(kFewTokens, (p.T + kClusterBlocks - 1) / kClusterBlocks) : tb;
     p.blocks = static_cast<int>((int64_t(p.T) + p.tb - 1) / p.tb);
     // the places can sum every block's counts themselves, without a scan, while all of

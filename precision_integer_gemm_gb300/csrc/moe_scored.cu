@@ -266,14 +266,18 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
     __shared__ float2 lists[kScoredThreads / 32][32];  // a warp's candidates: c, expert
     for (int e = threadIdx.x; e < p.E; e += kScoredThreads) mask[e] = make_uint2(0, 0);
     if (threadIdx.x == 0) again_count = 0;
+    // (through shared memory: lanes VPL floats apart would take a line each)
+    __shared__ float biases[32 * VPL + VPL];
+    if (sp.bias)
+        for (int e = threadIdx.x; e < p.E; e += kScoredThreads) biases[e + e / 32] = sp.bias[e];
+    __syncthreads();
     float bias[VPL];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) bias[j] = sp.bias && e0 + j < p.E ? sp.bias[e0 + j] : 0.0f;
+    for (int j = 0; j < VPL; ++j) bias[j] = sp.bias && e0 + j < p.E ? biases[e0 + j + (e0 + j) / 32] : 0.0f;
     bool any = false;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) any |= bias[j] != 0.0f;
     const bool biased = __any_sync(0xffffffffu, any);
-    __syncthreads();
     const int t0 = blockIdx.x * p.tb;
     const int mine = min(p.tb, p.T - t0);  // (t0 + tb may pass 2^31)
     const bool grouped = sp.groups > 1;
@@ -646,7 +650,7 @@ static int launch_scored_vpl(ScoredParams p, int smem, cudaStream_t stream)
     constexpr int V = VPL < 16 / int(sizeof(T)) ? VPL : 16 / int(sizeof(T));
     p.vec = p.r.E % V == 0 && reinterpret_cast<uintptr_t>(p.r.logits) % (V * sizeof(T)) == 0;
     const auto kernel = moe_choose_scored_kernel<T, VPL>;
-    if (p.r.T > kClusterBlocks * kTB)
+    if (p.r.counts || p.r.packed_counts)
         return launch_overlapped(kernel, dim3(p.r.blocks), dim3(kScoredThreads), smem + kTB * p.r.k * 4, stream, p);
     int cluster = 1;
     while (cluster < p.r.blocks) cluster *= 2;  // (blocks without tokens fill it up)
@@ -685,7 +689,10 @@ int launch_moe_route_scored(const MoeScoredCall &c, cudaStream_t stream)
                : c.route.x_type == 1 ? launch_scored<__nv_bfloat16>(sp, smem, stream)
                                      : launch_scored<__half>(sp, smem, stream);
     };
-    return route_launch(p, stream, choose, tb);
+    // One cluster is eight blocks: for more than 2^16 scores (or 512 tokens) many blocks are
+    // faster in spite of a second launch (us, one cluster and two launches: 512 x 128 10.6 and
+    // 11.2, 256 x 256 12.2 and 11.7, 512 x 256 18.8 and 11.8, 512 x 1024 47.5 and 24.4).
+    return route_launch(p, stream, choose, tb, std::min(kClusterBlocks * kTB, (1 << 16) / std::max(1, p.E)));
 }
 
 // ---------------------------------------------------------------- gradient

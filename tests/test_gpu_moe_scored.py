@@ -190,6 +190,37 @@ def test_scores_of_very_different_size(T, E, k, groups, group_k, score, spread, 
     check(logits, bias, k, score, groups, group_k, 2)
 
 
+@pytest.mark.parametrize("k", [1, 2, 7, 8, 15, 16, 17, 31, 32])
+@pytest.mark.parametrize("T,E", [(70, 40), (300, 256), (40, 512)])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_numbers_of_choices_and_of_candidates(T, E, k, with_bias):
+    # logits of a few values, so that from k to E experts are as large as the last choice, all of it in one lane's
+    # experts or one in each
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    bias = (torch.randint(0, 3, (E,), generator=g, device="cuda") / 64).float() if with_bias else None
+    for values in (2, 9, 60):
+        logits = torch.randint(0, values, (T, E), generator=g, device="cuda").float() / 8
+        logits[0], logits[1, 1:] = 0.5, -math.inf
+        logits[2] = torch.arange(E, 0, -1, device="cuda") / 16
+        logits[3] = torch.arange(E, device="cuda") % 32
+        for typ in ("f32", "bf16"):
+            check(logits.to(TYPES[typ]), bias, k, "sigmoid", normalize=False)
+            check(logits.to(TYPES[typ]), bias, k, "softmax")
+
+
+@pytest.mark.parametrize("E,one", [(64, 512), (128, 512), (256, 256), (1024, 64)])
+def test_launches(E, one):
+    # one cluster up to 2^16 scores or 512 tokens; above, the choices and the places
+    g = torch.Generator(device="cuda").manual_seed(E)
+    bias = 0.1 * torch.randn((E,), generator=g, device="cuda")
+    for T, launches in ((one - 1, 1), (one, 1), (one + 1, 2)):
+        logits = torch.randn((T, E), generator=g, device="cuda")
+        before = pig.igemm_kernels_launched()
+        route(logits, bias, 8, "sigmoid", 8, 4, 2)
+        assert pig.igemm_kernels_launched() - before == launches
+        check(logits, bias, 8, "sigmoid", 8, 4, 2)
+
+
 @pytest.mark.parametrize("offset", [1, 3])
 def test_logits_off_16_bytes(offset):
     T, E = 600, 128
