@@ -20,9 +20,14 @@
 // and the first lane with the largest value holds the lowest expert.  From the choices to
 // the sorted pairs everything is as without scores (moe_route.cuh).
 //
-// Bound by instructions: 16384 x 256 float32, 8 choices, by sigmoid 24.6 us without bias or
-// groups, 30.2 with a bias, 37.1 with 8 groups by their two best as well (1414 warp
-// instructions a token, issue slots 64 % busy; reading the logits is 2.5 us).
+// The k largest: the k-th largest of the lanes' largest bounds the k-th largest of all from
+// below, so the few experts not below it go to a list, one a lane, and are ranked there (one
+// maximum after another, a lane's next looked for in turn: 37.1 us where this takes 32.1).
+// The weights come last, several tokens a warp (29.2 us).
+//
+// Bound by instructions: 16384 x 256 float32, 8 choices, by sigmoid 20.0 us without bias or
+// groups, 24.6 with a bias, 29.0 with 8 groups by their two best as well (1040 warp
+// instructions a token, issue slots 67 % busy; reading the logits is 2.5 us).
 #include <algorithm>
 #include <math_constants.h>
 #include "launch.cuh"
