@@ -338,7 +338,10 @@ static int launch_pack_format(const Bsfp8PackCall &c, cudaStream_t stream)
 
 // Packed rows copied to their places; where the index is out of range, a row of zeros.
 // A thread takes one 16-byte piece of four rows, a quarter of the rows apart, all in flight.
-// (32768 rows of 4096 out of 4096: 27 us from a cold cache, 138 MB written.)
+// (32768 rows of 4096 out of 4096: 24 us, 138 MB written; two or eight rows a thread 2 and 4
+// us more, bulk copies through shared memory 3.  What is written is the first to leave L2,
+// so that the packed rows stay: 32.8 us for both launches instead of 36.0, and a product
+// that reads the copies next takes as long as before.)
 __global__ void __launch_bounds__(256) bsfp8_copy_rows_kernel(const uint4 *codes, const uint4 *scales, const Bsfp8PackParams p)
 {
     overlap_wait();
@@ -369,14 +372,14 @@ __global__ void __launch_bounds__(256) bsfp8_copy_rows_kernel(const uint4 *codes
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t r = row + i * quarter;
-        if (r < rows) to[r * pitch] = v[i];
+        if (r < rows) __stcs(to + r * pitch, v[i]);
     }
     overlap_release();
 }
 
 // Rows that are gathered twice or more on average are packed once, into a workspace,
 // and copied from there, where that saves reading 32 MB of x at least.  (32768 rows of 4096
-// bfloat16 out of 4096: 35.1 us so, 50 row by row; a second launch costs 4.)
+// bfloat16 out of 4096: 32.8 us so, 50 row by row; a second launch costs 4.)
 static bool pack_once(const Bsfp8PackCall &c)
 {
     const int64_t pieces = bsfp8_code_bytes(c.K) / 16 + bsfp8_scale_pitch(c.K) / 4;
