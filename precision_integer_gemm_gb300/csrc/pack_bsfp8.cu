@@ -338,10 +338,10 @@ static int launch_pack_format(const Bsfp8PackCall &c, cudaStream_t stream)
 
 // Packed rows copied to their places; where the index is out of range, a row of zeros.
 // A thread takes one 16-byte piece of four rows, a quarter of the rows apart, all in flight.
-// (32768 rows of 4096 out of 4096: 24 us, 138 MB written; two or eight rows a thread 2 and 4
-// us more, bulk copies through shared memory 3.  What is written is the first to leave L2,
-// so that the packed rows stay: 32.8 us for both launches instead of 36.0, and a product
-// that reads the copies next takes as long as before.)
+// (32768 rows of 4096 out of 4096, 138 MB written: 36.0 us for both launches, with two or eight
+// rows a thread 38.1 and 40.4, by bulk copies through shared memory 35.5.  With what is written
+// the first to leave L2, so that the packed rows stay, 32.8; a product that reads the
+// copies next takes as long as before.)
 __global__ void __launch_bounds__(256) bsfp8_copy_rows_kernel(const uint4 *codes, const uint4 *scales, const Bsfp8PackParams p)
 {
     overlap_wait();
