@@ -488,11 +488,14 @@ def igemm_moe_route_scored(logits, bias, experts, weights, offsets, tokens, slot
     experts in them; weights = scale * score, over the sum of the chosen scores (normalize)."""
     w = "igemm_moe_route_scored"
     t, size = _type(logits, w)
-    pairs = _n(T, k)
+    if T < 0 or E < 0 or k < 0:
+        scores = pairs = e = 0  # (the library rejects those itself)
+    else:
+        scores, pairs, e = T * E, T * k, E
     _check(load().igemm_moe_route_scored(
-        _dev(logits, size * _n(T, E), w, "logits"), t, _typed(bias, "torch.float32", _n(E), w, "bias"),
+        _dev(logits, size * scores, w, "logits"), t, _typed(bias, "torch.float32", e, w, "bias"),
         _typed(experts, "torch.int32", pairs, w, "experts"), _typed(weights, "torch.float32", pairs, w, "weights"),
-        _typed(offsets, "torch.int32", _n(E + 1), w, "offsets"), _typed(tokens, "torch.int32", pairs, w, "tokens"),
+        _typed(offsets, "torch.int32", e + 1, w, "offsets"), _typed(tokens, "torch.int32", pairs, w, "tokens"),
         _typed(slots, "torch.int32", pairs, w, "slots"), T, E, k, _score(score, w), groups, group_k, group_top,
         1 if normalize else 0, scale, _stream(stream)), w)
 
@@ -505,10 +508,13 @@ def igemm_moe_route_scored_grad(logits, experts, dweights, dlogits, T: int, E: i
     t, size = _type(logits, w)
     if dlogits.dtype != logits.dtype:
         raise ValueError(f"{w}: dlogits must have logits' type")
-    pairs = _n(T, k)
+    if T < 0 or E < 0 or k < 0:
+        scores = pairs = 0  # (the library rejects those itself)
+    else:
+        scores, pairs = T * E, T * k
     _check(load().igemm_moe_route_scored_grad(
-        _dev(logits, size * _n(T, E), w, "logits"), t, _typed(experts, "torch.int32", pairs, w, "experts"),
-        _typed(dweights, "torch.float32", pairs, w, "dweights"), _dev(dlogits, size * _n(T, E), w, "dlogits"), T, E, k,
+        _dev(logits, size * scores, w, "logits"), t, _typed(experts, "torch.int32", pairs, w, "experts"),
+        _typed(dweights, "torch.float32", pairs, w, "dweights"), _dev(dlogits, size * scores, w, "dlogits"), T, E, k,
         _score(score, w), 1 if normalize else 0, scale, _stream(stream)), w)
 
 
@@ -553,7 +559,7 @@ def pack_bsfp8(x, codes, scales, rows: int, K: int, tile_rows: int = 1, format: 
     pack_mxfp4 (index with tile_rows 1 only)."""
     w = "pack_bsfp8"
     t, ld, transposed, r = _pack_operand(w, x, rows, K, index)
-    n = _n(rows)
+    n = rows if rows > 0 else 0
     tiles = n if tile_rows == 1 else -(-n // 128)
     _check(load().pack_bsfp8(x.data_ptr(), t, ld, transposed, _typed(index, "torch.int32", n, w, "index"), r, tile_rows,
                              _fp8_format(format, w), _dev(codes, n * bsfp8_code_bytes(K), w, "codes"),
@@ -562,13 +568,15 @@ def pack_bsfp8(x, codes, scales, rows: int, K: int, tile_rows: int = 1, format: 
 
 
 def _bsfp8_args(A, B, SFA, SFB, C, M, E, N, K, where):
-    kb, pitch = bsfp8_code_bytes(K), bsfp8_scale_pitch(K)
     t, size = _type(C, where)
-    m = _n(M)
-    return ((_dev(A, m * kb, where, "A"), _dev(B, _n(E, N) * kb, where, "B"),
-             _typed(SFA, "torch.float32", m * pitch, where, "SFA"),
-             _typed(SFB, "torch.float32", _n(E, -(-N // 128)) * pitch, where, "SFB")),
-            (_dev(C, size * _n(M, N), where, "C"), t))
+    if M < 0 or E < 0 or N < 0 or K < 0:
+        m = rows = tiles = c = kb = pitch = 0  # (the library rejects those itself)
+    else:
+        kb, pitch = -(-K // 16) * 16, -(-K // 512) * 4
+        m, rows, tiles, c = M, E * N, E * -(-N // 128), size * M * N
+    return ((_dev(A, m * kb, where, "A"), _dev(B, rows * kb, where, "B"),
+             _typed(SFA, "torch.float32", m * pitch, where, "SFA"), _typed(SFB, "torch.float32", tiles * pitch, where, "SFB")),
+            (_dev(C, c, where, "C"), t))
 
 
 def igemm_bsfp8(A, B, SFA, SFB, C, M: int, N: int, K: int, format: str = "e4m3", stream=None) -> None:
