@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
     // groups of whole lanes, a power of two of them
     const int lanes = sp.per / VPL;
     const bool runs = sp.per % VPL == 0 && (lanes & (lanes - 1)) == 0;
-    // up to so many choices the candidates of one search mostly fit a warp's lanes
+    // up to so many choices the candidates of one search mostly fit a warp's lanes (4096 x 512,
+    // 32 choices: 39 us with the search first, 35.5 without)
     const bool few = p.k <= 16;
     const bool scores = biased || (grouped && sp.two);  // every expert's is needed
     constexpr int kWarps = kScoredThreads / 32;
@@ -322,7 +323,8 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
             if (my_e >= 0) atomicOr(i < 32 ? &mask[my_e].x : &mask[my_e].y, 1u << (i & 31));
         }
     };
-    // a token's at once, or (more than two tokens a warp) after the last one
+    // a token's at once, or (more than two tokens a warp) after the last one (2048 x 256: 11.9 us
+    // at once, 13.3 after; 16384 x 256: 32.1 and 29.2)
     const bool at_once = p.tb <= 2 * kWarps;
     for (int i = warp; i < mine; i += kWarps) {
         const int64_t t = t0 + i;
