@@ -595,12 +595,15 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
             }
         }
         if (biased) {
-            // neighbours nearer than the rounding, but for those that are equal in both parts
+            // Neighbours nearer than the rounding, but for those that are equal in both parts: among
+            // the chosen, and behind them as far as the last one chosen does not surely exceed (of
+            // equal ones there another may be the larger).
             const float x = my_e >= 0 ? scored_logit(row, my_e) : kNone;
             const float b = my_e >= 0 ? sp.bias[my_e] : 0.0f, v = my_c;
             const float x2 = __shfl_down_sync(0xffffffffu, x, 1), b2 = __shfl_down_sync(0xffffffffu, b, 1);
-            const float v2 = __shfl_down_sync(0xffffffffu, v, 1);
-            const bool unsure = lane < p.k && lane + 1 < n && !apart(v, v2) && !(x == x2 && b == b2);
+            const float v2 = __shfl_down_sync(0xffffffffu, v, 1), last = __shfl_sync(0xffffffffu, v, p.k - 1);
+            const bool unsure = lane + 1 < n && (lane + 1 < p.k || !apart(last, v2)) && !apart(v, v2) &&
+                                !(x == x2 && b == b2);
             if (__any_sync(0xffffffffu, unsure)) {
                 const double sum64 = sp.sigmoid ? 1.0 : scored_sum_64<T, VPL>(sp, row, m);
                 my_e = scored_order_64(sp, my_e, x, n, m, sum64);
