@@ -100,6 +100,17 @@ __device__ __forceinline__ float scored_group(float a1, float a2, bool two)
     return two && a2 > -CUDART_INF_F ? a1 + a2 : a1;
 }
 
+// How far a group's score may be off its value: twice the error of a c's score (`slack`), and
+// relative to the sizes of its parts, which a sum of both signs does not show, the roundings of
+// the two c (2^-24 each of its own), of their sum and of the bounds that the score is compared by.
+// Without a bias the parts are positive and within 143 2^-23 (e^-y, y up to 84), or below 2^-120.
+__device__ __forceinline__ float scored_slip(float a1, float a2, bool two, float slack, bool biased)
+{
+    const float size = fabsf(a1) + (two && a2 > -CUDART_INF_F ? fabsf(a2) : 0.0f);
+    const float slip = slack + 0x1p-22f * size;
+    return biased ? slip : fminf(slip, 0x1p-15f * size + 0x1p-120f);
+}
+
 // Bit g: group g is taken; lane g holds its score (`none`: nothing to choose).
 template <class F>
 __device__ __forceinline__ uint32_t scored_groups(F score, F none, int groups, int group_k)
@@ -385,7 +396,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
         }
         bool near = false;
         if (grouped) {
-            float score = kNone;  // of group `lane`
+            float score = kNone, slip = 0.0f;  // of group `lane`
             if (runs) {
                 float a1 = kNone, a2 = kNone;
                 if (sp.two && !biased) {
@@ -401,6 +412,7 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
                 }
                 const float mine_score = scored_group(a1, a2, sp.two);
                 score = __shfl_sync(0xffffffffu, mine_score, (lane * lanes) & 31);
+                if (scores) slip = __shfl_sync(0xffffffffu, scored_slip(a1, a2, sp.two, slack, biased), (lane * lanes) & 31);
                 if (lane >= sp.groups) score = kNone;
             } else {
                 for (int g = 0; g < sp.groups; ++g) {
@@ -414,21 +426,21 @@ __global__ void __launch_bounds__(kScoredThreads, VPL <= 8 ? 2 : 1) moe_choose_s
                         const float b1 = __shfl_xor_sync(0xffffffffu, a1, d), b2 = __shfl_xor_sync(0xffffffffu, a2, d);
                         scored_join(a1, a2, b1, b2);
                     }
-                    if (lane == g) score = scored_group(a1, a2, sp.two);
+                    if (lane == g) {
+                        score = scored_group(a1, a2, sp.two);
+                        slip = scored_slip(a1, a2, sp.two, slack, biased);
+                    }
                 }
             }
             uint32_t taken = scored_groups(score, kNone, sp.groups, sp.group_k);
             if (scores) {
-                // the last group taken and the best one left
-                const bool in = taken >> lane & 1u, some = lane < sp.groups && score > kNone;
-                const float least = route_value(__reduce_min_sync(0xffffffffu, in ? route_key(score) : 0xFF800000u));
-                const float most = route_value(__reduce_max_sync(0xffffffffu, in ? kKeyNone : route_key(score)));
-                // (without a bias also by relative errors: two of e^-y, y up to 84, in 143 2^-23)
-                float margin = 2.0f * slack + 0x1p-21f * fabsf(least);
-                if (!biased) margin = fminf(margin, 0x1p-14f * least + 0x1p-119f);
-                if (most > kNone && !(least - most > margin)) {
-                    const uint32_t border =
-                        __ballot_sync(0xffffffffu, some && (in ? !(score - most > margin) : !(least - score > margin)));
+                // the least that a group taken, and the most that one left, may be worth
+                const bool in = taken >> lane & 1u, out = !in && lane < sp.groups && score > kNone;
+                const float low = fmaxf(score - slip, kNone), high = score + slip;  // (+inf less +inf: -inf)
+                const float least = route_value(__reduce_min_sync(0xffffffffu, in ? route_key(low) : 0xFF800000u));
+                const float most = route_value(__reduce_max_sync(0xffffffffu, out ? route_key(high) : kKeyNone));
+                if (most > kNone && !(least > most)) {
+                    const uint32_t border = __ballot_sync(0xffffffffu, (in && !(low > most)) || (out && !(high < least)));
                     // their experts that may be the largest, or the two largest
                     uint32_t cand = 0;
                     for (uint32_t open = border; open; open &= open - 1) {

@@ -1,5 +1,5 @@
-"""The scored routing where float32 cannot tell: equal choices at the border of the k-th with a better one behind them.
-The choice is compared exactly with that of the scores in 64 bits.
+"""The scored routing where float32 cannot tell: equal choices at the border of the k-th with a better one behind them,
+group scores whose parts cancel.  The choice is compared exactly with that of the scores in 64 bits.
 """
 
 import pytest
@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import precision_integer_gemm_gb300 as pig  # noqa: E402
-from test_gpu_moe_scored import check, plain_choice  # noqa: E402
+from test_gpu_moe_scored import check, plain_choice, scores_of  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,45 @@ def test_a_better_one_behind_equal_ones_with_ordinary_biases():
     for k in (1, 3, 8, 17):
         check(logits, bias, k, "sigmoid")
         check(logits, bias, k, "softmax")
+
+
+def cancelling(T, E, groups, size, seed, step):
+    """Logits and a bias of +-size whose two largest of a group cancel: one expert of a group at +size, the others at
+    -size, the groups' logits `step` apart."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    per = E // groups
+    one = torch.randn((T, 1, per), generator=g, device="cuda")
+    logits = one + step * torch.randn((T, groups, per), generator=g, device="cuda")
+    sign = torch.full((groups, per), -1.0, device="cuda")
+    sign[torch.arange(groups), torch.randint(0, per, (groups,), generator=g, device="cuda").cpu()] = 1.0
+    return logits.view(T, E).contiguous(), (size * sign).view(E).contiguous()
+
+
+def decided(logits, bias, score, groups, group_k, group_top):
+    """Tokens whose border between groups taken and left 64 bits can tell.  A score's relative error is at most (E + 8)
+    2^-53 (an exponential, a sum over the experts in some order, a quotient), that of c = s + bias 2^-53 of |c|, that of
+    a group's sum 2^-53 of it; two groups of equal experts with the signs of the biases swapped are equal by the formula
+    and differ by such errors alone (token 2361 of 3000 x 64, softmax, size 0.5: 0 apart in 128 bits)."""
+    T, E = logits.shape
+    s = scores_of(logits.double(), score)[0]
+    v = torch.sort((s + bias.double()).view(T, groups, -1), dim=-1, descending=True)[0][..., :group_top]
+    slip = 2.0 ** -53 * ((E + 8) * group_top * s.amax(-1, keepdim=True) + v.abs().sum(-1) + v.sum(-1).abs())
+    best, at = torch.sort(v.sum(-1), dim=-1, descending=True, stable=True)
+    slip = slip.gather(1, at)
+    low = (best - slip)[:, :group_k].amin(-1)
+    return low > (best + slip)[:, group_k:].amax(-1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [0.5, 4.0, 16.0, 64.0, 100.0, 1000.0])
+@pytest.mark.parametrize("T,E,k,groups,group_k", [(3000, 256, 8, 8, 4), (3000, 64, 4, 32, 5), (1000, 160, 6, 20, 7),
+                                                  (500, 96, 3, 2, 1), (600, 1024, 8, 16, 3)])
+def test_group_scores_of_parts_that_cancel(T, E, k, groups, group_k, size, score):
+    # c is rounded at the size of the bias, the sum of the two is as small as the scores
+    for step in (1e-6, 1e-5, 1e-4):
+        logits, bias = cancelling(T, E, groups, size, E + groups, step)
+        for group_top in (1, 2):
+            sure = decided(logits, bias, score, groups, group_k, group_top)
+            # (32 groups 1e-6 apart, float32 logits 2^-23 apart: one border in seven is between equal groups)
+            assert sure.float().mean().item() > 0.5
+            check(logits[sure], bias, k, score, groups, group_k, group_top)
