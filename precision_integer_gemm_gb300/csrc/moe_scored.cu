@@ -94,10 +94,13 @@ __device__ __forceinline__ void scored_join(float &a1, float &a2, float b1, floa
     a1 = fmaxf(a1, b1);
 }
 
-// The sum of a group's largest, or of its two largest where there are two.
+// The sum of a group's largest, or of its two largest where there are two.  (Sums past the range
+// stay at its end: -inf is a group of no experts, and the bounds of such sums are infinite, so that
+// 64 bits decide.)
 __device__ __forceinline__ float scored_group(float a1, float a2, bool two)
 {
-    return two && a2 > -CUDART_INF_F ? a1 + a2 : a1;
+    if (!two || !(a2 > -CUDART_INF_F)) return a1;
+    return fmaxf(fminf(a1 + a2, CUDART_MAX_NORMAL_F), -CUDART_MAX_NORMAL_F);
 }
 
 // How far a group's score may be off its value: twice the error of a c's score (`slack`), and

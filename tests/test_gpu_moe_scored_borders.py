@@ -1,6 +1,9 @@
 """The scored routing where float32 cannot tell: equal choices at the border of the k-th with a better one behind them,
-group scores whose parts cancel.  The choice is compared exactly with that of the scores in 64 bits.
+group scores whose parts cancel, biases at the ends of float32's range.  The choice is compared exactly with that of the
+scores in 64 bits.
 """
+
+import math
 
 import pytest
 
@@ -101,3 +104,35 @@ def test_group_scores_of_parts_that_cancel(T, E, k, groups, group_k, size, score
             # (32 groups 1e-6 apart, float32 logits 2^-23 apart: one border in seven is between equal groups)
             assert sure.float().mean().item() > 0.5
             check(logits[sure], bias, k, score, groups, group_k, group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("low", [torch.finfo(torch.float32).min, -1e38, -3e38])
+def test_groups_switched_off_by_the_lowest_bias(low, group_top, score):
+    # only -inf and NaN are never chosen: with more groups to take than are left, those of the lowest finite bias follow
+    g = torch.Generator(device="cuda").manual_seed(11)
+    for T, E, k, groups, group_k, on in ((200, 64, 32, 8, 5, 3), (50, 256, 8, 8, 4, 2), (40, 256, 32, 32, 8, 1),
+                                         (30, 60, 12, 20, 4, 0)):
+        logits = torch.randn((T, E), generator=g, device="cuda")
+        bias = 0.1 * torch.randn((E,), generator=g, device="cuda")
+        bias.view(groups, -1)[on:] = low
+        check(logits, bias, k, score, groups, group_k, group_top)
+        bias.view(groups, -1)[on:, 1:] = 0.0  # one expert of a group off
+        check(logits, bias, k, score, groups, group_k, group_top)
+        bias.view(groups, -1)[-1] = -math.inf
+        check(logits, bias, k, score, groups, group_k, group_top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_groups_of_the_largest_bias(group_top, score):
+    g = torch.Generator(device="cuda").manual_seed(12)
+    T, E, k, groups = 100, 64, 8, 8
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    for high in (torch.finfo(torch.float32).max, math.inf, 2e38):
+        bias = 0.1 * torch.randn((E,), generator=g, device="cuda")
+        bias[8:16] = bias[40:48] = high
+        bias[56] = high
+        for group_k in (1, 2, 4):
+            check(logits, bias, k, score, groups, group_k, group_top)
