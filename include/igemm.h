@@ -495,8 +495,10 @@ IGEMM_API int igemm_moe_route_scored(const void *logits, int logits_type, const 
  * Its gradient: that of the logits for that of the weights (the choice has none, nor the
  * bias).  Arguments as for igemm_moe_route_scored.
  *   logits    [T, E], experts [T, k] (device), read only; experts outside [0, E), and those
- *             whose logit is -inf or NaN, have no weight; one that a token names twice gets
- *             the sum
+ *             whose logit is -inf or NaN, have no weight, nor with softmax have those of a
+ *             token that names one of logit +inf; one that a token names twice gets the sum.
+ *             (With softmax and normalize the logits of experts that are not named are not
+ *             read: a +inf among them, on which the routing chooses nothing, is not seen.)
  *   dweights  [T, k] float32 (device), read only
  *   dlogits   [T, E] of logits_type (device), written: every element, 0 where the weights do
  *             not depend on it

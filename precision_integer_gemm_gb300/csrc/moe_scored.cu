@@ -756,6 +756,12 @@ __global__ void __launch_bounds__(256) moe_scored_grad_kernel(const T *logits, c
             e = -1;
             g = 0.0f;
         }
+        // a softmax row with +inf has no scores (renormalised, the other logits are not read: only
+        // where it is named)
+        if (!sigmoid && __any_sync(0xffffffffu, x == CUDART_INF_F)) {
+            e = -1;
+            g = 0.0f;
+        }
         float m = 0.0f, inv = 0.0f;
         if (dense) {
             // the row's largest and the sum, a lane's running ones joined

@@ -1,6 +1,6 @@
 """The scored routing where float32 cannot tell: equal choices at the border of the k-th with a better one behind them,
-group scores whose parts cancel, biases at the ends of float32's range.  The choice is compared exactly with that of the
-scores in 64 bits.
+group scores whose parts cancel, biases at the ends of float32's range; its gradient on rows without scores.  The choice
+is compared exactly with that of the scores in 64 bits.
 """
 
 import math
@@ -10,7 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import precision_integer_gemm_gb300 as pig  # noqa: E402
-from test_gpu_moe_scored import check, plain_choice, scores_of  # noqa: E402
+from test_gpu_moe_scored import check, grad, plain_choice, scores_of  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +136,23 @@ def test_groups_of_the_largest_bias(group_top, score):
         bias[56] = high
         for group_k in (1, 2, 4):
             check(logits, bias, k, score, groups, group_k, group_top)
+
+
+@pytest.mark.parametrize("typ", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gradient_of_a_named_expert_without_scores(normalize, typ):
+    # a softmax row with +inf has no scores, also where its experts are named; a sigmoid of +inf is 1 and flat
+    T, E, k = 6, 40, 3
+    g = torch.Generator(device="cuda").manual_seed(2)
+    logits = torch.randn((T, E), generator=g, device="cuda").to(typ)
+    experts = torch.tensor([[3, 1, 2]] * T, device="cuda")
+    dw = torch.randn((T, k), generator=g, device="cuda")
+    logits[0, 3] = math.inf
+    logits[1, 2] = math.inf
+    logits[2, 1:4] = math.inf
+    rest = grad(logits, experts, dw, "softmax", normalize, 1.0)
+    assert bool(torch.isfinite(rest).all()) and bool((rest[:3] == 0).all()) and bool((rest[3:] != 0).any(-1).all())
+    alone = grad(logits[3:].contiguous(), experts[3:].contiguous(), dw[3:].contiguous(), "softmax", normalize, 1.0)
+    assert torch.equal(alone, rest[3:])
+    flat = grad(logits, experts, dw, "sigmoid", normalize, 1.0)
+    assert bool(torch.isfinite(flat).all()) and flat[0, 3] == 0 and flat[1, 2] == 0 and bool((flat[2, 1:4] == 0).all())
