@@ -1,7 +1,9 @@
 // Block-scaled fp8 with one float32 scale per 128 k of a row (activations) or per
 // 128 rows and 128 k (weights): layout and the calls of its entry points.
 #pragma once
+#include <atomic>
 #include <cstdint>
+#include <mutex>
 #include <cuda_runtime.h>
 
 namespace igemm {
@@ -14,6 +16,22 @@ constexpr int kBsfp8MaxTiles = 0x3FFFFFFF;  // of one call
 constexpr int bsfp8_code_bytes(int K) { return (K / 16 + (K % 16 ? 1 : 0)) * 16; }
 // Scales of a row: one per 128 k, rounded up to four (16 bytes).
 constexpr int bsfp8_scale_pitch(int K) { return ((K - 1) / 512 + 1) * 4; }
+
+// The answer of ask(), 0 or more, asked for once: `known` keeps one more than it (0: not
+// asked yet; no lock once known, a small call asks several times).  Below 0 the question
+// failed: 0 this time, and asked again the next.
+template <class Ask>
+int bsfp8_ask_once(std::atomic<int> &known, std::mutex &mu, Ask ask)
+{
+    if (const int kept = known.load(std::memory_order_acquire)) return kept - 1;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known) {
+        const int n = ask();
+        if (n < 0) return 0;
+        known.store(n + 1, std::memory_order_release);
+    }
+    return known - 1;
+}
 
 // A product: rows x N, dense (offsets null, experts 1) or grouped by expert.
 struct Bsfp8Call {

@@ -28,49 +28,49 @@ struct Bsfp8Smem {
 };
 
 // Clusters of `csize` CTAs of igemm_bsfp8_kernel<Cfg> that can be resident at once, 0
-// if none fits (asked once per device and size); sets the kernel's shared-memory limit.
+// if none fits, below 0 where the runtime does not say; sets the kernel's shared-memory limit.
+template <class Cfg>
+int bsfp8_ask_clusters(int csize)
+{
+    auto kernel = igemm_bsfp8_kernel<Cfg>;
+    int n = sm_count();
+    cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (Cfg::PAIR && rc == cudaSuccess) {
+        // the warps' shares of registers are dealt out of 168 a thread
+        cudaFuncAttributes attr;
+        rc = cudaFuncGetAttributes(&attr, kernel);
+        if (rc == cudaSuccess && attr.numRegs != 168) return 0;
+    }
+    if (rc == cudaSuccess && csize > 1) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = csize;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(csize * sm_count(), 1, 1);
+        cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+        cfg.dynamicSmemBytes = 227 * 1024;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        rc = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    }
+    if (rc != cudaSuccess) {
+        cudaGetLastError();  // (the launch of another kernel is not to report it)
+        return -1;
+    }
+    return std::max(n, 0);
+}
+
+// ... asked once per device and size.
 template <class Cfg>
 int bsfp8_clusters(int csize)
 {
     static std::mutex mu;
-    // one more than the clusters (a small call asks several times: no lock once known)
-    static std::atomic<int> cache[64][3] = {};
+    static std::atomic<int> known[64][3] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    const int slot = csize == 1 ? 0 : csize == 2 ? 1 : 2;
-    if (const int known = cache[dev][slot].load(std::memory_order_acquire)) return known - 1;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!cache[dev][slot]) {
-        auto kernel = igemm_bsfp8_kernel<Cfg>;
-        int n = sm_count();
-        cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-        if (Cfg::PAIR && rc == cudaSuccess) {
-            // the warps' shares of registers are dealt out of 168 a thread
-            cudaFuncAttributes attr;
-            rc = cudaFuncGetAttributes(&attr, kernel);
-            if (rc == cudaSuccess && attr.numRegs != 168) return 0;
-        }
-        if (rc == cudaSuccess && csize > 1) {
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = csize;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.gridDim = dim3(csize * sm_count(), 1, 1);
-            cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
-            cfg.dynamicSmemBytes = 227 * 1024;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            rc = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-        }
-        if (rc != cudaSuccess) {
-            cudaGetLastError();  // (the launch of another kernel is not to report it)
-            return 0;
-        }
-        cache[dev][slot].store(std::max(n, 0) + 1, std::memory_order_release);
-    }
-    return cache[dev][slot] - 1;
+    return bsfp8_ask_once(known[dev][csize == 1 ? 0 : csize == 2 ? 1 : 2], mu, [&] { return bsfp8_ask_clusters<Cfg>(csize); });
 }
 
 template <class Cfg>
