@@ -149,12 +149,6 @@ __device__ __forceinline__ Fp4Tile bsfp8_tile(const Bsfp8Params &prm, const Fp4G
     return x;
 }
 
-__device__ __forceinline__ unsigned long long bsfp8_pair(float lo, float hi)
-{
-    unsigned long long p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-    return p;
-}
 using F2 = float2;
 __device__ __forceinline__ void bsfp8_fma2(F2 &t, uint32_t v0, uint32_t v1, F2 s)
 {

@@ -590,16 +590,6 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t smem_addr, uint32_t a
 // registers as rewritten after the wait (an empty asm per register, ordered
 // after the wait like every volatile asm), so no use of a loaded value can be
 // scheduled before the wait.
-// The wait alone: for values that are next touched by volatile asm (tmem_pair), which
-// stays behind it.  (Marked one by one, every loaded register is copied once.)
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ unsigned long long tmem_pair(uint32_t lo, uint32_t hi)
-{
-    unsigned long long p;
-    asm volatile("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
-    return p;
-}
-
 template <int N>
 __device__ __forceinline__ void tmem_ld_wait_regs(uint32_t (&r)[N])
 {
