@@ -1,6 +1,6 @@
 """The scored routing where float32 cannot tell: equal choices at the border of the k-th with a better one behind them,
-group scores whose parts cancel, biases at the ends of float32's range; its gradient on rows without scores.  The choice
-is compared exactly with that of the scores in 64 bits.
+group scores whose parts cancel, biases at the ends of float32's range; its launches for long prompts; its
+gradient on rows without scores.  The choice is compared exactly with that of the scores in 64 bits.
 """
 
 import math
@@ -10,7 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import precision_integer_gemm_gb300 as pig  # noqa: E402
-from test_gpu_moe_scored import check, grad, plain_choice, scores_of  # noqa: E402
+from test_gpu_moe_scored import check, grad, plain_choice, route, scores_of  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -136,6 +136,24 @@ def test_groups_of_the_largest_bias(group_top, score):
         bias[56] = high
         for group_k in (1, 2, 4):
             check(logits, bias, k, score, groups, group_k, group_top)
+
+
+@pytest.mark.parametrize("T,E,launches", [(4864, 256, 3), (4865, 256, 3), (16384, 256, 3), (19456, 256, 3), (20000, 256, 3),
+                                          (1025, 1024, 3), (9000, 64, 3), (9000, 16, 2)])
+@pytest.mark.parametrize("typ", [torch.float32, torch.bfloat16])
+def test_long_prompts(T, E, launches, typ):
+    # blocks of more than 16 tokens and of more than 32 (a mask's second word), more than one wave of them, the scan
+    g = torch.Generator(device="cuda").manual_seed(T)
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    logits[torch.rand((T, E), generator=g, device="cuda") < 0.1] = -math.inf
+    logits[T - T // 20:] = -math.inf
+    logits = logits.to(typ)
+    bias = 0.1 * torch.randn((E,), generator=g, device="cuda")
+    before = pig.igemm_kernels_launched()
+    route(logits, bias, 4, "sigmoid", 8, 4, 2)
+    assert pig.igemm_kernels_launched() - before == launches
+    check(logits, bias, 4, "sigmoid", 8, 4, 2, scale=2.5)
+    check(logits, None, 4, "softmax", 8, 3, 1, normalize=False)
 
 
 @pytest.mark.parametrize("typ", [torch.float32, torch.bfloat16, torch.float16])
