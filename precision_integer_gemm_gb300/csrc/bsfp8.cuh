@@ -50,6 +50,7 @@ struct Bsfp8Plan {
     int cs;        // CTAs that split k
     int group_p;   // weight tiles per group of the tile order
     double groups;  // expected groups with any rows
+    bool stream;   // the weights leave L2 first
 };
 
 // The kernel, tile and split for a call; max_clusters(bn, pair, csize) says how

@@ -51,7 +51,7 @@ bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Pl
         const double cost = full * wave(clusters) + (rest > 0.01 ? wave(rest) : 0.0) + (bn >= 64 ? 0.0 : split);
         if (best < 0 || cost < best) {
             best = cost;
-            *plan = Bsfp8Plan{bn, pair, cs, 1, groups};
+            *plan = Bsfp8Plan{bn, pair, cs, 1, groups, false};
         }
     };
     for (int bn = 16; bn <= 128; bn *= 2) {
@@ -68,6 +68,13 @@ bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Pl
     const int64_t slot_bytes = int64_t(plan->pair ? 256 : 128) * bsfp8_code_bytes(c.K);
     plan->group_p = static_cast<int>(
         std::max<int64_t>(1, std::min<int64_t>(p_tiles, (int64_t(32) << 20) / slot_bytes)));
+    // Weights from 24 MB on leave L2 first, before what other kernels left there (us, with and
+    // without: 64 x 28672 x 8192 42.4 and 43.3, two tiles of 64 50.9 and 51.7; 512 rows over 64
+    // experts of 4096 x 4096 157.3 and 158.5), but where many groups of several have more rows than
+    // a tile and read theirs again (4096 rows over 64 experts 196 and 184, 3600 over 128 359 and
+    // 328, 8192 389 and 362; with fewer rows a group than two thirds of a tile within 1 %).
+    plan->stream = !plan->pair && groups * c.N * double(bsfp8_code_bytes(c.K)) >= 24.0 * (1 << 20) &&
+                   (!c.offsets || 3 * typical <= 2 * plan->bn);
     return true;
 }
 

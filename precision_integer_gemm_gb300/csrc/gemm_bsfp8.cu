@@ -112,8 +112,7 @@ static int launch_bsfp8_cfg(const Bsfp8Call &c, const Bsfp8Plan &plan, cudaStrea
     prm.slice = ((prm.blocks + 3) / 4 + plan.cs - 1) / plan.cs * 4;
     // every slice of k holds at least one block
     if (plan.cs > 1 && prm.slice * (plan.cs - 1) >= prm.blocks) return kUnsupportedShape;
-    // weights from 24 MB on leave L2 first, before what other kernels left there
-    prm.stream = !Cfg::PAIR && plan.groups * c.N * double(pitch) >= 24.0 * (1 << 20);
+    prm.stream = plan.stream;
     prm.format = c.format;
     const uintptr_t rows_at = reinterpret_cast<uintptr_t>(c.C) | (static_cast<uintptr_t>(c.N) * (c.c_type == kOutF32 ? 4 : 2));
     prm.store_bytes = rows_at % 16 == 0 ? 16 : rows_at % 4 == 0 ? 4 : 2;

@@ -27,6 +27,20 @@ def test_answers_are_kept(tmp_path):
     assert r.stdout.startswith("ask once ok")
 
 
+def test_weights_that_leave_l2_first(tmp_path):
+    cuda = "/usr/local/cuda/include"
+    if not shutil.which("g++") or not os.path.isdir(cuda):
+        pytest.skip("g++ or the CUDA headers are missing")
+    exe = str(tmp_path / "stream")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", CSRC, "-I", cuda, "-x", "c++",
+                        os.path.join(ROOT, "tests", "c", "bsfp8_stream_check.cpp"), os.path.join(CSRC, "bsfp8_plan.cu"), "-o", exe],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
+    assert r.stdout.startswith("bsfp8 stream ok")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K,grouped,kernel", [(4096, 4096, 1024, False, "<256, true>"), (2048, 4096, 512, True, "<256, true>"),
                                                   (16, 512, 1024, False, "<16, false>")])
