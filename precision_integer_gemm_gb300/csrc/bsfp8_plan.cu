@@ -59,7 +59,9 @@ bool bsfp8_plan(const Bsfp8Call &c, int (*max_clusters)(int, bool, int), Bsfp8Pl
         if (typical > 16 * bn) continue;
         for (int cs = 1; cs <= 4; cs *= 2) consider(bn, false, cs);
     }
-    // (not with rows of C that only 2-byte pieces reach, a lane a row)
+    // (Not with rows of C that only 2-byte pieces reach, a lane a row.  What that costs 16-bit C of
+    // odd N, N = 8191 and 8190, K = 8192, us: 600 rows 80 and 61, 2048 186 and 120, 4096 369 and 207;
+    // float32 C of odd N stays on pairs, 226 at 4096.)
     if (typical > 64 && rows_at % 4 == 0) consider(256, true, 1);
     if (best < 0) consider(128, false, 1);  // (no pairs, and more rows than the loop above takes)
     if (best < 0) return false;

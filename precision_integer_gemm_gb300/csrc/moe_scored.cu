@@ -25,8 +25,8 @@
 // maximum after another, a lane's next looked for in turn: 37.1 us where this takes 32.1).
 // The weights come last, several tokens a warp (29.2 us).
 //
-// Bound by instructions: 16384 x 256 float32, 8 choices, by sigmoid 20.0 us without bias or
-// groups, 24.6 with a bias, 29.0 with 8 groups by their two best as well (1040 warp
+// Bound by instructions: 16384 x 256 float32, 8 choices, by sigmoid 20.4 us without bias or
+// groups, 24.7 with a bias, 29.5 with 8 groups by their two best as well (1057 warp
 // instructions a token, issue slots 67 % busy; reading the logits is 2.5 us).
 #include <algorithm>
 #include <math_constants.h>
@@ -715,8 +715,12 @@ int launch_moe_route_scored(const MoeScoredCall &c, cudaStream_t stream)
                                      : launch_scored<__half>(sp, smem, stream);
     };
     // One cluster is eight blocks: for more than 2^16 scores (or 512 tokens) many blocks are
-    // faster in spite of a second launch (us, one cluster and two launches: 512 x 128 10.6 and
-    // 11.2, 256 x 256 12.2 and 11.7, 512 x 256 18.8 and 11.8, 512 x 1024 47.5 and 24.4).
+    // faster in spite of a second launch (us a call, one cluster and two launches, softmax alone:
+    // 256 x 256 9.0 and 10.6, 512 x 128 10.6 and 10.5, 512 x 256 12.2 and 10.6, 512 x 1024 24.6 and
+    // 12.6; sigmoids, a bias, 8 groups by two: 256 x 128 10.3 and 11.2, 256 x 256 12.3 and 10.9, 512
+    // x 128 15.2 and 11.3, 512 x 256 18.4 and 10.8, 512 x 1024 39.7 and 17.0.  In a captured graph,
+    // without the host's time, two launches gain from half of that size on: 512 x 128 10.2 and 6.8,
+    // 14.8 and 8.1).
     return route_launch(p, stream, choose, tb, std::min(kClusterBlocks * kTB, (1 << 16) / std::max(1, p.E)));
 }
 

@@ -131,7 +131,8 @@ __device__ __forceinline__ void bsfp8_pad_scales(const Bsfp8PackParams &p, float
 
 // Row-major x, a scale per 128 rows and 128 k: a CTA per such tile, eight lanes a row
 // and four rows a thread, held in registers as they were read until the tile's largest
-// is known (one reading of x; a second one would be half as much traffic again).
+// is known (one reading of x; a second one would be half as much traffic again).  (28672 x
+// 8192: float32 177 us, 6.6 TB/s, bfloat16 106, 6.6; 4096 x 4096 bfloat16 10.2.)
 template <int FMT, class T, bool VEC>
 __global__ void __launch_bounds__(256) pack_bsfp8_tiles_kernel(const T *x, const Bsfp8PackParams p)
 {
@@ -172,8 +173,9 @@ __global__ void __launch_bounds__(256) pack_bsfp8_tiles_kernel(const T *x, const
 // Transposed x [K, rows]: a CTA takes 128 k (16 per warp) by P times 32 R rows (R a
 // lane, so loads run along x's rows; R = 2 for pairs of 16-bit values), held in
 // registers until the largest of each row, or (TILE) of 128 rows, is known.  The codes
-// go through shared memory to leave as runs of 128 bytes.  (28672 x 8192 float32, a scale
-// per 128 x 128: 188 us, 6.2 TB/s.)
+// go through shared memory to leave as runs of 128 bytes.  (28672 x 8192, a scale
+// per 128 x 128: float32 189 us, 6.2 TB/s, bfloat16 109, 6.5; a scale per row 176, 6.7, and 127,
+// 5.6.)
 template <int FMT, class T, int R, bool TILE>
 __global__ void __launch_bounds__(256) pack_bsfp8_transposed_kernel(const T *x, const Bsfp8PackParams p)
 {
