@@ -49,7 +49,11 @@ struct ScoredParams {
     int vec;  // rows of whole runs
 };
 
-__device__ __forceinline__ float scored_sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+// (Below -80 it is e^x to every bit, down to the smallest float32, where e^-x would pass the largest.)
+__device__ __forceinline__ float scored_sigmoid(float x)
+{
+    return x < -80.0f ? expf(x) : __fdiv_rn(1.0f, 1.0f + expf(-x));
+}
 // For the choice: within 1.63 2^-22 (an exponential of 2 + 1.173 |x| ulp counts s (1 - s),
 // the sum 2^-24, the quotient 2 ulp).
 __device__ __forceinline__ float scored_sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }

@@ -174,3 +174,22 @@ def test_gradient_of_a_named_expert_without_scores(normalize, typ):
     assert torch.equal(alone, rest[3:])
     flat = grad(logits, experts, dw, "sigmoid", normalize, 1.0)
     assert bool(torch.isfinite(flat).all()) and flat[0, 3] == 0 and flat[1, 2] == 0 and bool((flat[2, 1:4] == 0).all())
+
+
+@pytest.mark.parametrize("typ", [torch.float32, torch.bfloat16])
+def test_sigmoids_below_the_smallest_normal_number(typ):
+    # e^-88.8 .. e^-103: float32 holds them to fewer and fewer bits, the weights and the gradients that are made of them
+    # to half of its smallest step, 2^-150, and the rounding of a product or two
+    T, E, k = 40, 64, 8
+    logits = torch.linspace(-104.0, -86.0, T * E, device="cuda").view(T, E).to(typ).contiguous()
+    got = route(logits, None, k, "sigmoid", normalize=False, scale=1.0)
+    want = torch.sigmoid(logits.double().gather(1, got["experts"].long()))
+    tol = 250 * 2.0 ** -24 * want + 2.0 ** -149  # (spread 104: as in test_gpu_moe_scored)
+    assert bool(((got["weights"].double() - want).abs() <= tol).all()) and bool((got["weights"][:-1] > 0).any())
+    # above: s (1 - s) of logits whose 1 - s is as small
+    dw = torch.ones((T, k), device="cuda")
+    for x in (logits, -logits):
+        d = grad(x.contiguous(), got["experts"].long(), dw, "sigmoid", False, 1.0).gather(1, got["experts"].long())
+        s = torch.sigmoid(-x.double().abs()).gather(1, got["experts"].long())
+        rounded = torch.finfo(typ).eps / 2 * s + (2.0 ** -134 if typ == torch.bfloat16 else 0.0)  # (half bfloat16's smallest)
+        assert bool(((d.double() - s * (1 - s)).abs() <= 250 * 2.0 ** -24 * s + 2.0 ** -148 + rounded).all())
