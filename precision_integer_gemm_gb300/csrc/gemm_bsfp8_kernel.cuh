@@ -25,8 +25,8 @@
 // 28672 x 8192 39.7 us for 37.6), one that loads codes, one for the scales.  Persistent CTAs
 // (or CTA pairs, or clusters that split k).  Every wait is bounded.
 //
-// What bounds it.  A few activations: HBM, the weights once (16 x 28672 x 8192: 37.7 us, 6.3
-// TB/s).  Many: the epilogue, which reads a block's 128 x 256 sums of each CTA from tensor
+// What bounds it.  A few activations: HBM, the weights once (16 x 28672 x 8192: 37.7 to 38.3 us,
+// 6.2 TB/s).  Many: the epilogue, which reads a block's 128 x 256 sums of each CTA from tensor
 // memory and adds them in some 900 cycles, where the block's MMAs take 512 (8192^3: 427 to
 // 460 us, 2390 to 2575 TFLOP/s at 1.7 to 2.0 GHz; the MMAs alone, without scales, 342 to
 // 368 at 1.4 GHz and the part's power limit).

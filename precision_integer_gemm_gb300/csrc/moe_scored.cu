@@ -49,10 +49,10 @@ struct ScoredParams {
     int vec;  // rows of whole runs
 };
 
-// (Below -80 it is e^x to every bit, down to the smallest float32, where e^-x would pass the largest.)
+// (Below -88 it is e^x to every bit, down to the smallest float32; e^-x passes the largest at 88.7.)
 __device__ __forceinline__ float scored_sigmoid(float x)
 {
-    return x < -80.0f ? expf(x) : __fdiv_rn(1.0f, 1.0f + expf(-x));
+    return x < -88.0f ? expf(x) : __fdiv_rn(1.0f, 1.0f + expf(-x));
 }
 // For the choice: within 1.63 2^-22 (an exponential of 2 + 1.173 |x| ulp counts s (1 - s),
 // the sum 2^-24, the quotient 2 ulp).
